@@ -33,6 +33,8 @@ EXPORTS = ("lstm_fwd_workspace_size", "lstm_bwd_workspace_size", "lstm_fwd_works
            "lstm_fwd_ex", "lstm_bwd_ex", "lstm_stack_fwd_workspace_size",
            "lstm_stack_bwd_workspace_size", "lstm_stack_bwd_workspace_size_min",
            "lstm_stack_fwd", "lstm_stack_bwd",
+           "lstm_embed_fwd", "lstm_embed_bwd_workspace_size", "lstm_embed_bwd",
+           "lstm_logprob_fwd_workspace_size", "lstm_logprob_fwd", "lstm_logprob_bwd",
            "lstm_status", "lstm_profile_begin", "lstm_profile_end", "lstm_launch_count",
            "lstm_strerror", "lstm_abi_version")
 
@@ -61,6 +63,16 @@ class Options(ctypes.Structure):
     (LSTM_GATES_IFJO / LSTM_GATES_IJFO)."""
     _fields_ = [("seq_mask", ctypes.c_void_p), ("direction", ctypes.c_int),
                 ("gate_order", ctypes.c_int)]
+
+
+class EmbedDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("vocab", ctypes.c_int), ("I", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("id_bytes", ctypes.c_int)]
+
+
+class LogprobDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("vocab", ctypes.c_int), ("ld", ctypes.c_longlong),
+                ("top", ctypes.c_int), ("dtype", ctypes.c_int), ("id_bytes", ctypes.c_int)]
 
 
 _lib = None
@@ -138,6 +150,19 @@ def load(path: str = LIB_PATH):
     lib.lstm_test_bwd_chunks.restype = ip
     lib.lstm_test_chunk_bound.argtypes = [ip, ip, ip]
     lib.lstm_test_chunk_bound.restype = ip
+    ep, lp, fp = ctypes.POINTER(EmbedDims), ctypes.POINTER(LogprobDims), ctypes.c_float
+    lib.lstm_embed_fwd.argtypes = [ep, vp, vp, fp, vp, vp]
+    lib.lstm_embed_fwd.restype = ip
+    lib.lstm_embed_bwd_workspace_size.argtypes = [ep]
+    lib.lstm_embed_bwd_workspace_size.restype = sz
+    lib.lstm_embed_bwd.argtypes = [ep, vp, vp, fp, ip, vp, vp, sz, vp]
+    lib.lstm_embed_bwd.restype = ip
+    lib.lstm_logprob_fwd_workspace_size.argtypes = [lp]
+    lib.lstm_logprob_fwd_workspace_size.restype = sz
+    lib.lstm_logprob_fwd.argtypes = [lp, vp, vp, fp] + [vp] * 5 + [vp, sz, vp]
+    lib.lstm_logprob_fwd.restype = ip
+    lib.lstm_logprob_bwd.argtypes = [lp, vp, vp, fp] + [vp] * 5 + [ll, vp]
+    lib.lstm_logprob_bwd.restype = ip
     v = lib.lstm_abi_version()
     if v // 100 != ABI_VERSION // 100 or v < ABI_VERSION:
         raise RuntimeError(f"{path}: ABI version {v}, this binding needs {ABI_VERSION} "
@@ -512,3 +537,185 @@ def backward_stack(st: StackState, x, Ws, h0=None, c0=None, dy=None, dhT=None, d
                    g.db, g.dh0, g.dc0, ws, stream=stream, mask=mask, reverse=reverse,
                    gate_order=gate_order)
     return g
+
+
+# ------------------------------------------- operators of a language model
+LOGPROB_MAX_TOP = 64
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(ref: torch.Tensor, **ts) -> None:
+    """Every tensor given is on ref's CUDA device."""
+    _need(ref.is_cuda, "tensors must be on a CUDA device")
+    for name, t in ts.items():
+        _need(t is None or t.device == ref.device, f"{name} is on another device")
+
+
+def _dense(**ts) -> None:
+    for name, t in ts.items():
+        _need(t is None or t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype=None) -> None:
+    if t is not None:
+        _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
+        _need(dtype is None or t.dtype == dtype, f"{name}: {t.dtype}, want {dtype}")
+
+
+def _id_bytes(ids: Optional[torch.Tensor]) -> int:
+    if ids is None:
+        return 8
+    _need(ids.dtype in (torch.int32, torch.int64), f"token ids must be int32 or int64, not {ids.dtype}")
+    return ids.element_size()
+
+
+def _run(code: int, where: str) -> None:
+    if code != LSTM_OK:
+        raise LstmError(code, where)
+
+
+def _ws_bytes(ws: torch.Tensor) -> int:
+    return ws.numel() * ws.element_size()
+
+
+def embed_dims(N: int, vocab: int, I: int, dtype, id_bytes: int = 8) -> EmbedDims:
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    return EmbedDims(int(N), int(vocab), int(I), code, int(id_bytes))
+
+
+def embed(ids, table, scale: float = 1.0, out=None, stream=None) -> torch.Tensor:
+    """lstm_embed_fwd: x[..., I] = scale * table[ids] (table [vocab, I], ids
+    int32 / int64 of any shape, e.g. [T, B] for an x [T, B, I]); ids outside
+    the table are padding and give zeros."""
+    _need(table.dim() == 2, "table must be [vocab, I]")
+    _on(table, ids=ids, out=out)
+    _dense(ids=ids, table=table, out=out)
+    vocab, I = table.shape
+    shape = (*ids.shape, I)
+    _shaped(out, "out", shape, table.dtype)
+    with torch.cuda.device(table.device):
+        if out is None:
+            out = torch.empty(shape, dtype=table.dtype, device=table.device)
+        d = embed_dims(ids.numel(), vocab, I, table.dtype, _id_bytes(ids))
+        _run(load().lstm_embed_fwd(ctypes.byref(d), _p(ids), _p(table), float(scale), _p(out),
+                                   _stream(stream)), "lstm_embed_fwd")
+    return out
+
+
+def embed_bwd_workspace_size(d: EmbedDims) -> int:
+    return int(load().lstm_embed_bwd_workspace_size(ctypes.byref(d)))
+
+
+def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate: bool = False,
+                   ws=None, stream=None) -> torch.Tensor:
+    """lstm_embed_bwd: the table's gradient [vocab, I] (float32) of
+    embed(ids, table, scale) for dx [..., I] (float32, bfloat16 or float16).
+    accumulate adds to `out` instead of overwriting it."""
+    I = dx.shape[-1]
+    _on(dx, ids=ids, out=out, ws=ws)
+    _dense(ids=ids, dx=dx, out=out, ws=ws)
+    _shaped(dx, "dx", (*ids.shape, I))
+    _need(not accumulate or out is not None, "accumulate needs out")
+    _shaped(out, "out", (vocab, I), torch.float32)
+    with torch.cuda.device(dx.device):
+        if out is None:
+            out = torch.empty((vocab, I), dtype=torch.float32, device=dx.device)
+        d = embed_dims(ids.numel(), vocab, I, dx.dtype, _id_bytes(ids))
+        if ws is None:
+            ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
+        _run(load().lstm_embed_bwd(ctypes.byref(d), _p(ids), _p(dx), float(scale), int(accumulate),
+                                   _p(out), _p(ws), _ws_bytes(ws), _stream(stream)),
+             "lstm_embed_bwd")
+    return out
+
+
+class LogProbs:
+    """Outputs of one logprobs() call (float32; top_ids int32), kept for the
+    backward.  logp is None without targets, top_ids / top_logp with top = 0."""
+
+    def __init__(self, N, top, has_targets, inv_temp, device):
+        f = dict(dtype=torch.float32, device=device)
+        self.inv_temp = inv_temp
+        self.logp = torch.empty((N,), **f) if has_targets else None
+        self.entropy = torch.empty((N,), **f)
+        self.stats = torch.empty((N, 2), **f)
+        self.top_ids = torch.empty((N, top), dtype=torch.int32, device=device) if top else None
+        self.top_logp = torch.empty((N, top), **f) if top else None
+
+    @property
+    def lse(self) -> torch.Tensor:
+        """log sum exp(logits / temperature) of every row."""
+        return self.stats[:, 0] * self.inv_temp + self.stats[:, 1]
+
+
+def logprob_dims(N: int, vocab: int, dtype, ld: Optional[int] = None, top: int = 0,
+                 id_bytes: int = 8) -> LogprobDims:
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    return LogprobDims(int(N), int(vocab), int(vocab if ld is None else ld), int(top), code,
+                       int(id_bytes))
+
+
+def logprob_fwd_workspace_size(d: LogprobDims) -> int:
+    return int(load().lstm_logprob_fwd_workspace_size(ctypes.byref(d)))
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of a [N, vocab] tensor whose rows are dense."""
+    _need(t.dim() == 2, f"{name} must be [N, vocab]")
+    N, vocab = t.shape
+    _need(vocab <= 1 or t.stride(1) == 1, f"{name}: rows must be dense")
+    ld = t.stride(0) if N > 1 else vocab
+    _need(ld >= vocab, f"{name}: rows overlap")
+    return ld
+
+
+def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0, ws=None,
+             stream=None) -> LogProbs:
+    """lstm_logprob_fwd on logits [N, vocab] (dense rows, any row stride):
+    log-probability of targets [N], entropy, and the `top` best alternatives
+    of every row at softmax(logits / temperature)."""
+    ld = _rows(logits, "logits")
+    N, vocab = logits.shape
+    _on(logits, targets=targets, ws=ws)
+    _dense(targets=targets, ws=ws)
+    _shaped(targets, "targets", (N,))
+    _need(temperature > 0, "temperature must be positive")
+    with torch.cuda.device(logits.device):
+        st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
+        d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
+        if ws is None:
+            ws = empty_workspace(logprob_fwd_workspace_size(d), logits.device)
+        _run(load().lstm_logprob_fwd(ctypes.byref(d), _p(logits), _p(targets), st.inv_temp,
+                                     _p(st.logp), _p(st.entropy), _p(st.stats), _p(st.top_ids),
+                                     _p(st.top_logp), _p(ws), _ws_bytes(ws), _stream(stream)),
+             "lstm_logprob_fwd")
+    return st
+
+
+def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=None,
+                      temperature: float = 1.0, out=None, stream=None) -> torch.Tensor:
+    """lstm_logprob_bwd: the gradient [N, vocab] of the logits, in their type
+    and (unless `out` is given) with their row stride; out may be logits."""
+    ld = _rows(logits, "logits")
+    N, vocab = logits.shape
+    _on(logits, targets=targets, dlogp=dlogp, dentropy=dentropy, out=out, stats=st.stats)
+    _dense(targets=targets, dlogp=dlogp, dentropy=dentropy)
+    _shaped(targets, "targets", (N,))
+    _shaped(dlogp, "dlogp", (N,), torch.float32)
+    _shaped(dentropy, "dentropy", (N,), torch.float32)
+    _shaped(st.stats, "stats", (N, 2), torch.float32)
+    _shaped(out, "out", (N, vocab), logits.dtype)
+    _need(1.0 / temperature == st.inv_temp, "temperature differs from the forward's")
+    with torch.cuda.device(logits.device):
+        if out is None:
+            out = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
+        d = logprob_dims(N, vocab, logits.dtype, ld, 0, _id_bytes(targets))
+        _run(load().lstm_logprob_bwd(ctypes.byref(d), _p(logits), _p(targets), st.inv_temp,
+                                     _p(st.stats), _p(st.entropy), _p(dlogp), _p(dentropy),
+                                     _p(out), _rows(out, "out"), _stream(stream)),
+             "lstm_logprob_bwd")
+    return out

@@ -31,7 +31,7 @@ def _nvcc() -> str:
 def _sources():
     return (sorted(glob.glob(os.path.join(CSRC, "*.cu")))
             + sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
-            + [os.path.join(ROOT, "include", "liblstm.h")])
+            + sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))))
 
 
 def _stale(out: str) -> bool:
@@ -44,13 +44,29 @@ def _stale(out: str) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale(LIB_PATH):
         return LIB_PATH
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared",
-           "-Xcompiler", "-fPIC,-O2,-Wall", "-I", os.path.join(ROOT, "include"),
-           "-o", tmp, os.path.join(CSRC, "liblstm.cu")]
+    obj_dir = os.path.join(PKG, "_build")
+    os.makedirs(obj_dir, exist_ok=True)
+    flags = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2,-Wall",
+             "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd += ["-Xptxas", "-v"]
-    subprocess.run(cmd, check=True)
+        flags += ["-Xptxas", "-v"]
+    headers = [s for s in _sources() if not s.endswith(".cu")] + [__file__]
+    objs, jobs = [], []
+    for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):  # one object each, side by side
+        obj = os.path.join(obj_dir, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        if not force and os.path.exists(obj) and all(
+                os.path.getmtime(s) <= os.path.getmtime(obj) for s in headers + [src]):
+            continue
+        tmp = obj + f".tmp{os.getpid()}.o"
+        jobs.append((subprocess.Popen([*flags, "-c", "-o", tmp, src]), tmp, obj, src))
+    failed = [src for p, _, _, src in jobs if p.wait() != 0]
+    if failed:
+        raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
+    for _, tmp, obj, _ in jobs:
+        os.replace(tmp, obj)
+    tmp = LIB_PATH + f".tmp{os.getpid()}"
+    subprocess.run([*flags, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -1,0 +1,560 @@
+// embed.cu -- token embedding (declared in include/liblstm.h): the lookup
+// x_r = scale table[id_r] and the gradient of the table,
+//   dtable[w] = scale sum_{r : id_r = w} dx_r,
+// summed in a fixed order (positions sorted stably by token), so that equal
+// inputs give equal bits whatever the token frequencies.
+//
+// Bound: bytes.  The lookup reads each id and row once and writes x; the
+// gradient reads dx once and writes every table row once (rows without a
+// token as zeros).
+//
+// Gradient, in launches on one stream:
+//   sort    least-significant-digit radix sort of (token, position), 9 bits a
+//           pass; per pass one launch of block histograms and one of stable
+//           scatters (the histograms only where more than one block sorts);
+//   grad    units of 32 sorted positions x column tiles: a thread adds its
+//           columns of up to 32 rows in order and stores each token that lies
+//           inside the unit; a token that crosses a unit's border leaves
+//           partial sums.  Further blocks of the same launch write the zero
+//           rows, found by binary searches in the sorted tokens;
+//   join    adds the partial sums of a token that spans units, in order.
+#include "host.cuh"
+
+#include <algorithm>
+#include <climits>
+
+using namespace lstm;
+
+namespace {
+
+typedef __nv_bfloat16 bf16;
+typedef __half f16;
+
+// A token id as a row of the table, or -1 for padding (any id outside it).
+template <class ID> __device__ __forceinline__ int row_of(const ID *ids, long long r, int vocab) {
+    const ID w = ids[r];
+    return w >= 0 && w < (ID)vocab ? (int)w : -1;
+}
+
+// ------------------------------------------------------------------ lookup
+// Vector path: rows of whole 16-byte groups.  One warp copies U x 32 groups.
+template <class T> __device__ __forceinline__ uint4 scaled(uint4 v, float scale);
+template <> __device__ __forceinline__ uint4 scaled<float>(uint4 v, float s) {
+    return make_uint4(__float_as_uint(__uint_as_float(v.x) * s), __float_as_uint(__uint_as_float(v.y) * s),
+                      __float_as_uint(__uint_as_float(v.z) * s), __float_as_uint(__uint_as_float(v.w) * s));
+}
+template <class T> __device__ __forceinline__ uint4 scaled16(uint4 v, float s) {
+    float f[8];
+    x8_to_f32<T>(v, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= s;
+    return f32x8_to<T>(f);
+}
+template <> __device__ __forceinline__ uint4 scaled<bf16>(uint4 v, float s) { return scaled16<bf16>(v, s); }
+template <> __device__ __forceinline__ uint4 scaled<f16>(uint4 v, float s) { return scaled16<f16>(v, s); }
+
+template <class T, class ID, int U>
+__global__ void __launch_bounds__(256) lookup_kernel(const ID *ids, const uint4 *table, float scale,
+                                                     uint4 *x, int N, int vocab, int groups,
+                                                     int tiles) {
+    const long long job = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (job >= (long long)N * tiles) return;
+    const int r = (int)(job / tiles), g0 = (int)(job % tiles) * (32 * U) + (threadIdx.x & 31);
+    const int w = row_of(ids, r, vocab);
+    const uint4 *src = table + (long long)max(w, 0) * groups;
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (w >= 0 && g0 + 32 * u < groups) v[u] = __ldg(src + g0 + 32 * u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (g0 + 32 * u < groups) x[(long long)r * groups + g0 + 32 * u] = scaled<T>(v[u], scale);
+}
+
+// Element path: rows that are not whole 16-byte groups.
+template <class T, class ID>
+__global__ void __launch_bounds__(256) lookup_elem_kernel(const ID *ids, const T *table, float scale,
+                                                          T *x, int N, int vocab, int I) {
+    const int r = blockIdx.x;
+    const int w = row_of(ids, r, vocab);
+    for (int i = threadIdx.x; i < I; i += 256)
+        x[(long long)r * I + i] = w >= 0 ? from_f<T>(to_f(table[(long long)w * I + i]) * scale) : from_f<T>(0.f);
+}
+
+template <class T, class ID>
+int lookup(const lstm_embed_dims *d, const void *ids, const void *table, float scale, void *x,
+           cudaStream_t s) {
+    const size_t row = (size_t)d->I * sizeof(T);
+    if (row % 16) {
+        lookup_elem_kernel<T, ID><<<d->N, 256, 0, s>>>((const ID *)ids, (const T *)table, scale, (T *)x,
+                                                      d->N, d->vocab, d->I);
+        LSTM_CUDA_TRY(host::launched());
+        return LSTM_OK;
+    }
+    const int groups = (int)(row / 16);
+    // Four groups a lane keep enough loads in flight once the rows fill the
+    // card; below that one group a lane spreads the call over more SMs.
+    const bool wide = (long long)d->N * groups >= 148LL * 2048 * 4;
+    const int tiles = (groups + (wide ? 128 : 32) - 1) / (wide ? 128 : 32);
+    const long long blocks = ((long long)d->N * tiles + 7) / 8;
+    if (blocks > INT_MAX) return LSTM_ERR_UNSUPPORTED;
+    if (wide)
+        lookup_kernel<T, ID, 4><<<(unsigned)blocks, 256, 0, s>>>((const ID *)ids, (const uint4 *)table, scale,
+                                                                (uint4 *)x, d->N, d->vocab, groups, tiles);
+    else
+        lookup_kernel<T, ID, 1><<<(unsigned)blocks, 256, 0, s>>>((const ID *)ids, (const uint4 *)table, scale,
+                                                                (uint4 *)x, d->N, d->vocab, groups, tiles);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
+// -------------------------------------------------------------------- sort
+constexpr int kBits = 9, kBins = 1 << kBits;
+constexpr int kSortWarps = 16, kSortThreads = 32 * kSortWarps;
+constexpr int kWarpKeys = 128, kTile = kSortWarps * kWarpKeys;  // 2048 keys a tile
+constexpr int kSortBlocks = 128;                                // most blocks of a sort
+static_assert(kSortThreads == kBins, "one thread per digit");
+
+struct SortArgs {
+    const void *ids;         // pass 0: token ids (id64 or not); later passes: NULL
+    int id64, vocab;
+    const int *key_in, *pos_in;
+    int *key_out, *pos_out;
+    int *hist;               // [blocks][kBins]
+    int N, shift, blocks, tiles;  // every block sorts `tiles` consecutive tiles
+};
+
+// The sort key of input i: its token, or vocab for padding.
+__device__ __forceinline__ int sort_key(const SortArgs &a, int i) {
+    if (!a.ids) return a.key_in[i];
+    const int w = a.id64 ? row_of((const long long *)a.ids, i, a.vocab)
+                         : row_of((const int *)a.ids, i, a.vocab);
+    return w >= 0 ? w : a.vocab;
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortArgs a) {
+    __shared__ int h[kBins];
+    h[threadIdx.x] = 0;
+    __syncthreads();
+    const long long b0 = (long long)blockIdx.x * a.tiles * kTile;
+    const int i1 = (int)min((long long)a.N, b0 + (long long)a.tiles * kTile);
+    for (int i = (int)min((long long)a.N, b0) + threadIdx.x; i < i1; i += kSortThreads)
+        atomicAdd(&h[(sort_key(a, i) >> a.shift) & (kBins - 1)], 1);
+    __syncthreads();
+    a.hist[blockIdx.x * kBins + threadIdx.x] = h[threadIdx.x];
+}
+
+// Exclusive prefix sum over the block's 512 threads.
+__device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int add = 0;
+    for (int w = 0; w < warp; ++w) add += warp_sums[w];
+    __syncthreads();
+    return add + x - v;
+}
+
+// Stable scatter by one digit.  Warp w of a tile owns 128 consecutive keys,
+// taken 32 at a time in order; equal digits among 32 are ranked by lane.
+__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) {
+    __shared__ int base[kBins];                     // next output place of each digit
+    __shared__ unsigned short cnt[kSortWarps][kBins];
+    __shared__ int warp_sums[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long b0 = (long long)blockIdx.x * a.tiles * kTile;
+    {
+        int before = 0, total = 0;
+        if (a.blocks > 1) {
+            for (int b = 0; b < a.blocks; ++b) {
+                const int h = a.hist[b * kBins + tid];
+                if (b < (int)blockIdx.x) before += h;
+                total += h;
+            }
+        } else {  // the only block: its own histogram
+            base[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < a.N; i += kSortThreads)
+                atomicAdd(&base[(sort_key(a, i) >> a.shift) & (kBins - 1)], 1);
+            __syncthreads();
+            total = base[tid];
+            __syncthreads();
+        }
+        const int off = block_exclusive(total, warp_sums);
+        base[tid] = off + before;
+    }
+    for (int t = 0; t < a.tiles; ++t) {
+        const long long t0 = b0 + (long long)t * kTile;
+        if (t0 >= a.N) break;  // the same for every thread
+        for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
+        __syncthreads();
+        int key[4], rank[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long i = t0 + warp * kWarpKeys + j * 32 + lane;
+            key[j] = i < a.N ? sort_key(a, (int)i) : -1;
+            const int dg = key[j] < 0 ? kBins : (key[j] >> a.shift) & (kBins - 1);
+            const unsigned peers = __match_any_sync(~0u, dg);
+            rank[j] = 0;
+            if (dg < kBins) {
+                const int r = __popc(peers & ((1u << lane) - 1u));
+                rank[j] = cnt[warp][dg] + r;
+            }
+            __syncwarp();
+            if (dg < kBins && lane == __ffs(peers) - 1)
+                cnt[warp][dg] = (unsigned short)(cnt[warp][dg] + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        {  // digit tid: counts of the warps -> first place of each warp
+            int run = base[tid];
+            const int first = run;
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int c = cnt[w][tid];
+                cnt[w][tid] = (unsigned short)(run - first);
+                run += c;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (key[j] < 0) continue;
+                const int dg = (key[j] >> a.shift) & (kBins - 1);
+                const int o = base[dg] + cnt[warp][dg] + rank[j];
+                const int i = (int)(t0 + warp * kWarpKeys + j * 32 + lane);
+                a.key_out[o] = key[j];
+                a.pos_out[o] = a.pos_in ? a.pos_in[i] : i;
+            }
+            __syncthreads();
+            base[tid] = run;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+constexpr int kUnit = 32;       // sorted positions of a unit
+constexpr int kZeroRows = 32;   // table rows a zero-fill block looks after
+constexpr int kColThreads = 256;
+
+struct GradArgs {
+    const int *key, *pos;  // [N] sorted tokens (padding = vocab, last) and their positions
+    const void *dx;
+    float *dtable, *pfirst, *plast;
+    float scale;
+    int N, vocab, I, units, accumulate;
+};
+
+// W consecutive columns a thread: 4 where rows are whole 16-byte groups of
+// both dx and dtable, else 1.
+template <class T, int W> __device__ __forceinline__ void load_cols(const T *p, float (&f)[W]);
+template <> __device__ __forceinline__ void load_cols<float, 1>(const float *p, float (&f)[1]) { f[0] = __ldg(p); }
+template <> __device__ __forceinline__ void load_cols<bf16, 1>(const bf16 *p, float (&f)[1]) { f[0] = to_f(*p); }
+template <> __device__ __forceinline__ void load_cols<f16, 1>(const f16 *p, float (&f)[1]) { f[0] = to_f(*p); }
+template <> __device__ __forceinline__ void load_cols<float, 4>(const float *p, float (&f)[4]) {
+    const float4 v = __ldg((const float4 *)p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+template <class T> __device__ __forceinline__ void load4_16(const T *p, float (&f)[4]) {
+    const uint2 v = __ldg((const uint2 *)p);
+    const typename Elem<T>::E2 *h = (const typename Elem<T>::E2 *)&v;
+    const float2 a = Elem<T>::to_f2(h[0]), b = Elem<T>::to_f2(h[1]);
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+template <> __device__ __forceinline__ void load_cols<bf16, 4>(const bf16 *p, float (&f)[4]) { load4_16(p, f); }
+template <> __device__ __forceinline__ void load_cols<f16, 4>(const f16 *p, float (&f)[4]) { load4_16(p, f); }
+template <int W> __device__ __forceinline__ void store_cols(float *p, const float (&f)[W]) {
+    if (W == 4)
+        *(float4 *)p = make_float4(f[0], f[W > 1 ? 1 : 0], f[W > 2 ? 2 : 0], f[W > 3 ? 3 : 0]);
+    else
+        p[0] = f[0];
+}
+template <int W>
+__device__ __forceinline__ void store_row(const GradArgs &a, int w, int col, const float (&acc)[W]) {
+    float *p = a.dtable + (long long)w * a.I + col;
+    float f[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = acc[i] * a.scale;
+    if (a.accumulate) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[i] += p[i];
+    }
+    store_cols<W>(p, f);
+}
+
+template <class T, int W>
+__global__ void __launch_bounds__(kColThreads) grad_kernel(GradArgs a) {
+    __shared__ int skey[kUnit + 2], spos[kUnit];
+    __shared__ unsigned present;
+    const int tid = threadIdx.x;
+    const int col = (blockIdx.y * kColThreads + tid) * W;
+    if ((int)blockIdx.x >= a.units) {  // rows of the table without a token: zeros
+        const int w0 = ((int)blockIdx.x - a.units) * kZeroRows;
+        if (tid < 32) {  // lane j: the first place in the sorted tokens that row w0 + j could have
+            int lo = 0, hi = a.N;
+            while (lo < hi) {
+                const int mid = (int)(((unsigned)lo + (unsigned)hi) / 2);
+                if (__ldg(a.key + mid) < w0 + tid) lo = mid + 1; else hi = mid;
+            }
+            const unsigned has = __ballot_sync(~0u, lo < a.N && __ldg(a.key + min(lo, a.N - 1)) == w0 + tid);
+            if (tid == 0) present = has;
+        }
+        __syncthreads();
+        if (col < a.I) {
+            const float z[W] = {};
+            for (int j = 0; j < kZeroRows && w0 + j < a.vocab; ++j)
+                if (!((present >> j) & 1u)) store_cols<W>(a.dtable + (long long)(w0 + j) * a.I + col, z);
+        }
+        return;
+    }
+    const int u0 = blockIdx.x * kUnit, n = min(kUnit, a.N - u0);
+    if (tid < n) {
+        skey[tid + 1] = a.key[u0 + tid];
+        spos[tid] = a.pos[u0 + tid];
+    }
+    if (tid == kColThreads - 1) skey[0] = u0 > 0 ? a.key[u0 - 1] : -1;
+    if (tid == kColThreads - 2) skey[n + 1] = u0 + n < a.N ? a.key[u0 + n] : -1;
+    __syncthreads();
+    if (col >= a.I) return;
+    const T *dx = (const T *)a.dx + col;
+    float acc[W] = {};
+    int start = 0;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float f[8][W];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j;
+            if (i < n && skey[i + 1] < a.vocab) load_cols<T, W>(dx + (long long)spos[i] * a.I, f[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j;
+            if (i >= n) break;
+            const int w = skey[i + 1];
+            if (w >= a.vocab) return;  // padding is last
+#pragma unroll
+            for (int c = 0; c < W; ++c) acc[c] += f[j][c];
+            const bool more = skey[i + 2] == w;  // the token goes on at i + 1
+            if (!more || i == n - 1) {
+                if (start == 0 && skey[0] == w)
+                    store_cols<W>(a.pfirst + (long long)blockIdx.x * a.I + col, acc);
+                else if (more)
+                    store_cols<W>(a.plast + (long long)blockIdx.x * a.I + col, acc);
+                else
+                    store_row<W>(a, w, col, acc);
+                start = i + 1;
+#pragma unroll
+                for (int c = 0; c < W; ++c) acc[c] = 0.f;
+            }
+        }
+    }
+}
+
+// One block per unit; only a unit in which a token begins that goes on in the
+// next one has work.  Four thread groups take every fourth of the units the
+// token goes on in; their sums are added in a fixed order.
+constexpr int kJoinGroups = 4, kJoinCols = 64;
+template <int W>
+__global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a) {
+    const int u = blockIdx.x, last = u * kUnit + kUnit - 1;
+    if (last + 1 >= a.N) return;
+    const int w = a.key[last];
+    if (w >= a.vocab || a.key[last + 1] != w) return;
+    if (u > 0 && a.key[u * kUnit - 1] == w) return;  // began before this unit
+    __shared__ int end_s;
+    __shared__ float part[kJoinGroups][kJoinCols * W];
+    // units u+1 .. end-1 hold the rest: a unit past u whose first token is w
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        int lo = u + 1, hi = a.units;  // key[unit * kUnit] == w for units in [u+1, lo)
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (a.key[(long long)mid * kUnit] <= w) lo = mid + 1; else hi = mid;
+        }
+        end_s = lo;
+    }
+    __syncthreads();
+    const int g = tid / kJoinCols, c0 = tid % kJoinCols;
+    const int col = (blockIdx.y * kJoinCols + c0) * W;
+    float acc[W] = {};
+    if (col < a.I) {
+        if (g == 0) load_cols<float, W>(a.plast + (long long)u * a.I + col, acc);
+        const int end = end_s;
+        for (int v0 = u + 1 + g; v0 < end; v0 += 8 * kJoinGroups) {
+            float f[8][W];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (v0 + j * kJoinGroups < end)
+                    load_cols<float, W>(a.pfirst + (long long)(v0 + j * kJoinGroups) * a.I + col, f[j]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (v0 + j * kJoinGroups < end) {
+#pragma unroll
+                    for (int c = 0; c < W; ++c) acc[c] += f[j][c];
+                }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < W; ++c) part[g][c0 * W + c] = acc[c];
+    __syncthreads();
+    if (g == 0 && col < a.I) {
+#pragma unroll
+        for (int c = 0; c < W; ++c)
+            acc[c] = ((part[0][c0 * W + c] + part[1][c0 * W + c]) + part[2][c0 * W + c]) + part[3][c0 * W + c];
+        store_row<W>(a, w, col, acc);
+    }
+}
+
+// --------------------------------------------------------------- workspace
+struct BwdLayout {
+    size_t key[2], pos[2], hist, pfirst, plast, total;
+    int units;
+};
+
+BwdLayout bwd_layout(const lstm_embed_dims *d) {
+    BwdLayout l;
+    size_t o = kCtrlBytes;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = align_up(o + bytes, 256);
+        return at;
+    };
+    l.units = (d->N + kUnit - 1) / kUnit;
+    for (int i = 0; i < 2; ++i) {
+        l.key[i] = take((size_t)d->N * 4);
+        l.pos[i] = take((size_t)d->N * 4);
+    }
+    l.hist = take((size_t)kSortBlocks * kBins * 4);
+    l.pfirst = take((size_t)l.units * d->I * 4);
+    l.plast = take((size_t)l.units * d->I * 4);
+    l.total = o;
+    return l;
+}
+
+bool dims_ok(const lstm_embed_dims *d) {
+    if (!d || d->N < 0 || d->vocab < 0 || d->I < 0) return false;
+    if (!host::dtype_ok(d->dtype) || (d->id_bytes != 4 && d->id_bytes != 8)) return false;
+    return true;
+}
+
+// A vocabulary of 2^30 rows or a row of 2^24 elements leaves room for every
+// 32-bit index of the kernels (sort keys up to vocab, columns + tile).
+bool dims_supported(const lstm_embed_dims *d) { return d->vocab <= (1 << 30) && d->I <= (1 << 24) && d->N <= INT_MAX - 4 * kTile * kSortBlocks; }
+
+template <class T, int W> int grad(const lstm_embed_dims *d, GradArgs &a, cudaStream_t s) {
+    const int zero_blocks = a.accumulate ? 0 : (d->vocab + kZeroRows - 1) / kZeroRows;
+    const int tiles = (d->I + kColThreads * W - 1) / (kColThreads * W);
+    const int jtiles = (d->I + kJoinCols * W - 1) / (kJoinCols * W);
+    if (tiles > 65535 || jtiles > 65535) return LSTM_ERR_UNSUPPORTED;
+    if (a.units + zero_blocks == 0) return LSTM_OK;
+    grad_kernel<T, W><<<dim3(a.units + zero_blocks, tiles), kColThreads, 0, s>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    if (a.units > 1) {
+        join_kernel<W><<<dim3(a.units, jtiles), kJoinGroups * kJoinCols, 0, s>>>(a);
+        LSTM_CUDA_TRY(host::launched());
+    }
+    return LSTM_OK;
+}
+
+template <class T> int grad_w(const lstm_embed_dims *d, GradArgs &a, cudaStream_t s) {
+    return d->I % 4 == 0 ? grad<T, 4>(d, a, s) : grad<T, 1>(d, a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int lstm_embed_fwd(const lstm_embed_dims *d, const void *ids, const void *table, float scale, void *x,
+                   void *stream) {
+    if (!dims_ok(d)) return LSTM_ERR_INVALID_ARG;
+    if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
+    const bool any = (long long)d->N * d->I > 0;
+    if (!host::ptr_ok(ids, any) || !host::ptr_ok(table, any && d->vocab > 0) || !host::ptr_ok(x, any))
+        return LSTM_ERR_INVALID_ARG;
+    if (!any) return LSTM_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool l = d->id_bytes == 8;
+    if (d->dtype == LSTM_F32)
+        return l ? lookup<float, long long>(d, ids, table, scale, x, s) : lookup<float, int>(d, ids, table, scale, x, s);
+    if (d->dtype == LSTM_F16)
+        return l ? lookup<f16, long long>(d, ids, table, scale, x, s) : lookup<f16, int>(d, ids, table, scale, x, s);
+    return l ? lookup<bf16, long long>(d, ids, table, scale, x, s) : lookup<bf16, int>(d, ids, table, scale, x, s);
+}
+
+size_t lstm_embed_bwd_workspace_size(const lstm_embed_dims *d) {
+    if (!dims_ok(d) || !dims_supported(d)) return 0;
+    return bwd_layout(d).total;
+}
+
+int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, float scale, int accumulate,
+                   float *dtable, void *ws, size_t ws_bytes, void *stream) {
+    if (!dims_ok(d) || (accumulate != 0 && accumulate != 1)) return LSTM_ERR_INVALID_ARG;
+    if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
+    const bool any = (long long)d->N * d->I > 0, out = (long long)d->vocab * d->I > 0;
+    if (!host::ptr_ok(ids, any) || !host::ptr_ok(dx, any) || !host::ptr_ok(dtable, out))
+        return LSTM_ERR_INVALID_ARG;
+    const BwdLayout l = bwd_layout(d);
+    const int rc = host::ws_check(ws, ws_bytes, l.total);
+    if (rc != LSTM_OK) return rc;
+    if (!out) return LSTM_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    char *w = (char *)ws;
+    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, s));
+
+    // sort: enough 9-bit passes for the largest key, which is vocab (padding)
+    int cur = 0;
+    if (d->N > 0) {
+        int bits = 1;
+        while (bits < 31 && (d->vocab >> bits) != 0) ++bits;
+        SortArgs a = {};
+        const long long tiles = ((long long)d->N + kTile - 1) / kTile;
+        a.tiles = (int)((tiles + kSortBlocks - 1) / kSortBlocks);
+        a.blocks = (int)((tiles + a.tiles - 1) / a.tiles);
+        a.id64 = d->id_bytes == 8;
+        a.vocab = d->vocab;
+        a.N = d->N;
+        a.hist = (int *)(w + l.hist);
+        a.ids = ids;
+        for (int shift = 0; shift < bits; shift += kBits) {
+            a.shift = shift;
+            a.key_out = (int *)(w + l.key[cur]);
+            a.pos_out = (int *)(w + l.pos[cur]);
+            if (a.blocks > 1) {
+                sort_hist_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
+                LSTM_CUDA_TRY(host::launched());
+            }
+            sort_scatter_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
+            LSTM_CUDA_TRY(host::launched());
+            a.ids = nullptr;
+            a.key_in = a.key_out;
+            a.pos_in = a.pos_out;
+            cur ^= 1;
+        }
+        cur ^= 1;
+    }
+    GradArgs g = {};
+    g.key = (const int *)(w + l.key[cur]);
+    g.pos = (const int *)(w + l.pos[cur]);
+    g.dx = dx;
+    g.dtable = dtable;
+    g.pfirst = (float *)(w + l.pfirst);
+    g.plast = (float *)(w + l.plast);
+    g.scale = scale;
+    g.N = d->N;
+    g.vocab = d->vocab;
+    g.I = d->I;
+    g.units = l.units;
+    g.accumulate = accumulate;
+    if (d->dtype == LSTM_F32) return grad_w<float>(d, g, s);
+    if (d->dtype == LSTM_F16) return grad_w<f16>(d, g, s);
+    return grad_w<bf16>(d, g, s);
+}
+
+}  // extern "C"

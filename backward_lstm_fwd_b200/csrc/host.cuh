@@ -1,0 +1,54 @@
+// host.cuh -- argument checks and launch helpers shared by the entry points
+// of the embedding, log-probability and gated-delta-rule operators.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/liblstm.h"
+#include "common.cuh"
+
+namespace lstm {
+namespace host {
+
+#define LSTM_CUDA_TRY(expr)                               \
+    do {                                                  \
+        cudaError_t e_ = (expr);                          \
+        if (e_ != cudaSuccess) return LSTM_ERR_CUDA;      \
+    } while (0)
+
+// A pointer argument: 16-byte aligned, and not NULL where it is needed.
+inline bool ptr_ok(const void *p, bool needed) {
+    return (p != nullptr || !needed) && ((uintptr_t)p & 15u) == 0;
+}
+
+inline bool dtype_ok(int dtype) {
+    return dtype == LSTM_F32 || dtype == LSTM_BF16 || dtype == LSTM_F16;
+}
+
+inline size_t elem_bytes(int dtype) { return dtype == LSTM_F32 ? 4 : 2; }
+
+inline int ws_check(const void *ws, size_t ws_bytes, size_t need) {
+    return (!ws || ws_bytes < need || ((uintptr_t)ws & 255u) != 0) ? LSTM_ERR_WORKSPACE : LSTM_OK;
+}
+
+// SMs of the current device (a B200's 148 where there is no device to ask).
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = 148;
+    }
+    return n;
+}
+
+// After a <<<>>> launch: count it, return its launch error.
+inline cudaError_t launched() {
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace host
+}  // namespace lstm

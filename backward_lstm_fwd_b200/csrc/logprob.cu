@@ -1,0 +1,568 @@
+// logprob.cu -- log-probabilities of given tokens (declared in
+// include/liblstm.h).  With z = logits / temperature, per row:
+//   lse = log sum exp z,  logp = z_target - lse,
+//   entropy = lse - sum p z,  p = exp(z - lse),
+// and the `top` largest logits (ties: the lowest index first).  The gradient is
+//   dlogits = (dlogp (1[target] - p) - dentropy p (z - lse + entropy)) / temperature.
+//
+// Bound: bytes.  The forward reads the logits once: every thread keeps the
+// running maximum m of its elements with s = sum e^{z-m} and
+// w = sum e^{z-m} (x - m), rescaled when a batch of elements raises m, and the
+// threads' triples are joined at the end.  The alternatives come from the same
+// pass: the first eighth of the range gives every thread its own maximum, the
+// top-th largest of those is a lower bound of the answer, and only elements at
+// or above it (a few times `top`) enter a candidate list; the eighth is looked
+// at twice (the second time from L1 / L2).  Rows are split over several blocks
+// where there are few of them, and a second launch joins the parts.  The
+// backward reads the logits and writes the gradient once.
+#include "host.cuh"
+
+#include <algorithm>
+#include <climits>
+
+using namespace lstm;
+
+namespace {
+
+typedef __nv_bfloat16 bf16;
+typedef __half f16;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCand = 1024;  // candidate list of a block
+constexpr int kMinPart = 2048;  // fewest elements of a part of a row
+static_assert(LSTM_LOGPROB_MAX_TOP <= 64, "the candidate list is sized for 64 alternatives");
+
+// ---------------------------------------------------------------- elements
+// 2^x (the hardware's approximation: relative error about 2^-22, results
+// below 2^-126 flush to zero).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// max(x, -1e28) that keeps NaN: -inf - m stays usable as a factor of zero.
+__device__ __forceinline__ float floor_nan(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-1e28f));
+    return y;
+}
+// Elements of one 16-byte group.
+template <class T> struct Group { static constexpr int n = 16 / sizeof(T); };
+template <class T> __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[Group<T>::n]);
+template <> __device__ __forceinline__ void unpack<float>(const uint4 &v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+template <> __device__ __forceinline__ void unpack<bf16>(const uint4 &v, float (&f)[8]) { x8_to_f32<bf16>(v, f); }
+template <> __device__ __forceinline__ void unpack<f16>(const uint4 &v, float (&f)[8]) { x8_to_f32<f16>(v, f); }
+template <class T> __device__ __forceinline__ uint4 pack(const float (&f)[Group<T>::n]);
+template <> __device__ __forceinline__ uint4 pack<float>(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <> __device__ __forceinline__ uint4 pack<bf16>(const float (&f)[8]) { return f32x8_to<bf16>(f); }
+template <> __device__ __forceinline__ uint4 pack<f16>(const float (&f)[8]) { return f32x8_to<f16>(f); }
+
+// Order of alternatives: larger value first, then lower index; one 64-bit key,
+// larger is better.  NaN sorts below every number.
+__device__ __forceinline__ unsigned ordered(float x) {
+    if (x != x) return 0u;
+    if (x == 0.f) x = 0.f;  // -0 and +0 are equal
+    const unsigned b = __float_as_uint(x);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(unsigned long long key) {
+    const unsigned o = (unsigned)(key >> 32);
+    if (o == 0u) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ unsigned long long key_of(float x, int i) {
+    return ((unsigned long long)ordered(x) << 32) | (unsigned)~i;
+}
+__device__ __forceinline__ int index_of(unsigned long long key) { return (int)~(unsigned)key; }
+
+// --------------------------------------------------- running softmax triple
+struct Stat {
+    float m, s, w;  // maximum; sum e^{c (x - m)}; sum e^{c (x - m)} (x - m)
+};
+__device__ __forceinline__ void raise(Stat &a, float m, float c) {  // m >= a.m
+    const float d = floor_nan(a.m - m), f = ex2(d * c);
+    a.w = (a.w + a.s * d) * f;
+    a.s *= f;
+    a.m = m;
+}
+__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    if (m == -INFINITY) return Stat{m, a.s + b.s, a.w + b.w};  // nothing but -inf (or NaN) yet
+    raise(a, m, c);
+    raise(b, m, c);
+    return Stat{m, a.s + b.s, a.w + b.w};
+}
+template <int n> __device__ __forceinline__ void add(Stat &a, const float (&f)[n], float c, float &gmax) {
+    gmax = f[0];
+#pragma unroll
+    for (int i = 1; i < n; ++i) gmax = fmaxf(gmax, f[i]);
+    if (gmax > a.m) raise(a, gmax, c);
+    const float m = a.m == -INFINITY ? 0.f : a.m;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        const float d = floor_nan(f[i] - m), e = ex2(d * c);
+        a.s += e;
+        a.w = fmaf(e, d, a.w);
+    }
+}
+__device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stat b;
+        b.m = __shfl_xor_sync(~0u, a.m, o);
+        b.s = __shfl_xor_sync(~0u, a.s, o);
+        b.w = __shfl_xor_sync(~0u, a.w, o);
+        a = join(a, b, c);
+    }
+    if ((threadIdx.x & 31) == 0) warp_stats[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = warp_stats[0];
+    for (int w = 1; w < kWarps; ++w) a = join(a, warp_stats[w], c);
+    return a;  // the same in every thread
+}
+
+struct Args {
+    const void *logits;
+    const void *targets;
+    int id64, N, vocab, top, parts;
+    long long ld;
+    float inv_temp;
+    float *logp, *entropy, *stats, *top_logp;
+    int *top_ids;
+    Stat *part_stats;                     // [N][parts]
+    unsigned long long *part_keys;        // [N][parts][top]
+};
+
+__device__ __forceinline__ long long target_of(const void *t, int id64, int r) {
+    return id64 ? ((const long long *)t)[r] : (long long)((const int *)t)[r];
+}
+
+// Row outputs from the row's triple and its sorted alternatives.
+template <class T>
+__device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsigned long long *keys) {
+    const bool empty = st.m == -INFINITY && st.s == 0.f;  // every logit is -inf
+    const float ls = logf(st.s);
+    if (threadIdx.x == 0) {
+        a.stats[2LL * r] = st.m;
+        a.stats[2LL * r + 1] = empty ? 0.f : ls;
+        if (a.entropy) a.entropy[r] = empty ? 0.f : ls - a.inv_temp * (st.w / st.s);
+        if (a.logp) {
+            const long long t = target_of(a.targets, a.id64, r);
+            float lp = 0.f;  // an ignored row
+            if (t >= 0 && t < a.vocab) {
+                const float x = to_f(((const T *)a.logits)[(long long)r * a.ld + t]);
+                lp = empty ? -INFINITY : (x - st.m) * a.inv_temp - ls;
+            }
+            a.logp[r] = lp;
+        }
+    }
+    for (int i = threadIdx.x; i < a.top; i += kThreads) {
+        const unsigned long long k = keys[i];
+        a.top_ids[(long long)r * a.top + i] = index_of(k);
+        a.top_logp[(long long)r * a.top + i] = empty ? -INFINITY : (value_of(k) - st.m) * a.inv_temp - ls;
+    }
+}
+
+// Of n <= kCand distinct keys in shared memory, the `top` largest in order.
+__device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, int top, unsigned long long *out) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const unsigned long long k = keys[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += keys[j] > k;
+        if (rank < top) out[rank] = k;
+    }
+    __syncthreads();
+}
+
+// The top-th largest of the block's 256 thread maxima (-inf where fewer than
+// `top` threads have one): at least `top` elements are at or above it.
+__device__ __forceinline__ float bound_of(float mine, int top, float *maxima, float *bound) {
+    maxima[threadIdx.x] = mine;
+    if (threadIdx.x == 0) *bound = -INFINITY;
+    __syncthreads();
+    int rank = 0;
+    for (int j = 0; j < kThreads; ++j) {
+        const float o = maxima[j];
+        rank += o > mine || (o == mine && j < (int)threadIdx.x);
+    }
+    if (rank == top - 1) *bound = mine;
+    __syncthreads();
+    return *bound;
+}
+
+// ----------------------------------------------------------------- forward
+// Block (r, p): part p of row r.  TOP: alternatives wanted.
+template <class T, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(Args a) {
+    constexpr int n = Group<T>::n, U = 4;
+    __shared__ Stat warp_stats[kWarps];
+    __shared__ unsigned long long cand[TOP ? kCand : 1], best[TOP ? LSTM_LOGPROB_MAX_TOP : 1];
+    __shared__ float maxima[TOP ? kThreads : 1], bound_s;
+    __shared__ int count;
+    const int tid = threadIdx.x;
+    const int r = blockIdx.x / a.parts, p = blockIdx.x % a.parts;
+    const T *row = (const T *)a.logits + (long long)r * a.ld;
+    const float c = a.inv_temp * 1.44269504088896340736f;  // log2(e)
+    // part p is the elements [e0, e1); its 16-byte groups [g0, g1)
+    const int e0 = (int)((long long)a.vocab * p / a.parts), e1 = (int)((long long)a.vocab * (p + 1) / a.parts);
+    const int mis = (int)(((uintptr_t)(row + e0) & 15u) / sizeof(T));
+    const int h = min(e1, e0 + (mis ? n - mis : 0));  // [e0, h): before the first whole group
+    const int groups = (e1 - h) / n;
+    const uint4 *gp = (const uint4 *)(row + h);
+    const int tail = h + groups * n;                  // [tail, e1): after the last one
+    Stat st = {-INFINITY, 0.f, 0.f};
+    float bound = -INFINITY, gmax;
+    if (TOP && tid == 0) count = 0;
+
+    auto push = [&](float x, int i) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kCand) cand[at] = key_of(x, i);
+    };
+    // groups [b, e): U loads in flight a thread
+    auto run = [&](int b, int e, auto &&each) {
+        for (int g = b + tid; g < e; g += U * kThreads) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (g + u * kThreads < e) v[u] = __ldg(gp + g + u * kThreads);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (g + u * kThreads < e) each(v[u], g + u * kThreads);
+        }
+    };
+    auto edge = [&](auto &&each) {  // the elements outside whole groups: fewer than 2 n
+        if (tid < h - e0) each(to_f(row[e0 + tid]), e0 + tid);
+        if (tid < e1 - tail) each(to_f(row[tail + tid]), tail + tid);
+    };
+
+    edge([&](float x, int) {
+        const float f[1] = {x};
+        add<1>(st, f, c, gmax);
+    });
+    const int first = TOP ? min(groups, max(groups / 8, U * kThreads)) : 0;
+    if (TOP) {
+        run(0, first, [&](const uint4 &v, int) {
+            float f[n];
+            unpack<T>(v, f);
+            add<n>(st, f, c, gmax);
+        });
+        bound = bound_of(st.m, a.top, maxima, &bound_s);
+        edge([&](float x, int i) {
+            if (!(x < bound)) push(x, i);
+        });
+        run(0, first, [&](const uint4 &v, int g) {
+            float f[n];
+            unpack<T>(v, f);
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (!(f[i] < bound)) push(f[i], h + g * n + i);
+        });
+    }
+    run(first, groups, [&](const uint4 &v, int g) {
+        float f[n];
+        unpack<T>(v, f);
+        add<n>(st, f, c, gmax);
+        if (TOP && !(gmax < bound)) {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (!(f[i] < bound)) push(f[i], h + g * n + i);
+        }
+    });
+    st = block_join(st, c, warp_stats);  // its barrier also closes the candidate list
+
+    if (TOP) {
+        if (count <= kCand) {
+            rank_keys(cand, count, a.top, best);
+        } else {
+            // More candidates than the list holds (long runs of equal values):
+            // one exact pass over the part per alternative.
+            unsigned long long prev = ~0ull;
+            for (int k = 0; k < a.top; ++k) {
+                unsigned long long mine = 0;
+                for (int i = e0 + tid; i < e1; i += kThreads) {
+                    const unsigned long long key = key_of(to_f(row[i]), i);
+                    if (key < prev && key > mine) mine = key;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const unsigned long long y = __shfl_xor_sync(~0u, mine, o);
+                    mine = y > mine ? y : mine;
+                }
+                __syncthreads();
+                if ((tid & 31) == 0) cand[tid >> 5] = mine;
+                __syncthreads();
+                for (int w = 0; w < kWarps; ++w) mine = cand[w] > mine ? cand[w] : mine;
+                prev = mine;
+                if (tid == 0) best[k] = mine;
+            }
+            __syncthreads();
+        }
+    }
+    if (a.parts == 1) {
+        finish<T>(a, r, st, best);
+        return;
+    }
+    if (tid == 0) a.part_stats[blockIdx.x] = st;
+    if (TOP)
+        for (int i = tid; i < a.top; i += kThreads) a.part_keys[(long long)blockIdx.x * a.top + i] = best[i];
+}
+
+// Join the parts of row blockIdx.x.
+template <class T>
+__global__ void __launch_bounds__(kThreads) join_kernel(Args a) {
+    __shared__ Stat warp_stats[kWarps];
+    __shared__ unsigned long long cand[kCand], best[LSTM_LOGPROB_MAX_TOP];
+    __shared__ float maxima[kThreads], bound_s;
+    __shared__ int count;
+    const int r = blockIdx.x, tid = threadIdx.x;
+    const float c = a.inv_temp * 1.44269504088896340736f;
+    Stat st = {-INFINITY, 0.f, 0.f};
+    if (tid < a.parts) st = a.part_stats[(long long)r * a.parts + tid];
+    if (tid == 0) count = 0;
+    st = block_join(st, c, warp_stats);
+    if (a.top) {
+        // a part's first alternative is its maximum; parts <= 256 = kThreads
+        const unsigned long long *keys = a.part_keys + (long long)r * a.parts * a.top;
+        const float mine = tid < a.parts ? value_of(keys[(long long)tid * a.top]) : -INFINITY;
+        const float bound = bound_of(mine == mine ? mine : -INFINITY, a.top, maxima, &bound_s);
+        for (int i = tid; i < a.parts * a.top; i += kThreads) {
+            const unsigned long long k = keys[i];
+            if (!(value_of(k) < bound)) {
+                const int at = atomicAdd(&count, 1);
+                if (at < kCand) cand[at] = k;
+            }
+        }
+        __syncthreads();
+        if (count <= kCand) {
+            rank_keys(cand, count, a.top, best);
+        } else {
+            unsigned long long prev = ~0ull;
+            for (int k = 0; k < a.top; ++k) {
+                unsigned long long m = 0;
+                for (int i = tid; i < a.parts * a.top; i += kThreads)
+                    if (keys[i] < prev && keys[i] > m) m = keys[i];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const unsigned long long y = __shfl_xor_sync(~0u, m, o);
+                    m = y > m ? y : m;
+                }
+                __syncthreads();
+                if ((tid & 31) == 0) cand[tid >> 5] = m;
+                __syncthreads();
+                for (int w = 0; w < kWarps; ++w) m = cand[w] > m ? cand[w] : m;
+                prev = m;
+                if (tid == 0) best[k] = m;
+            }
+            __syncthreads();
+        }
+    }
+    finish<T>(a, r, st, best);
+}
+
+// ---------------------------------------------------------------- backward
+struct BwdArgs {
+    const void *logits, *targets;
+    int id64, N, vocab, chunk, chunks;  // blocks of a row, elements each
+    long long ld, ldd;
+    float inv_temp;
+    const float *stats, *entropy, *dlogp, *dentropy;
+    void *dlogits;
+};
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kThreads) bwd_kernel(BwdArgs a) {
+    constexpr int n = Group<T>::n, U = 2;
+    const int tid = threadIdx.x;
+    const int r = blockIdx.x / a.chunks, p = blockIdx.x % a.chunks;
+    const T *x = (const T *)a.logits + (long long)r * a.ld;
+    T *y = (T *)a.dlogits + (long long)r * a.ldd;
+    const float m = a.stats[2LL * r], ls = a.stats[2LL * r + 1], c = a.inv_temp;
+    const float dh = a.dentropy ? a.dentropy[r] : 0.f, ent = a.dentropy ? a.entropy[r] : 0.f;
+    long long t = -1;
+    if (a.targets) t = target_of(a.targets, a.id64, r);
+    const bool hit = t >= 0 && t < a.vocab;
+    const float dl = hit && a.dlogp ? a.dlogp[r] : 0.f;
+    const bool empty = m == -INFINITY && ls == ls;
+    // d(z) = dl 1[target] - p (dl + dh (log p + entropy)), times 1 / temperature
+    auto grad = [&](float v, int i) {
+        const float lp = floor_nan((v - m) * c - ls);
+        const float pr = ex2(lp * 1.44269504088896340736f);
+        float g = -pr * (dl + dh * (lp + ent));
+        if (i == (int)t) g += dl;
+        return empty ? 0.f : g * c;
+    };
+    const int e0 = p * a.chunk, e1 = min(a.vocab, e0 + a.chunk);
+    if (!VEC) {
+        for (int i = e0 + tid; i < e1; i += kThreads) y[i] = from_f<T>(grad(to_f(x[i]), i));
+        return;
+    }
+    const int mis = (int)(((uintptr_t)(x + e0) & 15u) / sizeof(T));
+    const int h = min(e1, e0 + (mis ? n - mis : 0));
+    const int groups = (e1 - h) / n, tail = h + groups * n;
+    if (tid < h - e0) y[e0 + tid] = from_f<T>(grad(to_f(x[e0 + tid]), e0 + tid));
+    if (tid < e1 - tail) y[tail + tid] = from_f<T>(grad(to_f(x[tail + tid]), tail + tid));
+    const uint4 *xv = (const uint4 *)(x + h);
+    uint4 *yv = (uint4 *)(y + h);
+    for (int g = tid; g < groups; g += U * kThreads) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (g + u * kThreads < groups) v[u] = xv[g + u * kThreads];  // dlogits may be logits
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int gg = g + u * kThreads;
+            if (gg >= groups) break;
+            float f[n];
+            unpack<T>(v[u], f);
+#pragma unroll
+            for (int i = 0; i < n; ++i) f[i] = grad(f[i], h + gg * n + i);
+            yv[gg] = pack<T>(f);
+        }
+    }
+}
+
+// -------------------------------------------------------------------- host
+bool dims_ok(const lstm_logprob_dims *d) {
+    if (!d || d->N < 0 || d->vocab < 0 || d->ld < d->vocab || d->top < 0) return false;
+    if (!host::dtype_ok(d->dtype) || (d->id_bytes != 4 && d->id_bytes != 8)) return false;
+    if (d->top > d->vocab && d->N > 0) return false;
+    return true;
+}
+bool dims_supported(const lstm_logprob_dims *d) {
+    return d->top <= LSTM_LOGPROB_MAX_TOP && d->vocab <= (1 << 30) && d->N <= (1 << 30);
+}
+
+// Within these limits a masked logit (-1e28 or less below the maximum) has an
+// exponential of zero at every temperature.
+bool temp_ok(float inv_temp) { return inv_temp >= 1e-20f && inv_temp <= 1e20f; }
+
+// Parts of a row: one where the rows alone fill the card four blocks an SM
+// deep; else enough for two blocks an SM, of kMinPart elements at least.
+int parts_of(const lstm_logprob_dims *d, int sms) {
+    if (d->N >= 2 * sms) return 1;
+    const int want = (2 * sms + std::max(d->N, 1) - 1) / std::max(d->N, 1);
+    return std::max(1, std::min({want, d->vocab / kMinPart, kThreads}));
+}
+
+size_t fwd_need(const lstm_logprob_dims *d, int parts) {
+    if (parts == 1) return kCtrlBytes;
+    const size_t rows = (size_t)d->N * parts;
+    return kCtrlBytes + align_up(rows * sizeof(Stat), 256) + align_up(rows * d->top * 8, 256);
+}
+
+template <class T> int forward(Args &a, cudaStream_t s) {
+    const long long blocks = (long long)a.N * a.parts;
+    if (blocks > INT_MAX) return LSTM_ERR_UNSUPPORTED;
+    if (a.top)
+        fwd_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    else
+        fwd_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    if (a.parts > 1) {
+        join_kernel<T><<<a.N, kThreads, 0, s>>>(a);
+        LSTM_CUDA_TRY(host::launched());
+    }
+    return LSTM_OK;
+}
+
+template <class T> int backward(BwdArgs &a, cudaStream_t s) {
+    // Blocks of up to 8192 elements: 32 a thread, four 16-byte groups of a
+    // 16-bit type.
+    a.chunks = (a.vocab + 8191) / 8192;
+    a.chunk = ((a.vocab + a.chunks - 1) / a.chunks + 7) / 8 * 8;
+    const long long blocks = (long long)a.N * a.chunks;
+    if (blocks > INT_MAX) return LSTM_ERR_UNSUPPORTED;
+    // 16-byte groups need logits and dlogits rows that start alike
+    const bool vec = (a.ld - a.ldd) * (long long)sizeof(T) % 16 == 0;
+    if (vec)
+        bwd_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    else
+        bwd_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lstm_logprob_fwd_workspace_size(const lstm_logprob_dims *d) {
+    if (!dims_ok(d) || !dims_supported(d)) return 0;
+    return fwd_need(d, parts_of(d, host::sm_count()));
+}
+
+int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void *targets, float inv_temp,
+                     float *logp, float *entropy, float *stats, int *top_ids, float *top_logp, void *ws,
+                     size_t ws_bytes, void *stream) {
+    if (!dims_ok(d) || !temp_ok(inv_temp)) return LSTM_ERR_INVALID_ARG;
+    if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
+    const bool any = d->N > 0;
+    if (!host::ptr_ok(logits, any && d->vocab > 0) || !host::ptr_ok(targets, any && logp) ||
+        !host::ptr_ok(logp, any && targets) || !host::ptr_ok(entropy, false) || !host::ptr_ok(stats, any) ||
+        !host::ptr_ok(top_ids, any && d->top > 0) || !host::ptr_ok(top_logp, any && d->top > 0))
+        return LSTM_ERR_INVALID_ARG;
+    const int parts = parts_of(d, host::sm_count());
+    const int rc = host::ws_check(ws, ws_bytes, fwd_need(d, parts));
+    if (rc != LSTM_OK) return rc;
+    if (!any) return LSTM_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    Args a = {};
+    a.logits = logits;
+    a.targets = targets;
+    a.id64 = d->id_bytes == 8;
+    a.N = d->N;
+    a.vocab = d->vocab;
+    a.top = d->top;
+    a.parts = parts;
+    a.ld = d->ld;
+    a.inv_temp = inv_temp;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.stats = stats;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.part_stats = (Stat *)((char *)ws + kCtrlBytes);
+    a.part_keys = (unsigned long long *)((char *)ws + kCtrlBytes + align_up((size_t)d->N * parts * sizeof(Stat), 256));
+    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, s));
+    if (d->dtype == LSTM_F32) return forward<float>(a, s);
+    if (d->dtype == LSTM_F16) return forward<f16>(a, s);
+    return forward<bf16>(a, s);
+}
+
+int lstm_logprob_bwd(const lstm_logprob_dims *d, const void *logits, const void *targets, float inv_temp,
+                     const float *stats, const float *entropy, const float *dlogp, const float *dentropy,
+                     void *dlogits, long long ldd, void *stream) {
+    if (!dims_ok(d) || ldd < d->vocab || !temp_ok(inv_temp)) return LSTM_ERR_INVALID_ARG;
+    if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
+    const bool any = d->N > 0 && d->vocab > 0;
+    if (!host::ptr_ok(logits, any) || !host::ptr_ok(targets, any && dlogp) || !host::ptr_ok(stats, any) ||
+        !host::ptr_ok(entropy, any && dentropy) || !host::ptr_ok(dlogp, false) ||
+        !host::ptr_ok(dentropy, false) || !host::ptr_ok(dlogits, any))
+        return LSTM_ERR_INVALID_ARG;
+    if (dlogits == logits && ldd != d->ld && any) return LSTM_ERR_INVALID_ARG;
+    if (!any) return LSTM_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    BwdArgs a = {};
+    a.logits = logits;
+    a.targets = targets;
+    a.id64 = d->id_bytes == 8;
+    a.N = d->N;
+    a.vocab = d->vocab;
+    a.ld = d->ld;
+    a.ldd = ldd;
+    a.inv_temp = inv_temp;
+    a.stats = stats;
+    a.entropy = entropy;
+    a.dlogp = dlogp;
+    a.dentropy = dentropy;
+    a.dlogits = dlogits;
+    if (d->dtype == LSTM_F32) return backward<float>(a, s);
+    if (d->dtype == LSTM_F16) return backward<f16>(a, s);
+    return backward<bf16>(a, s);
+}
+
+}  // extern "C"

@@ -344,13 +344,97 @@ int lstm_fwd_noalloc(const lstm_dims *d, const void *x, const void *W, const voi
                      void *gates, float *cells, void *stream);
 int lstm_fwd_noalloc_status(void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators beside the LSTM in a recurrent language model: the token
+ * embedding that makes x, the gated delta rule (a recurrent layer with a
+ * matrix state) and the log-probabilities of tokens at its output.  The
+ * conventions above hold (16-byte aligned device pointers, caller-owned
+ * memory and workspaces of 256-byte alignment, status codes, asynchronous on
+ * `stream`, nothing enqueued after an argument error); no call reads a host
+ * value from the device, so each can be captured into a graph.  Empty
+ * problems are valid.
+ * --------------------------------------------------------------------- */
+
+/*
+ * lstm_embed_fwd / lstm_embed_bwd -- token embedding ("Embedding" of the "cmu
+ * 10-414 HW4" page, with a scale) and the gradient of its table:
+ *   x_r = scale table[ids_r],   dtable[w] = scale sum_{r : ids_r = w} dx_r.
+ *
+ * N ids, a table of `vocab` rows of I elements.  ids: int (id_bytes 4) or long
+ * long (8).  An id outside 0 .. vocab-1 is padding: a row of zeros, no
+ * gradient.  Forward: table [vocab][I] and x [N][I] are of type dtype; the
+ * product is rounded once.  Backward: dx [N][I] is of type dtype (LSTM_F32
+ * for lstm_bwd's dx), sums are float in the order of r (the same bits every
+ * time); dtable [vocab][I] float is overwritten (accumulate 0) or added to
+ * (1: rows without a token are neither read nor written).
+ */
+typedef struct lstm_embed_dims {
+    int N;
+    int vocab;
+    int I;
+    int dtype;
+    int id_bytes; /* 4 or 8 */
+} lstm_embed_dims;
+
+int lstm_embed_fwd(const lstm_embed_dims *d, const void *ids, const void *table, float scale,
+                   void *x, void *stream);
+size_t lstm_embed_bwd_workspace_size(const lstm_embed_dims *d);
+int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, float scale,
+                   int accumulate, float *dtable, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * lstm_logprob_fwd / lstm_logprob_bwd -- log-probabilities of given tokens.
+ * N rows of `vocab` logits (type dtype, row stride ld >= vocab elements),
+ * z = logits * inv_temp (inverse temperature, 1e-20 .. 1e20), p = softmax(z):
+ *   logp [N]       float  log p[targets_r]; 0 for a target outside
+ *                         0 .. vocab-1 (an ignored row); needs targets; or NULL
+ *   entropy [N]    float  -sum p log p, or NULL
+ *   stats [N][2]   float  the largest logit m and log sum exp(z - m inv_temp),
+ *                         for the backward
+ *   top_ids [N][top] int, top_logp [N][top] float: the `top` (0 ..
+ *                         LSTM_LOGPROB_MAX_TOP, at most vocab) largest logits,
+ *                         equal ones by lower id, and their log p; NULL at 0
+ * targets [N]: int or long long by id_bytes, or NULL.  Logits of -inf are
+ * masked: their p is 0 and counts as 0 in the entropy.  A row of nothing but
+ * -inf has logp and top_logp -inf, entropy 0 and a zero gradient.  A NaN or
+ * +inf makes its row's values NaN (NaN is listed after every number).
+ *
+ * lstm_logprob_bwd: dlogits [N][vocab] (type dtype, row stride ldd), the
+ * gradient for dlogp [N] and dentropy [N] (float, either NULL):
+ *   dlogits = inv_temp (dlogp (1[target] - p) - dentropy p (log p + entropy)).
+ * It reads the forward's logits, targets, stats and (for dentropy) entropy.
+ * dlogits may be logits itself (with ldd == ld).  Elements vocab .. ld-1 of a
+ * row are neither read nor written.  (top_logp has no gradient.)
+ */
+#define LSTM_LOGPROB_MAX_TOP 64
+typedef struct lstm_logprob_dims {
+    int N;
+    int vocab;
+    long long ld;
+    int top;
+    int dtype;
+    int id_bytes; /* 4 or 8 */
+} lstm_logprob_dims;
+
+/* (Depends on the current device: rows are split by its SM count.) */
+size_t lstm_logprob_fwd_workspace_size(const lstm_logprob_dims *d);
+int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void *targets,
+                     float inv_temp, float *logp, float *entropy, float *stats, int *top_ids,
+                     float *top_logp, void *ws, size_t ws_bytes, void *stream);
+int lstm_logprob_bwd(const lstm_logprob_dims *d, const void *logits, const void *targets,
+                     float inv_temp, const float *stats, const float *entropy,
+                     const float *dlogp, const float *dentropy, void *dlogits, long long ldd,
+                     void *stream);
+
 /* Static description of a status code. */
 const char *lstm_strerror(int code);
 
 /* ABI version: 100 * major + minor (1.1: lstm_options with gate_order, the
  * LSTM_F16 compute type and the stack entry points; 1.2: the plan-aware
  * forward workspace sizes and lstm_fwd_noalloc_status; 1.3: the stacked
- * layer wavefront and lstm_stack_bwd_workspace_size_min). */
+ * layer wavefront and lstm_stack_bwd_workspace_size_min).  The embedding,
+ * log-probability and gated-delta-rule entry points came later without a new
+ * number: nothing older changed, and a loader can look their symbols up. */
 #define LSTM_ABI_VERSION 103
 int lstm_abi_version(void);
 

@@ -1,0 +1,120 @@
+"""The boundary of the embedding and log-probability entry points, checked
+without a GPU: every rejected call returns before its first CUDA call."""
+import ctypes
+
+import pytest
+import torch
+
+from backward_lstm_fwd_b200 import binding as L
+from backward_lstm_fwd_b200 import build as lbuild
+
+FAKE = 0x10000  # a 16-byte aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    lbuild.build()
+    return L.load()
+
+
+# ---------------------------------------------------------------- embedding
+def embed_fwd(lib, d, ids=FAKE, table=FAKE, x=FAKE):
+    return lib.lstm_embed_fwd(ctypes.byref(d), ids, table, 1.0, x, None)
+
+
+def embed_bwd(lib, d, ids=FAKE, dx=FAKE, dtable=FAKE, ws=FAKE, ws_bytes=None, accumulate=0):
+    n = L.embed_bwd_workspace_size(d) if ws_bytes is None else ws_bytes
+    return lib.lstm_embed_bwd(ctypes.byref(d), ids, dx, 1.0, accumulate, dtable, ws, n, None)
+
+
+@pytest.mark.parametrize("bad", [(-1, 5, 8, 0, 8), (4, -5, 8, 0, 8), (4, 5, -8, 0, 8), (4, 5, 8, 3, 8), (4, 5, 8, 0, 2)])
+def test_embed_dims(lib, bad):
+    d = L.embed_dims(*bad[:3], bad[3], bad[4])
+    assert embed_fwd(lib, d) == L.LSTM_ERR_INVALID_ARG
+    assert embed_bwd(lib, d, ws_bytes=1 << 30) == L.LSTM_ERR_INVALID_ARG
+    assert L.embed_bwd_workspace_size(d) == 0
+
+
+def test_embed_pointers_and_workspace(lib):
+    d = L.embed_dims(4, 5, 8, L.LSTM_BF16)
+    for k in ("ids", "table", "x"):
+        assert embed_fwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
+        assert embed_fwd(lib, d, **{k: FAKE + 4}) == L.LSTM_ERR_INVALID_ARG
+    for k in ("ids", "dx", "dtable"):
+        assert embed_bwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
+        assert embed_bwd(lib, d, **{k: FAKE + 4}) == L.LSTM_ERR_INVALID_ARG
+    assert embed_bwd(lib, d, accumulate=2) == L.LSTM_ERR_INVALID_ARG
+    need = L.embed_bwd_workspace_size(d)
+    assert embed_bwd(lib, d, ws_bytes=need - 1) == L.LSTM_ERR_WORKSPACE
+    assert embed_bwd(lib, d, ws=None) == L.LSTM_ERR_WORKSPACE
+    assert embed_bwd(lib, d, ws=FAKE + 16) == L.LSTM_ERR_WORKSPACE
+    assert lib.lstm_embed_fwd(None, FAKE, FAKE, 1.0, FAKE, None) == L.LSTM_ERR_INVALID_ARG
+    # nothing to do: nothing is enqueued
+    assert embed_fwd(lib, L.embed_dims(0, 5, 8, 0), ids=None, x=None) == L.LSTM_OK
+    assert embed_bwd(lib, L.embed_dims(4, 0, 8, 0), dtable=None) == L.LSTM_OK
+
+
+def test_embed_extents(lib):
+    assert embed_fwd(lib, L.embed_dims(4, (1 << 30) + 1, 8, 0)) == L.LSTM_ERR_UNSUPPORTED
+    assert embed_bwd(lib, L.embed_dims(4, 5, (1 << 24) + 1, 0), ws_bytes=1 << 40) == L.LSTM_ERR_UNSUPPORTED
+
+
+# --------------------------------------------------------- log-probabilities
+def logprob_fwd(lib, d, inv_temp=1.0, logits=FAKE, targets=FAKE, logp=FAKE, entropy=FAKE, stats=FAKE, top_ids=FAKE,
+                top_logp=FAKE, ws=FAKE, ws_bytes=None):
+    n = L.logprob_fwd_workspace_size(d) if ws_bytes is None else ws_bytes
+    return lib.lstm_logprob_fwd(ctypes.byref(d), logits, targets, inv_temp, logp, entropy, stats, top_ids, top_logp,
+                                ws, n, None)
+
+
+def logprob_bwd(lib, d, inv_temp=1.0, logits=FAKE, targets=FAKE, stats=FAKE, entropy=FAKE, dlogp=FAKE, dentropy=FAKE,
+                dlogits=2 * FAKE, ldd=None):
+    return lib.lstm_logprob_bwd(ctypes.byref(d), logits, targets, inv_temp, stats, entropy, dlogp, dentropy, dlogits,
+                                d.vocab if ldd is None else ldd, None)
+
+
+@pytest.mark.parametrize("kw", [dict(N=-1, vocab=9), dict(N=2, vocab=-1), dict(N=2, vocab=9, ld=8), dict(N=2, vocab=9, top=10),
+                                dict(N=2, vocab=9, top=-1), dict(N=2, vocab=9, dtype=5), dict(N=2, vocab=9, id_bytes=1)])
+def test_logprob_dims(lib, kw):
+    kw.setdefault("dtype", L.LSTM_F32)
+    d = L.logprob_dims(**kw)
+    assert logprob_fwd(lib, d, ws_bytes=1 << 30) == L.LSTM_ERR_INVALID_ARG
+    assert logprob_bwd(lib, d) == L.LSTM_ERR_INVALID_ARG
+    assert L.logprob_fwd_workspace_size(d) == 0
+
+
+def test_logprob_arguments(lib):
+    d = L.logprob_dims(3, 100, L.LSTM_F16, top=4)
+    for t in (0.0, -1.0, float("nan"), float("inf"), 1e-30):
+        assert logprob_fwd(lib, d, inv_temp=t) == L.LSTM_ERR_INVALID_ARG
+        assert logprob_bwd(lib, d, inv_temp=t) == L.LSTM_ERR_INVALID_ARG
+    for k in ("logits", "targets", "stats", "top_ids", "top_logp"):
+        assert logprob_fwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
+    for k in ("logits", "targets", "logp", "entropy", "stats", "top_ids", "top_logp"):
+        assert logprob_fwd(lib, d, **{k: FAKE + 2}) == L.LSTM_ERR_INVALID_ARG
+    for k in ("logits", "targets", "stats", "entropy", "dlogits"):
+        assert logprob_bwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
+        assert logprob_bwd(lib, d, **{k: FAKE + 2}) == L.LSTM_ERR_INVALID_ARG
+    assert logprob_bwd(lib, d, ldd=99) == L.LSTM_ERR_INVALID_ARG
+    assert logprob_bwd(lib, d, dlogits=FAKE, ldd=104) == L.LSTM_ERR_INVALID_ARG  # in place with another stride
+    need = L.logprob_fwd_workspace_size(d)
+    assert logprob_fwd(lib, d, ws_bytes=need - 1) == L.LSTM_ERR_WORKSPACE
+    assert logprob_fwd(lib, d, ws=FAKE + 128) == L.LSTM_ERR_WORKSPACE
+    assert logprob_fwd(lib, L.logprob_dims(3, 100, 0, top=65), ws_bytes=1 << 30) == L.LSTM_ERR_UNSUPPORTED
+    # few long rows are split: the parts' sums and alternatives live in the workspace
+    assert L.logprob_fwd_workspace_size(L.logprob_dims(2, 128000, 0, top=20)) > 256
+    assert L.logprob_fwd_workspace_size(L.logprob_dims(4096, 128000, 0, top=20)) == 256
+
+
+def test_binding_refuses_host_tensors_and_shapes(lib):
+    ids, table = torch.zeros(3, dtype=torch.int64), torch.zeros(5, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.embed(ids, table)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.embed_backward(ids, torch.zeros(3, 8), 5)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.logprobs(torch.zeros(3, 5), ids)
+    with pytest.raises(ValueError, match="rows overlap"):
+        L.logprobs(torch.zeros(1, 5).expand(3, 5), ids)
+    with pytest.raises(ValueError, match="dense"):
+        L.logprobs(torch.zeros(5, 3).t(), ids)
