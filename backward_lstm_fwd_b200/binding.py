@@ -34,6 +34,8 @@ EXPORTS = ("lstm_fwd_workspace_size", "lstm_bwd_workspace_size", "lstm_fwd_works
            "lstm_stack_bwd_workspace_size", "lstm_stack_bwd_workspace_size_min",
            "lstm_stack_fwd", "lstm_stack_bwd",
            "lstm_embed_fwd", "lstm_embed_bwd_workspace_size", "lstm_embed_bwd",
+           "lstm_gdr_fwd_workspace_size", "lstm_gdr_bwd_workspace_size", "lstm_gdr_fwd",
+           "lstm_gdr_bwd",
            "lstm_logprob_fwd_workspace_size", "lstm_logprob_fwd", "lstm_logprob_bwd",
            "lstm_status", "lstm_profile_begin", "lstm_profile_end", "lstm_launch_count",
            "lstm_strerror", "lstm_abi_version")
@@ -68,6 +70,16 @@ class Options(ctypes.Structure):
 class EmbedDims(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int), ("vocab", ctypes.c_int), ("I", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("id_bytes", ctypes.c_int)]
+
+
+class GdrDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "B", "Hk", "Hv", "K", "V", "dtype")] + \
+        [(n, ctypes.c_longlong) for n in ("ldq", "ldk", "ldv")]
+
+
+class GdrOptions(ctypes.Structure):
+    """lstm_gdr_options: lengths [B] int32 (device pointer or None), scale."""
+    _fields_ = [("lengths", ctypes.c_void_p), ("scale", ctypes.c_float)]
 
 
 class LogprobDims(ctypes.Structure):
@@ -163,6 +175,15 @@ def load(path: str = LIB_PATH):
     lib.lstm_logprob_fwd.restype = ip
     lib.lstm_logprob_bwd.argtypes = [lp, vp, vp, fp] + [vp] * 5 + [ll, vp]
     lib.lstm_logprob_bwd.restype = ip
+    gp, go = ctypes.POINTER(GdrDims), ctypes.POINTER(GdrOptions)
+    lib.lstm_gdr_fwd_workspace_size.argtypes = [gp, ip]
+    lib.lstm_gdr_fwd_workspace_size.restype = sz
+    lib.lstm_gdr_bwd_workspace_size.argtypes = [gp]
+    lib.lstm_gdr_bwd_workspace_size.restype = sz
+    lib.lstm_gdr_fwd.argtypes = [gp, go] + [vp] * 10 + [vp, sz, vp]
+    lib.lstm_gdr_fwd.restype = ip
+    lib.lstm_gdr_bwd.argtypes = [gp, go] + [vp] * 15 + [vp, sz, vp]
+    lib.lstm_gdr_bwd.restype = ip
     v = lib.lstm_abi_version()
     if v // 100 != ABI_VERSION // 100 or v < ABI_VERSION:
         raise RuntimeError(f"{path}: ABI version {v}, this binding needs {ABI_VERSION} "
@@ -719,3 +740,124 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
                                      _p(out), _rows(out, "out"), _stream(stream)),
              "lstm_logprob_bwd")
     return out
+
+
+GDR_CHUNK = 64
+
+
+def gdr_dims(T: int, B: int, Hk: int, Hv: int, K: int, V: int, dtype, ldq: int = 0, ldk: int = 0,
+             ldv: int = 0) -> GdrDims:
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    return GdrDims(int(T), int(B), int(Hk), int(Hv), int(K), int(V), code, int(ldq), int(ldk),
+                   int(ldv))
+
+
+def gdr_fwd_workspace_size(d: GdrDims, save: bool = False) -> int:
+    return int(load().lstm_gdr_fwd_workspace_size(ctypes.byref(d), int(save)))
+
+
+def gdr_bwd_workspace_size(d: GdrDims) -> int:
+    return int(load().lstm_gdr_bwd_workspace_size(ctypes.byref(d)))
+
+
+class GdrState:
+    """Outputs of one gdr_forward() call; states and deltas (save=True) are
+    kept for the backward."""
+
+    def __init__(self, d: GdrDims, cd, device, save, sT=None):
+        f = dict(dtype=torch.float32, device=device)
+        self.dims = d
+        self.o = torch.empty((d.T, d.B, d.Hv, d.V), dtype=cd, device=device)
+        self.sT = torch.empty((d.B, d.Hv, d.K, d.V), **f) if sT is None else sT
+        nc = -(-d.T // GDR_CHUNK)
+        self.states = torch.empty((nc, d.B, d.Hv, d.K, d.V), **f) if save else None
+        self.deltas = torch.empty((d.T, d.B, d.Hv, d.V), **f) if save else None
+
+
+class GdrGrads:
+    def __init__(self, d: GdrDims, cd, device):
+        f = dict(dtype=torch.float32, device=device)
+        self.dq = torch.empty((d.T, d.B, d.Hk, d.K), dtype=cd, device=device)
+        self.dk = torch.empty((d.T, d.B, d.Hk, d.K), dtype=cd, device=device)
+        self.dv = torch.empty((d.T, d.B, d.Hv, d.V), dtype=cd, device=device)
+        self.dg = torch.empty((d.T, d.B, d.Hv), **f)
+        self.dbeta = torch.empty((d.T, d.B, d.Hv), **f)
+        self.ds0 = torch.empty((d.B, d.Hv, d.K, d.V), **f)
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the tokens (rows t * B + n) of a [T, B, H, D] tensor
+    whose heads are dense: a slice of a wider [T, B, ...] tensor qualifies."""
+    T, B, H, D = t.shape
+    dense = H * D
+    if t.is_contiguous():
+        return dense
+    _need((D <= 1 or t.stride(3) == 1) and (H <= 1 or t.stride(2) == D),
+          f"{name}: heads must be dense")
+    ld = t.stride(1) if B > 1 else t.stride(0) if T > 1 else dense
+    _need(T <= 1 or B <= 1 or t.stride(0) == B * ld, f"{name}: tokens must have one stride")
+    _need(ld >= dense, f"{name}: tokens overlap")
+    return ld
+
+
+def _gdr_call(q, k, v, g, beta, lengths, scale):
+    """(dims, options, K**-0.5 or scale) of one call, its arguments checked."""
+    _need(q.dim() == 4 and v.dim() == 4, "q, k [T, B, Hk, K] and v [T, B, Hv, V]")
+    T, B, Hk, K = q.shape
+    Hv, V = v.shape[2:]
+    _on(q, k=k, v=v, g=g, beta=beta, lengths=lengths)
+    _shaped(k, "k", q.shape, q.dtype)
+    _shaped(v, "v", (T, B, Hv, V), q.dtype)
+    _shaped(g, "g", (T, B, Hv), torch.float32)
+    _shaped(beta, "beta", (T, B, Hv), torch.float32)
+    _shaped(lengths, "lengths", (B,), torch.int32)
+    _dense(g=g, beta=beta, lengths=lengths)
+    d = gdr_dims(T, B, Hk, Hv, K, V, q.dtype, _token_stride(q, "q"), _token_stride(k, "k"),
+                 _token_stride(v, "v"))
+    return d, GdrOptions(_p(lengths), K ** -0.5 if scale is None else float(scale))
+
+
+def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool = False, sT=None,
+                ws=None, stream=None) -> GdrState:
+    """lstm_gdr_fwd: the gated delta rule on q, k [T,B,Hk,K] and v [T,B,Hv,V]
+    (one compute dtype; slices of one projection will do), log decay g and
+    beta [T,B,Hv] float32, state s0 [B,Hv,K,V] float32.  lengths [B] int32 marks
+    padding; scale defaults to K**-0.5.  save keeps what gdr_backward needs;
+    sT gives the final state's tensor (s0 itself for a state kept in place)."""
+    d, opt = _gdr_call(q, k, v, g, beta, lengths, scale)
+    _on(q, s0=s0, sT=sT, ws=ws)
+    _shaped(s0, "s0", (d.B, d.Hv, d.K, d.V), torch.float32)
+    _shaped(sT, "sT", (d.B, d.Hv, d.K, d.V), torch.float32)
+    _dense(s0=s0, sT=sT, ws=ws)
+    with torch.cuda.device(q.device):
+        st = GdrState(d, q.dtype, q.device, save, sT)
+        if ws is None:
+            ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
+        _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _p(q), _p(k), _p(v), _p(g),
+                                 _p(beta), _p(s0), _p(st.o), _p(st.sT), _p(st.states),
+                                 _p(st.deltas), _p(ws), _ws_bytes(ws), _stream(stream)),
+             "lstm_gdr_fwd")
+    return st
+
+
+def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=None, scale=None,
+                 ws=None, stream=None) -> GdrGrads:
+    """lstm_gdr_bwd on the saved state of gdr_forward(..., save=True), with
+    the forward's arguments: dout [T,B,Hv,V] (compute dtype), dsT float32."""
+    d, opt = _gdr_call(q, k, v, g, beta, lengths, scale)
+    _need(st.states is not None, "the forward kept nothing: call gdr_forward(..., save=True)")
+    _on(q, dout=dout, dsT=dsT, ws=ws, states=st.states)
+    _shaped(dout, "dout", (d.T, d.B, d.Hv, d.V), q.dtype)
+    _shaped(dsT, "dsT", (d.B, d.Hv, d.K, d.V), torch.float32)
+    _shaped(st.o, "the state's o", (d.T, d.B, d.Hv, d.V), q.dtype)
+    _dense(dout=dout, dsT=dsT, ws=ws)
+    with torch.cuda.device(q.device):
+        gr = GdrGrads(d, q.dtype, q.device)
+        if ws is None:
+            ws = empty_workspace(gdr_bwd_workspace_size(d), q.device)
+        _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _p(dout), _p(dsT), _p(q),
+                                 _p(k), _p(v), _p(g), _p(beta), _p(st.states), _p(st.deltas),
+                                 _p(gr.dq), _p(gr.dk), _p(gr.dv), _p(gr.dg), _p(gr.dbeta),
+                                 _p(gr.ds0), _p(ws), _ws_bytes(ws), _stream(stream)),
+             "lstm_gdr_bwd")
+    return gr

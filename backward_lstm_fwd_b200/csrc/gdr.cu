@@ -1,0 +1,251 @@
+// gdr.cu -- C ABI of the gated delta rule (declared in include/liblstm.h):
+// argument checks, workspace layout and the launches of gdr.cuh's kernels.
+#include <algorithm>
+#include <climits>
+
+#include "gdr.cuh"
+
+using namespace lstm;
+using namespace lstm::gdr;
+
+namespace {
+
+// Token by token or in chunks.  A token costs the step kernel two passes over
+// its registers and three barriers (about 0.6 us); a chunk costs a fixed
+// launch and chain more, whatever it holds.
+constexpr int kStepTokens = 16;
+
+bool dims_ok(const lstm_gdr_dims *d) {
+    if (!d || d->T < 0 || d->B < 0 || d->Hk < 0 || d->Hv < 0 || d->K < 0 || d->V < 0) return false;
+    if (!host::dtype_ok(d->dtype)) return false;
+    if ((d->Hk == 0) != (d->Hv == 0) || (d->Hk > 0 && d->Hv % d->Hk != 0)) return false;
+    // every row count fits an int
+    return (long long)d->T * d->B <= INT_MAX && (long long)d->Hv * std::max(d->K, d->V) <= INT_MAX;
+}
+
+long long or_dense(long long ld, long long dense) { return ld ? ld : dense; }
+
+int strides_check(const lstm_gdr_dims *d) {
+    const long long q = or_dense(d->ldq, (long long)d->Hk * d->K), k = or_dense(d->ldk, (long long)d->Hk * d->K),
+                    v = or_dense(d->ldv, (long long)d->Hv * d->V);
+    if (q < (long long)d->Hk * d->K || k < (long long)d->Hk * d->K || v < (long long)d->Hv * d->V) return LSTM_ERR_INVALID_ARG;
+    return LSTM_OK;
+}
+
+bool dims_supported(const lstm_gdr_dims *d) {
+    if (d->K % 8 || d->V % 8 || d->K > 128 || d->V > 256) return false;
+    if (or_dense(d->ldq, 0) % 8 || or_dense(d->ldk, 0) % 8 || or_dense(d->ldv, 0) % 8) return false;
+    const long long nc = (d->T + C - 1) / C;
+    return (long long)d->B * d->Hv * 4 <= INT_MAX && nc * d->B * std::max(d->Hk, d->Hv) <= INT_MAX;
+}
+
+int check(const lstm_gdr_dims *d) {
+    if (!dims_ok(d)) return LSTM_ERR_INVALID_ARG;
+    const int rc = strides_check(d);
+    if (rc != LSTM_OK) return rc;
+    return dims_supported(d) ? LSTM_OK : LSTM_ERR_UNSUPPORTED;
+}
+
+bool stepwise(const lstm_gdr_dims *d, bool save) { return !save && d->T <= kStepTokens; }
+
+int terms_of(int dtype) { return dtype == LSTM_BF16 ? 1 : dtype == LSTM_F16 ? 2 : 3; }
+
+struct Layout {
+    size_t qk, tp, dstates, dvf, total;
+};
+Layout layout(const lstm_gdr_dims *d, bool bwd) {
+    Layout l;
+    const size_t nc = (d->T + C - 1) / C, kd = d->K <= 64 ? 64 : 128;
+    size_t o = kCtrlBytes;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = align_up(o + bytes, 256);
+        return at;
+    };
+    l.qk = take(nc * d->B * d->Hk * (terms_of(d->dtype) * kd * 256));
+    l.tp = take(nc * d->B * d->Hv * (size_t)TP_BYTES);
+    l.dstates = bwd ? take(nc * d->B * d->Hv * (size_t)d->K * d->V * 4) : 0;
+    l.dvf = bwd ? take((size_t)d->T * d->B * d->Hv * d->V * 4) : 0;
+    l.total = o;
+    return l;
+}
+
+Shape shape_of(const lstm_gdr_dims *d, const lstm_gdr_options *opt) {
+    Shape s = {};
+    s.T = d->T;
+    s.B = d->B;
+    s.Hk = d->Hk;
+    s.Hv = d->Hv;
+    s.K = d->K;
+    s.V = d->V;
+    s.group = d->Hk ? d->Hv / d->Hk : 0;
+    s.NC = (d->T + C - 1) / C;
+    s.VT = (d->V + LANES - 1) / LANES;
+    s.ldq = or_dense(d->ldq, (long long)d->Hk * d->K);
+    s.ldk = or_dense(d->ldk, (long long)d->Hk * d->K);
+    s.ldv = or_dense(d->ldv, (long long)d->Hv * d->V);
+    s.scale = opt ? opt->scale : 1.0f;
+    s.lengths = opt ? opt->lengths : nullptr;
+    return s;
+}
+
+// (The attribute belongs to the function on the current device.)
+template <class Kern> cudaError_t allow_smem(Kern kern, size_t bytes) {
+    return cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <class E, int KD>
+int prep(const Shape &s, const void *q, const void *k, const float *g, const float *beta, char *w, const Layout &l,
+         cudaStream_t st) {
+    PrepArgs p = {s, q, k, g, beta, w + l.qk, w + l.tp, (Ctrl *)w};
+    LSTM_CUDA_TRY(allow_smem(prep_kernel<E, KD>, prep_smem<E, KD>()));
+    prep_kernel<E, KD><<<s.NC * s.B * s.Hk, 128, prep_smem<E, KD>(), st>>>(p);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
+template <class E, int KD>
+int chunked_fwd(const Shape &s, const void *q, const void *k, const void *v, const float *g, const float *beta,
+                const float *s0, void *o, float *sT, float *states, float *deltas, char *w, const Layout &l,
+                cudaStream_t st) {
+    if (s.NC > 0) {
+        const int rc = prep<E, KD>(s, q, k, g, beta, w, l, st);
+        if (rc != LSTM_OK) return rc;
+    }
+    SeqArgs a = {s, w + l.qk, w + l.tp, v, s0, o, sT, states, deltas, (Ctrl *)w};
+    LSTM_CUDA_TRY(allow_smem(seq_fwd_kernel<E, KD>, Seq<E, KD>::smem));
+    seq_fwd_kernel<E, KD><<<s.B * s.Hv * s.VT, SEQ_THREADS, Seq<E, KD>::smem, st>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
+template <class E>
+int stepwise_fwd(const Shape &s, const void *q, const void *k, const void *v, const float *g, const float *beta,
+                 const float *s0, void *o, float *sT, cudaStream_t st) {
+    StepArgs a = {s, q, k, v, g, beta, s0, o, sT, (s.V + STEP_COLS - 1) / STEP_COLS};
+    step_kernel<E><<<s.B * s.Hv * a.tiles, STEP_THREADS, 0, st>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
+template <class E>
+int fwd(const lstm_gdr_dims *d, const Shape &s, const void *q, const void *k, const void *v, const float *g,
+        const float *beta, const float *s0, void *o, float *sT, float *states, float *deltas, char *w,
+        cudaStream_t st) {
+    if (stepwise(d, states != nullptr)) return stepwise_fwd<E>(s, q, k, v, g, beta, s0, o, sT, st);
+    const Layout l = layout(d, false);
+    if (s.K <= 64) return chunked_fwd<E, 64>(s, q, k, v, g, beta, s0, o, sT, states, deltas, w, l, st);
+    return chunked_fwd<E, 128>(s, q, k, v, g, beta, s0, o, sT, states, deltas, w, l, st);
+}
+
+template <class E, int KD>
+int chunked_bwd(const lstm_gdr_dims *d, const Shape &s, const void *dout, const float *dsT, const void *q,
+                const void *k, const float *g, const float *beta, const float *states, const float *deltas, void *dq,
+                void *dk, void *dv, float *dg, float *dbeta, float *ds0, char *w, cudaStream_t st) {
+    const Layout l = layout(d, true);
+    if (s.NC > 0) {
+        const int rc = prep<E, KD>(s, q, k, g, beta, w, l, st);
+        if (rc != LSTM_OK) return rc;
+    }
+    float *dstates = (float *)(w + l.dstates), *dvf = (float *)(w + l.dvf);
+    SeqArgs a = {s, w + l.qk, w + l.tp, dout, dsT, dv, ds0, dstates, dvf, (Ctrl *)w};
+    LSTM_CUDA_TRY(allow_smem(seq_bwd_kernel<E, KD>, Seq<E, KD>::smem));
+    seq_bwd_kernel<E, KD><<<s.B * s.Hv * s.VT, SEQ_THREADS, Seq<E, KD>::smem, st>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    if (s.NC == 0) return LSTM_OK;
+    GradArgs ga = {s, w + l.qk, g, beta, dout, states, deltas, dstates, dvf, dq, dk, dg, dbeta, (Ctrl *)w};
+    LSTM_CUDA_TRY(allow_smem(grad_kernel<E, KD>, GradSmem<E, KD>::smem));
+    grad_kernel<E, KD><<<s.NC * s.B * s.Hk, GRAD_THREADS, GradSmem<E, KD>::smem, st>>>(ga);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
+template <class E, class... A> int bwd(const lstm_gdr_dims *d, A... args) {
+    return d->K <= 64 ? chunked_bwd<E, 64>(d, args...) : chunked_bwd<E, 128>(d, args...);
+}
+
+bool scale_ok(const lstm_gdr_options *opt) { return !opt || (opt->scale == opt->scale && opt->scale - opt->scale == 0.f); }
+
+}  // namespace
+
+extern "C" {
+
+size_t lstm_gdr_fwd_workspace_size(const lstm_gdr_dims *d, int save) {
+    if (check(d) != LSTM_OK) return 0;
+    return stepwise(d, save != 0) ? kCtrlBytes : layout(d, false).total;
+}
+
+size_t lstm_gdr_bwd_workspace_size(const lstm_gdr_dims *d) {
+    if (check(d) != LSTM_OK) return 0;
+    return layout(d, true).total;
+}
+
+int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *q, const void *k, const void *v,
+                 const float *g, const float *beta, const float *s0, void *o, float *sT, float *states, float *deltas,
+                 void *ws, size_t ws_bytes, void *stream) {
+    int rc = check(d);
+    if (rc != LSTM_OK) return rc;
+    if (!scale_ok(opt)) return LSTM_ERR_INVALID_ARG;
+    const long long rows = (long long)d->T * d->B * d->Hv;
+    const bool any = rows > 0, state = (long long)d->B * d->Hv * d->K * d->V > 0;
+    if (!host::ptr_ok(q, any && d->K) || !host::ptr_ok(k, any && d->K) || !host::ptr_ok(v, any && d->V) ||
+        !host::ptr_ok(g, any) || !host::ptr_ok(beta, any) || !host::ptr_ok(s0, false) ||
+        !host::ptr_ok(o, any && d->V) || !host::ptr_ok(sT, state) || !host::ptr_ok(states, false) ||
+        !host::ptr_ok(deltas, false) || !host::ptr_ok(opt ? opt->lengths : nullptr, false) ||
+        (states != nullptr) != (deltas != nullptr))
+        return LSTM_ERR_INVALID_ARG;
+    rc = host::ws_check(ws, ws_bytes, lstm_gdr_fwd_workspace_size(d, states != nullptr));
+    if (rc != LSTM_OK) return rc;
+    if ((long long)d->B * d->Hv * d->V == 0) return LSTM_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, st));
+    const Shape s = shape_of(d, opt);
+    char *w = (char *)ws;
+    if (d->dtype == LSTM_F32) return fwd<float>(d, s, q, k, v, g, beta, s0, o, sT, states, deltas, w, st);
+    if (d->dtype == LSTM_F16) return fwd<f16>(d, s, q, k, v, g, beta, s0, o, sT, states, deltas, w, st);
+    return fwd<bf16>(d, s, q, k, v, g, beta, s0, o, sT, states, deltas, w, st);
+}
+
+int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *dout, const float *dsT, const void *q,
+                 const void *k, const void *v, const float *g, const float *beta, const float *states,
+                 const float *deltas, void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0, void *ws,
+                 size_t ws_bytes, void *stream) {
+    int rc = check(d);
+    if (rc != LSTM_OK) return rc;
+    if (!scale_ok(opt)) return LSTM_ERR_INVALID_ARG;
+    const long long rows = (long long)d->T * d->B * d->Hv;
+    const bool any = rows > 0, state = any && d->K && d->V;
+    if (!host::ptr_ok(dout, false) || !host::ptr_ok(dsT, false) || !host::ptr_ok(q, any && d->K) ||
+        !host::ptr_ok(k, any && d->K) || !host::ptr_ok(v, false) || !host::ptr_ok(g, any) ||
+        !host::ptr_ok(beta, any) || !host::ptr_ok(states, state) || !host::ptr_ok(deltas, any && d->V) ||
+        !host::ptr_ok(dq, any && d->K) || !host::ptr_ok(dk, any && d->K) || !host::ptr_ok(dv, any && d->V) ||
+        !host::ptr_ok(dg, any) || !host::ptr_ok(dbeta, any) || !host::ptr_ok(ds0, false) ||
+        !host::ptr_ok(opt ? opt->lengths : nullptr, false))
+        return LSTM_ERR_INVALID_ARG;
+    rc = host::ws_check(ws, ws_bytes, layout(d, true).total);
+    if (rc != LSTM_OK) return rc;
+    if ((long long)d->B * d->Hv == 0) return LSTM_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (d->V == 0) {  // no outputs depend on q, k, g and beta
+        if (any) {
+            if (d->K) {
+                const size_t n = (size_t)d->T * d->B * d->Hk * d->K * host::elem_bytes(d->dtype);
+                LSTM_CUDA_TRY(cudaMemsetAsync(dq, 0, n, st));
+                LSTM_CUDA_TRY(cudaMemsetAsync(dk, 0, n, st));
+            }
+            LSTM_CUDA_TRY(cudaMemsetAsync(dg, 0, (size_t)rows * 4, st));
+            LSTM_CUDA_TRY(cudaMemsetAsync(dbeta, 0, (size_t)rows * 4, st));
+        }
+        return LSTM_OK;
+    }
+    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, st));
+    const Shape s = shape_of(d, opt);
+    char *w = (char *)ws;
+    if (d->dtype == LSTM_F32)
+        return bwd<float>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, w, st);
+    if (d->dtype == LSTM_F16)
+        return bwd<f16>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, w, st);
+    return bwd<bf16>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, w, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,1329 @@
+// gdr.cuh -- kernels of the gated delta rule, a recurrent layer whose state
+// of a head is a matrix S [K][V]:
+//   S' = e^{g_t} S_{t-1},  x_t = v_t - S'^T k_t,  S_t = S' + beta_t k_t x_t^T,
+//   o_t = scale S_t^T q_t.
+//
+// Chunked form (64 tokens).  With b_i the running sum of g in the chunk,
+// gamma_i = e^{b_i}, Gamma_ij = e^{b_i - b_j} for i >= j, left_i = e^{b_63 - b_i}:
+//   N  = strictly lower part of Gamma o (K K^T),   T2 = (1 + N diag(beta))^-1
+//   P  = scale (lower part of Gamma o (Q K^T))
+//   X  = T2 (V - diag(gamma) K S0),                U  = diag(beta) X
+//   O  = scale diag(gamma) Q S0 + P U
+//   S1 = gamma_63 S0 + K^T diag(left) U
+// and backward, from dO and dS1:
+//   dU  = P^T dO + diag(left) K dS1,               dV = T2^T diag(beta) dU
+//   dS0 = gamma_63 dS1 + scale Q^T diag(gamma) dO - K^T diag(gamma) dV
+//   Y = dO X^T, Z = dV X^T, E = X dS1^T, F = dO S0^T, G = dV S0^T
+//   Yh = scale Gamma o Y diag(beta) (i >= j), Zh = Gamma o Z diag(beta) (i > j)
+//   dQ = scale diag(gamma) F + Yh K
+//   dK = Yh^T Q - (Zh + Zh^T) K + diag(left beta) E - diag(gamma) G
+//   w_rj = Gamma_rj (scale (q_r.k_j) Y_rj - [r > j] (k_r.k_j) Z_rj)
+//   dbeta_j = sum_r w_rj + left_j k_j.E_j
+//   dg_i = sum_{r >= i > j} w_rj beta_j + sum_{r >= i} gamma_r (scale q_r.F_r - k_r.G_r)
+//        + sum_{j < i} left_j beta_j k_j.E_j + gamma_63 <dS1, S0>
+//
+// Kernels: prep (every chunk at once: operand tiles, T2, P, gates), seq_fwd /
+// seq_bwd (one block per head walks its chunks, the state in registers), grad
+// (every chunk at once) and step (token by token, for a few tokens).
+//
+// Numbers.  The contractions run on the tensor cores in bf16 with float
+// accumulators, every float operand split into three bf16 terms (8 + 8 + 8
+// bits of its 24) and the products of orders 0, 1 and 2 kept: what is dropped
+// is 2^-24 of the operands, below the rounding of a float sum.  bf16 inputs are
+// one term, fp16 two, fp32 three, each exactly the input.  Running sums of g
+// are double: b_i - b_j of a float sum would lose the digits that a strong
+// decay needs between its neighbours.
+#pragma once
+
+#include "host.cuh"
+#include "tc_ptx.cuh"
+
+namespace lstm {
+namespace gdr {
+
+typedef __nv_bfloat16 bf16;
+typedef __half f16;
+
+constexpr int C = LSTM_GDR_CHUNK;  // tokens of a chunk
+static_assert(C == 64, "tiles and tensor-memory columns are laid out for 64 tokens");
+constexpr int NT = 3;              // bf16 terms of a float operand
+constexpr int TILE = C * 128;      // 64 rows x 64 bf16, 128-byte swizzled: 8 KB
+constexpr int LANES = 128;         // columns of the state a block looks after (TMEM lanes)
+constexpr int GATES = 3 * C * 4;   // bytes of a chunk's gates: gamma, left, beta [64] floats
+
+template <class E> struct Terms;   // bf16 terms of an input type
+template <> struct Terms<bf16> { static constexpr int n = 1; };
+template <> struct Terms<f16> { static constexpr int n = 2; };
+template <> struct Terms<float> { static constexpr int n = 3; };
+
+// One chunk of one key head: for each term, KD / 64 chunks of [q 64 rows][k 64 rows] x 64.
+template <class E, int KD> struct QK {
+    static constexpr int term = KD / 64 * 2 * TILE, bytes = Terms<E>::n * term;
+};
+// One chunk of one value head: T2 terms, P terms, gates.
+constexpr int TP_BYTES = 2 * NT * TILE + GATES;
+
+struct Shape {
+    int T, B, Hk, Hv, K, V, group, NC, VT;  // NC chunks, VT blocks of 128 state columns
+    long long ldq, ldk, ldv;                // elements between tokens (rows t * B + b)
+    float scale;
+    const int *lengths;
+};
+
+__device__ __forceinline__ int length_of(const Shape &s, int b) {
+    return s.lengths ? max(0, min(s.T, s.lengths[b])) : s.T;
+}
+
+// ------------------------------------------------------------ conversions
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float low_f(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// Two floats -> n packed bf16 pairs whose sum is the floats (n = 3: to 2^-24).
+template <int n> __device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        t[i] = pack2(a, b);
+        if (i + 1 < n) {
+            a -= low_f(t[i]);
+            b -= high_f(t[i]);
+        }
+    }
+}
+
+// byte offset of (row, byte column) in a 128-byte swizzled tile
+__device__ __forceinline__ uint32_t swz(int row, int cb) { return row * 128 + (cb ^ ((row & 7) << 4)); }
+
+// Eight consecutive elements as floats.
+template <class E> __device__ __forceinline__ void load8(const E *p, float (&f)[8]) { x8_to_f32<E>(__ldg((const uint4 *)p), f); }
+template <> __device__ __forceinline__ void load8<float>(const float *p, float (&f)[8]) {
+    const float4 a = __ldg((const float4 *)p), b = __ldg((const float4 *)p + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+// n terms of eight floats as 16-byte groups.
+template <int n> __device__ __forceinline__ void split8(const float (&f)[8], uint4 (&o)[n]) {
+    uint32_t t[4][n];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2<n>(f[2 * i], f[2 * i + 1], t[i]);
+#pragma unroll
+    for (int k = 0; k < n; ++k) o[k] = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
+}
+
+// ------------------------------------------------------------ descriptors
+// Tiles are [rows][64] bf16, 128-byte swizzled.  As a K-major operand the rows
+// are M or N and a K = 16 step moves 32 bytes; as an MN-major operand the rows
+// are K (a step moves 16 rows, 2048 bytes) and 64-wide chunks are lbo apart.
+__device__ __forceinline__ uint64_t k_major(uint32_t tile, int ks) { return tc::smem_desc_sw128(tile + ks * 32, 16, 1024); }
+__device__ __forceinline__ uint64_t mn_major(uint32_t tile, int ks, uint32_t lbo) {
+    return tc::smem_desc_sw128(tile + ks * 2048, lbo, 1024);
+}
+
+// Write 2 n floats of this thread's lane as terms: term t of pair i goes to
+// column col + t * stride + i.  n a multiple of 8.
+template <int n, int terms>
+__device__ __forceinline__ void put_terms(uint32_t col, int stride, const float (&f)[2 * n]) {
+#pragma unroll
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        uint32_t r[terms][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t t[terms];
+            split2<terms>(f[2 * (i0 + i)], f[2 * (i0 + i) + 1], t);
+#pragma unroll
+            for (int k = 0; k < terms; ++k) r[k][i] = t[k];
+        }
+#pragma unroll
+        for (int k = 0; k < terms; ++k) tc::tmem_st8(col + k * stride + i0, r[k]);
+    }
+}
+
+__device__ __forceinline__ void get32(uint32_t col, float (&f)[32]) {
+    uint32_t r[32];
+    tc::tmem_ld32(col, r);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A bounded wait of a whole warp, ordered before its tensor-memory accesses.
+// After a time-out every later wait returns at once: the block runs to its
+// end on what is there, and the status word says so.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, Ctrl *ctrl, volatile int *abort_flag, uint32_t site) {
+    tc::mbar_wait(bar, parity, ctrl, abort_flag, site);
+    __syncwarp();
+    tc::tc_fence_after();
+}
+
+// Untiled bulk copy global -> this block's shared memory (16-byte aligned).
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// ------------------------------------------------------------------- gates
+// Warp 0: the chunk's running sums b (double) and beta in shared memory, two
+// tokens a lane.  Padding (t >= len) has g = 0 and beta = 0.  g = -inf (or
+// below -1e5) counts as -1e5: its exponential is zero all the same.
+__device__ __forceinline__ void load_gates(const Shape &s, const float *g, const float *beta, int c, int b,
+                                           int h, int len, double *bs, float *betas) {
+    const int lane = threadIdx.x & 31;
+    double v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = 2 * lane + i, t = c * C + j;
+        const long long at = ((long long)t * s.B + b) * s.Hv + h;
+        const float gv = t < len ? g[at] : 0.f;
+        v[i] = gv < -1e5f ? -1e5 : (double)gv;
+        betas[j] = t < len ? beta[at] : 0.f;
+    }
+    v[1] += v[0];
+    double sum = v[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += y;
+    }
+    const double before = sum - v[1];
+    bs[2 * lane] = before + v[0];
+    bs[2 * lane + 1] = before + v[1];
+}
+__device__ __forceinline__ float decay(double hi, double lo) { return expf((float)(hi - lo)); }
+
+// -------------------------------------------------------------------- prep
+// Block (c, b, hk), 128 threads: the operand tiles of q and k (swizzled, in
+// terms, zero for padding and past K), then per value head of the group T2,
+// P and the gates, all in the layout the other kernels copy in bulk.
+//
+// Q K^T and K K^T are one product of the stacked [Q; K] with K.  T2's columns
+// are solved by forward substitution, one thread a column, the column in
+// registers: warps 2 and 3 solve while warps 0 and 1 write P.
+struct PrepArgs {
+    Shape s;
+    const void *q, *k;
+    const float *g, *beta;
+    char *qk, *tp;
+    Ctrl *ctrl;
+};
+constexpr int PREP_LD = 68;  // floats of a row of the triangular matrix in shared memory
+
+template <class E, int KD> constexpr size_t prep_smem() {
+    // the solved matrix goes where the operand tiles were
+    return (QK<E, KD>::bytes > C * PREP_LD * 4 ? QK<E, KD>::bytes : C * PREP_LD * 4) + C * PREP_LD * 4 + 1024;
+}
+
+template <class E, int KD>
+__global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
+    constexpr int TB = Terms<E>::n;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    float *solved = (float *)tiles;
+    constexpr int first = QK<E, KD>::bytes > C * PREP_LD * 4 ? QK<E, KD>::bytes : C * PREP_LD * 4;
+    float *tri = (float *)(tiles + first);
+    __shared__ double bs[C];
+    __shared__ float betas[C];
+    __shared__ uint64_t done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const Shape &s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    int id = blockIdx.x;
+    const int hk = id % s.Hk;
+    id /= s.Hk;
+    const int b = id % s.B, c = id / s.B;
+    const int len = length_of(s, b);
+    if (tid == 0) {
+        tc::mbar_init(&done, 1);
+        abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&tmem_slot, 64);
+        tc::tmem_relinquish();
+    }
+    // tiles: rows 0..63 q, 64..127 k; 16-byte groups of 8 dims
+    char *out = a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes;
+    for (int i = tid; i < 128 * (KD / 8); i += 128) {
+        const int row = i / (KD / 8), gr = i % (KD / 8), t = c * C + (row & 63);
+        float f[8] = {};
+        if (t < len && gr * 8 < s.K) {
+            const long long r = (long long)t * s.B + b;
+            load8<E>(row < 64 ? (const E *)a.q + r * s.ldq + (long long)hk * s.K + gr * 8
+                              : (const E *)a.k + r * s.ldk + (long long)hk * s.K + gr * 8, f);
+        }
+        uint4 o[TB];
+        split8<TB>(f, o);
+        const uint32_t off = (gr >> 3) * 2 * TILE + swz(row, (gr & 7) * 16);
+#pragma unroll
+        for (int t2 = 0; t2 < TB; ++t2) {
+            *(uint4 *)(tiles + t2 * QK<E, KD>::term + off) = o[t2];
+            *(uint4 *)(out + t2 * QK<E, KD>::term + off) = o[t2];
+        }
+    }
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    if (tid == 0) {
+        const uint32_t base = tc::smem_u32(tiles);
+        constexpr uint32_t idesc = tc::idesc_bf16_f32(128, 64, 0, 0);
+        uint32_t acc = 0;
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int u = 0; u < TB; ++u) {
+                if (t + u >= NT) continue;
+                for (int ks = 0; ks < KD / 16; ++ks) {
+                    const uint32_t chunk = (ks >> 2) * 2 * TILE;
+                    tc::mma_bf16(tmem, k_major(base + t * QK<E, KD>::term + chunk, ks & 3),
+                                 k_major(base + u * QK<E, KD>::term + chunk + TILE, ks & 3), idesc, acc);
+                    acc = 1;
+                }
+            }
+        tc::mma_commit(&done);
+    }
+    wait(&done, 0, a.ctrl, &abort_flag, 0x601);
+    const int row = tid & 63;  // warps 0, 1: Q K^T; warps 2, 3: K K^T
+    for (int m = 0; m < s.group; ++m) {
+        const int h = hk * s.group + m;
+        char *tp = a.tp + (((size_t)c * s.B + b) * s.Hv + h) * TP_BYTES;
+        __syncthreads();  // the last head's sums and solved matrix are read
+        if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, bs, betas);
+        __syncthreads();
+        const double bi = bs[row];
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        if (warp < 2) {
+            for (int j0 = 0; j0 < C; j0 += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(lanes + j0, r);
+                tc::tmem_ld_wait();
+                float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    f[j] = j0 + j <= row ? s.scale * decay(bi, bs[j0 + j]) * __uint_as_float(r[j]) : 0.f;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float e[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = f[8 * hf + j];
+                    uint4 o[NT];
+                    split8<NT>(e, o);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        *(uint4 *)(tp + (NT + t) * TILE + swz(row, (j0 + 8 * hf) * 2)) = o[t];
+                }
+            }
+            float *gates = (float *)(tp + 2 * NT * TILE);
+            gates[tid] = decay(bi, 0.0);
+            gates[C + tid] = decay(bs[C - 1], bi);
+            gates[2 * C + tid] = betas[tid];
+        } else {
+            for (int j0 = 0; j0 < C; j0 += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(lanes + j0, r);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    float f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int jj = j0 + j + i;
+                        f[i] = jj < row ? decay(bi, bs[jj]) * betas[jj] * __uint_as_float(r[j + i]) : 0.f;
+                    }
+                    *(float4 *)(tri + row * PREP_LD + j0 + j) = make_float4(f[0], f[1], f[2], f[3]);
+                }
+            }
+            group_sync(1, 64);
+            // column `row` of the inverse: x_i = [i == row] - sum_{m < i} tri[i][m] x_m;
+            // columns 32.. start at row 32
+            float x[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                float p0 = i == row ? 1.f : 0.f, p1 = 0.f;
+                if (i < 32 && warp == 3) {
+                    x[i] = 0.f;
+                    continue;
+                }
+#pragma unroll
+                for (int mm = 0; mm < (i + 3) / 4; ++mm) {
+                    if (mm < 8 && warp == 3) continue;
+                    const float4 v = *(const float4 *)(tri + i * PREP_LD + 4 * mm);
+                    p0 = fmaf(-v.x, x[4 * mm], p0);
+                    if (4 * mm + 1 < i) p1 = fmaf(-v.y, x[4 * mm + 1], p1);
+                    if (4 * mm + 2 < i) p0 = fmaf(-v.z, x[4 * mm + 2], p0);
+                    if (4 * mm + 3 < i) p1 = fmaf(-v.w, x[4 * mm + 3], p1);
+                }
+                x[i] = p0 + p1;
+            }
+#pragma unroll
+            for (int i = 0; i < C; ++i) solved[i * PREP_LD + row] = x[i];
+        }
+        __syncthreads();
+        {  // T2's terms: half a row a thread
+            const int r = tid >> 1, j0 = (tid & 1) * 32;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = solved[r * PREP_LD + j0 + j + i];
+                uint4 o[NT];
+                split8<NT>(f, o);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) *(uint4 *)(tp + t * TILE + swz(r, (j0 + j) * 2)) = o[t];
+            }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, 64);
+}
+
+// -------------------------------------------------------------- sequential
+// Block (b, h, 128 columns of V): the chunks of one head in order.  Thread
+// (wg, lane) of the 256 compute threads holds column `lane` of S^T -- the
+// state is kept transposed, V on the tensor-memory lanes -- for half of K in
+// registers.  Every contraction of the chain has its left operand in tensor
+// memory, where the thread that owns the lane writes it, so nothing in the
+// chain crosses lanes or goes through shared memory:
+//   [Q|K] S  ->  R = V - gamma K S  ->  X = T2 R  ->  U  ->  S += K^T U.
+// The chunks' tiles come by bulk copies, a chunk ahead where two stages fit.
+// Bound: the chain's latency (three products and three passes over registers
+// a chunk), since few heads means few blocks.
+constexpr int SEQ_THREADS = 256;
+constexpr uint32_t COL_S = 0, COL_D = 192, COL_R = 320, COL_X = 416;  // tensor-memory columns
+constexpr uint32_t COL_U = COL_S, COL_W = COL_S + 96;
+
+template <class E, int KD> struct Seq {
+    static constexpr int stage = QK<E, KD>::bytes + 2 * NT * TILE;  // tiles; the gates lie behind the stages
+    static constexpr int extra = 1024 + 256;                        // alignment, barriers
+    static constexpr int stages = 2 * (stage + GATES) + extra <= 232448 ? 2 : 1;
+    static constexpr size_t smem = (size_t)stages * (stage + GATES) + extra;
+};
+
+struct SeqArgs {
+    Shape s;
+    const char *qk, *tp;
+    const void *v;            // forward: v; backward: dout
+    const float *s0;          // forward: s0; backward: dsT
+    void *o;                  // forward: o; backward: dv
+    float *sT;                // forward: sT; backward: ds0
+    float *states, *deltas;   // forward (or NULL): S and X; backward: dS and dV, in the workspace
+    Ctrl *ctrl;
+};
+
+struct SeqBars {
+    uint64_t full[2], m1, m2, m3, m4;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+// One thread: copy the tiles of the n-th chunk in order to its stage.  The
+// caller has seen the last products that read that stage complete.
+template <class E, int KD>
+__device__ __forceinline__ void seq_load(const SeqArgs &a, uint8_t *smem, SeqBars *bar, int b, int h, int n, bool reverse) {
+    using Q = Seq<E, KD>;
+    const Shape &s = a.s;
+    const int st = n % Q::stages, c = reverse ? s.NC - 1 - n : n;
+    uint8_t *dst = smem + st * Q::stage;
+    tc::mbar_arrive_expect_tx(&bar->full[st], Q::stage + GATES);
+    const size_t cb = (size_t)c * s.B + b;
+    bulk_load(dst, a.qk + (cb * s.Hk + h / s.group) * QK<E, KD>::bytes, QK<E, KD>::bytes, &bar->full[st]);
+    const char *tp = a.tp + (cb * s.Hv + h) * TP_BYTES;
+    bulk_load(dst + QK<E, KD>::bytes, tp, 2 * NT * TILE, &bar->full[st]);
+    bulk_load(smem + Q::stages * Q::stage + st * GATES, tp + 2 * NT * TILE, GATES, &bar->full[st]);
+}
+// After a time-out the block may leave only when its copies have landed.
+template <class E, int KD> __device__ __forceinline__ void seq_drain(SeqBars *bar, int chunks) {
+    using Q = Seq<E, KD>;
+    for (int n = max(0, chunks - Q::stages); n < chunks; ++n)
+        tc::mbar_wait(&bar->full[n % Q::stages], (n / Q::stages) & 1, nullptr, nullptr, 0, 200000000ull);
+}
+
+template <class E, int KD>
+__global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_constant__ SeqArgs a) {
+    using Q = Seq<E, KD>;
+    constexpr int TB = Terms<E>::n, H2 = KD / 2, TERM = QK<E, KD>::term;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
+    const Shape &s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    int id = blockIdx.x;
+    const int vt = id % s.VT;
+    id /= s.VT;
+    const int h = id % s.Hv, b = id / s.Hv;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&bar->full[i], 1);
+        tc::mbar_init(&bar->m1, 1);
+        tc::mbar_init(&bar->m2, 1);
+        tc::mbar_init(&bar->m3, 1);
+        tc::mbar_init(&bar->m4, 1);
+        bar->abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&bar->tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = bar->tmem_slot;
+    if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, false);
+    __syncwarp();
+    {
+        const int wg = tid >> 7, lane = tid & 127, v = vt * LANES + lane;
+        const bool own = v < s.V;
+        const int len = length_of(s, b);
+        const uint32_t lanes = tmem + ((uint32_t)(lane & 96) << 16);
+        const long long head = (long long)b * s.Hv + h;
+        const long long row = (long long)s.B * s.Hv * s.V;  // elements of o, deltas between tokens
+        volatile int *ab = &bar->abort_flag;
+        float S[H2];
+#pragma unroll
+        for (int i = 0; i < H2; ++i) {
+            const int k = wg * H2 + i;
+            S[i] = a.s0 && own && k < s.K ? a.s0[(head * s.K + k) * s.V + v] : 0.f;
+        }
+        float o[32];
+        auto store_o = [&](int c) {
+            if (!own) return;
+            E *p = (E *)a.o + head * s.V + v;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int t = c * C + wg * 32 + i;
+                if (t < s.T) p[t * row] = from_f<E>(o[i]);
+            }
+        };
+        for (int c = 0; c < s.NC; ++c) {
+            const int st = c % Q::stages;
+            const uint32_t ph = c & 1;
+            if (Q::stages == 2 && tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
+            __syncwarp();
+            const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
+            const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + wg * 32;
+            E vr[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int t = c * C + wg * 32 + i;
+                vr[i] = own && t < len ? ((const E *)a.v)[((long long)t * s.B + b) * s.ldv + (long long)h * s.V + v]
+                                       : from_f<E>(0.f);
+            }
+            put_terms<H2 / 2, NT>(lanes + COL_S + wg * (H2 / 2), KD / 2, S);
+            tc::tmem_st_wait();
+            wait(&bar->full[st], (c / Q::stages) & 1, a.ctrl, ab, 0x612);
+            tc::tc_fence_before();
+            group_sync(1, SEQ_THREADS);
+            if (tid == 0) {  // D = [q | k] S, tokens on the columns
+                tc::tc_fence_after();
+                uint32_t acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) {
+                        if (t + u >= NT) continue;
+#pragma unroll
+                        for (int ks = 0; ks < KD / 16; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_S + t * (KD / 2) + 8 * ks,
+                                            k_major(qk + u * TERM + (ks >> 2) * 2 * TILE, ks & 3),
+                                            tc::idesc_bf16_f32(128, 128, 0, 0), acc);
+                            acc = 1;
+                        }
+                    }
+                tc::mma_commit(&bar->m1);
+            }
+            __syncwarp();
+            if (c > 0) store_o(c - 1);
+            if (a.states && own) {
+                float *p = a.states + (((long long)c * s.B * s.Hv + head) * s.K) * s.V + v;
+#pragma unroll
+                for (int i = 0; i < H2; ++i) {
+                    const int k = wg * H2 + i;
+                    if (k < s.K) p[(long long)k * s.V] = S[i];
+                }
+            }
+            __syncwarp();
+            const float last = gates[(1 - wg) * 32 + 31];  // gamma of token 63
+            wait(&bar->m1, ph, a.ctrl, ab, 0x613);
+            float f[32];
+            get32(lanes + COL_D + 64 + wg * 32, f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = fmaf(-gates[i], f[i], to_f(vr[i]));
+            put_terms<16, NT>(lanes + COL_R + wg * 16, 32, f);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            group_sync(1, SEQ_THREADS);
+            if (tid == 0) {  // X = T2 R
+                tc::tc_fence_after();
+                uint32_t acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < NT - t; ++u)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_X, tmem + COL_R + t * 32 + 8 * ks, k_major(tp + u * TILE, ks),
+                                            tc::idesc_bf16_f32(128, 64, 0, 0), acc);
+                            acc = 1;
+                        }
+                tc::mma_commit(&bar->m2);
+            }
+            __syncwarp();
+            get32(lanes + COL_D + wg * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= s.scale * gates[i];
+            wait(&bar->m2, ph, a.ctrl, ab, 0x614);
+            get32(lanes + COL_X + wg * 32, f);
+            if (a.deltas && own) {
+                float *p = a.deltas + head * s.V + v;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int t = c * C + wg * 32 + i;
+                    if (t < s.T) p[t * row] = f[i];
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= gates[2 * C + i];  // U
+            put_terms<16, NT>(lanes + COL_U + wg * 16, 32, f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= gates[C + i];      // left U
+            put_terms<16, NT>(lanes + COL_W + wg * 16, 32, f);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            group_sync(1, SEQ_THREADS);
+            if (tid == 0) {
+                tc::tc_fence_after();
+                uint32_t acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)  // D = K^T (left U)
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) {
+                        if (t + u >= NT) continue;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_W + t * 32 + 8 * ks,
+                                            mn_major(qk + u * TERM + TILE, ks, 2 * TILE),
+                                            tc::idesc_bf16_f32(128, KD, 0, 1), acc);
+                            acc = 1;
+                        }
+                    }
+                tc::mma_commit(&bar->m4);
+                acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)  // P U
+#pragma unroll
+                    for (int u = 0; u < NT - t; ++u)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_X, tmem + COL_U + t * 32 + 8 * ks,
+                                            k_major(tp + (NT + u) * TILE, ks), tc::idesc_bf16_f32(128, 64, 0, 0), acc);
+                            acc = 1;
+                        }
+                tc::mma_commit(&bar->m3);
+            }
+            __syncwarp();
+            wait(&bar->m4, ph, a.ctrl, ab, 0x615);
+#pragma unroll
+            for (int i0 = 0; i0 < H2; i0 += 32) {
+                get32(lanes + COL_D + wg * H2 + i0, f);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
+            }
+            wait(&bar->m3, ph, a.ctrl, ab, 0x616);
+            if (Q::stages == 1 && tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
+            __syncwarp();
+            get32(lanes + COL_X + wg * 32, f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] += f[i];
+        }
+        if (s.NC > 0) store_o(s.NC - 1);
+        if (own && a.sT) {
+#pragma unroll
+            for (int i = 0; i < H2; ++i) {
+                const int k = wg * H2 + i;
+                if (k < s.K) a.sT[(head * s.K + k) * s.V + v] = S[i];
+            }
+        }
+    }
+    if (tid == 32) seq_drain<E, KD>(bar, s.NC);
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// The adjoint, chunks in reverse, the same layout (dS^T in registers):
+//   K dS and P^T dO  ->  dU  ->  dV = T2^T (beta dU)  ->  dS += scale Q^T gamma dO - K^T gamma dV.
+template <class E, int KD>
+__global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_constant__ SeqArgs a) {
+    using Q = Seq<E, KD>;
+    constexpr int TB = Terms<E>::n, H2 = KD / 2, TERM = QK<E, KD>::term;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
+    const Shape &s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    int id = blockIdx.x;
+    const int vt = id % s.VT;
+    id /= s.VT;
+    const int h = id % s.Hv, b = id / s.Hv;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&bar->full[i], 1);
+        tc::mbar_init(&bar->m1, 1);
+        tc::mbar_init(&bar->m2, 1);
+        tc::mbar_init(&bar->m4, 1);
+        bar->abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&bar->tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = bar->tmem_slot;
+    if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, true);
+    __syncwarp();
+    {
+        const int wg = tid >> 7, lane = tid & 127, v = vt * LANES + lane;
+        const bool own = v < s.V;
+        const int len = length_of(s, b);
+        const uint32_t lanes = tmem + ((uint32_t)(lane & 96) << 16);
+        const long long head = (long long)b * s.Hv + h;
+        const long long row = (long long)s.B * s.Hv * s.V;
+        volatile int *ab = &bar->abort_flag;
+        float S[H2];
+#pragma unroll
+        for (int i = 0; i < H2; ++i) {
+            const int k = wg * H2 + i;
+            S[i] = a.s0 && own && k < s.K ? a.s0[(head * s.K + k) * s.V + v] : 0.f;
+        }
+        for (int n = 0; n < s.NC; ++n) {
+            const int c = s.NC - 1 - n, st = n % Q::stages;
+            const uint32_t ph = n & 1;
+            if (Q::stages == 2 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
+            __syncwarp();
+            const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
+            const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + wg * 32;
+            float f[32], d[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int t = c * C + wg * 32 + i;
+                d[i] = a.v && own && t < len ? to_f(((const E *)a.v)[t * row + head * s.V + v]) : 0.f;
+            }
+            put_terms<H2 / 2, NT>(lanes + COL_S + wg * (H2 / 2), KD / 2, S);
+            put_terms<16, TB>(lanes + COL_R + wg * 16, 32, d);
+            tc::tmem_st_wait();
+            wait(&bar->full[st], (n / Q::stages) & 1, a.ctrl, ab, 0x622);
+            tc::tc_fence_before();
+            group_sync(1, SEQ_THREADS);
+            if (tid == 0) {
+                tc::tc_fence_after();
+                uint32_t acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)  // D[0..63] = K dS
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) {
+                        if (t + u >= NT) continue;
+#pragma unroll
+                        for (int ks = 0; ks < KD / 16; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_S + t * (KD / 2) + 8 * ks,
+                                            k_major(qk + u * TERM + (ks >> 2) * 2 * TILE + TILE, ks & 3),
+                                            tc::idesc_bf16_f32(128, 64, 0, 0), acc);
+                            acc = 1;
+                        }
+                    }
+                acc = 0;
+#pragma unroll
+                for (int t = 0; t < TB; ++t)  // D[64..127] = P^T dO
+#pragma unroll
+                    for (int u = 0; u < NT - t; ++u)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_D + 64, tmem + COL_R + t * 32 + 8 * ks,
+                                            mn_major(tp + (NT + u) * TILE, ks, TILE),
+                                            tc::idesc_bf16_f32(128, 64, 0, 1), acc);
+                            acc = 1;
+                        }
+                tc::mma_commit(&bar->m1);
+            }
+            __syncwarp();
+            if (own) {
+                float *p = a.states + (((long long)c * s.B * s.Hv + head) * s.K) * s.V + v;
+#pragma unroll
+                for (int i = 0; i < H2; ++i) {
+                    const int k = wg * H2 + i;
+                    if (k < s.K) p[(long long)k * s.V] = S[i];
+                }
+            }
+            __syncwarp();
+            const float last = gates[(1 - wg) * 32 + 31];
+            wait(&bar->m1, ph, a.ctrl, ab, 0x623);
+            get32(lanes + COL_D + wg * 32, f);
+            {
+                float e[32];
+                get32(lanes + COL_D + 64 + wg * 32, e);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = gates[2 * C + i] * fmaf(gates[C + i], f[i], e[i]);  // beta dU
+            }
+            put_terms<16, NT>(lanes + COL_R + wg * 16, 32, f);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            group_sync(1, SEQ_THREADS);
+            if (tid == 0) {  // dV = T2^T (beta dU)
+                tc::tc_fence_after();
+                uint32_t acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < NT - t; ++u)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_X, tmem + COL_R + t * 32 + 8 * ks,
+                                            mn_major(tp + u * TILE, ks, TILE), tc::idesc_bf16_f32(128, 64, 0, 1), acc);
+                            acc = 1;
+                        }
+                tc::mma_commit(&bar->m2);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) d[i] *= s.scale * gates[i];
+            put_terms<16, NT>(lanes + COL_U + wg * 16, 32, d);
+            wait(&bar->m2, ph, a.ctrl, ab, 0x624);
+            get32(lanes + COL_X + wg * 32, f);
+            if (own) {
+                float *p = a.deltas + head * s.V + v;
+                E *pv = (E *)a.o + head * s.V + v;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int t = c * C + wg * 32 + i;
+                    if (t < s.T) {
+                        p[t * row] = f[i];
+                        pv[t * row] = from_f<E>(f[i]);
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= -gates[i];
+            put_terms<16, NT>(lanes + COL_W + wg * 16, 32, f);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            group_sync(1, SEQ_THREADS);
+            if (tid == 0) {  // D = scale Q^T gamma dO - K^T gamma dV
+                tc::tc_fence_after();
+                uint32_t acc = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) {
+                        if (t + u >= NT) continue;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_W + t * 32 + 8 * ks,
+                                            mn_major(qk + u * TERM + TILE, ks, 2 * TILE),
+                                            tc::idesc_bf16_f32(128, KD, 0, 1), acc);
+                            acc = 1;
+                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_U + t * 32 + 8 * ks,
+                                            mn_major(qk + u * TERM, ks, 2 * TILE),
+                                            tc::idesc_bf16_f32(128, KD, 0, 1), 1);
+                        }
+                    }
+                tc::mma_commit(&bar->m4);
+            }
+            __syncwarp();
+            wait(&bar->m4, ph, a.ctrl, ab, 0x625);
+            if (Q::stages == 1 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
+            __syncwarp();
+#pragma unroll
+            for (int i0 = 0; i0 < H2; i0 += 32) {
+                get32(lanes + COL_D + wg * H2 + i0, f);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
+            }
+        }
+        if (own && a.sT) {
+#pragma unroll
+            for (int i = 0; i < H2; ++i) {
+                const int k = wg * H2 + i;
+                if (k < s.K) a.sT[(head * s.K + k) * s.V + v] = S[i];
+            }
+        }
+    }
+    if (tid == 32) seq_drain<E, KD>(bar, s.NC);
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- gradients
+// Block (c, b, hk), 256 threads: dq, dk of the chunk, and dg, dbeta of every
+// value head of the group, from the saved S0 and X and seq_bwd's dS1 and dV.
+// Rows are stacked so that every product has the 128 rows the tensor core
+// takes: [dO; dV] with X gives Y over Z, with S0 gives F over G; X sits in the
+// lower rows for E; the last product is [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K].
+// dg's double sum needs no matrix: sum_{r >= i > j} M_rj is the sum over
+// r >= i of (row sum - column sum), for the lower triangle M.
+constexpr int GRAD_THREADS = 256;
+constexpr uint32_t COL_QK = 0, COL_YZ = 64, COL_FG = 128, COL_E = 256, COL_OUT = 384;
+
+template <class E, int KD> struct GradSmem {
+    static constexpr int a = QK<E, KD>::bytes;       // [dO; dV], 64 columns: NT x 16 KB
+    static constexpr int x = a + NT * 2 * TILE;      // X: NT x 8 KB
+    static constexpr int st = x + NT * TILE;         // S0, then dS1: NT x KD rows x 128 bytes
+    static constexpr int m_end = a + NT * 4 * TILE;  // the last product's left operand lies over all three
+    static constexpr int end = st + NT * KD * 128 > m_end ? st + NT * KD * 128 : m_end;
+    static constexpr size_t smem = end + 1024;
+};
+
+struct GradArgs {
+    Shape s;
+    const char *qk;
+    const float *g, *beta;
+    const void *dout;
+    const float *states, *deltas, *dstates, *dvf;
+    void *dq, *dk;
+    float *dg, *dbeta;
+    Ctrl *ctrl;
+};
+
+// Sum of f[j] over the 32 lanes for every j; lane j returns the j-th sum.
+__device__ __forceinline__ float transpose_sum(float (&f)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float keep = up ? f[j + o] : f[j], give = up ? f[j] : f[j + o];
+            f[j] = keep + __shfl_xor_sync(~0u, give, o);
+        }
+    }
+    return f[0];
+}
+
+template <class E, int KD>
+__global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_constant__ GradArgs a) {
+    using L = GradSmem<E, KD>;
+    constexpr int TB = Terms<E>::n, TERM = QK<E, KD>::term, H2 = KD / 2, SI = KD / 32;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ double bs[C];
+    __shared__ float betas[C], colp[4][C], rowp[2][2 * C], rp[2][2 * C], ep[2][C], dots[8];
+    __shared__ uint64_t loaded, m1, m2, m3;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_s;
+    const Shape &s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, r128 = tid & 127, r = r128 & 63;
+    const bool isq = r128 < 64;
+    int id = blockIdx.x;
+    const int hk = id % s.Hk;
+    id /= s.Hk;
+    const int b = id % s.B, c = id / s.B;
+    const int len = length_of(s, b);
+    volatile int *ab = &abort_s;
+    if (tid == 0) {
+        tc::mbar_init(&loaded, 1);
+        tc::mbar_init(&m1, 1);
+        tc::mbar_init(&m2, 1);
+        tc::mbar_init(&m3, 1);
+        abort_s = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot, lanes = tmem + ((uint32_t)(r128 & 96) << 16);
+    const uint32_t qk = tc::smem_u32(smem), sa = qk + L::a, sx = qk + L::x, ss = qk + L::st;
+    if (tid == 0) {
+        tc::mbar_arrive_expect_tx(&loaded, QK<E, KD>::bytes);
+        bulk_load(smem, a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes, QK<E, KD>::bytes, &loaded);
+    }
+    wait(&loaded, 0, a.ctrl, ab, 0x631);
+    float acc[H2];  // this thread's half row of dq (rows 0..63) or dk, but for the last product
+#pragma unroll
+    for (int i = 0; i < H2; ++i) acc[i] = 0.f;
+    uint32_t p12 = 0;
+    const int passes = (s.V + 63) / 64;
+    for (int m = 0; m < s.group; ++m) {
+        const int h = hk * s.group + m;
+        const long long head = (long long)b * s.Hv + h;
+        const float *s0 = a.states + ((long long)c * s.B * s.Hv + head) * s.K * s.V;
+        const float *ds = a.dstates + ((long long)c * s.B * s.Hv + head) * s.K * s.V;
+        if (m > 0) wait(&m3, (m - 1) & 1, a.ctrl, ab, 0x632);  // the tiles are free
+        __syncthreads();
+        if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, bs, betas);
+        float dot = 0.f;
+        for (int p = 0; p < passes; ++p) {
+            const int v0 = p * 64;
+            // [dO; dV]: 128 rows x 8 groups of 8 columns
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7, t = c * C + (row & 63);
+                float f[8] = {};
+                if (t < len && v0 + gr * 8 < s.V) {
+                    const long long at = ((long long)t * s.B * s.Hv + head) * s.V + v0 + gr * 8;
+                    if (row >= 64) load8<float>(a.dvf + at, f);
+                    else if (a.dout) load8<E>((const E *)a.dout + at, f);
+                }
+                uint4 o[NT];
+                split8<NT>(f, o);
+#pragma unroll
+                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::a + k * 2 * TILE + swz(row, gr * 16)) = o[k];
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7, t = c * C + row;
+                float f[8] = {};
+                if (t < len && v0 + gr * 8 < s.V)
+                    load8<float>(a.deltas + ((long long)t * s.B * s.Hv + head) * s.V + v0 + gr * 8, f);
+                uint4 o[NT];
+                split8<NT>(f, o);
+#pragma unroll
+                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::x + k * TILE + swz(row, gr * 16)) = o[k];
+            }
+            float sv[SI][8], dv[SI][8];
+#pragma unroll
+            for (int n = 0; n < SI; ++n) {
+                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sv[n][k] = dv[n][k] = 0.f;
+                if (row < s.K && v0 + gr * 8 < s.V) {
+                    load8<float>(s0 + (long long)row * s.V + v0 + gr * 8, sv[n]);
+                    load8<float>(ds + (long long)row * s.V + v0 + gr * 8, dv[n]);
+                }
+                uint4 o[NT];
+                split8<NT>(sv[n], o);
+#pragma unroll
+                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::st + k * KD * 128 + swz(row, gr * 16)) = o[k];
+            }
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc::tc_fence_after();
+                uint32_t cc = 0;
+                if (m == 0 && p == 0) {  // [q; k] k^T, once
+#pragma unroll
+                    for (int t = 0; t < TB; ++t)
+#pragma unroll
+                        for (int u = 0; u < TB; ++u) {
+                            if (t + u >= NT) continue;
+                            for (int ks = 0; ks < KD / 16; ++ks) {
+                                const uint32_t chunk = (ks >> 2) * 2 * TILE;
+                                tc::mma_bf16(tmem + COL_QK, k_major(qk + t * TERM + chunk, ks & 3),
+                                             k_major(qk + u * TERM + chunk + TILE, ks & 3),
+                                             tc::idesc_bf16_f32(128, 64, 0, 0), cc);
+                                cc = 1;
+                            }
+                        }
+                }
+                cc = p > 0;
+                for (int t = 0; t < NT; ++t)
+                    for (int u = 0; u < NT - t; ++u)
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16(tmem + COL_YZ, k_major(sa + t * 2 * TILE, ks), k_major(sx + u * TILE, ks),
+                                         tc::idesc_bf16_f32(128, 64, 0, 0), cc);
+                            tc::mma_bf16(tmem + COL_FG, k_major(sa + t * 2 * TILE, ks), k_major(ss + u * KD * 128, ks),
+                                         tc::idesc_bf16_f32(128, KD, 0, 0), cc);
+                            cc = 1;
+                        }
+                tc::mma_commit(&m1);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < SI; ++n)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dot = fmaf(sv[n][k], dv[n][k], dot);
+            wait(&m1, p12, a.ctrl, ab, 0x633);
+#pragma unroll
+            for (int n = 0; n < SI; ++n) {
+                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7;
+                uint4 o[NT];
+                split8<NT>(dv[n], o);
+#pragma unroll
+                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::st + k * KD * 128 + swz(row, gr * 16)) = o[k];
+            }
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {  // rows 64..127: E = X dS1^T (the rows above X are not used)
+                tc::tc_fence_after();
+                uint32_t cc = p > 0;
+                for (int t = 0; t < NT; ++t)
+                    for (int u = 0; u < NT - t; ++u)
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc::mma_bf16(tmem + COL_E, k_major(sx + t * TILE - TILE, ks), k_major(ss + u * KD * 128, ks),
+                                         tc::idesc_bf16_f32(128, KD, 0, 0), cc);
+                            cc = 1;
+                        }
+                tc::mma_commit(&m2);
+            }
+            __syncwarp();
+            wait(&m2, p12, a.ctrl, ab, 0x634);
+            p12 ^= 1;
+        }
+        // ---- the triangle: weights, their row and column sums, the last product's left operand
+        {
+            float y[32], kq[32], w[32];
+            get32(lanes + COL_QK + wg * 32, kq);
+            get32(lanes + COL_YZ + wg * 32, y);
+            const double br = bs[r];
+            float rowsum = 0.f;
+            if (isq) {  // rows 0..63 have no product with Q
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int gr = 0; gr < 4; ++gr)
+                        *(uint4 *)(smem + L::a + k * 4 * TILE + swz(r, (wg * 4 + gr) * 16)) = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 8) {
+                float e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = wg * 32 + j0 + i;
+                    const bool in = isq ? j <= r : j < r;
+                    const float z = in ? decay(br, bs[j]) * (isq ? s.scale * y[j0 + i] : -y[j0 + i]) : 0.f;
+                    w[j0 + i] = z * kq[j0 + i];
+                    e[i] = z * betas[j];
+                    rowsum = fmaf(betas[j], w[j0 + i], rowsum);
+                }
+                uint4 o[NT];
+                split8<NT>(e, o);
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    uint8_t *base = smem + L::a + k * 4 * TILE;  // [cols 0..63: Q][cols 64..127: K], 128 rows each
+                    const uint32_t *q4 = (const uint32_t *)&o[k];
+                    if (isq) *(uint4 *)(base + 2 * TILE + swz(r, (wg * 32 + j0) * 2)) = o[k];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = wg * 32 + j0 + i;
+                        const uint16_t hv = (uint16_t)(q4[i >> 1] >> (16 * (i & 1)));
+                        if (isq) {
+                            *(uint16_t *)(base + swz(64 + j, r * 2)) = hv;
+                        } else if (j <= r) {
+                            *(uint16_t *)(base + 2 * TILE + swz(64 + r, j * 2)) = hv;
+                            *(uint16_t *)(base + 2 * TILE + swz(64 + j, r * 2)) = hv;
+                        }
+                    }
+                }
+            }
+            rowp[wg][r128] = rowsum;
+            __syncwarp();
+            const float cs = transpose_sum(w);
+            colp[warp & 3][wg * 32 + lane] = cs;
+        }
+        // ---- F | G and E: half a row of K a thread
+        {
+            const float gam = decay(bs[r], 0.0), left = decay(bs[C - 1], bs[r]), be = betas[r];
+            float dotf = 0.f, dote = 0.f;
+#pragma unroll
+            for (int i0 = 0; i0 < H2; i0 += 32) {
+                float f[32], e[32];
+                get32(lanes + COL_FG + wg * H2 + i0, f);
+                get32(lanes + COL_E + wg * H2 + i0, e);
+#pragma unroll
+                for (int gr = 0; gr < 4; ++gr) {
+                    const int col = wg * H2 + i0 + gr * 8;
+                    float x[8] = {};
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) {
+                        float xt[8];
+                        x8_to_f32<bf16>(*(const uint4 *)(smem + t * TERM + (col >> 6) * 2 * TILE + swz(r128, (col & 63) * 2)), xt);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] += xt[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int n = gr * 8 + i;
+                        dotf = fmaf(x[i], f[n], dotf);
+                        if (isq) {
+                            acc[i0 + n] = fmaf(s.scale * gam, f[n], acc[i0 + n]);
+                        } else {
+                            dote = fmaf(x[i], e[n], dote);
+                            acc[i0 + n] += left * be * e[n] - gam * f[n];
+                        }
+                    }
+                }
+            }
+            rp[wg][r128] = dotf;
+            if (!isq) ep[wg][r] = dote;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+            if (lane == 0) dots[warp] = dot;
+        }
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {  // [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K]
+            tc::tc_fence_after();
+            uint32_t cc = m > 0;
+            for (int t = 0; t < NT; ++t)
+                for (int u = 0; u < TB && u < NT - t; ++u)
+                    for (int ks = 0; ks < 8; ++ks) {
+                        tc::mma_bf16(tmem + COL_OUT, k_major(sa + t * 4 * TILE + (ks >> 2) * 2 * TILE, ks & 3),
+                                     mn_major(qk + u * TERM, ks, 2 * TILE), tc::idesc_bf16_f32(128, KD, 0, 1), cc);
+                        cc = 1;
+                    }
+            tc::mma_commit(&m3);
+        }
+        __syncwarp();
+        if (warp == 1) {  // dg and dbeta, two tokens a lane
+            double d[2], e[2];
+            float db[2];
+            double all = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) all += dots[i];
+            all *= decay(bs[C - 1], 0.0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = 2 * lane + i;
+                const float col = (colp[0][j] + colp[1][j]) + (colp[2][j] + colp[3][j]);
+                const double row = ((double)rowp[0][j] + rowp[1][j]) + ((double)rowp[0][C + j] + rowp[1][C + j]);
+                const float gam = decay(bs[j], 0.0), left = decay(bs[C - 1], bs[j]), ke = ep[0][j] + ep[1][j];
+                d[i] = row - (double)betas[j] * col +
+                       (double)gam * ((double)s.scale * (rp[0][j] + rp[1][j]) - (rp[0][C + j] + rp[1][C + j]));
+                e[i] = (double)left * betas[j] * ke;
+                db[i] = col + left * ke;
+            }
+            // suffix sums of d, prefix sums (exclusive) of e
+            double sd = d[0] + d[1], se = e[0] + e[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_down_sync(~0u, sd, o), y = __shfl_up_sync(~0u, se, o);
+                if (lane + o < 32) sd += x;
+                if (lane >= o) se += y;
+            }
+            const double after = sd - d[0] - d[1], before = se - e[0] - e[1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = c * C + 2 * lane + i;
+                if (t >= s.T) continue;
+                const double v = i == 0 ? after + d[1] + d[0] + before : after + d[1] + before + e[0];
+                const long long at = ((long long)t * s.B + b) * s.Hv + h;
+                // (where e^g is zero so is its gradient, and not the rounding of the sums)
+                a.dg[at] = t < len && !(a.g[at] < -104.f) ? (float)(v + all) : 0.f;
+                a.dbeta[at] = t < len ? db[i] : 0.f;
+            }
+        }
+        __syncwarp();
+    }
+    wait(&m3, (s.group - 1) & 1, a.ctrl, ab, 0x635);
+    const int t = c * C + r;
+    E *out = (E *)(isq ? a.dq : a.dk) + (((long long)t * s.B + b) * s.Hk + hk) * s.K + wg * H2;
+#pragma unroll
+    for (int i0 = 0; i0 < H2; i0 += 32) {
+        float f[32];
+        get32(lanes + COL_OUT + wg * H2 + i0, f);
+        if (t < s.T)
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr) {
+                if (wg * H2 + i0 + gr * 8 >= s.K) continue;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = acc[i0 + gr * 8 + i] + f[gr * 8 + i];
+                if constexpr (sizeof(E) == 4) {
+                    *(float4 *)(out + i0 + gr * 8) = make_float4(x[0], x[1], x[2], x[3]);
+                    *(float4 *)(out + i0 + gr * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                } else {
+                    *(uint4 *)(out + i0 + gr * 8) = f32x8_to<E>(x);
+                }
+            }
+        __syncwarp();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// -------------------------------------------------------------------- step
+// A few tokens, token by token: block (b, h, 64 columns of V), thread (part,
+// column) holds the column's state for a quarter of K in registers.  Bound:
+// the state's read and write.
+constexpr int STEP_THREADS = 256, STEP_COLS = 64, STEP_PARTS = 4, STEP_K = 128 / STEP_PARTS;
+
+struct StepArgs {
+    Shape s;
+    const void *q, *k, *v;
+    const float *g, *beta, *s0;
+    void *o;
+    float *sT;
+    int tiles;  // blocks of 64 columns
+};
+
+template <class E>
+__global__ void __launch_bounds__(STEP_THREADS) step_kernel(StepArgs a) {
+    __shared__ float qs[128], ks[128], part[2][STEP_PARTS][STEP_COLS];
+    const Shape &s = a.s;
+    const int tid = threadIdx.x, part_id = tid / STEP_COLS, v0 = (blockIdx.x % a.tiles) * STEP_COLS;
+    const int col = tid % STEP_COLS, v = v0 + col, id = blockIdx.x / a.tiles, h = id % s.Hv, b = id / s.Hv, hk = h / s.group;
+    const long long head = (long long)b * s.Hv + h;
+    const int len = length_of(s, b), k0 = part_id * STEP_K;
+    const bool own = v < s.V;
+    float S[STEP_K];
+#pragma unroll
+    for (int i = 0; i < STEP_K; ++i)
+        S[i] = a.s0 && own && k0 + i < s.K ? __ldcs(a.s0 + (head * s.K + k0 + i) * s.V + v) : 0.f;
+    for (int t = 0; t < s.T; ++t) {
+        const long long r = (long long)t * s.B + b;
+        E *o = (E *)a.o + (r * s.Hv + h) * s.V + v;
+        if (t >= len) {  // padding: the same for the whole block
+            if (part_id == 0 && own) *o = from_f<E>(0.f);
+            continue;
+        }
+        const float x = own ? to_f(((const E *)a.v)[r * s.ldv + (long long)h * s.V + v]) : 0.f;
+        const float gt = a.g[r * s.Hv + h], be = a.beta[r * s.Hv + h];
+        if (tid < 128)
+            qs[tid] = tid < s.K ? to_f(((const E *)a.q)[r * s.ldq + (long long)hk * s.K + tid]) : 0.f;
+        else
+            ks[tid - 128] = tid - 128 < s.K ? to_f(((const E *)a.k)[r * s.ldk + (long long)hk * s.K + tid - 128]) : 0.f;
+        const float dec = expf(gt);
+        __syncthreads();
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEP_K; i += 2) {
+            S[i] *= dec;
+            S[i + 1] *= dec;
+            d0 = fmaf(ks[k0 + i], S[i], d0);
+            d1 = fmaf(ks[k0 + i + 1], S[i + 1], d1);
+        }
+        part[0][part_id][col] = d0 + d1;
+        __syncthreads();
+        const float u = be * (x - ((part[0][0][col] + part[0][1][col]) + (part[0][2][col] + part[0][3][col])));
+        d0 = d1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEP_K; i += 2) {
+            S[i] = fmaf(ks[k0 + i], u, S[i]);
+            S[i + 1] = fmaf(ks[k0 + i + 1], u, S[i + 1]);
+            d0 = fmaf(qs[k0 + i], S[i], d0);
+            d1 = fmaf(qs[k0 + i + 1], S[i + 1], d1);
+        }
+        part[1][part_id][col] = d0 + d1;
+        __syncthreads();
+        if (part_id == 0 && own)
+            *o = from_f<E>(s.scale * ((part[1][0][col] + part[1][1][col]) + (part[1][2][col] + part[1][3][col])));
+    }
+#pragma unroll
+    for (int i = 0; i < STEP_K; ++i)
+        if (own && k0 + i < s.K) __stcs(a.sT + (head * s.K + k0 + i) * s.V + v, S[i]);
+}
+
+}  // namespace gdr
+}  // namespace lstm

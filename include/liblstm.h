@@ -383,6 +383,79 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
                    int accumulate, float *dtable, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * lstm_gdr_fwd / lstm_gdr_bwd -- the gated delta rule, a recurrent layer
+ * whose state of a head is a matrix S [K][V] (float).  For t = 0 .. T-1, per
+ * sequence and value head:
+ *   S' = exp(g_t) S_{t-1}
+ *   x_t = v_t - S'^T k_t                   (what the state has wrong at k_t)
+ *   S_t = S' + beta_t k_t x_t^T
+ *   o_t = scale S_t^T q_t
+ * Hv value heads share Hk key heads (Hv a multiple of Hk; value head h reads
+ * the q and k of key head h / (Hv / Hk)).
+ *
+ *   q, k   [T][B][Hk][K]  compute type   (row t*B + n at a stride of ldq, ldk)
+ *   v      [T][B][Hv][V]  compute type   (ldv)
+ *   g      [T][B][Hv]     float, log decay, <= 0 as a rule; -inf forgets all
+ *   beta   [T][B][Hv]     float
+ *   s0     [B][Hv][K][V]  float, or NULL for zero
+ * outputs (overwritten):
+ *   o      [T][B][Hv][V]  compute type
+ *   sT     [B][Hv][K][V]  float; may be s0 (a state kept in place)
+ *   states [ceil(T / LSTM_GDR_CHUNK)][B][Hv][K][V], deltas [T][B][Hv][V] float:
+ *          kept for the backward, or both NULL (serving).  states[c] is the
+ *          state before token 64 c, deltas is x.
+ * A call of up to 16 tokens that keeps nothing runs token by token (one token
+ * is a decoding step); any other in chunks of 64 tokens on the tensor cores,
+ * with the sums and states of a float computation in every compute type.
+ *
+ * ldq, ldk, ldv: elements between the rows of two tokens (0 = dense), so that
+ * q, k and v may be slices of one projection; a multiple of 8.
+ * options: lengths [B] int (or NULL): steps t >= lengths[n] (clamped to
+ * 0 .. T) are padding: the state stays, o_t is zero, and gradients are zero.
+ * opt NULL: no lengths, scale 1.
+ *
+ * lstm_gdr_bwd: the gradients for dout [T][B][Hv][V] (compute type, or NULL)
+ * and dsT [B][Hv][K][V] (float, or NULL), with the forward's options, q, k,
+ * g, beta, states and deltas (v is not read; it may be NULL):
+ *   dq, dk [T][B][Hk][K], dv [T][B][Hv][V]  compute type, dense (they feed the
+ *          16-bit products of a projection's backward, as dy does), heads that
+ *          share a key summed in float
+ *   dg, dbeta [T][B][Hv]  float;  ds0 [B][Hv][K][V]  float, or NULL
+ *
+ * K and V are multiples of 8 with K <= 128 and V <= 256 (else
+ * LSTM_ERR_UNSUPPORTED).
+ */
+#define LSTM_GDR_CHUNK 64
+typedef struct lstm_gdr_dims {
+    int T;
+    int B;
+    int Hk;
+    int Hv;
+    int K;
+    int V;
+    int dtype;
+    long long ldq;
+    long long ldk;
+    long long ldv;
+} lstm_gdr_dims;
+typedef struct lstm_gdr_options {
+    const int *lengths;
+    float scale;
+} lstm_gdr_options;
+
+/* save: whether the forward call gets states and deltas. */
+size_t lstm_gdr_fwd_workspace_size(const lstm_gdr_dims *d, int save);
+size_t lstm_gdr_bwd_workspace_size(const lstm_gdr_dims *d);
+int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *q, const void *k,
+                 const void *v, const float *g, const float *beta, const float *s0, void *o,
+                 float *sT, float *states, float *deltas, void *ws, size_t ws_bytes, void *stream);
+int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *dout,
+                 const float *dsT, const void *q, const void *k, const void *v, const float *g,
+                 const float *beta, const float *states, const float *deltas, void *dq, void *dk,
+                 void *dv, float *dg, float *dbeta, float *ds0, void *ws, size_t ws_bytes,
+                 void *stream);
+
+/*
  * lstm_logprob_fwd / lstm_logprob_bwd -- log-probabilities of given tokens.
  * N rows of `vocab` logits (type dtype, row stride ld >= vocab elements),
  * z = logits * inv_temp (inverse temperature, 1e-20 .. 1e20), p = softmax(z):

@@ -1,0 +1,296 @@
+"""lstm_gdr_fwd / lstm_gdr_bwd against the recurrence itself in 64 bits (token
+by token, gradients by torch's autograd of it).
+
+Tolerance.  The kernels compute as floats do: a value goes through sums of
+K + 64 + 64 products a chunk (forward; the same again backward, and once more
+for the gradients of q, k, g and beta), each addition rounding by 2^-24 of
+the sums' magnitude at most.  Over `chunks` chunks that is
+384 * chunks * 2^-24 of the largest value for forward results, three times
+that for gradients, plus the rounding to the output's type."""
+import pytest
+import torch
+
+from backward_lstm_fwd_b200 import binding as L
+from backward_lstm_fwd_b200 import build as lbuild
+
+pytestmark = pytest.mark.gpu
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    lbuild.build()
+
+
+def make(T, B, Hk, Hv, K, V, dt, seed=0, s0=True):
+    gen = torch.Generator(device="cuda").manual_seed(seed + T + B + K)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x = {"q": torch.nn.functional.normalize(rn(T, B, Hk, K), dim=-1).to(DT[dt]),
+         "k": torch.nn.functional.normalize(rn(T, B, Hk, K), dim=-1).to(DT[dt]),
+         "v": rn(T, B, Hv, V).to(DT[dt]),
+         "g": -torch.nn.functional.softplus(rn(T, B, Hv) - 2), "beta": torch.sigmoid(rn(T, B, Hv)),
+         "s0": 0.3 * rn(B, Hv, K, V) if s0 else None}
+    return x, rn(T, B, Hv, V).to(DT[dt]), rn(B, Hv, K, V)
+
+
+def reference(q, k, v, g, beta, s0, lengths, scale):
+    """The recurrence in float64 (differentiable in its inputs)."""
+    T, B, Hk, K = q.shape
+    Hv, V = v.shape[2:]
+    q, k = (t.repeat_interleave(Hv // Hk, dim=2) for t in (q, k))
+    S = s0 if s0 is not None else torch.zeros(B, Hv, K, V, dtype=torch.float64, device=q.device)
+    out = []
+    for t in range(T):
+        Sd = torch.exp(g[t])[..., None, None] * S
+        x = v[t] - (k[t][..., None] * Sd).sum(2)
+        Sn = Sd + k[t][..., None] * (beta[t][..., None] * x)[:, :, None]
+        o = scale * (q[t][..., None] * Sn).sum(2)
+        if lengths is not None:
+            real = (t < lengths)[:, None, None]
+            o = torch.where(real, o, torch.zeros_like(o))
+            Sn = torch.where(real[..., None], Sn, S)
+        S = Sn
+        out.append(o)
+    return (torch.stack(out) if out else v), S
+
+
+def close(name, got, ref, chunks, times=1):
+    assert got.shape == ref.shape, name
+    if not ref.numel():
+        return
+    assert bool(torch.isfinite(got).all()), name
+    half = torch.finfo(got.dtype).eps / 2
+    tiny = torch.finfo(got.dtype).smallest_normal * torch.finfo(got.dtype).eps
+    tol = half * ref.abs() + times * 384 * chunks * 2.0 ** -24 * ref.abs().max() + tiny
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), f"{name}: {float((err / tol).max()):.3g} of the tolerance"
+
+
+def check(x, dout, dsT, lengths=None, scale=None, grads=True):
+    T, B, Hk, K = x["q"].shape
+    scale = K ** -0.5 if scale is None else scale
+    chunks = max(1, -(-T // 64))
+    names = [n for n in ("q", "k", "v", "g", "beta", "s0") if x[n] is not None]
+    d = {n: x[n].double().requires_grad_(grads) if x[n] is not None else None for n in x}
+    o, S = reference(**d, lengths=lengths, scale=scale)
+    st = L.gdr_forward(**x, lengths=lengths, scale=scale, save=grads)
+    close("o", st.o, o.detach(), chunks)
+    close("sT", st.sT, S.detach(), chunks)
+    if not grads:
+        return st
+    gr = L.gdr_backward(st, x["q"], x["k"], x["v"], x["g"], x["beta"], dout=dout, dsT=dsT, lengths=lengths, scale=scale)
+    loss = (o * dout.double()).sum() if dout is not None else 0
+    loss = loss + ((S * dsT.double()).sum() if dsT is not None else 0)
+    want = torch.autograd.grad(loss, [d[n] for n in names], allow_unused=True)
+    for n, w in zip(names, want):
+        w = torch.zeros_like(d[n]) if w is None else w
+        close("d" + n, getattr(gr, "d" + n), w, chunks, 3)
+    return st, gr
+
+
+SHAPES = [(1, 1, 1, 1, 8, 8), (5, 2, 1, 2, 16, 24), (16, 3, 2, 2, 64, 128), (17, 1, 1, 1, 64, 64), (64, 2, 1, 1, 128, 128),
+          (65, 1, 2, 4, 128, 64), (130, 2, 1, 3, 40, 72), (200, 1, 1, 1, 96, 256), (129, 1, 2, 2, 72, 136), (333, 2, 1, 2, 128, 128)]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape, dt):
+    x, _, _ = make(*shape, dt)
+    check(x, None, None, grads=False)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_gradients(shape, dt):
+    check(*make(*shape, dt))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_lengths(dt):
+    x, dout, dsT = make(150, 6, 1, 2, 64, 40, dt)
+    lengths = torch.tensor([150, 0, 1, 64, 65, 149], dtype=torch.int32, device="cuda")
+    st, gr = check(x, dout, dsT, lengths=lengths, scale=0.7)
+    for b, n in enumerate(lengths.tolist()):
+        for t in (st.o, gr.dq, gr.dk, gr.dv, gr.dg, gr.dbeta):
+            assert not t[n:, b].any()
+    assert torch.equal(st.sT[1], x["s0"][1]) and torch.equal(gr.ds0[1], dsT[1])
+    clamped = torch.tensor([999, -5, 1, 64, 65, 149], dtype=torch.int32, device="cuda")
+    assert torch.equal(L.gdr_forward(**x, lengths=clamped, scale=0.7, save=True).o, st.o)
+    y = {n: t[:9].contiguous() if n != "s0" else t for n, t in x.items()}  # token by token
+    check(y, None, None, lengths=torch.tensor([9, 0, 1, 8, 4, 2], dtype=torch.int32, device="cuda"), grads=False)
+
+
+def test_optional_inputs():
+    x, dout, dsT = make(70, 2, 1, 1, 32, 16, "bf16", s0=False)
+    check(x, dout, dsT)
+    check(x, dout, None)
+    st, gr = check(x, None, dsT)
+    x, dout, _ = make(70, 2, 1, 1, 32, 16, "bf16")
+    check(x, None, None, grads=False)
+
+
+def test_padding_values_do_not_matter():
+    """NaN and infinities behind a sequence's length reach nothing."""
+    x, dout, dsT = make(100, 2, 1, 1, 64, 64, "bf16")
+    lengths = torch.tensor([70, 100], dtype=torch.int32, device="cuda")
+    want = L.gdr_forward(**x, lengths=lengths, save=True)
+    wg = L.gdr_backward(want, *(x[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT, lengths=lengths)
+    y = {n: t.clone() for n, t in x.items()}
+    for n in ("q", "k", "v", "g", "beta"):
+        y[n][70:, 0] = float("nan") if n != "v" else float("inf")
+    dout = dout.clone()
+    dout[70:, 0] = float("nan")
+    got = L.gdr_forward(**y, lengths=lengths, save=True)
+    gg = L.gdr_backward(got, *(y[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT, lengths=lengths)
+    assert torch.equal(got.o, want.o) and torch.equal(got.sT, want.sT)
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"):
+        assert torch.equal(getattr(gg, n), getattr(wg, n)), n
+
+
+@pytest.mark.parametrize("T", [9, 140])
+def test_forgetting(T):
+    """Strong decays keep their neighbours' digits; -inf forgets everything before it."""
+    x, dout, dsT = make(T, 1, 1, 2, 32, 24, "fp32")
+    x["g"][:, :, 0] = -30.0
+    x["g"][::3, :, 0] = -0.01
+    check(x, dout, dsT)
+    x["g"][5, :, 1] = float("-inf")
+    x["g"][T // 2, :, 1] = float("-inf")
+    st = L.gdr_forward(**x, save=True)
+    d = {n: t.double() for n, t in x.items()}
+    o, S = reference(**d, lengths=None, scale=32 ** -0.5)
+    close("o", st.o, o, -(-T // 64))
+    close("sT", st.sT, S, -(-T // 64))
+    gr = L.gdr_backward(st, *(x[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT)
+    assert all(bool(torch.isfinite(getattr(gr, n)).all()) for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"))
+    assert not gr.dg[5, :, 1].any()
+    late = dout.clone()
+    late[:5, :, 1] = 0  # nothing that saw s0 counts: token 5 forgets it
+    gr = L.gdr_backward(st, *(x[n] for n in ("q", "k", "v", "g", "beta")), dout=late, dsT=dsT)
+    assert not gr.ds0[:, 1].any() and gr.ds0[:, 0].any()
+
+
+def test_beta_and_decay_limits():
+    """beta 0 (nothing is written), beta 1 with g 0 (a pure delta rule), beta above 1."""
+    x, dout, dsT = make(100, 1, 1, 3, 64, 32, "fp32")
+    x["beta"][:, :, 0] = 0.0
+    x["beta"][:, :, 1] = 1.0
+    x["g"][:, :, 1] = 0.0
+    x["beta"][:, :, 2] = 1.7
+    check(x, dout, dsT)
+
+
+def test_equal_keys():
+    """One key for a whole chunk: the triangular system is as full as it gets."""
+    x, dout, dsT = make(64, 1, 1, 1, 16, 16, "fp32")
+    x["k"][:] = x["k"][:1]
+    x["g"][:] = 0
+    check(x, dout, dsT)
+
+
+def test_slices_of_one_projection():
+    T, B, Hk, Hv, K, V = 90, 3, 2, 4, 32, 24
+    x, dout, dsT = make(T, B, Hk, Hv, K, V, "bf16")
+    wide = torch.zeros(T, B, 2 * Hk * K + Hv * V + 8, dtype=torch.bfloat16, device="cuda")
+    q = wide[..., : Hk * K].view(T, B, Hk, K)
+    k = wide[..., Hk * K: 2 * Hk * K].view(T, B, Hk, K)
+    v = wide[..., 2 * Hk * K: 2 * Hk * K + Hv * V].view(T, B, Hv, V)
+    for a, n in ((q, "q"), (k, "k"), (v, "v")):
+        a.copy_(x[n])
+    want = L.gdr_forward(**x, save=True)
+    got = L.gdr_forward(q, k, v, x["g"], x["beta"], x["s0"], save=True)
+    assert torch.equal(got.o, want.o) and torch.equal(got.sT, want.sT)
+    a = L.gdr_backward(want, x["q"], x["k"], x["v"], x["g"], x["beta"], dout=dout, dsT=dsT)
+    b = L.gdr_backward(got, q, k, v, x["g"], x["beta"], dout=dout, dsT=dsT)
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"):
+        assert torch.equal(getattr(a, n), getattr(b, n))
+    few = L.gdr_forward(q[:4], k[:4], v[:4], x["g"][:4], x["beta"][:4], x["s0"])
+    assert torch.equal(few.o, L.gdr_forward(*(x[n][:4].contiguous() for n in ("q", "k", "v", "g", "beta")), x["s0"]).o)
+
+
+def test_a_sequence_in_parts():
+    """A prompt in chunks, then token by token with the state in place, is the whole sequence."""
+    T, B, Hk, Hv, K, V = 150, 2, 1, 2, 64, 64
+    x, _, _ = make(T, B, Hk, Hv, K, V, "bf16")
+    whole = L.gdr_forward(**x)
+    part = {n: x[n][:131] for n in ("q", "k", "v", "g", "beta")}
+    st = L.gdr_forward(**part, s0=x["s0"])
+    state, outs = st.sT, [st.o]
+    for t in range(131, T):
+        y = {n: x[n][t:t + 1] for n in ("q", "k", "v", "g", "beta")}
+        r = L.gdr_forward(**y, s0=state, sT=state)
+        assert r.sT is state
+        outs.append(r.o)
+    ref, S = reference(**{n: t.double() for n, t in x.items()}, lengths=None, scale=K ** -0.5)
+    close("o", torch.cat(outs), ref, 3)
+    close("sT", state, S, 3)
+    close("whole", whole.o, ref, 3)
+
+
+def test_long():
+    x, dout, dsT = make(2050, 1, 1, 1, 128, 128, "bf16")
+    check(x, dout, dsT)
+
+
+def test_gradient_by_differences():
+    """dg and dbeta against central differences of the 64-bit recurrence."""
+    T, B, Hk, Hv, K, V = 80, 1, 1, 1, 16, 8
+    x, dout, dsT = make(T, B, Hk, Hv, K, V, "fp32")
+    st = L.gdr_forward(**x, save=True)
+    gr = L.gdr_backward(st, *(x[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT)
+    d = {n: t.double() for n, t in x.items()}
+
+    def loss(y):
+        o, S = reference(**y, lengths=None, scale=K ** -0.5)
+        return float((o * dout.double()).sum() + (S * dsT.double()).sum())
+
+    for n, got in (("g", gr.dg), ("beta", gr.dbeta)):
+        for t in (0, 1, 40, 63, 64, 79):
+            lo, hi = ({**d, n: d[n].clone()} for _ in range(2))
+            lo[n][t] -= 1e-5
+            hi[n][t] += 1e-5
+            slope = (loss(hi) - loss(lo)) / 2e-5
+            # differences: about 1e-10 of truncation and 1e-16 / 1e-5 of cancellation, of values near the largest gradient
+            assert abs(slope - float(got[t])) <= 3 * 384 * 2 * 2.0 ** -24 * float(got.abs().max()) + 1e-6 * abs(slope) + 1e-7
+
+
+def test_empty():
+    e = dict(device="cuda")
+    z = lambda *s: torch.zeros(*s, **e)  # noqa: E731
+    s0 = torch.randn(2, 2, 8, 8, **e)
+    st = L.gdr_forward(z(0, 2, 1, 8), z(0, 2, 1, 8), z(0, 2, 2, 8), z(0, 2, 2), z(0, 2, 2), s0)
+    assert torch.equal(st.sT, s0) and st.o.shape == (0, 2, 2, 8)
+    st = L.gdr_forward(z(0, 2, 1, 8), z(0, 2, 1, 8), z(0, 2, 2, 8), z(0, 2, 2), z(0, 2, 2), s0, save=True)
+    gr = L.gdr_backward(st, z(0, 2, 1, 8), z(0, 2, 1, 8), z(0, 2, 2, 8), z(0, 2, 2), z(0, 2, 2), dsT=s0)
+    assert torch.equal(gr.ds0, s0)
+    L.gdr_forward(z(70, 0, 1, 8), z(70, 0, 1, 8), z(70, 0, 2, 8), z(70, 0, 2), z(70, 0, 2))
+
+
+def test_streams_graphs_and_status():
+    x, dout, dsT = make(100, 2, 1, 2, 64, 64, "bf16")
+    five = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    want = L.gdr_forward(**x, save=True)
+    wg = L.gdr_backward(want, *five, dout=dout, dsT=dsT)
+    torch.cuda.synchronize()
+    outs = []
+    for s in [torch.cuda.Stream() for _ in range(2)]:
+        with torch.cuda.stream(s):
+            st = L.gdr_forward(**x, save=True)
+            outs.append((st, L.gdr_backward(st, *five, dout=dout, dsT=dsT)))
+    torch.cuda.synchronize()
+    for st, gr in outs:
+        assert torch.equal(st.o, want.o) and torch.equal(gr.dk, wg.dk) and torch.equal(gr.dg, wg.dg)
+    buf = {n: torch.zeros_like(t) for n, t in x.items()}
+    ws = L.empty_workspace(L.gdr_bwd_workspace_size(want.dims), "cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st = L.gdr_forward(**buf, save=True, ws=ws)
+        gr = L.gdr_backward(st, *(buf[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT, ws=ws)
+    for n in x:
+        buf[n].copy_(x[n])
+    g.replay()
+    torch.cuda.synchronize()
+    assert L.lstm_status(ws) == L.LSTM_OK
+    assert torch.equal(st.o, want.o) and torch.equal(st.sT, want.sT)
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"):
+        assert torch.equal(getattr(gr, n), getattr(wg, n)), n

@@ -118,3 +118,78 @@ def test_binding_refuses_host_tensors_and_shapes(lib):
         L.logprobs(torch.zeros(1, 5).expand(3, 5), ids)
     with pytest.raises(ValueError, match="dense"):
         L.logprobs(torch.zeros(5, 3).t(), ids)
+
+
+# ----------------------------------------------------------- gated delta rule
+def gdr_fwd(lib, d, opt=None, q=FAKE, k=FAKE, v=FAKE, g=FAKE, beta=FAKE, s0=None, o=FAKE, sT=FAKE, states=None, deltas=None,
+            ws=FAKE, ws_bytes=None):
+    n = L.gdr_fwd_workspace_size(d, states is not None) if ws_bytes is None else ws_bytes
+    return lib.lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt) if opt else None, q, k, v, g, beta, s0, o, sT, states, deltas,
+                            ws, n, None)
+
+
+def gdr_bwd(lib, d, opt=None, dout=FAKE, dsT=FAKE, q=FAKE, k=FAKE, v=None, g=FAKE, beta=FAKE, states=FAKE, deltas=FAKE, dq=FAKE,
+            dk=FAKE, dv=FAKE, dg=FAKE, dbeta=FAKE, ds0=FAKE, ws=FAKE, ws_bytes=None):
+    n = L.gdr_bwd_workspace_size(d) if ws_bytes is None else ws_bytes
+    return lib.lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt) if opt else None, dout, dsT, q, k, v, g, beta, states, deltas,
+                            dq, dk, dv, dg, dbeta, ds0, ws, n, None)
+
+
+GDR = dict(T=100, B=2, Hk=2, Hv=4, K=64, V=64, dtype=L.LSTM_BF16)
+
+
+@pytest.mark.parametrize("bad", [dict(T=-1), dict(B=-1), dict(Hk=-1), dict(Hv=-2), dict(K=-8), dict(V=-8), dict(dtype=3),
+                                 dict(Hv=3), dict(Hk=0), dict(ldq=64), dict(ldk=64), dict(ldv=64), dict(T=1 << 20, B=1 << 12)])
+def test_gdr_dims(lib, bad):
+    d = L.gdr_dims(**{**GDR, **bad})
+    assert gdr_fwd(lib, d, ws_bytes=1 << 40) == L.LSTM_ERR_INVALID_ARG
+    assert gdr_bwd(lib, d, ws_bytes=1 << 40) == L.LSTM_ERR_INVALID_ARG
+    assert L.gdr_fwd_workspace_size(d) == 0 == L.gdr_bwd_workspace_size(d)
+
+
+@pytest.mark.parametrize("big", [dict(K=136), dict(V=264), dict(K=60), dict(V=60), dict(ldq=132), dict(ldv=260)])
+def test_gdr_extents(lib, big):
+    d = L.gdr_dims(**{**GDR, **big})
+    assert gdr_fwd(lib, d, ws_bytes=1 << 40) == L.LSTM_ERR_UNSUPPORTED
+    assert gdr_bwd(lib, d, ws_bytes=1 << 40) == L.LSTM_ERR_UNSUPPORTED
+    assert L.gdr_fwd_workspace_size(d) == 0 == L.gdr_bwd_workspace_size(d)
+
+
+def test_gdr_arguments(lib):
+    d = L.gdr_dims(**GDR)
+    for n in ("q", "k", "v", "g", "beta", "o", "sT"):
+        assert gdr_fwd(lib, d, **{n: None}) == L.LSTM_ERR_INVALID_ARG
+        assert gdr_fwd(lib, d, **{n: FAKE + 8}) == L.LSTM_ERR_INVALID_ARG
+    assert gdr_fwd(lib, d, s0=FAKE + 8) == L.LSTM_ERR_INVALID_ARG
+    assert gdr_fwd(lib, d, states=FAKE) == L.LSTM_ERR_INVALID_ARG  # the backward needs both
+    assert gdr_fwd(lib, d, deltas=FAKE) == L.LSTM_ERR_INVALID_ARG
+    for n in ("q", "k", "g", "beta", "states", "deltas", "dq", "dk", "dv", "dg", "dbeta"):
+        assert gdr_bwd(lib, d, **{n: None}) == L.LSTM_ERR_INVALID_ARG
+        assert gdr_bwd(lib, d, **{n: FAKE + 8}) == L.LSTM_ERR_INVALID_ARG
+    for opt in (L.GdrOptions(FAKE + 4, 1.0), L.GdrOptions(None, float("nan")), L.GdrOptions(None, float("inf"))):
+        assert gdr_fwd(lib, d, opt=opt) == L.LSTM_ERR_INVALID_ARG
+        assert gdr_bwd(lib, d, opt=opt) == L.LSTM_ERR_INVALID_ARG
+    for save in (None, FAKE):
+        need = L.gdr_fwd_workspace_size(d, save is not None)
+        assert need > 256
+        assert gdr_fwd(lib, d, states=save, deltas=save, ws_bytes=need - 1) == L.LSTM_ERR_WORKSPACE
+        assert gdr_fwd(lib, d, states=save, deltas=save, ws=None) == L.LSTM_ERR_WORKSPACE
+    assert gdr_bwd(lib, d, ws_bytes=L.gdr_bwd_workspace_size(d) - 1) == L.LSTM_ERR_WORKSPACE
+    # a few tokens that keep nothing need the control block alone
+    few = L.gdr_dims(**{**GDR, "T": 1})
+    assert L.gdr_fwd_workspace_size(few) == 256 < L.gdr_fwd_workspace_size(few, True)
+    # nothing to do: nothing is enqueued
+    none = L.gdr_dims(**{**GDR, "B": 0})
+    assert gdr_fwd(lib, none, q=None, k=None, v=None, g=None, beta=None, o=None, sT=None) == L.LSTM_OK
+    assert gdr_bwd(lib, none) == L.LSTM_OK
+
+
+def test_gdr_binding_refusals(lib):
+    q = torch.zeros(4, 2, 1, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.gdr_forward(q, q, q, torch.zeros(4, 2, 1), torch.zeros(4, 2, 1))
+    with pytest.raises(ValueError, match="heads must be dense"):
+        L._token_stride(torch.zeros(4, 2, 2, 16)[..., :8], "q")
+    with pytest.raises(ValueError, match="one stride"):
+        L._token_stride(torch.zeros(4, 3, 1, 8)[:, :2], "q")
+    assert L._token_stride(torch.zeros(4, 2, 24)[..., 8:16].view(4, 2, 1, 8), "q") == 24
