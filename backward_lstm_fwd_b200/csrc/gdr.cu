@@ -98,8 +98,8 @@ template <class E, int KD>
 int prep(const Shape &s, const void *q, const void *k, const float *g, const float *beta, char *w, const Layout &l,
          cudaStream_t st) {
     PrepArgs p = {s, q, k, g, beta, w + l.qk, w + l.tp, (Ctrl *)w};
-    LSTM_CUDA_TRY(allow_smem(prep_kernel<E, KD>, prep_smem<E, KD>()));
-    prep_kernel<E, KD><<<s.NC * s.B * s.Hk, 128, prep_smem<E, KD>(), st>>>(p);
+    LSTM_CUDA_TRY(allow_smem(prep_kernel<E, KD>, PrepSmem<E, KD>::smem));
+    prep_kernel<E, KD><<<s.NC * s.B * s.Hk, 128, PrepSmem<E, KD>::smem, st>>>(p);
     LSTM_CUDA_TRY(host::launched());
     return LSTM_OK;
 }

@@ -141,16 +141,61 @@ __device__ __forceinline__ void put_terms(uint32_t col, int stride, const float 
     }
 }
 
+// One thread: D (+)= A B^T over the products of term t of A and u of B with
+// t + u < orders, t < ta, u < tb, the smallest products first (a float
+// accumulator of the tensor core drops what lies below its last bit, so the
+// small ones are summed while it is small).  A in tensor memory (a_term
+// columns between terms) or shared memory (A_SMEM: a is a descriptor); b a
+// descriptor; term and step distances in 16-byte units.  steps K = 16 each,
+// in chunks of four `chunk` apart.
+struct Steps {
+    uint32_t term, step, chunk;  // 16-byte units
+};
+__device__ __forceinline__ uint32_t at_step(const Steps &x, int t, int ks) {
+    return t * x.term + (ks >> 2) * x.chunk + (ks & 3) * x.step;
+}
+template <int steps>
+__device__ __forceinline__ void products_ts(uint32_t d, uint32_t a, uint32_t a_term, int ta, uint64_t b, Steps bs, int tb,
+                                            int orders, uint32_t idesc, uint32_t acc = 0) {
+#pragma unroll 1
+    for (int o = orders - 1; o >= 0; --o)
+#pragma unroll 1
+        for (int t = max(0, o - tb + 1); t < ta && t <= o; ++t) {
+#pragma unroll
+            for (int ks = 0; ks < steps; ++ks) {
+                tc::mma_bf16_ts(d, a + t * a_term + 8 * ks, b + at_step(bs, o - t, ks), idesc, acc);
+                acc = 1;
+            }
+        }
+}
+template <int steps>
+__device__ __forceinline__ void products_ss(uint32_t d, uint64_t a, Steps as, int ta, uint64_t b, Steps bs, int tb,
+                                            int orders, uint32_t idesc, uint32_t acc = 0) {
+#pragma unroll 1
+    for (int o = orders - 1; o >= 0; --o)
+#pragma unroll 1
+        for (int t = max(0, o - tb + 1); t < ta && t <= o; ++t) {
+#pragma unroll
+            for (int ks = 0; ks < steps; ++ks) {
+                tc::mma_bf16(d, a + at_step(as, t, ks), b + at_step(bs, o - t, ks), idesc, acc);
+                acc = 1;
+            }
+        }
+}
+
+__device__ __forceinline__ void get16(uint32_t col, float (&f)[16]) {
+    uint32_t r[16];
+    tc::tmem_ld16(col, r);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void get32(uint32_t col, float (&f)[32]) {
     uint32_t r[32];
     tc::tmem_ld32(col, r);
     tc::tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // A bounded wait of a whole warp, ordered before its tensor-memory accesses.
@@ -205,9 +250,11 @@ __device__ __forceinline__ float decay(double hi, double lo) { return expf((floa
 // terms, zero for padding and past K), then per value head of the group T2,
 // P and the gates, all in the layout the other kernels copy in bulk.
 //
-// Q K^T and K K^T are one product of the stacked [Q; K] with K.  T2's columns
-// are solved by forward substitution, one thread a column, the column in
-// registers: warps 2 and 3 solve while warps 0 and 1 write P.
+// Q K^T and K K^T are one product of the stacked [Q; K] with K.  T2 is the
+// inverse of a unit lower triangular matrix [A 0; B D] of 32 x 32 blocks:
+// [A' 0; -D' B A', D'].  A' and D' come from forward substitution, a thread a
+// column, one warp a block, while the other two warps form P; the block below
+// is two products by all four warps.
 struct PrepArgs {
     Shape s;
     const void *q, *k;
@@ -215,28 +262,28 @@ struct PrepArgs {
     char *qk, *tp;
     Ctrl *ctrl;
 };
-constexpr int PREP_LD = 68;  // floats of a row of the triangular matrix in shared memory
+constexpr int PREP_LD = 68;                    // floats between rows of a 64 x 64 matrix in shared memory
+constexpr int PREP_MAT = C * PREP_LD * 4;
 
-template <class E, int KD> constexpr size_t prep_smem() {
-    // the solved matrix goes where the operand tiles were
-    return (QK<E, KD>::bytes > C * PREP_LD * 4 ? QK<E, KD>::bytes : C * PREP_LD * 4) + C * PREP_LD * 4 + 1024;
-}
+template <class E, int KD> struct PrepSmem {
+    // T2 and P go where the operand tiles were; the triangle behind them
+    static constexpr int tri = QK<E, KD>::bytes > 2 * PREP_MAT ? QK<E, KD>::bytes : 2 * PREP_MAT;
+    static constexpr size_t smem = tri + PREP_MAT + 1024;
+};
 
 template <class E, int KD>
 __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
     constexpr int TB = Terms<E>::n;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float *solved = (float *)tiles;
-    constexpr int first = QK<E, KD>::bytes > C * PREP_LD * 4 ? QK<E, KD>::bytes : C * PREP_LD * 4;
-    float *tri = (float *)(tiles + first);
+    float *t2 = (float *)tiles, *pm = (float *)(tiles + PREP_MAT), *tri = (float *)(tiles + PrepSmem<E, KD>::tri);
     __shared__ double bs[C];
     __shared__ float betas[C];
     __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Shape &s = a.s;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int id = blockIdx.x;
     const int hk = id % s.Hk;
     id /= s.Hk;
@@ -251,23 +298,34 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
         tc::tmem_alloc(&tmem_slot, 64);
         tc::tmem_relinquish();
     }
-    // tiles: rows 0..63 q, 64..127 k; 16-byte groups of 8 dims
+    // tiles: rows 0..63 q, 64..127 k; 16-byte groups of 8 dims, eight loads in flight
     char *out = a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes;
-    for (int i = tid; i < 128 * (KD / 8); i += 128) {
-        const int row = i / (KD / 8), gr = i % (KD / 8), t = c * C + (row & 63);
-        float f[8] = {};
-        if (t < len && gr * 8 < s.K) {
-            const long long r = (long long)t * s.B + b;
-            load8<E>(row < 64 ? (const E *)a.q + r * s.ldq + (long long)hk * s.K + gr * 8
-                              : (const E *)a.k + r * s.ldk + (long long)hk * s.K + gr * 8, f);
-        }
-        uint4 o[TB];
-        split8<TB>(f, o);
-        const uint32_t off = (gr >> 3) * 2 * TILE + swz(row, (gr & 7) * 16);
+    constexpr int U = sizeof(E) == 2 ? 8 : 4;
+#pragma unroll 1
+    for (int i0 = tid; i0 < 128 * (KD / 8); i0 += U * 128) {
+        float f[U][8];
 #pragma unroll
-        for (int t2 = 0; t2 < TB; ++t2) {
-            *(uint4 *)(tiles + t2 * QK<E, KD>::term + off) = o[t2];
-            *(uint4 *)(out + t2 * QK<E, KD>::term + off) = o[t2];
+        for (int n = 0; n < U; ++n) {
+            const int i = i0 + n * 128, row = i / (KD / 8), gr = i % (KD / 8), t = c * C + (row & 63);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[n][j] = 0.f;
+            if (t < len && gr * 8 < s.K) {
+                const long long r = (long long)t * s.B + b;
+                load8<E>(row < 64 ? (const E *)a.q + r * s.ldq + (long long)hk * s.K + gr * 8
+                                  : (const E *)a.k + r * s.ldk + (long long)hk * s.K + gr * 8, f[n]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < U; ++n) {
+            const int i = i0 + n * 128, row = i / (KD / 8), gr = i % (KD / 8);
+            uint4 o[TB];
+            split8<TB>(f[n], o);
+            const uint32_t off = (gr >> 3) * 2 * TILE + swz(row, (gr & 7) * 16);
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                *(uint4 *)(tiles + t * QK<E, KD>::term + off) = o[t];
+                *(uint4 *)(out + t * QK<E, KD>::term + off) = o[t];
+            }
         }
     }
     tc::fence_proxy_async_smem();
@@ -277,112 +335,114 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
     const uint32_t tmem = tmem_slot;
     if (tid == 0) {
         const uint32_t base = tc::smem_u32(tiles);
-        constexpr uint32_t idesc = tc::idesc_bf16_f32(128, 64, 0, 0);
-        uint32_t acc = 0;
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-            for (int u = 0; u < TB; ++u) {
-                if (t + u >= NT) continue;
-                for (int ks = 0; ks < KD / 16; ++ks) {
-                    const uint32_t chunk = (ks >> 2) * 2 * TILE;
-                    tc::mma_bf16(tmem, k_major(base + t * QK<E, KD>::term + chunk, ks & 3),
-                                 k_major(base + u * QK<E, KD>::term + chunk + TILE, ks & 3), idesc, acc);
-                    acc = 1;
-                }
-            }
+        const Steps st = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};
+        products_ss<KD / 16>(tmem, k_major(base, 0), st, TB, k_major(base + TILE, 0), st, TB, NT,
+                             tc::idesc_bf16_f32(128, 64, 0, 0));
         tc::mma_commit(&done);
     }
+    __syncwarp();
+    if (warp == 0) load_gates(s, a.g, a.beta, c, b, hk * s.group, len, bs, betas);
     wait(&done, 0, a.ctrl, &abort_flag, 0x601);
+    __syncthreads();
     const int row = tid & 63;  // warps 0, 1: Q K^T; warps 2, 3: K K^T
+    const int half = warp & 1;  // rows 32 half ..
     for (int m = 0; m < s.group; ++m) {
         const int h = hk * s.group + m;
         char *tp = a.tp + (((size_t)c * s.B + b) * s.Hv + h) * TP_BYTES;
-        __syncthreads();  // the last head's sums and solved matrix are read
-        if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, bs, betas);
-        __syncthreads();
         const double bi = bs[row];
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        if (warp < 2) {
-            for (int j0 = 0; j0 < C; j0 += 16) {
-                uint32_t r[16];
-                tc::tmem_ld16(lanes + j0, r);
-                tc::tmem_ld_wait();
-                float f[16];
+        float *dst = (warp < 2 ? pm : tri) + row * PREP_LD;
+#pragma unroll 1
+        for (int j0 = 0; j0 < 32 * (half + 1); j0 += 16) {
+            float f[16];
+            get16(lanes + j0, f);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    f[j] = j0 + j <= row ? s.scale * decay(bi, bs[j0 + j]) * __uint_as_float(r[j]) : 0.f;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float e[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) e[j] = f[8 * hf + j];
-                    uint4 o[NT];
-                    split8<NT>(e, o);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        *(uint4 *)(tp + (NT + t) * TILE + swz(row, (j0 + 8 * hf) * 2)) = o[t];
-                }
+            for (int j = 0; j < 16; ++j) {
+                const int jj = j0 + j;
+                if (warp < 2) f[j] = jj <= row ? s.scale * decay(bi, bs[jj]) * f[j] : 0.f;
+                else f[j] = jj < row ? decay(bi, bs[jj]) * betas[jj] * f[j] : 0.f;
             }
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) *(float4 *)(dst + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+        }
+        if (warp < 2) {
+            if (!half)
+#pragma unroll
+                for (int j = 32; j < 64; j += 4) *(float4 *)(dst + j) = make_float4(0.f, 0.f, 0.f, 0.f);
             float *gates = (float *)(tp + 2 * NT * TILE);
             gates[tid] = decay(bi, 0.0);
             gates[C + tid] = decay(bs[C - 1], bi);
             gates[2 * C + tid] = betas[tid];
         } else {
-            for (int j0 = 0; j0 < C; j0 += 16) {
-                uint32_t r[16];
-                tc::tmem_ld16(lanes + j0, r);
-                tc::tmem_ld_wait();
+            __syncwarp();
+            // column `lane` of the inverse of block (half, half): x_i = [i == lane] - sum_{m < i} tri[i][m] x_m
+            const float *blk = tri + half * 32 * PREP_LD + half * 32;
+            float x[32];
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    float f[4];
+            for (int i = 0; i < 32; ++i) {
+                float p0 = i == lane ? 1.f : 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int jj = j0 + j + i;
-                        f[i] = jj < row ? decay(bi, bs[jj]) * betas[jj] * __uint_as_float(r[j + i]) : 0.f;
-                    }
-                    *(float4 *)(tri + row * PREP_LD + j0 + j) = make_float4(f[0], f[1], f[2], f[3]);
+                for (int mm = 0; mm < i; mm += 4) {
+                    const float4 v = *(const float4 *)(blk + i * PREP_LD + mm);
+                    p0 = fmaf(-v.x, x[mm], p0);
+                    if (mm + 1 < i) p1 = fmaf(-v.y, x[mm + 1], p1);
+                    if (mm + 2 < i) p2 = fmaf(-v.z, x[mm + 2], p2);
+                    if (mm + 3 < i) p3 = fmaf(-v.w, x[mm + 3], p3);
                 }
+                x[i] = (p0 + p1) + (p2 + p3);
             }
-            group_sync(1, 64);
-            // column `row` of the inverse: x_i = [i == row] - sum_{m < i} tri[i][m] x_m;
-            // columns 32.. start at row 32
-            float x[C];
+            float *o = t2 + half * 32 * PREP_LD + half * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                float p0 = i == row ? 1.f : 0.f, p1 = 0.f;
-                if (i < 32 && warp == 3) {
-                    x[i] = 0.f;
-                    continue;
-                }
+            for (int i = 0; i < 32; ++i) o[i * PREP_LD] = x[i];
+            if (half)
 #pragma unroll
-                for (int mm = 0; mm < (i + 3) / 4; ++mm) {
-                    if (mm < 8 && warp == 3) continue;
-                    const float4 v = *(const float4 *)(tri + i * PREP_LD + 4 * mm);
-                    p0 = fmaf(-v.x, x[4 * mm], p0);
-                    if (4 * mm + 1 < i) p1 = fmaf(-v.y, x[4 * mm + 1], p1);
-                    if (4 * mm + 2 < i) p0 = fmaf(-v.z, x[4 * mm + 2], p0);
-                    if (4 * mm + 3 < i) p1 = fmaf(-v.w, x[4 * mm + 3], p1);
-                }
-                x[i] = p0 + p1;
-            }
-#pragma unroll
-            for (int i = 0; i < C; ++i) solved[i * PREP_LD + row] = x[i];
+                for (int i = 0; i < 32; ++i) t2[i * PREP_LD + 32 + lane] = 0.f;  // above the diagonal
         }
         __syncthreads();
-        {  // T2's terms: half a row a thread
-            const int r = tid >> 1, j0 = (tid & 1) * 32;
+        {  // block (1, 0): W = B A', into the triangle's upper right corner; then -D' W
+            const int i = tid >> 2, j0 = (tid & 3) * 8;
+            float acc[8];
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = solved[r * PREP_LD + j0 + j + i];
-                uint4 o[NT];
-                split8<NT>(f, o);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) *(uint4 *)(tp + t * TILE + swz(r, (j0 + j) * 2)) = o[t];
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float l = tri[(32 + i) * PREP_LD + k];
+                const float4 u = *(const float4 *)(t2 + k * PREP_LD + j0), v = *(const float4 *)(t2 + k * PREP_LD + j0 + 4);
+                acc[0] = fmaf(l, u.x, acc[0]); acc[1] = fmaf(l, u.y, acc[1]); acc[2] = fmaf(l, u.z, acc[2]); acc[3] = fmaf(l, u.w, acc[3]);
+                acc[4] = fmaf(l, v.x, acc[4]); acc[5] = fmaf(l, v.y, acc[5]); acc[6] = fmaf(l, v.z, acc[6]); acc[7] = fmaf(l, v.w, acc[7]);
             }
+            *(float4 *)(tri + i * PREP_LD + 32 + j0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            *(float4 *)(tri + i * PREP_LD + 32 + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float l = -t2[(32 + i) * PREP_LD + 32 + k];
+                const float4 u = *(const float4 *)(tri + k * PREP_LD + 32 + j0), v = *(const float4 *)(tri + k * PREP_LD + 32 + j0 + 4);
+                acc[0] = fmaf(l, u.x, acc[0]); acc[1] = fmaf(l, u.y, acc[1]); acc[2] = fmaf(l, u.z, acc[2]); acc[3] = fmaf(l, u.w, acc[3]);
+                acc[4] = fmaf(l, v.x, acc[4]); acc[5] = fmaf(l, v.y, acc[5]); acc[6] = fmaf(l, v.z, acc[6]); acc[7] = fmaf(l, v.w, acc[7]);
+            }
+            *(float4 *)(t2 + (32 + i) * PREP_LD + j0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            *(float4 *)(t2 + (32 + i) * PREP_LD + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
         }
+        __syncthreads();
+        if (warp == 0 && m + 1 < s.group) load_gates(s, a.g, a.beta, c, b, h + 1, len, bs, betas);
+        // terms of T2 and P: eight threads a row, whole 128-byte lines a warp
+#pragma unroll 2
+        for (int i = tid; i < 2 * C * 8; i += 128) {
+            const int mat = i >> 9, r = (i >> 3) & 63, gr = i & 7;
+            float f[8];
+            const float4 *src = (const float4 *)((mat ? pm : t2) + r * PREP_LD + gr * 8);
+            const float4 u = src[0], v = src[1];
+            f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+            f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+            uint4 o[NT];
+            split8<NT>(f, o);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) *(uint4 *)(tp + (mat * NT + t) * TILE + swz(r, gr * 16)) = o[t];
+        }
+        __syncthreads();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -391,24 +451,32 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
 
 // -------------------------------------------------------------- sequential
 // Block (b, h, 128 columns of V): the chunks of one head in order.  Thread
-// (wg, lane) of the 256 compute threads holds column `lane` of S^T -- the
-// state is kept transposed, V on the tensor-memory lanes -- for half of K in
-// registers.  Every contraction of the chain has its left operand in tensor
-// memory, where the thread that owns the lane writes it, so nothing in the
-// chain crosses lanes or goes through shared memory:
-//   [Q|K] S  ->  R = V - gamma K S  ->  X = T2 R  ->  U  ->  S += K^T U.
-// The chunks' tiles come by bulk copies, a chunk ahead where two stages fit.
+// (wg, lane) holds column `lane` of S^T -- the state is kept transposed, V on
+// the tensor-memory lanes -- for a quarter of K in registers.  Every
+// contraction of the chain has its left operand in tensor memory, where the
+// thread that owns the lane writes it, so nothing in the chain crosses lanes
+// or goes through shared memory:
+//   K S  ->  R = V - gamma K S  ->  X = T2 R  ->  U  ->  S += K^T (left U).
+// Q S and P U run beside the chain; their sum is stored a chunk later.  The
+// chunks' tiles come by bulk copies, a chunk ahead where two stages fit.
 // Bound: the chain's latency (three products and three passes over registers
-// a chunk), since few heads means few blocks.
-constexpr int SEQ_THREADS = 256;
-constexpr uint32_t COL_S = 0, COL_D = 192, COL_R = 320, COL_X = 416;  // tensor-memory columns
-constexpr uint32_t COL_U = COL_S, COL_W = COL_S + 96;
+// a chunk) where there are few heads.  512 threads rather than 256: a pass
+// over the registers is short code for many warps (with 256 threads the warps
+// waited for instructions more than for anything else).
+constexpr int SEQ_THREADS = 512;
+// tensor-memory columns: S terms, then left U terms | K S, Q S, then K^T (left
+// U) | R terms, then U terms | X, then P U
+constexpr uint32_t COL_S = 0, COL_D = 192, COL_R = 320, COL_X = 416, COL_W = 96;
 
 template <class E, int KD> struct Seq {
     static constexpr int stage = QK<E, KD>::bytes + 2 * NT * TILE;  // tiles; the gates lie behind the stages
     static constexpr int extra = 1024 + 256;                        // alignment, barriers
     static constexpr int stages = 2 * (stage + GATES) + extra <= 232448 ? 2 : 1;
     static constexpr size_t smem = (size_t)stages * (stage + GATES) + extra;
+    static constexpr int TB = Terms<E>::n;
+    // terms and orders of what only an output of type E sees: two terms leave
+    // 2^-17 of the product, far below a 16-bit output's rounding
+    static constexpr int NO = sizeof(E) == 2 ? 2 : NT;
 };
 
 struct SeqArgs {
@@ -449,21 +517,8 @@ template <class E, int KD> __device__ __forceinline__ void seq_drain(SeqBars *ba
     for (int n = max(0, chunks - Q::stages); n < chunks; ++n)
         tc::mbar_wait(&bar->full[n % Q::stages], (n / Q::stages) & 1, nullptr, nullptr, 0, 200000000ull);
 }
-
-template <class E, int KD>
-__global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_constant__ SeqArgs a) {
-    using Q = Seq<E, KD>;
-    constexpr int TB = Terms<E>::n, H2 = KD / 2, TERM = QK<E, KD>::term;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
-    const Shape &s = a.s;
-    const int tid = threadIdx.x, warp = tid >> 5;
-    int id = blockIdx.x;
-    const int vt = id % s.VT;
-    id /= s.VT;
-    const int h = id % s.Hv, b = id / s.Hv;
-    if (tid == 0) {
+__device__ __forceinline__ void seq_setup(SeqBars *bar) {
+    if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) tc::mbar_init(&bar->full[i], 1);
         tc::mbar_init(&bar->m1, 1);
         tc::mbar_init(&bar->m2, 1);
@@ -472,411 +527,340 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         bar->abort_flag = 0;
         tc::fence_mbar_init();
     }
-    if (warp == 0) {
+    if (threadIdx.x < 32) {
         tc::tmem_alloc(&bar->tmem_slot, 512);
         tc::tmem_relinquish();
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = bar->tmem_slot;
-    if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, false);
-    __syncwarp();
-    {
-        const int wg = tid >> 7, lane = tid & 127, v = vt * LANES + lane;
-        const bool own = v < s.V;
-        const int len = length_of(s, b);
-        const uint32_t lanes = tmem + ((uint32_t)(lane & 96) << 16);
-        const long long head = (long long)b * s.Hv + h;
-        const long long row = (long long)s.B * s.Hv * s.V;  // elements of o, deltas between tokens
-        volatile int *ab = &bar->abort_flag;
-        float S[H2];
-#pragma unroll
-        for (int i = 0; i < H2; ++i) {
-            const int k = wg * H2 + i;
-            S[i] = a.s0 && own && k < s.K ? a.s0[(head * s.K + k) * s.V + v] : 0.f;
-        }
-        float o[32];
-        auto store_o = [&](int c) {
-            if (!own) return;
-            E *p = (E *)a.o + head * s.V + v;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int t = c * C + wg * 32 + i;
-                if (t < s.T) p[t * row] = from_f<E>(o[i]);
-            }
-        };
-        for (int c = 0; c < s.NC; ++c) {
-            const int st = c % Q::stages;
-            const uint32_t ph = c & 1;
-            if (Q::stages == 2 && tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
-            __syncwarp();
-            const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
-            const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + wg * 32;
-            E vr[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int t = c * C + wg * 32 + i;
-                vr[i] = own && t < len ? ((const E *)a.v)[((long long)t * s.B + b) * s.ldv + (long long)h * s.V + v]
-                                       : from_f<E>(0.f);
-            }
-            put_terms<H2 / 2, NT>(lanes + COL_S + wg * (H2 / 2), KD / 2, S);
-            tc::tmem_st_wait();
-            wait(&bar->full[st], (c / Q::stages) & 1, a.ctrl, ab, 0x612);
-            tc::tc_fence_before();
-            group_sync(1, SEQ_THREADS);
-            if (tid == 0) {  // D = [q | k] S, tokens on the columns
-                tc::tc_fence_after();
-                uint32_t acc = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) {
-                        if (t + u >= NT) continue;
-#pragma unroll
-                        for (int ks = 0; ks < KD / 16; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_S + t * (KD / 2) + 8 * ks,
-                                            k_major(qk + u * TERM + (ks >> 2) * 2 * TILE, ks & 3),
-                                            tc::idesc_bf16_f32(128, 128, 0, 0), acc);
-                            acc = 1;
-                        }
-                    }
-                tc::mma_commit(&bar->m1);
-            }
-            __syncwarp();
-            if (c > 0) store_o(c - 1);
-            if (a.states && own) {
-                float *p = a.states + (((long long)c * s.B * s.Hv + head) * s.K) * s.V + v;
-#pragma unroll
-                for (int i = 0; i < H2; ++i) {
-                    const int k = wg * H2 + i;
-                    if (k < s.K) p[(long long)k * s.V] = S[i];
-                }
-            }
-            __syncwarp();
-            const float last = gates[(1 - wg) * 32 + 31];  // gamma of token 63
-            wait(&bar->m1, ph, a.ctrl, ab, 0x613);
-            float f[32];
-            get32(lanes + COL_D + 64 + wg * 32, f);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = fmaf(-gates[i], f[i], to_f(vr[i]));
-            put_terms<16, NT>(lanes + COL_R + wg * 16, 32, f);
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            group_sync(1, SEQ_THREADS);
-            if (tid == 0) {  // X = T2 R
-                tc::tc_fence_after();
-                uint32_t acc = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < NT - t; ++u)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_X, tmem + COL_R + t * 32 + 8 * ks, k_major(tp + u * TILE, ks),
-                                            tc::idesc_bf16_f32(128, 64, 0, 0), acc);
-                            acc = 1;
-                        }
-                tc::mma_commit(&bar->m2);
-            }
-            __syncwarp();
-            get32(lanes + COL_D + wg * 32, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= s.scale * gates[i];
-            wait(&bar->m2, ph, a.ctrl, ab, 0x614);
-            get32(lanes + COL_X + wg * 32, f);
-            if (a.deltas && own) {
-                float *p = a.deltas + head * s.V + v;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int t = c * C + wg * 32 + i;
-                    if (t < s.T) p[t * row] = f[i];
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= gates[2 * C + i];  // U
-            put_terms<16, NT>(lanes + COL_U + wg * 16, 32, f);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= gates[C + i];      // left U
-            put_terms<16, NT>(lanes + COL_W + wg * 16, 32, f);
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            group_sync(1, SEQ_THREADS);
-            if (tid == 0) {
-                tc::tc_fence_after();
-                uint32_t acc = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)  // D = K^T (left U)
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) {
-                        if (t + u >= NT) continue;
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_W + t * 32 + 8 * ks,
-                                            mn_major(qk + u * TERM + TILE, ks, 2 * TILE),
-                                            tc::idesc_bf16_f32(128, KD, 0, 1), acc);
-                            acc = 1;
-                        }
-                    }
-                tc::mma_commit(&bar->m4);
-                acc = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)  // P U
-#pragma unroll
-                    for (int u = 0; u < NT - t; ++u)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_X, tmem + COL_U + t * 32 + 8 * ks,
-                                            k_major(tp + (NT + u) * TILE, ks), tc::idesc_bf16_f32(128, 64, 0, 0), acc);
-                            acc = 1;
-                        }
-                tc::mma_commit(&bar->m3);
-            }
-            __syncwarp();
-            wait(&bar->m4, ph, a.ctrl, ab, 0x615);
-#pragma unroll
-            for (int i0 = 0; i0 < H2; i0 += 32) {
-                get32(lanes + COL_D + wg * H2 + i0, f);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
-            }
-            wait(&bar->m3, ph, a.ctrl, ab, 0x616);
-            if (Q::stages == 1 && tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
-            __syncwarp();
-            get32(lanes + COL_X + wg * 32, f);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] += f[i];
-        }
-        if (s.NC > 0) store_o(s.NC - 1);
-        if (own && a.sT) {
-#pragma unroll
-            for (int i = 0; i < H2; ++i) {
-                const int k = wg * H2 + i;
-                if (k < s.K) a.sT[(head * s.K + k) * s.V + v] = S[i];
-            }
-        }
-    }
-    if (tid == 32) seq_drain<E, KD>(bar, s.NC);
+}
+__device__ __forceinline__ void seq_finish(SeqBars *bar) {
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    if (threadIdx.x < 32) tc::tmem_dealloc(bar->tmem_slot, 512);
+}
+// Every thread's tensor-memory writes are done; the one thread that issues
+// the products that read them goes on in the branch.
+__device__ __forceinline__ bool hand_over() {
+    tc::tmem_st_wait();
+    tc::tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x != 0) return false;
+    tc::tc_fence_after();
+    return true;
 }
 
-// The adjoint, chunks in reverse, the same layout (dS^T in registers):
-//   K dS and P^T dO  ->  dU  ->  dV = T2^T (beta dU)  ->  dS += scale Q^T gamma dO - K^T gamma dV.
+// What a thread of the sequential kernels works on.
+template <int KD> struct Lane {
+    int wg, v, len;
+    bool own;
+    uint32_t lanes;
+    long long head, row;  // row: elements of o, deltas between tokens
+    __device__ __forceinline__ Lane(const Shape &s, uint32_t tmem, int b, int h, int vt) {
+        const int lane = threadIdx.x & 127;
+        wg = threadIdx.x >> 7;
+        v = vt * LANES + lane;
+        own = v < s.V;
+        len = length_of(s, b);
+        lanes = tmem + ((uint32_t)(lane & 96) << 16);
+        head = (long long)b * s.Hv + h;
+        row = (long long)s.B * s.Hv * s.V;
+    }
+    // rows k of a [K][V] state at `base`, this thread's quarter
+    __device__ __forceinline__ void load(const Shape &s, const float *base, float (&S)[KD / 4]) const {
+#pragma unroll
+        for (int i = 0; i < KD / 4; ++i) {
+            const int k = wg * (KD / 4) + i;
+            S[i] = base && own && k < s.K ? base[(long long)k * s.V + v] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void store(const Shape &s, float *base, const float (&S)[KD / 4]) const {
+        if (base && own) {
+            float *p = base + (long long)wg * (KD / 4) * s.V + v;
+#pragma unroll
+            for (int i = 0; i < KD / 4; ++i)
+                if (wg * (KD / 4) + i < s.K) p[(long long)i * s.V] = S[i];
+        }
+        __syncwarp();
+    }
+};
+
 template <class E, int KD>
-__global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_constant__ SeqArgs a) {
+__global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_constant__ SeqArgs a) {
     using Q = Seq<E, KD>;
-    constexpr int TB = Terms<E>::n, H2 = KD / 2, TERM = QK<E, KD>::term;
+    constexpr int TB = Q::TB, H4 = KD / 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
     const Shape &s = a.s;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x;
     int id = blockIdx.x;
     const int vt = id % s.VT;
     id /= s.VT;
     const int h = id % s.Hv, b = id / s.Hv;
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) tc::mbar_init(&bar->full[i], 1);
-        tc::mbar_init(&bar->m1, 1);
-        tc::mbar_init(&bar->m2, 1);
-        tc::mbar_init(&bar->m4, 1);
-        bar->abort_flag = 0;
-        tc::fence_mbar_init();
-    }
-    if (warp == 0) {
-        tc::tmem_alloc(&bar->tmem_slot, 512);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
+    seq_setup(bar);
     const uint32_t tmem = bar->tmem_slot;
+    const Lane<KD> L(s, tmem, b, h, vt);
+    volatile int *ab = &bar->abort_flag;
+    constexpr Steps rows = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};   // K-major q or k: K over the dims
+    constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};       // MN-major k: K over the tokens
+    constexpr Steps mat = {TILE >> 4, 2, 0};                           // K-major T2, P
+    if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, false);
+    __syncwarp();
+    float S[H4], o[16];
+    L.load(s, a.s0 ? a.s0 + L.head * s.K * s.V : nullptr, S);
+    const E *vp = (const E *)a.v + (long long)b * s.ldv + (long long)h * s.V + L.v;
+    auto store_o = [&](int c) {
+        const int t0 = c * C + L.wg * 16;
+        E *p = (E *)a.o + L.head * s.V + L.v + t0 * L.row;
+        if (L.own)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (t0 + i < s.T) p[i * L.row] = from_f<E>(o[i]);
+        __syncwarp();
+    };
+#pragma unroll 1
+    for (int c = 0; c < s.NC; ++c) {
+        const int st = c % Q::stages, t0 = c * C + L.wg * 16;
+        const uint32_t ph = c & 1;
+        const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
+        const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + L.wg * 16;
+        E vr[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            vr[i] = L.own && t0 + i < L.len ? vp[(long long)(t0 + i) * s.B * s.ldv] : from_f<E>(0.f);
+        put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
+        wait(&bar->full[st], (c / Q::stages) & 1, a.ctrl, ab, 0x612);
+        if (hand_over()) {  // D = K S and Q S, tokens on the columns
+            products_ts<KD / 16>(tmem + COL_D, tmem + COL_S, KD / 2, NT, k_major(qk + TILE, 0), rows, TB, NT,
+                                 tc::idesc_bf16_f32(128, 64, 0, 0));
+            tc::mma_commit(&bar->m1);
+            products_ts<KD / 16>(tmem + COL_D + 64, tmem + COL_S, KD / 2, Q::NO, k_major(qk, 0), rows, TB, Q::NO,
+                                 tc::idesc_bf16_f32(128, 64, 0, 0));
+        }
+        __syncwarp();
+        if (c > 0) {  // the last chunk's output
+            wait(&bar->m3, ph ^ 1, a.ctrl, ab, 0x616);
+            float f[16];
+            get16(L.lanes + COL_X + L.wg * 16, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] += f[i];
+            store_o(c - 1);
+        }
+        // (the products of chunk c - 1, whose stage this is, are complete)
+        if (Q::stages == 2 && tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
+        __syncwarp();
+        L.store(s, a.states ? a.states + ((long long)c * s.B * s.Hv + L.head) * s.K * s.V : nullptr, S);
+        const float last = gates[C - 1 - L.wg * 16];  // gamma of token 63
+        float f[16];
+        wait(&bar->m1, ph, a.ctrl, ab, 0x613);
+        get16(L.lanes + COL_D + L.wg * 16, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = fmaf(-gates[i], f[i], to_f(vr[i]));
+        put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
+        if (hand_over()) {  // X = T2 R
+            products_ts<4>(tmem + COL_X, tmem + COL_R, 32, NT, k_major(tp, 0), mat, NT, NT,
+                           tc::idesc_bf16_f32(128, 64, 0, 0));
+            tc::mma_commit(&bar->m2);
+        }
+        __syncwarp();
+        wait(&bar->m2, ph, a.ctrl, ab, 0x614);  // Q S came before X
+        get16(L.lanes + COL_X + L.wg * 16, f);
+        get16(L.lanes + COL_D + 64 + L.wg * 16, o);
+        float u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = f[i] * (gates[2 * C + i] * gates[C + i]);  // left U
+        put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, u);
+        if (hand_over()) {  // D = K^T (left U)
+            products_ts<4>(tmem + COL_D, tmem + COL_W, 32, NT, mn_major(qk + TILE, 0, 2 * TILE), cols, TB, NT,
+                           tc::idesc_bf16_f32(128, KD, 0, 1));
+            tc::mma_commit(&bar->m4);
+        }
+        __syncwarp();
+        if (a.deltas && L.own) {
+            float *p = a.deltas + L.head * s.V + L.v + t0 * L.row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (t0 + i < s.T) p[i * L.row] = f[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            o[i] *= s.scale * gates[i];
+            f[i] *= gates[2 * C + i];  // U
+        }
+        put_terms<8, Q::NO>(L.lanes + COL_R + L.wg * 8, 32, f);
+        if (hand_over()) {  // P U
+            products_ts<4>(tmem + COL_X, tmem + COL_R, 32, Q::NO, k_major(tp + NT * TILE, 0), mat, Q::NO, Q::NO,
+                           tc::idesc_bf16_f32(128, 64, 0, 0));
+            tc::mma_commit(&bar->m3);
+        }
+        __syncwarp();
+        wait(&bar->m4, ph, a.ctrl, ab, 0x615);
+#pragma unroll
+        for (int i0 = 0; i0 < H4; i0 += 16) {
+            get16(L.lanes + COL_D + L.wg * H4 + i0, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
+        }
+        if (Q::stages == 1) {
+            wait(&bar->m3, ph, a.ctrl, ab, 0x617);
+            if (tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
+            __syncwarp();
+        }
+    }
+    if (s.NC > 0) {
+        wait(&bar->m3, (s.NC - 1) & 1, a.ctrl, ab, 0x618);
+        float f[16];
+        get16(L.lanes + COL_X + L.wg * 16, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] += f[i];
+        store_o(s.NC - 1);
+    }
+    L.store(s, a.sT + L.head * s.K * s.V, S);
+    if (tid == 32) seq_drain<E, KD>(bar, s.NC);
+    seq_finish(bar);
+}
+
+// The adjoint, chunks in reverse, the same layout (dS^T in registers):
+//   K dS and P^T dO  ->  dU  ->  dV = T2^T (beta dU)  ->  dS += scale Q^T gamma dO - K^T gamma dV.
+// P^T dO of the next chunk runs beside the last product of this one.
+template <class E, int KD>
+__global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_constant__ SeqArgs a) {
+    using Q = Seq<E, KD>;
+    constexpr int TB = Q::TB, H4 = KD / 4;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
+    const Shape &s = a.s;
+    const int tid = threadIdx.x;
+    int id = blockIdx.x;
+    const int vt = id % s.VT;
+    id /= s.VT;
+    const int h = id % s.Hv, b = id / s.Hv;
+    seq_setup(bar);
+    const uint32_t tmem = bar->tmem_slot;
+    const Lane<KD> L(s, tmem, b, h, vt);
+    volatile int *ab = &bar->abort_flag;
+    constexpr Steps rows = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};
+    constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};
+    constexpr Steps mat = {TILE >> 4, 2048 >> 4, 0};                   // MN-major T2, P: transposed
     if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, true);
     __syncwarp();
-    {
-        const int wg = tid >> 7, lane = tid & 127, v = vt * LANES + lane;
-        const bool own = v < s.V;
-        const int len = length_of(s, b);
-        const uint32_t lanes = tmem + ((uint32_t)(lane & 96) << 16);
-        const long long head = (long long)b * s.Hv + h;
-        const long long row = (long long)s.B * s.Hv * s.V;
-        volatile int *ab = &bar->abort_flag;
-        float S[H2];
+    float S[H4];
+    E d[16];
+    L.load(s, a.s0 ? a.s0 + L.head * s.K * s.V : nullptr, S);
+    const E *dop = (const E *)a.v + L.head * s.V + L.v;
+    auto load_do = [&](int c) {
+        const int t0 = c * C + L.wg * 16;
 #pragma unroll
-        for (int i = 0; i < H2; ++i) {
-            const int k = wg * H2 + i;
-            S[i] = a.s0 && own && k < s.K ? a.s0[(head * s.K + k) * s.V + v] : 0.f;
+        for (int i = 0; i < 16; ++i) d[i] = a.v && L.own && t0 + i < L.len ? dop[(t0 + i) * L.row] : from_f<E>(0.f);
+    };
+    auto product_pdo = [&](int st) {  // X = P^T dO (one thread)
+        const uint32_t tp = tc::smem_u32(smem + st * Q::stage) + QK<E, KD>::bytes;
+        products_ts<4>(tmem + COL_X, tmem + COL_R, 32, TB, mn_major(tp + NT * TILE, 0, TILE), mat, NT, NT,
+                       tc::idesc_bf16_f32(128, 64, 0, 1));
+    };
+    auto put_do = [&]() {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = to_f(d[i]);
+        put_terms<8, TB>(L.lanes + COL_R + L.wg * 8, 32, x);
+    };
+    if (s.NC > 0) load_do(s.NC - 1);
+#pragma unroll 1
+    for (int n = 0; n < s.NC; ++n) {
+        const int c = s.NC - 1 - n, st = n % Q::stages, t0 = c * C + L.wg * 16;
+        const uint32_t ph = n & 1;
+        const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
+        const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + L.wg * 16;
+        const bool early = Q::stages == 2 && n > 0;  // P^T dO was issued a chunk ago
+        if (Q::stages == 2 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
+        __syncwarp();
+        put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
+        if (!early) put_do();
+        wait(&bar->full[st], (n / Q::stages) & 1, a.ctrl, ab, 0x622);
+        if (hand_over()) {  // D = K dS
+            if (!early) product_pdo(st);
+            products_ts<KD / 16>(tmem + COL_D, tmem + COL_S, KD / 2, NT, k_major(qk + TILE, 0), rows, TB, NT,
+                                 tc::idesc_bf16_f32(128, 64, 0, 0));
+            tc::mma_commit(&bar->m1);
         }
-        for (int n = 0; n < s.NC; ++n) {
-            const int c = s.NC - 1 - n, st = n % Q::stages;
-            const uint32_t ph = n & 1;
-            if (Q::stages == 2 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
-            __syncwarp();
-            const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
-            const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + wg * 32;
-            float f[32], d[32];
+        __syncwarp();
+        L.store(s, a.states + ((long long)c * s.B * s.Hv + L.head) * s.K * s.V, S);
+        const float last = gates[C - 1 - L.wg * 16];
+        float f[16], e[16];
+        wait(&bar->m1, ph, a.ctrl, ab, 0x623);
+        get16(L.lanes + COL_D + L.wg * 16, f);
+        get16(L.lanes + COL_X + L.wg * 16, e);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int t = c * C + wg * 32 + i;
-                d[i] = a.v && own && t < len ? to_f(((const E *)a.v)[t * row + head * s.V + v]) : 0.f;
+        for (int i = 0; i < 16; ++i) f[i] = gates[2 * C + i] * fmaf(gates[C + i], f[i], e[i]);  // beta dU
+        put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
+        if (hand_over()) {  // dV = T2^T (beta dU)
+            products_ts<4>(tmem + COL_X, tmem + COL_R, 32, NT, mn_major(tp, 0, TILE), mat, NT, NT,
+                           tc::idesc_bf16_f32(128, 64, 0, 1));
+            tc::mma_commit(&bar->m2);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = s.scale * gates[i] * to_f(d[i]);
+        put_terms<8, NT>(L.lanes + COL_S + L.wg * 8, 32, e);
+        if (c > 0) load_do(c - 1);
+        wait(&bar->m2, ph, a.ctrl, ab, 0x624);
+        get16(L.lanes + COL_X + L.wg * 16, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = -gates[i] * f[i];
+        put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, e);
+        if (Q::stages == 2 && c > 0) put_do();
+        if (hand_over()) {  // D = scale Q^T gamma dO - K^T gamma dV
+            products_ts<4>(tmem + COL_D, tmem + COL_S, 32, NT, mn_major(qk, 0, 2 * TILE), cols, TB, NT,
+                           tc::idesc_bf16_f32(128, KD, 0, 1));
+            products_ts<4>(tmem + COL_D, tmem + COL_W, 32, NT, mn_major(qk + TILE, 0, 2 * TILE), cols, TB, NT,
+                           tc::idesc_bf16_f32(128, KD, 0, 1), 1);
+            tc::mma_commit(&bar->m4);
+            if (Q::stages == 2 && c > 0) {
+                tc::mbar_wait(&bar->full[st ^ 1], ((n + 1) / Q::stages) & 1, a.ctrl, ab, 0x626);
+                product_pdo(st ^ 1);
             }
-            put_terms<H2 / 2, NT>(lanes + COL_S + wg * (H2 / 2), KD / 2, S);
-            put_terms<16, TB>(lanes + COL_R + wg * 16, 32, d);
-            tc::tmem_st_wait();
-            wait(&bar->full[st], (n / Q::stages) & 1, a.ctrl, ab, 0x622);
-            tc::tc_fence_before();
-            group_sync(1, SEQ_THREADS);
-            if (tid == 0) {
-                tc::tc_fence_after();
-                uint32_t acc = 0;
+        }
+        __syncwarp();
+        if (L.own) {
+            float *p = a.deltas + L.head * s.V + L.v + t0 * L.row;
+            E *pv = (E *)a.o + L.head * s.V + L.v + t0 * L.row;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)  // D[0..63] = K dS
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) {
-                        if (t + u >= NT) continue;
-#pragma unroll
-                        for (int ks = 0; ks < KD / 16; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_S + t * (KD / 2) + 8 * ks,
-                                            k_major(qk + u * TERM + (ks >> 2) * 2 * TILE + TILE, ks & 3),
-                                            tc::idesc_bf16_f32(128, 64, 0, 0), acc);
-                            acc = 1;
-                        }
-                    }
-                acc = 0;
-#pragma unroll
-                for (int t = 0; t < TB; ++t)  // D[64..127] = P^T dO
-#pragma unroll
-                    for (int u = 0; u < NT - t; ++u)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_D + 64, tmem + COL_R + t * 32 + 8 * ks,
-                                            mn_major(tp + (NT + u) * TILE, ks, TILE),
-                                            tc::idesc_bf16_f32(128, 64, 0, 1), acc);
-                            acc = 1;
-                        }
-                tc::mma_commit(&bar->m1);
-            }
-            __syncwarp();
-            if (own) {
-                float *p = a.states + (((long long)c * s.B * s.Hv + head) * s.K) * s.V + v;
-#pragma unroll
-                for (int i = 0; i < H2; ++i) {
-                    const int k = wg * H2 + i;
-                    if (k < s.K) p[(long long)k * s.V] = S[i];
+            for (int i = 0; i < 16; ++i)
+                if (t0 + i < s.T) {
+                    p[i * L.row] = f[i];
+                    pv[i * L.row] = from_f<E>(f[i]);
                 }
-            }
-            __syncwarp();
-            const float last = gates[(1 - wg) * 32 + 31];
-            wait(&bar->m1, ph, a.ctrl, ab, 0x623);
-            get32(lanes + COL_D + wg * 32, f);
-            {
-                float e[32];
-                get32(lanes + COL_D + 64 + wg * 32, e);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = gates[2 * C + i] * fmaf(gates[C + i], f[i], e[i]);  // beta dU
-            }
-            put_terms<16, NT>(lanes + COL_R + wg * 16, 32, f);
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            group_sync(1, SEQ_THREADS);
-            if (tid == 0) {  // dV = T2^T (beta dU)
-                tc::tc_fence_after();
-                uint32_t acc = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < NT - t; ++u)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_X, tmem + COL_R + t * 32 + 8 * ks,
-                                            mn_major(tp + u * TILE, ks, TILE), tc::idesc_bf16_f32(128, 64, 0, 1), acc);
-                            acc = 1;
-                        }
-                tc::mma_commit(&bar->m2);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) d[i] *= s.scale * gates[i];
-            put_terms<16, NT>(lanes + COL_U + wg * 16, 32, d);
-            wait(&bar->m2, ph, a.ctrl, ab, 0x624);
-            get32(lanes + COL_X + wg * 32, f);
-            if (own) {
-                float *p = a.deltas + head * s.V + v;
-                E *pv = (E *)a.o + head * s.V + v;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int t = c * C + wg * 32 + i;
-                    if (t < s.T) {
-                        p[t * row] = f[i];
-                        pv[t * row] = from_f<E>(f[i]);
-                    }
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= -gates[i];
-            put_terms<16, NT>(lanes + COL_W + wg * 16, 32, f);
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            group_sync(1, SEQ_THREADS);
-            if (tid == 0) {  // D = scale Q^T gamma dO - K^T gamma dV
-                tc::tc_fence_after();
-                uint32_t acc = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) {
-                        if (t + u >= NT) continue;
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_W + t * 32 + 8 * ks,
-                                            mn_major(qk + u * TERM + TILE, ks, 2 * TILE),
-                                            tc::idesc_bf16_f32(128, KD, 0, 1), acc);
-                            acc = 1;
-                            tc::mma_bf16_ts(tmem + COL_D, tmem + COL_U + t * 32 + 8 * ks,
-                                            mn_major(qk + u * TERM, ks, 2 * TILE),
-                                            tc::idesc_bf16_f32(128, KD, 0, 1), 1);
-                        }
-                    }
-                tc::mma_commit(&bar->m4);
-            }
-            __syncwarp();
-            wait(&bar->m4, ph, a.ctrl, ab, 0x625);
-            if (Q::stages == 1 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
-            __syncwarp();
-#pragma unroll
-            for (int i0 = 0; i0 < H2; i0 += 32) {
-                get32(lanes + COL_D + wg * H2 + i0, f);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
-            }
         }
-        if (own && a.sT) {
+        __syncwarp();
+        wait(&bar->m4, ph, a.ctrl, ab, 0x625);
 #pragma unroll
-            for (int i = 0; i < H2; ++i) {
-                const int k = wg * H2 + i;
-                if (k < s.K) a.sT[(head * s.K + k) * s.V + v] = S[i];
-            }
+        for (int i0 = 0; i0 < H4; i0 += 16) {
+            get16(L.lanes + COL_D + L.wg * H4 + i0, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
         }
+        if (Q::stages == 1 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
+        __syncwarp();
     }
+    L.store(s, a.sT ? a.sT + L.head * s.K * s.V : nullptr, S);
     if (tid == 32) seq_drain<E, KD>(bar, s.NC);
-    tc::tc_fence_before();
-    __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    seq_finish(bar);
 }
 
 // ---------------------------------------------------------------- gradients
-// Block (c, b, hk), 256 threads: dq, dk of the chunk, and dg, dbeta of every
+// Block (c, b, hk), 512 threads: dq, dk of the chunk, and dg, dbeta of every
 // value head of the group, from the saved S0 and X and seq_bwd's dS1 and dV.
 // Rows are stacked so that every product has the 128 rows the tensor core
 // takes: [dO; dV] with X gives Y over Z, with S0 gives F over G; X sits in the
 // lower rows for E; the last product is [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K].
+// V is contracted 64 columns a pass, S0 and dS1 in turn in one buffer.
 // dg's double sum needs no matrix: sum_{r >= i > j} M_rj is the sum over
 // r >= i of (row sum - column sum), for the lower triangle M.
-constexpr int GRAD_THREADS = 256;
+constexpr int GRAD_THREADS = 512;
 constexpr uint32_t COL_QK = 0, COL_YZ = 64, COL_FG = 128, COL_E = 256, COL_OUT = 384;
 
 template <class E, int KD> struct GradSmem {
@@ -899,29 +883,37 @@ struct GradArgs {
     Ctrl *ctrl;
 };
 
-// Sum of f[j] over the 32 lanes for every j; lane j returns the j-th sum.
-__device__ __forceinline__ float transpose_sum(float (&f)[32]) {
+// Sums over the warp's 32 lanes of f[0..15]: lane 2 j (and 2 j + 1) returns the j-th.
+__device__ __forceinline__ float transpose_sum(float (&f)[16]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const bool up = lane & o;
+    for (int o = 8; o > 0; o >>= 1) {
+        const bool up = lane & (2 * o);
 #pragma unroll
         for (int j = 0; j < o; ++j) {
             const float keep = up ? f[j + o] : f[j], give = up ? f[j] : f[j + o];
-            f[j] = keep + __shfl_xor_sync(~0u, give, o);
+            f[j] = keep + __shfl_xor_sync(~0u, give, 2 * o);
         }
     }
-    return f[0];
+    return f[0] + __shfl_xor_sync(~0u, f[0], 1);
+}
+
+// n terms of eight floats into a tile row's 16-byte group.
+template <int n> __device__ __forceinline__ void put8(uint8_t *tile, int term, uint32_t off, const float (&f)[8]) {
+    uint4 o[n];
+    split8<n>(f, o);
+#pragma unroll
+    for (int k = 0; k < n; ++k) *(uint4 *)(tile + k * term + off) = o[k];
 }
 
 template <class E, int KD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_constant__ GradArgs a) {
     using L = GradSmem<E, KD>;
-    constexpr int TB = Terms<E>::n, TERM = QK<E, KD>::term, H2 = KD / 2, SI = KD / 32;
+    constexpr int TB = Terms<E>::n, TERM = QK<E, KD>::term, H4 = KD / 4, SI = KD / 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ double bs[C];
-    __shared__ float betas[C], colp[4][C], rowp[2][2 * C], rp[2][2 * C], ep[2][C], dots[8];
+    __shared__ float betas[C], colp[4][C], rowp[4][2 * C], rp[4][2 * C], ep[4][C], dots[16];
     __shared__ uint64_t loaded, m1, m2, m3;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
@@ -955,124 +947,81 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
         tc::mbar_arrive_expect_tx(&loaded, QK<E, KD>::bytes);
         bulk_load(smem, a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes, QK<E, KD>::bytes, &loaded);
     }
-    wait(&loaded, 0, a.ctrl, ab, 0x631);
-    float acc[H2];  // this thread's half row of dq (rows 0..63) or dk, but for the last product
+    __syncwarp();
+    const int row = tid >> 3, gr = tid & 7;  // loads: eight threads a row, eight columns each
+    const int t_row = c * C + row;
+    float acc[H4];  // this thread's quarter row of dq (rows 0..63) or dk, but for the last product
 #pragma unroll
-    for (int i = 0; i < H2; ++i) acc[i] = 0.f;
+    for (int i = 0; i < H4; ++i) acc[i] = 0.f;
     uint32_t p12 = 0;
     const int passes = (s.V + 63) / 64;
+    float ro[8], rv[8], rx[8], rs[SI][8], rd[SI][8];  // dO, dV, X, S0, dS1 of the pass ahead
+    auto load_pass = [&](int h, int v0) {
+        const long long head = (long long)b * s.Hv + h;
+        const long long at = ((long long)t_row * s.B * s.Hv + head) * s.V + v0 + gr * 8;
+        const long long sb = ((long long)c * s.B * s.Hv + head) * s.K * s.V + v0 + gr * 8;
+        const bool in = v0 + gr * 8 < s.V;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ro[i] = rv[i] = rx[i] = 0.f;
+        if (in && t_row < len) {
+            if (a.dout) load8<E>((const E *)a.dout + at, ro);
+            load8<float>(a.dvf + at, rv);
+            load8<float>(a.deltas + at, rx);
+        }
+#pragma unroll
+        for (int n = 0; n < SI; ++n) {
+            const int k = n * 64 + row;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rs[n][i] = rd[n][i] = 0.f;
+            if (in && k < s.K) {
+                load8<float>(a.states + sb + (long long)k * s.V, rs[n]);
+                load8<float>(a.dstates + sb + (long long)k * s.V, rd[n]);
+            }
+        }
+    };
+    constexpr Steps qk_rows = {TERM >> 4, 2, 2 * TILE >> 4}, a_rows = {2 * TILE >> 4, 2, 0}, x_rows = {TILE >> 4, 2, 0},
+                    s_rows = {KD * 128 >> 4, 2, 0}, m_rows = {4 * TILE >> 4, 2, 2 * TILE >> 4},
+                    qk_cols = {TERM >> 4, 2048 >> 4, 4 * 2048 >> 4};
+    wait(&loaded, 0, a.ctrl, ab, 0x631);
+#pragma unroll 1
     for (int m = 0; m < s.group; ++m) {
         const int h = hk * s.group + m;
-        const long long head = (long long)b * s.Hv + h;
-        const float *s0 = a.states + ((long long)c * s.B * s.Hv + head) * s.K * s.V;
-        const float *ds = a.dstates + ((long long)c * s.B * s.Hv + head) * s.K * s.V;
+        load_pass(h, 0);
         if (m > 0) wait(&m3, (m - 1) & 1, a.ctrl, ab, 0x632);  // the tiles are free
         __syncthreads();
         if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, bs, betas);
         float dot = 0.f;
+#pragma unroll 1
         for (int p = 0; p < passes; ++p) {
-            const int v0 = p * 64;
-            // [dO; dV]: 128 rows x 8 groups of 8 columns
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7, t = c * C + (row & 63);
-                float f[8] = {};
-                if (t < len && v0 + gr * 8 < s.V) {
-                    const long long at = ((long long)t * s.B * s.Hv + head) * s.V + v0 + gr * 8;
-                    if (row >= 64) load8<float>(a.dvf + at, f);
-                    else if (a.dout) load8<E>((const E *)a.dout + at, f);
-                }
-                uint4 o[NT];
-                split8<NT>(f, o);
-#pragma unroll
-                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::a + k * 2 * TILE + swz(row, gr * 16)) = o[k];
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7, t = c * C + row;
-                float f[8] = {};
-                if (t < len && v0 + gr * 8 < s.V)
-                    load8<float>(a.deltas + ((long long)t * s.B * s.Hv + head) * s.V + v0 + gr * 8, f);
-                uint4 o[NT];
-                split8<NT>(f, o);
-#pragma unroll
-                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::x + k * TILE + swz(row, gr * 16)) = o[k];
-            }
-            float sv[SI][8], dv[SI][8];
+            put8<NT>(smem + L::a, 2 * TILE, swz(row, gr * 16), ro);
+            put8<NT>(smem + L::a, 2 * TILE, swz(C + row, gr * 16), rv);
+            put8<NT>(smem + L::x, TILE, swz(row, gr * 16), rx);
 #pragma unroll
             for (int n = 0; n < SI; ++n) {
-                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7;
+                put8<NT>(smem + L::st, KD * 128, swz(n * 64 + row, gr * 16), rs[n]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sv[n][k] = dv[n][k] = 0.f;
-                if (row < s.K && v0 + gr * 8 < s.V) {
-                    load8<float>(s0 + (long long)row * s.V + v0 + gr * 8, sv[n]);
-                    load8<float>(ds + (long long)row * s.V + v0 + gr * 8, dv[n]);
-                }
-                uint4 o[NT];
-                split8<NT>(sv[n], o);
-#pragma unroll
-                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::st + k * KD * 128 + swz(row, gr * 16)) = o[k];
+                for (int i = 0; i < 8; ++i) dot = fmaf(rs[n][i], rd[n][i], dot);
             }
             tc::fence_proxy_async_smem();
-            tc::tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tc::tc_fence_after();
-                uint32_t cc = 0;
-                if (m == 0 && p == 0) {  // [q; k] k^T, once
-#pragma unroll
-                    for (int t = 0; t < TB; ++t)
-#pragma unroll
-                        for (int u = 0; u < TB; ++u) {
-                            if (t + u >= NT) continue;
-                            for (int ks = 0; ks < KD / 16; ++ks) {
-                                const uint32_t chunk = (ks >> 2) * 2 * TILE;
-                                tc::mma_bf16(tmem + COL_QK, k_major(qk + t * TERM + chunk, ks & 3),
-                                             k_major(qk + u * TERM + chunk + TILE, ks & 3),
-                                             tc::idesc_bf16_f32(128, 64, 0, 0), cc);
-                                cc = 1;
-                            }
-                        }
-                }
-                cc = p > 0;
-                for (int t = 0; t < NT; ++t)
-                    for (int u = 0; u < NT - t; ++u)
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16(tmem + COL_YZ, k_major(sa + t * 2 * TILE, ks), k_major(sx + u * TILE, ks),
-                                         tc::idesc_bf16_f32(128, 64, 0, 0), cc);
-                            tc::mma_bf16(tmem + COL_FG, k_major(sa + t * 2 * TILE, ks), k_major(ss + u * KD * 128, ks),
-                                         tc::idesc_bf16_f32(128, KD, 0, 0), cc);
-                            cc = 1;
-                        }
+            if (hand_over()) {
+                if (m == 0 && p == 0)  // [q; k] k^T, once
+                    products_ss<KD / 16>(tmem + COL_QK, k_major(qk, 0), qk_rows, TB, k_major(qk + TILE, 0), qk_rows, TB, NT,
+                                         tc::idesc_bf16_f32(128, 64, 0, 0));
+                products_ss<4>(tmem + COL_FG, k_major(sa, 0), a_rows, NT, k_major(ss, 0), s_rows, NT, NT,
+                               tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
                 tc::mma_commit(&m1);
+                products_ss<4>(tmem + COL_YZ, k_major(sa, 0), a_rows, NT, k_major(sx, 0), x_rows, NT, NT,
+                               tc::idesc_bf16_f32(128, 64, 0, 0), p > 0);
             }
             __syncwarp();
+            wait(&m1, p12, a.ctrl, ab, 0x633);  // S0's buffer is free
 #pragma unroll
-            for (int n = 0; n < SI; ++n)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) dot = fmaf(sv[n][k], dv[n][k], dot);
-            wait(&m1, p12, a.ctrl, ab, 0x633);
-#pragma unroll
-            for (int n = 0; n < SI; ++n) {
-                const int i = n * GRAD_THREADS + tid, row = i >> 3, gr = i & 7;
-                uint4 o[NT];
-                split8<NT>(dv[n], o);
-#pragma unroll
-                for (int k = 0; k < NT; ++k) *(uint4 *)(smem + L::st + k * KD * 128 + swz(row, gr * 16)) = o[k];
-            }
+            for (int n = 0; n < SI; ++n) put8<NT>(smem + L::st, KD * 128, swz(n * 64 + row, gr * 16), rd[n]);
+            if (p + 1 < passes) load_pass(h, (p + 1) * 64);
             tc::fence_proxy_async_smem();
-            tc::tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {  // rows 64..127: E = X dS1^T (the rows above X are not used)
-                tc::tc_fence_after();
-                uint32_t cc = p > 0;
-                for (int t = 0; t < NT; ++t)
-                    for (int u = 0; u < NT - t; ++u)
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc::mma_bf16(tmem + COL_E, k_major(sx + t * TILE - TILE, ks), k_major(ss + u * KD * 128, ks),
-                                         tc::idesc_bf16_f32(128, KD, 0, 0), cc);
-                            cc = 1;
-                        }
+            if (hand_over()) {  // rows 64..127: E = X dS1^T (the rows above X are not used)
+                products_ss<4>(tmem + COL_E, k_major(sx - TILE, 0), x_rows, NT, k_major(ss, 0), s_rows, NT, NT,
+                               tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
                 tc::mma_commit(&m2);
             }
             __syncwarp();
@@ -1081,40 +1030,40 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
         }
         // ---- the triangle: weights, their row and column sums, the last product's left operand
         {
-            float y[32], kq[32], w[32];
-            get32(lanes + COL_QK + wg * 32, kq);
-            get32(lanes + COL_YZ + wg * 32, y);
+            float y[16], kq[16];
+            get16(lanes + COL_QK + wg * 16, kq);
+            get16(lanes + COL_YZ + wg * 16, y);
             const double br = bs[r];
             float rowsum = 0.f;
             if (isq) {  // rows 0..63 have no product with Q
 #pragma unroll
                 for (int k = 0; k < NT; ++k)
 #pragma unroll
-                    for (int gr = 0; gr < 4; ++gr)
-                        *(uint4 *)(smem + L::a + k * 4 * TILE + swz(r, (wg * 4 + gr) * 16)) = make_uint4(0, 0, 0, 0);
+                    for (int g2 = 0; g2 < 2; ++g2)
+                        *(uint4 *)(smem + L::a + k * 4 * TILE + swz(r, (wg * 2 + g2) * 16)) = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 8) {
+            for (int j0 = 0; j0 < 16; j0 += 8) {
                 float e[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int j = wg * 32 + j0 + i;
+                    const int j = wg * 16 + j0 + i;
                     const bool in = isq ? j <= r : j < r;
                     const float z = in ? decay(br, bs[j]) * (isq ? s.scale * y[j0 + i] : -y[j0 + i]) : 0.f;
-                    w[j0 + i] = z * kq[j0 + i];
+                    kq[j0 + i] *= z;  // w_rj
                     e[i] = z * betas[j];
-                    rowsum = fmaf(betas[j], w[j0 + i], rowsum);
+                    rowsum = fmaf(betas[j], kq[j0 + i], rowsum);
                 }
                 uint4 o[NT];
                 split8<NT>(e, o);
 #pragma unroll
                 for (int k = 0; k < NT; ++k) {
                     uint8_t *base = smem + L::a + k * 4 * TILE;  // [cols 0..63: Q][cols 64..127: K], 128 rows each
-                    const uint32_t *q4 = (const uint32_t *)&o[k];
-                    if (isq) *(uint4 *)(base + 2 * TILE + swz(r, (wg * 32 + j0) * 2)) = o[k];
+                    const uint32_t q4[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+                    if (isq) *(uint4 *)(base + 2 * TILE + swz(r, (wg * 16 + j0) * 2)) = o[k];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int j = wg * 32 + j0 + i;
+                        const int j = wg * 16 + j0 + i;
                         const uint16_t hv = (uint16_t)(q4[i >> 1] >> (16 * (i & 1)));
                         if (isq) {
                             *(uint16_t *)(base + swz(64 + j, r * 2)) = hv;
@@ -1127,21 +1076,21 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
             }
             rowp[wg][r128] = rowsum;
             __syncwarp();
-            const float cs = transpose_sum(w);
-            colp[warp & 3][wg * 32 + lane] = cs;
+            const float cs = transpose_sum(kq);
+            if (!(lane & 1)) colp[warp & 3][wg * 16 + (lane >> 1)] = cs;
         }
-        // ---- F | G and E: half a row of K a thread
+        // ---- F | G and E: a quarter row of K a thread
         {
-            const float gam = decay(bs[r], 0.0), left = decay(bs[C - 1], bs[r]), be = betas[r];
+            const float gam = decay(bs[r], 0.0), lb = decay(bs[C - 1], bs[r]) * betas[r];
             float dotf = 0.f, dote = 0.f;
 #pragma unroll
-            for (int i0 = 0; i0 < H2; i0 += 32) {
-                float f[32], e[32];
-                get32(lanes + COL_FG + wg * H2 + i0, f);
-                get32(lanes + COL_E + wg * H2 + i0, e);
+            for (int i0 = 0; i0 < H4; i0 += 16) {
+                float f[16], e[16];
+                get16(lanes + COL_FG + wg * H4 + i0, f);
+                get16(lanes + COL_E + wg * H4 + i0, e);
 #pragma unroll
-                for (int gr = 0; gr < 4; ++gr) {
-                    const int col = wg * H2 + i0 + gr * 8;
+                for (int g2 = 0; g2 < 2; ++g2) {
+                    const int col = wg * H4 + i0 + g2 * 8;
                     float x[8] = {};
 #pragma unroll
                     for (int t = 0; t < TB; ++t) {
@@ -1152,56 +1101,50 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int n = gr * 8 + i;
+                        const int n = g2 * 8 + i;
                         dotf = fmaf(x[i], f[n], dotf);
                         if (isq) {
                             acc[i0 + n] = fmaf(s.scale * gam, f[n], acc[i0 + n]);
                         } else {
                             dote = fmaf(x[i], e[n], dote);
-                            acc[i0 + n] += left * be * e[n] - gam * f[n];
+                            acc[i0 + n] += lb * e[n] - gam * f[n];
                         }
                     }
                 }
             }
             rp[wg][r128] = dotf;
             if (!isq) ep[wg][r] = dote;
+            __syncwarp();
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
             if (lane == 0) dots[warp] = dot;
         }
         tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K]
-            tc::tc_fence_after();
-            uint32_t cc = m > 0;
-            for (int t = 0; t < NT; ++t)
-                for (int u = 0; u < TB && u < NT - t; ++u)
-                    for (int ks = 0; ks < 8; ++ks) {
-                        tc::mma_bf16(tmem + COL_OUT, k_major(sa + t * 4 * TILE + (ks >> 2) * 2 * TILE, ks & 3),
-                                     mn_major(qk + u * TERM, ks, 2 * TILE), tc::idesc_bf16_f32(128, KD, 0, 1), cc);
-                        cc = 1;
-                    }
+        if (hand_over()) {  // [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K]
+            products_ss<8>(tmem + COL_OUT, k_major(sa, 0), m_rows, NT, mn_major(qk, 0, 2 * TILE), qk_cols, TB, NT,
+                           tc::idesc_bf16_f32(128, KD, 0, 1), m > 0);
             tc::mma_commit(&m3);
         }
         __syncwarp();
         if (warp == 1) {  // dg and dbeta, two tokens a lane
-            double d[2], e[2];
+            auto sum4 = [&](const float *x, int stride, int j) {
+                return ((double)x[j] + x[stride + j]) + ((double)x[2 * stride + j] + x[3 * stride + j]);
+            };
+            double d[2], e[2], all = 0;
             float db[2];
-            double all = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) all += dots[i];
+            for (int i = 0; i < 16; ++i) all += dots[i];
             all *= decay(bs[C - 1], 0.0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 2 * lane + i;
-                const float col = (colp[0][j] + colp[1][j]) + (colp[2][j] + colp[3][j]);
-                const double row = ((double)rowp[0][j] + rowp[1][j]) + ((double)rowp[0][C + j] + rowp[1][C + j]);
-                const float gam = decay(bs[j], 0.0), left = decay(bs[C - 1], bs[j]), ke = ep[0][j] + ep[1][j];
-                d[i] = row - (double)betas[j] * col +
-                       (double)gam * ((double)s.scale * (rp[0][j] + rp[1][j]) - (rp[0][C + j] + rp[1][C + j]));
-                e[i] = (double)left * betas[j] * ke;
-                db[i] = col + left * ke;
+                const double col = sum4(&colp[0][0], C, j);
+                const double rows = sum4(&rowp[0][0], 2 * C, j) + sum4(&rowp[0][0], 2 * C, C + j);
+                const double ke = sum4(&ep[0][0], C, j);
+                const double gam = decay(bs[j], 0.0), left = decay(bs[C - 1], bs[j]);
+                d[i] = rows - betas[j] * col + gam * (s.scale * sum4(&rp[0][0], 2 * C, j) - sum4(&rp[0][0], 2 * C, C + j));
+                e[i] = left * betas[j] * ke;
+                db[i] = (float)(col + left * ke);
             }
             // suffix sums of d, prefix sums (exclusive) of e
             double sd = d[0] + d[1], se = e[0] + e[1];
@@ -1227,23 +1170,23 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     }
     wait(&m3, (s.group - 1) & 1, a.ctrl, ab, 0x635);
     const int t = c * C + r;
-    E *out = (E *)(isq ? a.dq : a.dk) + (((long long)t * s.B + b) * s.Hk + hk) * s.K + wg * H2;
+    E *out = (E *)(isq ? a.dq : a.dk) + (((long long)t * s.B + b) * s.Hk + hk) * s.K + wg * H4;
 #pragma unroll
-    for (int i0 = 0; i0 < H2; i0 += 32) {
-        float f[32];
-        get32(lanes + COL_OUT + wg * H2 + i0, f);
+    for (int i0 = 0; i0 < H4; i0 += 16) {
+        float f[16];
+        get16(lanes + COL_OUT + wg * H4 + i0, f);
         if (t < s.T)
 #pragma unroll
-            for (int gr = 0; gr < 4; ++gr) {
-                if (wg * H2 + i0 + gr * 8 >= s.K) continue;
+            for (int g2 = 0; g2 < 2; ++g2) {
+                if (wg * H4 + i0 + g2 * 8 >= s.K) continue;
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = acc[i0 + gr * 8 + i] + f[gr * 8 + i];
+                for (int i = 0; i < 8; ++i) x[i] = acc[i0 + g2 * 8 + i] + f[g2 * 8 + i];
                 if constexpr (sizeof(E) == 4) {
-                    *(float4 *)(out + i0 + gr * 8) = make_float4(x[0], x[1], x[2], x[3]);
-                    *(float4 *)(out + i0 + gr * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                    *(float4 *)(out + i0 + g2 * 8) = make_float4(x[0], x[1], x[2], x[3]);
+                    *(float4 *)(out + i0 + g2 * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
                 } else {
-                    *(uint4 *)(out + i0 + gr * 8) = f32x8_to<E>(x);
+                    *(uint4 *)(out + i0 + g2 * 8) = f32x8_to<E>(x);
                 }
             }
         __syncwarp();
