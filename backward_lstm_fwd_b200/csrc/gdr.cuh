@@ -97,6 +97,18 @@ template <int n> __device__ __forceinline__ void split2(float a, float b, uint32
 // byte offset of (row, byte column) in a 128-byte swizzled tile
 __device__ __forceinline__ uint32_t swz(int row, int cb) { return row * 128 + (cb ^ ((row & 7) << 4)); }
 
+// Eight consecutive elements, raw, and their terms.
+template <class E> struct Raw8 { uint4 a; };
+template <> struct Raw8<float> { uint4 a, b; };
+template <class E> __device__ __forceinline__ Raw8<E> raw8(const E *p, bool in) {
+    Raw8<E> r = {};
+    if (in) {
+        r.a = __ldg((const uint4 *)p);
+        if constexpr (sizeof(E) == 4) r.b = __ldg((const uint4 *)p + 1);
+    }
+    return r;
+}
+
 // Eight consecutive elements as floats.
 template <class E> __device__ __forceinline__ void load8(const E *p, float (&f)[8]) { x8_to_f32<E>(__ldg((const uint4 *)p), f); }
 template <> __device__ __forceinline__ void load8<float>(const float *p, float (&f)[8]) {
@@ -111,6 +123,21 @@ template <int n> __device__ __forceinline__ void split8(const float (&f)[8], uin
     for (int i = 0; i < 4; ++i) split2<n>(f[2 * i], f[2 * i + 1], t[i]);
 #pragma unroll
     for (int k = 0; k < n; ++k) o[k] = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
+}
+
+template <class E> __device__ __forceinline__ void terms8(const Raw8<E> &r, uint4 (&o)[Terms<E>::n]) {
+    if constexpr (Terms<E>::n == 1) {
+        o[0] = r.a;
+    } else {
+        float f[8];
+        if constexpr (sizeof(E) == 4) {
+            f[0] = __uint_as_float(r.a.x); f[1] = __uint_as_float(r.a.y); f[2] = __uint_as_float(r.a.z); f[3] = __uint_as_float(r.a.w);
+            f[4] = __uint_as_float(r.b.x); f[5] = __uint_as_float(r.b.y); f[6] = __uint_as_float(r.b.z); f[7] = __uint_as_float(r.b.w);
+        } else {
+            x8_to_f32<E>(r.a, f);
+        }
+        split8<Terms<E>::n>(f, o);
+    }
 }
 
 // ------------------------------------------------------------ descriptors
@@ -151,16 +178,17 @@ __device__ __forceinline__ void put_terms(uint32_t col, int stride, const float 
 struct Steps {
     uint32_t term, step, chunk;  // 16-byte units
 };
-__device__ __forceinline__ uint32_t at_step(const Steps &x, int t, int ks) {
+__device__ __forceinline__ constexpr uint32_t at_step(const Steps &x, int t, int ks) {
     return t * x.term + (ks >> 2) * x.chunk + (ks & 3) * x.step;
 }
-template <int steps>
-__device__ __forceinline__ void products_ts(uint32_t d, uint32_t a, uint32_t a_term, int ta, uint64_t b, Steps bs, int tb,
-                                            int orders, uint32_t idesc, uint32_t acc = 0) {
-#pragma unroll 1
+template <int steps, int ta, int tb, int orders>
+__device__ __forceinline__ void products_ts(uint32_t d, uint32_t a, uint32_t a_term, uint64_t b, const Steps bs,
+                                            uint32_t idesc, uint32_t acc = 0) {
+#pragma unroll
     for (int o = orders - 1; o >= 0; --o)
-#pragma unroll 1
-        for (int t = max(0, o - tb + 1); t < ta && t <= o; ++t) {
+#pragma unroll
+        for (int t = 0; t < ta; ++t) {
+            if (t > o || o - t >= tb) continue;
 #pragma unroll
             for (int ks = 0; ks < steps; ++ks) {
                 tc::mma_bf16_ts(d, a + t * a_term + 8 * ks, b + at_step(bs, o - t, ks), idesc, acc);
@@ -168,13 +196,14 @@ __device__ __forceinline__ void products_ts(uint32_t d, uint32_t a, uint32_t a_t
             }
         }
 }
-template <int steps>
-__device__ __forceinline__ void products_ss(uint32_t d, uint64_t a, Steps as, int ta, uint64_t b, Steps bs, int tb,
-                                            int orders, uint32_t idesc, uint32_t acc = 0) {
-#pragma unroll 1
+template <int steps, int ta, int tb, int orders>
+__device__ __forceinline__ void products_ss(uint32_t d, uint64_t a, const Steps as, uint64_t b, const Steps bs,
+                                            uint32_t idesc, uint32_t acc = 0) {
+#pragma unroll
     for (int o = orders - 1; o >= 0; --o)
-#pragma unroll 1
-        for (int t = max(0, o - tb + 1); t < ta && t <= o; ++t) {
+#pragma unroll
+        for (int t = 0; t < ta; ++t) {
+            if (t > o || o - t >= tb) continue;
 #pragma unroll
             for (int ks = 0; ks < steps; ++ks) {
                 tc::mma_bf16(d, a + at_step(as, t, ks), b + at_step(bs, o - t, ks), idesc, acc);
@@ -199,13 +228,44 @@ __device__ __forceinline__ void get32(uint32_t col, float (&f)[32]) {
 }
 
 // A bounded wait of a whole warp, ordered before its tensor-memory accesses.
-// After a time-out every later wait returns at once: the block runs to its
-// end on what is there, and the status word says so.
+// The hint lets the hardware hold the warp for up to 20 us a try, so that
+// waiting warps leave the issue slots to the others.  After a time-out (2 s)
+// every later wait returns at once: the block runs to its end on what is
+// there, and the status word says so.
+__device__ __forceinline__ bool try_wait_hint(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, Ctrl *ctrl, volatile int *abort_flag, uint32_t site) {
-    tc::mbar_wait(bar, parity, ctrl, abort_flag, site);
+    if (!try_wait_hint(bar, parity)) {
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (!try_wait_hint(bar, parity) && !*abort_flag) {
+            if (tc::globaltimer_ns() - t0 > 2000000000ull) {
+                atomicCAS(&ctrl->status, 0u, 5u);
+                atomicCAS(&ctrl->fail_site, 0u, site);
+                *abort_flag = 1;
+            }
+        }
+    }
     __syncwarp();
     tc::tc_fence_after();
 }
+// One lane of a converged warp (the same one every time).  A branch on it
+// inside a warp-uniform branch keeps addresses and descriptors in uniform
+// registers: 38 cycles per N = 64 product against 51 under threadIdx.x == 0.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int warp_id() { return __shfl_sync(~0u, threadIdx.x >> 5, 0); }
 
 // Untiled bulk copy global -> this block's shared memory (16-byte aligned).
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -217,11 +277,25 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 }
 
 // ------------------------------------------------------------------- gates
-// Warp 0: the chunk's running sums b (double) and beta in shared memory, two
-// tokens a lane.  Padding (t >= len) has g = 0 and beta = 0.  g = -inf (or
-// below -1e5) counts as -1e5: its exponential is zero all the same.
+// Running sums b of the chunk's g, times log2(e), as float pairs hi + lo of a
+// double sum: b_i - b_j keeps its digits where a strong decay made both large,
+// and e^{b_i - b_j} is three additions and one exponential (2^-22 relative).
+struct Sums {
+    float2 b[C];    // (hi, lo)
+    float beta[C];
+};
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float decay(float2 i, float2 j) { return ex2((i.x - j.x) + (i.y - j.y)); }
+__device__ __forceinline__ float decay(float2 i) { return ex2(i.x + i.y); }
+
+// Warp 0, two tokens a lane.  Padding (t >= len) has g = 0 and beta = 0.  g =
+// -inf (or below -1e5) counts as -1e5: its exponential is zero all the same.
 __device__ __forceinline__ void load_gates(const Shape &s, const float *g, const float *beta, int c, int b,
-                                           int h, int len, double *bs, float *betas) {
+                                           int h, int len, Sums &out) {
     const int lane = threadIdx.x & 31;
     double v[2];
 #pragma unroll
@@ -229,8 +303,8 @@ __device__ __forceinline__ void load_gates(const Shape &s, const float *g, const
         const int j = 2 * lane + i, t = c * C + j;
         const long long at = ((long long)t * s.B + b) * s.Hv + h;
         const float gv = t < len ? g[at] : 0.f;
-        v[i] = gv < -1e5f ? -1e5 : (double)gv;
-        betas[j] = t < len ? beta[at] : 0.f;
+        v[i] = (gv < -1e5f ? -1e5 : (double)gv) * 1.4426950408889634;
+        out.beta[j] = t < len ? beta[at] : 0.f;
     }
     v[1] += v[0];
     double sum = v[1];
@@ -239,11 +313,13 @@ __device__ __forceinline__ void load_gates(const Shape &s, const float *g, const
         const double y = __shfl_up_sync(~0u, sum, o);
         if (lane >= o) sum += y;
     }
-    const double before = sum - v[1];
-    bs[2 * lane] = before + v[0];
-    bs[2 * lane + 1] = before + v[1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const double x = sum - v[1] + v[i];
+        const float hi = (float)x;
+        out.b[2 * lane + i] = make_float2(hi, (float)(x - hi));
+    }
 }
-__device__ __forceinline__ float decay(double hi, double lo) { return expf((float)(hi - lo)); }
 
 // -------------------------------------------------------------------- prep
 // Block (c, b, hk), 128 threads: the operand tiles of q and k (swizzled, in
@@ -277,13 +353,12 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     float *t2 = (float *)tiles, *pm = (float *)(tiles + PREP_MAT), *tri = (float *)(tiles + PrepSmem<E, KD>::tri);
-    __shared__ double bs[C];
-    __shared__ float betas[C];
+    __shared__ Sums sums;
     __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Shape &s = a.s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_id(), lane = tid & 31;
     int id = blockIdx.x;
     const int hk = id % s.Hk;
     id /= s.Hk;
@@ -298,29 +373,27 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
         tc::tmem_alloc(&tmem_slot, 64);
         tc::tmem_relinquish();
     }
-    // tiles: rows 0..63 q, 64..127 k; 16-byte groups of 8 dims, eight loads in flight
+    // tiles: rows 0..63 q, 64..127 k; 16-byte groups of 8 dims, eight loads in flight a thread
     char *out = a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes;
-    constexpr int U = sizeof(E) == 2 ? 8 : 4;
+    // (thread tid keeps its group gr and takes rows row0, row0 + step, ...)
+    constexpr int step = 128 / (KD / 8), U = 8;
+    const int row0 = tid / (KD / 8), gr = tid % (KD / 8);
+    const uint32_t col = (gr >> 3) * 2 * TILE, cb = (gr & 7) * 16;
 #pragma unroll 1
-    for (int i0 = tid; i0 < 128 * (KD / 8); i0 += U * 128) {
-        float f[U][8];
+    for (int i0 = row0; i0 < 128; i0 += U * step) {
+        Raw8<E> f[U];
 #pragma unroll
         for (int n = 0; n < U; ++n) {
-            const int i = i0 + n * 128, row = i / (KD / 8), gr = i % (KD / 8), t = c * C + (row & 63);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[n][j] = 0.f;
-            if (t < len && gr * 8 < s.K) {
-                const long long r = (long long)t * s.B + b;
-                load8<E>(row < 64 ? (const E *)a.q + r * s.ldq + (long long)hk * s.K + gr * 8
-                                  : (const E *)a.k + r * s.ldk + (long long)hk * s.K + gr * 8, f[n]);
-            }
+            const int row = i0 + n * step, t = c * C + (row & 63);
+            const long long r = (long long)t * s.B + b;
+            f[n] = raw8<E>((row < 64 ? (const E *)a.q + r * s.ldq : (const E *)a.k + r * s.ldk) + (long long)hk * s.K + gr * 8,
+                           t < len && gr * 8 < s.K);
         }
 #pragma unroll
         for (int n = 0; n < U; ++n) {
-            const int i = i0 + n * 128, row = i / (KD / 8), gr = i % (KD / 8);
             uint4 o[TB];
-            split8<TB>(f[n], o);
-            const uint32_t off = (gr >> 3) * 2 * TILE + swz(row, (gr & 7) * 16);
+            terms8<E>(f[n], o);
+            const uint32_t off = col + swz(i0 + n * step, cb);
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
                 *(uint4 *)(tiles + t * QK<E, KD>::term + off) = o[t];
@@ -333,15 +406,14 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
         const uint32_t base = tc::smem_u32(tiles);
         const Steps st = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};
-        products_ss<KD / 16>(tmem, k_major(base, 0), st, TB, k_major(base + TILE, 0), st, TB, NT,
-                             tc::idesc_bf16_f32(128, 64, 0, 0));
+        products_ss<KD / 16, TB, TB, NT>(tmem, k_major(base, 0), st, k_major(base + TILE, 0), st, tc::idesc_bf16_f32(128, 64, 0, 0));
         tc::mma_commit(&done);
     }
     __syncwarp();
-    if (warp == 0) load_gates(s, a.g, a.beta, c, b, hk * s.group, len, bs, betas);
+    if (warp == 0) load_gates(s, a.g, a.beta, c, b, hk * s.group, len, sums);
     wait(&done, 0, a.ctrl, &abort_flag, 0x601);
     __syncthreads();
     const int row = tid & 63;  // warps 0, 1: Q K^T; warps 2, 3: K K^T
@@ -349,7 +421,7 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
     for (int m = 0; m < s.group; ++m) {
         const int h = hk * s.group + m;
         char *tp = a.tp + (((size_t)c * s.B + b) * s.Hv + h) * TP_BYTES;
-        const double bi = bs[row];
+        const float2 bi = sums.b[row];
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         float *dst = (warp < 2 ? pm : tri) + row * PREP_LD;
 #pragma unroll 1
@@ -359,8 +431,9 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const int jj = j0 + j;
-                if (warp < 2) f[j] = jj <= row ? s.scale * decay(bi, bs[jj]) * f[j] : 0.f;
-                else f[j] = jj < row ? decay(bi, bs[jj]) * betas[jj] * f[j] : 0.f;
+                const float dec = decay(bi, sums.b[jj]);
+                if (warp < 2) f[j] = jj <= row ? s.scale * dec * f[j] : 0.f;
+                else f[j] = jj < row ? dec * sums.beta[jj] * f[j] : 0.f;
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 4) *(float4 *)(dst + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
@@ -370,9 +443,9 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
 #pragma unroll
                 for (int j = 32; j < 64; j += 4) *(float4 *)(dst + j) = make_float4(0.f, 0.f, 0.f, 0.f);
             float *gates = (float *)(tp + 2 * NT * TILE);
-            gates[tid] = decay(bi, 0.0);
-            gates[C + tid] = decay(bs[C - 1], bi);
-            gates[2 * C + tid] = betas[tid];
+            gates[tid] = decay(bi);
+            gates[C + tid] = decay(sums.b[C - 1], bi);
+            gates[2 * C + tid] = sums.beta[tid];
         } else {
             __syncwarp();
             // column `lane` of the inverse of block (half, half): x_i = [i == lane] - sum_{m < i} tri[i][m] x_m
@@ -427,7 +500,7 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
             *(float4 *)(t2 + (32 + i) * PREP_LD + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
         }
         __syncthreads();
-        if (warp == 0 && m + 1 < s.group) load_gates(s, a.g, a.beta, c, b, h + 1, len, bs, betas);
+        if (warp == 0 && m + 1 < s.group) load_gates(s, a.g, a.beta, c, b, h + 1, len, sums);
         // terms of T2 and P: eight threads a row, whole 128-byte lines a warp
 #pragma unroll 2
         for (int i = tid; i < 2 * C * 8; i += 128) {
@@ -540,15 +613,45 @@ __device__ __forceinline__ void seq_finish(SeqBars *bar) {
     __syncthreads();
     if (threadIdx.x < 32) tc::tmem_dealloc(bar->tmem_slot, 512);
 }
-// Every thread's tensor-memory writes are done; the one thread that issues
-// the products that read them goes on in the branch.
-__device__ __forceinline__ bool hand_over() {
+// Every thread's tensor-memory writes are done; one thread of warp 0 issues
+// the products that read them, in the branch.
+__device__ __forceinline__ bool hand_over(int warp) {
     tc::tmem_st_wait();
     tc::tc_fence_before();
     __syncthreads();
-    if (threadIdx.x != 0) return false;
+    if (warp != 0) return false;
     tc::tc_fence_after();
-    return true;
+    return elect_one();
+}
+
+// 16 consecutive values of shared memory (16-byte aligned).
+__device__ __forceinline__ void load16(const float *p, float (&f)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = ((const float4 *)p)[i];
+        f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+    }
+}
+// Elements p[i stride], i < n, of up to N (zero past n); and their stores.
+template <int N, class T> __device__ __forceinline__ void load_col(const T *p, long long stride, int n, T (&r)[N]) {
+    if (n >= N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += stride) r[i] = *p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += stride) r[i] = i < n ? *p : from_f<T>(0.f);
+    }
+}
+template <int N, class T> __device__ __forceinline__ void store_col(T *p, long long stride, int n, const float (&r)[N]) {
+    if (n >= N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += stride) *p = from_f<T>(r[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += stride)
+            if (i < n) *p = from_f<T>(r[i]);
+    }
+    __syncwarp();
 }
 
 // What a thread of the sequential kernels works on.
@@ -568,22 +671,16 @@ template <int KD> struct Lane {
         row = (long long)s.B * s.Hv * s.V;
     }
     // rows k of a [K][V] state at `base`, this thread's quarter
+    __device__ __forceinline__ int rows(const Shape &s, const float *base) const { return base && own ? s.K - wg * (KD / 4) : 0; }
     __device__ __forceinline__ void load(const Shape &s, const float *base, float (&S)[KD / 4]) const {
-#pragma unroll
-        for (int i = 0; i < KD / 4; ++i) {
-            const int k = wg * (KD / 4) + i;
-            S[i] = base && own && k < s.K ? base[(long long)k * s.V + v] : 0.f;
-        }
-    }
-    __device__ __forceinline__ void store(const Shape &s, float *base, const float (&S)[KD / 4]) const {
-        if (base && own) {
-            float *p = base + (long long)wg * (KD / 4) * s.V + v;
-#pragma unroll
-            for (int i = 0; i < KD / 4; ++i)
-                if (wg * (KD / 4) + i < s.K) p[(long long)i * s.V] = S[i];
-        }
+        load_col(base + (long long)wg * (KD / 4) * s.V + v, s.V, rows(s, base), S);
         __syncwarp();
     }
+    __device__ __forceinline__ void store(const Shape &s, float *base, const float (&S)[KD / 4]) const {
+        store_col(base + (long long)wg * (KD / 4) * s.V + v, s.V, rows(s, base), S);
+    }
+    // how many of the 16 tokens from t0 on are below `end`, for a lane that has a column
+    __device__ __forceinline__ int tokens(int t0, int end) const { return own ? end - t0 : 0; }
 };
 
 template <class E, int KD>
@@ -594,7 +691,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
     const Shape &s = a.s;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = warp_id();
     int id = blockIdx.x;
     const int vt = id % s.VT;
     id /= s.VT;
@@ -613,12 +710,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     const E *vp = (const E *)a.v + (long long)b * s.ldv + (long long)h * s.V + L.v;
     auto store_o = [&](int c) {
         const int t0 = c * C + L.wg * 16;
-        E *p = (E *)a.o + L.head * s.V + L.v + t0 * L.row;
-        if (L.own)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (t0 + i < s.T) p[i * L.row] = from_f<E>(o[i]);
-        __syncwarp();
+        store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), o);
     };
 #pragma unroll 1
     for (int c = 0; c < s.NC; ++c) {
@@ -627,17 +719,14 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
         const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + L.wg * 16;
         E vr[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            vr[i] = L.own && t0 + i < L.len ? vp[(long long)(t0 + i) * s.B * s.ldv] : from_f<E>(0.f);
+        load_col(vp + (long long)t0 * s.B * s.ldv, s.B * s.ldv, L.tokens(t0, L.len), vr);
+        __syncwarp();
         put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
         wait(&bar->full[st], (c / Q::stages) & 1, a.ctrl, ab, 0x612);
-        if (hand_over()) {  // D = K S and Q S, tokens on the columns
-            products_ts<KD / 16>(tmem + COL_D, tmem + COL_S, KD / 2, NT, k_major(qk + TILE, 0), rows, TB, NT,
-                                 tc::idesc_bf16_f32(128, 64, 0, 0));
+        if (hand_over(warp)) {  // D = K S and Q S, tokens on the columns
+            products_ts<KD / 16, NT, TB, NT>(tmem + COL_D, tmem + COL_S, KD / 2, k_major(qk + TILE, 0), rows, tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m1);
-            products_ts<KD / 16>(tmem + COL_D + 64, tmem + COL_S, KD / 2, Q::NO, k_major(qk, 0), rows, TB, Q::NO,
-                                 tc::idesc_bf16_f32(128, 64, 0, 0));
+            products_ts<KD / 16, Q::NO, TB, Q::NO>(tmem + COL_D + 64, tmem + COL_S, KD / 2, k_major(qk, 0), rows, tc::idesc_bf16_f32(128, 64, 0, 0));
         }
         __syncwarp();
         if (c > 0) {  // the last chunk's output
@@ -653,47 +742,40 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         __syncwarp();
         L.store(s, a.states ? a.states + ((long long)c * s.B * s.Hv + L.head) * s.K * s.V : nullptr, S);
         const float last = gates[C - 1 - L.wg * 16];  // gamma of token 63
-        float f[16];
+        float f[16], gam[16], be[16], u[16];
+        load16(gates, gam);
         wait(&bar->m1, ph, a.ctrl, ab, 0x613);
         get16(L.lanes + COL_D + L.wg * 16, f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = fmaf(-gates[i], f[i], to_f(vr[i]));
+        for (int i = 0; i < 16; ++i) f[i] = fmaf(-gam[i], f[i], to_f(vr[i]));
         put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
-        if (hand_over()) {  // X = T2 R
-            products_ts<4>(tmem + COL_X, tmem + COL_R, 32, NT, k_major(tp, 0), mat, NT, NT,
-                           tc::idesc_bf16_f32(128, 64, 0, 0));
+        if (hand_over(warp)) {  // X = T2 R
+            products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, k_major(tp, 0), mat, tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m2);
         }
         __syncwarp();
+        load16(gates + C, u);
+        load16(gates + 2 * C, be);
         wait(&bar->m2, ph, a.ctrl, ab, 0x614);  // Q S came before X
         get16(L.lanes + COL_X + L.wg * 16, f);
         get16(L.lanes + COL_D + 64 + L.wg * 16, o);
-        float u[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = f[i] * (gates[2 * C + i] * gates[C + i]);  // left U
+        for (int i = 0; i < 16; ++i) u[i] *= f[i] * be[i];  // left U
         put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, u);
-        if (hand_over()) {  // D = K^T (left U)
-            products_ts<4>(tmem + COL_D, tmem + COL_W, 32, NT, mn_major(qk + TILE, 0, 2 * TILE), cols, TB, NT,
-                           tc::idesc_bf16_f32(128, KD, 0, 1));
+        if (hand_over(warp)) {  // D = K^T (left U)
+            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols, tc::idesc_bf16_f32(128, KD, 0, 1));
             tc::mma_commit(&bar->m4);
         }
         __syncwarp();
-        if (a.deltas && L.own) {
-            float *p = a.deltas + L.head * s.V + L.v + t0 * L.row;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (t0 + i < s.T) p[i * L.row] = f[i];
-        }
-        __syncwarp();
+        if (a.deltas) store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            o[i] *= s.scale * gates[i];
-            f[i] *= gates[2 * C + i];  // U
+            o[i] *= s.scale * gam[i];
+            f[i] *= be[i];  // U
         }
         put_terms<8, Q::NO>(L.lanes + COL_R + L.wg * 8, 32, f);
-        if (hand_over()) {  // P U
-            products_ts<4>(tmem + COL_X, tmem + COL_R, 32, Q::NO, k_major(tp + NT * TILE, 0), mat, Q::NO, Q::NO,
-                           tc::idesc_bf16_f32(128, 64, 0, 0));
+        if (hand_over(warp)) {  // P U
+            products_ts<4, Q::NO, Q::NO, Q::NO>(tmem + COL_X, tmem + COL_R, 32, k_major(tp + NT * TILE, 0), mat, tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m3);
         }
         __syncwarp();
@@ -734,7 +816,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
     const Shape &s = a.s;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = warp_id();
     int id = blockIdx.x;
     const int vt = id % s.VT;
     id /= s.VT;
@@ -754,13 +836,12 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     const E *dop = (const E *)a.v + L.head * s.V + L.v;
     auto load_do = [&](int c) {
         const int t0 = c * C + L.wg * 16;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) d[i] = a.v && L.own && t0 + i < L.len ? dop[(t0 + i) * L.row] : from_f<E>(0.f);
+        load_col(dop + t0 * L.row, L.row, a.v ? L.tokens(t0, L.len) : 0, d);
+        __syncwarp();
     };
     auto product_pdo = [&](int st) {  // X = P^T dO (one thread)
         const uint32_t tp = tc::smem_u32(smem + st * Q::stage) + QK<E, KD>::bytes;
-        products_ts<4>(tmem + COL_X, tmem + COL_R, 32, TB, mn_major(tp + NT * TILE, 0, TILE), mat, NT, NT,
-                       tc::idesc_bf16_f32(128, 64, 0, 1));
+        products_ts<4, TB, NT, NT>(tmem + COL_X, tmem + COL_R, 32, mn_major(tp + NT * TILE, 0, TILE), mat, tc::idesc_bf16_f32(128, 64, 0, 1));
     };
     auto put_do = [&]() {
         float x[16];
@@ -781,43 +862,42 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
         if (!early) put_do();
         wait(&bar->full[st], (n / Q::stages) & 1, a.ctrl, ab, 0x622);
-        if (hand_over()) {  // D = K dS
+        if (hand_over(warp)) {  // D = K dS
             if (!early) product_pdo(st);
-            products_ts<KD / 16>(tmem + COL_D, tmem + COL_S, KD / 2, NT, k_major(qk + TILE, 0), rows, TB, NT,
-                                 tc::idesc_bf16_f32(128, 64, 0, 0));
+            products_ts<KD / 16, NT, TB, NT>(tmem + COL_D, tmem + COL_S, KD / 2, k_major(qk + TILE, 0), rows, tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m1);
         }
         __syncwarp();
         L.store(s, a.states + ((long long)c * s.B * s.Hv + L.head) * s.K * s.V, S);
         const float last = gates[C - 1 - L.wg * 16];
-        float f[16], e[16];
+        float f[16], e[16], left[16], be[16];
+        load16(gates + C, left);
+        load16(gates + 2 * C, be);
         wait(&bar->m1, ph, a.ctrl, ab, 0x623);
         get16(L.lanes + COL_D + L.wg * 16, f);
         get16(L.lanes + COL_X + L.wg * 16, e);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = gates[2 * C + i] * fmaf(gates[C + i], f[i], e[i]);  // beta dU
+        for (int i = 0; i < 16; ++i) f[i] = be[i] * fmaf(left[i], f[i], e[i]);  // beta dU
         put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
-        if (hand_over()) {  // dV = T2^T (beta dU)
-            products_ts<4>(tmem + COL_X, tmem + COL_R, 32, NT, mn_major(tp, 0, TILE), mat, NT, NT,
-                           tc::idesc_bf16_f32(128, 64, 0, 1));
+        if (hand_over(warp)) {  // dV = T2^T (beta dU)
+            products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, mn_major(tp, 0, TILE), mat, tc::idesc_bf16_f32(128, 64, 0, 1));
             tc::mma_commit(&bar->m2);
         }
         __syncwarp();
+        load16(gates, be);  // gamma
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e[i] = s.scale * gates[i] * to_f(d[i]);
+        for (int i = 0; i < 16; ++i) e[i] = s.scale * be[i] * to_f(d[i]);
         put_terms<8, NT>(L.lanes + COL_S + L.wg * 8, 32, e);
         if (c > 0) load_do(c - 1);
         wait(&bar->m2, ph, a.ctrl, ab, 0x624);
         get16(L.lanes + COL_X + L.wg * 16, f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e[i] = -gates[i] * f[i];
+        for (int i = 0; i < 16; ++i) e[i] = -be[i] * f[i];
         put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, e);
         if (Q::stages == 2 && c > 0) put_do();
-        if (hand_over()) {  // D = scale Q^T gamma dO - K^T gamma dV
-            products_ts<4>(tmem + COL_D, tmem + COL_S, 32, NT, mn_major(qk, 0, 2 * TILE), cols, TB, NT,
-                           tc::idesc_bf16_f32(128, KD, 0, 1));
-            products_ts<4>(tmem + COL_D, tmem + COL_W, 32, NT, mn_major(qk + TILE, 0, 2 * TILE), cols, TB, NT,
-                           tc::idesc_bf16_f32(128, KD, 0, 1), 1);
+        if (hand_over(warp)) {  // D = scale Q^T gamma dO - K^T gamma dV
+            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_S, 32, mn_major(qk, 0, 2 * TILE), cols, tc::idesc_bf16_f32(128, KD, 0, 1));
+            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols, tc::idesc_bf16_f32(128, KD, 0, 1), 1);
             tc::mma_commit(&bar->m4);
             if (Q::stages == 2 && c > 0) {
                 tc::mbar_wait(&bar->full[st ^ 1], ((n + 1) / Q::stages) & 1, a.ctrl, ab, 0x626);
@@ -825,17 +905,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
             }
         }
         __syncwarp();
-        if (L.own) {
-            float *p = a.deltas + L.head * s.V + L.v + t0 * L.row;
-            E *pv = (E *)a.o + L.head * s.V + L.v + t0 * L.row;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (t0 + i < s.T) {
-                    p[i * L.row] = f[i];
-                    pv[i * L.row] = from_f<E>(f[i]);
-                }
-        }
-        __syncwarp();
+        store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+        store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
         wait(&bar->m4, ph, a.ctrl, ab, 0x625);
 #pragma unroll
         for (int i0 = 0; i0 < H4; i0 += 16) {
@@ -856,20 +927,27 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
 // value head of the group, from the saved S0 and X and seq_bwd's dS1 and dV.
 // Rows are stacked so that every product has the 128 rows the tensor core
 // takes: [dO; dV] with X gives Y over Z, with S0 gives F over G; X sits in the
-// lower rows for E; the last product is [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K].
-// V is contracted 64 columns a pass, S0 and dS1 in turn in one buffer.
+// lower rows for E; [dQ; dK] += [Yh; -Zh] K, and dK += [Yh; -Zh]^T [Q; K] from
+// the same tiles read the other way.  V is contracted 64 columns a pass.
 // dg's double sum needs no matrix: sum_{r >= i > j} M_rj is the sum over
 // r >= i of (row sum - column sum), for the lower triangle M.
 constexpr int GRAD_THREADS = 512;
-constexpr uint32_t COL_QK = 0, COL_YZ = 64, COL_FG = 128, COL_E = 256, COL_OUT = 384;
+// [q; k] k^T | F over G, then Y over Z | E, then the transposed triangle's product | [dQ; dK]
+constexpr uint32_t COL_QK = 0, COL_FG = 64, COL_E = 256, COL_OUT = 384;
 
+// Tiles, 64 columns of V (NT terms each): `a` [dO; dV] 16 KB, `st` [S0 (KD
+// rows); X (64 rows)], and dS1 in a buffer of its own where there is room,
+// else in S0's rows after their products.  The triangle's operand [Yh; -Zh]
+// lies over `a`.  (The 16 KB before `a`, q and k tiles, and the 64 rows before
+// X, serve as rows of operands whose results are not used.)
 template <class E, int KD> struct GradSmem {
-    static constexpr int a = QK<E, KD>::bytes;       // [dO; dV], 64 columns: NT x 16 KB
-    static constexpr int x = a + NT * 2 * TILE;      // X: NT x 8 KB
-    static constexpr int st = x + NT * TILE;         // S0, then dS1: NT x KD rows x 128 bytes
-    static constexpr int m_end = a + NT * 4 * TILE;  // the last product's left operand lies over all three
-    static constexpr int end = st + NT * KD * 128 > m_end ? st + NT * KD * 128 : m_end;
-    static constexpr size_t smem = end + 1024;
+    static constexpr int a = QK<E, KD>::bytes;
+    static constexpr int st = a + NT * 2 * TILE, st_term = KD * 128 + TILE;
+    static constexpr int ds = st + NT * st_term;
+    static constexpr int fixed = 1024 + 8192;        // alignment; the static arrays
+    static constexpr bool own_ds = ds + NT * KD * 128 + fixed <= 232448;
+    static constexpr int ds_at = own_ds ? ds : st, ds_term = own_ds ? KD * 128 : st_term;
+    static constexpr size_t smem = (own_ds ? ds + NT * KD * 128 : ds) + 1024;
 };
 
 struct GradArgs {
@@ -898,27 +976,19 @@ __device__ __forceinline__ float transpose_sum(float (&f)[16]) {
     return f[0] + __shfl_xor_sync(~0u, f[0], 1);
 }
 
-// n terms of eight floats into a tile row's 16-byte group.
-template <int n> __device__ __forceinline__ void put8(uint8_t *tile, int term, uint32_t off, const float (&f)[8]) {
-    uint4 o[n];
-    split8<n>(f, o);
-#pragma unroll
-    for (int k = 0; k < n; ++k) *(uint4 *)(tile + k * term + off) = o[k];
-}
-
 template <class E, int KD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_constant__ GradArgs a) {
     using L = GradSmem<E, KD>;
     constexpr int TB = Terms<E>::n, TERM = QK<E, KD>::term, H4 = KD / 4, SI = KD / 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ double bs[C];
-    __shared__ float betas[C], colp[4][C], rowp[4][2 * C], rp[4][2 * C], ep[4][C], dots[16];
+    __shared__ Sums sums;
+    __shared__ float colp[4][C], rowp[4][2 * C], rp[4][2 * C], ep[4][C], dots[16];
     __shared__ uint64_t loaded, m1, m2, m3;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     const Shape &s = a.s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, r128 = tid & 127, r = r128 & 63;
+    const int tid = threadIdx.x, warp = warp_id(), lane = tid & 31, wg = tid >> 7, r128 = tid & 127, r = r128 & 63;
     const bool isq = r128 < 64;
     int id = blockIdx.x;
     const int hk = id % s.Hk;
@@ -942,7 +1012,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot, lanes = tmem + ((uint32_t)(r128 & 96) << 16);
-    const uint32_t qk = tc::smem_u32(smem), sa = qk + L::a, sx = qk + L::x, ss = qk + L::st;
+    const uint32_t qk = tc::smem_u32(smem), sa = qk + L::a, ss = qk + L::st, sx = ss + KD * 128, sd = qk + L::ds_at;
     if (tid == 0) {
         tc::mbar_arrive_expect_tx(&loaded, QK<E, KD>::bytes);
         bulk_load(smem, a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes, QK<E, KD>::bytes, &loaded);
@@ -950,37 +1020,41 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     __syncwarp();
     const int row = tid >> 3, gr = tid & 7;  // loads: eight threads a row, eight columns each
     const int t_row = c * C + row;
-    float acc[H4];  // this thread's quarter row of dq (rows 0..63) or dk, but for the last product
+    const uint32_t off = swz(row, gr * 16);  // rows 64 apart keep it
+    float acc[H4];  // this thread's quarter row of dq (rows 0..63) or dk, but for COL_OUT
 #pragma unroll
     for (int i = 0; i < H4; ++i) acc[i] = 0.f;
     uint32_t p12 = 0;
     const int passes = (s.V + 63) / 64;
-    float ro[8], rv[8], rx[8], rs[SI][8], rd[SI][8];  // dO, dV, X, S0, dS1 of the pass ahead
+    Raw8<E> ro;                                // dO, dV, X, S0, dS1 of the pass ahead
+    Raw8<float> rv, rx, rs[SI], rd[SI];
     auto load_pass = [&](int h, int v0) {
         const long long head = (long long)b * s.Hv + h;
         const long long at = ((long long)t_row * s.B * s.Hv + head) * s.V + v0 + gr * 8;
-        const long long sb = ((long long)c * s.B * s.Hv + head) * s.K * s.V + v0 + gr * 8;
-        const bool in = v0 + gr * 8 < s.V;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ro[i] = rv[i] = rx[i] = 0.f;
-        if (in && t_row < len) {
-            if (a.dout) load8<E>((const E *)a.dout + at, ro);
-            load8<float>(a.dvf + at, rv);
-            load8<float>(a.deltas + at, rx);
-        }
+        const long long sb = (((long long)c * s.B * s.Hv + head) * s.K + row) * s.V + v0 + gr * 8;
+        const bool in = v0 + gr * 8 < s.V, live = in && t_row < len;
+        ro = raw8<E>((const E *)a.dout + at, live && a.dout);
+        rv = raw8<float>(a.dvf + at, live);
+        rx = raw8<float>(a.deltas + at, live);
 #pragma unroll
         for (int n = 0; n < SI; ++n) {
-            const int k = n * 64 + row;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) rs[n][i] = rd[n][i] = 0.f;
-            if (in && k < s.K) {
-                load8<float>(a.states + sb + (long long)k * s.V, rs[n]);
-                load8<float>(a.dstates + sb + (long long)k * s.V, rd[n]);
-            }
+            const bool has = in && n * 64 + row < s.K;
+            rs[n] = raw8<float>(a.states + sb + (long long)n * 64 * s.V, has);
+            rd[n] = raw8<float>(a.dstates + sb + (long long)n * 64 * s.V, has);
         }
     };
-    constexpr Steps qk_rows = {TERM >> 4, 2, 2 * TILE >> 4}, a_rows = {2 * TILE >> 4, 2, 0}, x_rows = {TILE >> 4, 2, 0},
-                    s_rows = {KD * 128 >> 4, 2, 0}, m_rows = {4 * TILE >> 4, 2, 2 * TILE >> 4},
+    auto put = [&](uint8_t *tile, int term, const Raw8<float> &x) {
+        uint4 o[NT];
+        terms8<float>(x, o);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) *(uint4 *)(tile + k * term + off) = o[k];
+    };
+    auto put_ds = [&]() {
+#pragma unroll
+        for (int n = 0; n < SI; ++n) put(smem + L::ds_at + n * TILE, L::ds_term, rd[n]);
+    };
+    constexpr Steps qk_rows = {TERM >> 4, 2, 2 * TILE >> 4}, a_rows = {2 * TILE >> 4, 2, 0}, x_rows = {L::st_term >> 4, 2, 0},
+                    d_rows = {L::ds_term >> 4, 2, 0}, a_cols = {2 * TILE >> 4, 2048 >> 4, 4 * 2048 >> 4},
                     qk_cols = {TERM >> 4, 2048 >> 4, 4 * 2048 >> 4};
     wait(&loaded, 0, a.ctrl, ab, 0x631);
 #pragma unroll 1
@@ -988,91 +1062,96 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
         const int h = hk * s.group + m;
         load_pass(h, 0);
         if (m > 0) wait(&m3, (m - 1) & 1, a.ctrl, ab, 0x632);  // the tiles are free
+        if (m > 0 && !isq) {  // dK's transposed part of the last head
+#pragma unroll
+            for (int i0 = 0; i0 < H4; i0 += 16) {
+                float f[16];
+                get16(lanes + COL_E + wg * H4 + i0, f);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i0 + i] += f[i];
+            }
+        }
+        tc::tc_fence_before();
         __syncthreads();
-        if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, bs, betas);
+        if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, sums);
         float dot = 0.f;
 #pragma unroll 1
         for (int p = 0; p < passes; ++p) {
-            put8<NT>(smem + L::a, 2 * TILE, swz(row, gr * 16), ro);
-            put8<NT>(smem + L::a, 2 * TILE, swz(C + row, gr * 16), rv);
-            put8<NT>(smem + L::x, TILE, swz(row, gr * 16), rx);
+            {
+                uint4 o[TB];
+                terms8<E>(ro, o);
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+                    *(uint4 *)(smem + L::a + k * 2 * TILE + off) = k < TB ? o[k < TB ? k : 0] : make_uint4(0, 0, 0, 0);
+            }
+            put(smem + L::a + TILE, 2 * TILE, rv);
+            put(smem + L::st + KD * 128, L::st_term, rx);
 #pragma unroll
             for (int n = 0; n < SI; ++n) {
-                put8<NT>(smem + L::st, KD * 128, swz(n * 64 + row, gr * 16), rs[n]);
+                put(smem + L::st + n * TILE, L::st_term, rs[n]);
+                const uint4 *x = &rs[n].a, *y = &rd[n].a;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dot = fmaf(rs[n][i], rd[n][i], dot);
+                for (int i = 0; i < 2; ++i) {
+                    dot = fmaf(__uint_as_float(x[i].x), __uint_as_float(y[i].x), dot);
+                    dot = fmaf(__uint_as_float(x[i].y), __uint_as_float(y[i].y), dot);
+                    dot = fmaf(__uint_as_float(x[i].z), __uint_as_float(y[i].z), dot);
+                    dot = fmaf(__uint_as_float(x[i].w), __uint_as_float(y[i].w), dot);
+                }
             }
+            if (L::own_ds) put_ds();
             tc::fence_proxy_async_smem();
-            if (hand_over()) {
-                if (m == 0 && p == 0)  // [q; k] k^T, once
-                    products_ss<KD / 16>(tmem + COL_QK, k_major(qk, 0), qk_rows, TB, k_major(qk + TILE, 0), qk_rows, TB, NT,
-                                         tc::idesc_bf16_f32(128, 64, 0, 0));
-                products_ss<4>(tmem + COL_FG, k_major(sa, 0), a_rows, NT, k_major(ss, 0), s_rows, NT, NT,
-                               tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
-                tc::mma_commit(&m1);
-                products_ss<4>(tmem + COL_YZ, k_major(sa, 0), a_rows, NT, k_major(sx, 0), x_rows, NT, NT,
-                               tc::idesc_bf16_f32(128, 64, 0, 0), p > 0);
-            }
-            __syncwarp();
-            wait(&m1, p12, a.ctrl, ab, 0x633);  // S0's buffer is free
-#pragma unroll
-            for (int n = 0; n < SI; ++n) put8<NT>(smem + L::st, KD * 128, swz(n * 64 + row, gr * 16), rd[n]);
-            if (p + 1 < passes) load_pass(h, (p + 1) * 64);
-            tc::fence_proxy_async_smem();
-            if (hand_over()) {  // rows 64..127: E = X dS1^T (the rows above X are not used)
-                products_ss<4>(tmem + COL_E, k_major(sx - TILE, 0), x_rows, NT, k_major(ss, 0), s_rows, NT, NT,
-                               tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
+            const auto product_e = [&]() {  // rows 64..127: E = X dS1^T (the rows above X are not used)
+                products_ss<4, NT, NT, NT>(tmem + COL_E, k_major(sx - TILE, 0), x_rows, k_major(sd, 0), d_rows,
+                                           tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
                 tc::mma_commit(&m2);
+            };
+            if (hand_over(warp)) {
+                if (m == 0 && p == 0)  // [q; k] k^T, once
+                    products_ss<KD / 16, TB, TB, NT>(tmem + COL_QK, k_major(qk, 0), qk_rows, k_major(qk + TILE, 0), qk_rows,
+                                                     tc::idesc_bf16_f32(128, 64, 0, 0));
+                // [F; G | Y; Z] = [dO; dV] [S0; X]^T
+                products_ss<4, NT, NT, NT>(tmem + COL_FG, k_major(sa, 0), a_rows, k_major(ss, 0), x_rows,
+                                           tc::idesc_bf16_f32(128, KD + 64, 0, 0), p > 0);
+                tc::mma_commit(&m1);
+                if (L::own_ds) product_e();
             }
             __syncwarp();
+            if (!L::own_ds) {
+                wait(&m1, p12, a.ctrl, ab, 0x633);  // S0's rows are free
+                put_ds();
+                tc::fence_proxy_async_smem();
+                if (hand_over(warp)) product_e();
+                __syncwarp();
+            }
+            if (p + 1 < passes) load_pass(h, (p + 1) * 64);
             wait(&m2, p12, a.ctrl, ab, 0x634);
             p12 ^= 1;
         }
-        // ---- the triangle: weights, their row and column sums, the last product's left operand
+        // ---- the triangle: weights w, their row and column sums, and [Yh; -Zh]
         {
             float y[16], kq[16];
             get16(lanes + COL_QK + wg * 16, kq);
-            get16(lanes + COL_YZ + wg * 16, y);
-            const double br = bs[r];
+            get16(lanes + COL_FG + KD + wg * 16, y);
+            const float2 br = sums.b[r];
+            const float sign = isq ? s.scale : -1.f;
+            const int last = isq ? r : r - 1;  // last column of this row
             float rowsum = 0.f;
-            if (isq) {  // rows 0..63 have no product with Q
-#pragma unroll
-                for (int k = 0; k < NT; ++k)
-#pragma unroll
-                    for (int g2 = 0; g2 < 2; ++g2)
-                        *(uint4 *)(smem + L::a + k * 4 * TILE + swz(r, (wg * 2 + g2) * 16)) = make_uint4(0, 0, 0, 0);
-            }
 #pragma unroll
             for (int j0 = 0; j0 < 16; j0 += 8) {
                 float e[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int j = wg * 16 + j0 + i;
-                    const bool in = isq ? j <= r : j < r;
-                    const float z = in ? decay(br, bs[j]) * (isq ? s.scale * y[j0 + i] : -y[j0 + i]) : 0.f;
+                    const float z = j <= last ? decay(br, sums.b[j]) * sign * y[j0 + i] : 0.f;
                     kq[j0 + i] *= z;  // w_rj
-                    e[i] = z * betas[j];
-                    rowsum = fmaf(betas[j], kq[j0 + i], rowsum);
+                    e[i] = z * sums.beta[j];
+                    rowsum = fmaf(sums.beta[j], kq[j0 + i], rowsum);
                 }
                 uint4 o[NT];
                 split8<NT>(e, o);
 #pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    uint8_t *base = smem + L::a + k * 4 * TILE;  // [cols 0..63: Q][cols 64..127: K], 128 rows each
-                    const uint32_t q4[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
-                    if (isq) *(uint4 *)(base + 2 * TILE + swz(r, (wg * 16 + j0) * 2)) = o[k];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int j = wg * 16 + j0 + i;
-                        const uint16_t hv = (uint16_t)(q4[i >> 1] >> (16 * (i & 1)));
-                        if (isq) {
-                            *(uint16_t *)(base + swz(64 + j, r * 2)) = hv;
-                        } else if (j <= r) {
-                            *(uint16_t *)(base + 2 * TILE + swz(64 + r, j * 2)) = hv;
-                            *(uint16_t *)(base + 2 * TILE + swz(64 + j, r * 2)) = hv;
-                        }
-                    }
-                }
+                for (int k = 0; k < NT; ++k)
+                    *(uint4 *)(smem + L::a + k * 2 * TILE + swz(r128, (wg * 16 + j0) * 2)) = o[k];
             }
             rowp[wg][r128] = rowsum;
             __syncwarp();
@@ -1081,7 +1160,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
         }
         // ---- F | G and E: a quarter row of K a thread
         {
-            const float gam = decay(bs[r], 0.0), lb = decay(bs[C - 1], bs[r]) * betas[r];
+            const float gam = decay(sums.b[r]), lb = decay(sums.b[C - 1], sums.b[r]) * sums.beta[r];
             float dotf = 0.f, dote = 0.f;
 #pragma unroll
             for (int i0 = 0; i0 < H4; i0 += 16) {
@@ -1120,9 +1199,12 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
             if (lane == 0) dots[warp] = dot;
         }
         tc::fence_proxy_async_smem();
-        if (hand_over()) {  // [dQ; dK] += [0, Yh; Yh^T, -(Zh + Zh^T)] [Q; K]
-            products_ss<8>(tmem + COL_OUT, k_major(sa, 0), m_rows, NT, mn_major(qk, 0, 2 * TILE), qk_cols, TB, NT,
-                           tc::idesc_bf16_f32(128, KD, 0, 1), m > 0);
+        if (hand_over(warp)) {
+            // [dQ; dK] += [Yh; -Zh] K; and in the lower rows of COL_E: [Yh; -Zh]^T [Q; K]
+            products_ss<4, NT, TB, NT>(tmem + COL_OUT, k_major(sa, 0), a_rows, mn_major(qk + TILE, 0, 2 * TILE), qk_cols,
+                                       tc::idesc_bf16_f32(128, KD, 0, 1), m > 0);
+            products_ss<8, NT, TB, NT>(tmem + COL_E, mn_major(sa - 2 * TILE, 0, 2 * TILE), a_cols, mn_major(qk, 0, 2 * TILE),
+                                       qk_cols, tc::idesc_bf16_f32(128, KD, 1, 1));
             tc::mma_commit(&m3);
         }
         __syncwarp();
@@ -1134,27 +1216,27 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
             float db[2];
 #pragma unroll
             for (int i = 0; i < 16; ++i) all += dots[i];
-            all *= decay(bs[C - 1], 0.0);
+            all *= decay(sums.b[C - 1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 2 * lane + i;
                 const double col = sum4(&colp[0][0], C, j);
                 const double rows = sum4(&rowp[0][0], 2 * C, j) + sum4(&rowp[0][0], 2 * C, C + j);
                 const double ke = sum4(&ep[0][0], C, j);
-                const double gam = decay(bs[j], 0.0), left = decay(bs[C - 1], bs[j]);
-                d[i] = rows - betas[j] * col + gam * (s.scale * sum4(&rp[0][0], 2 * C, j) - sum4(&rp[0][0], 2 * C, C + j));
-                e[i] = left * betas[j] * ke;
+                const double gam = decay(sums.b[j]), left = decay(sums.b[C - 1], sums.b[j]);
+                d[i] = rows - sums.beta[j] * col + gam * (s.scale * sum4(&rp[0][0], 2 * C, j) - sum4(&rp[0][0], 2 * C, C + j));
+                e[i] = left * sums.beta[j] * ke;
                 db[i] = (float)(col + left * ke);
             }
             // suffix sums of d, prefix sums (exclusive) of e
-            double sd = d[0] + d[1], se = e[0] + e[1];
+            double sd2 = d[0] + d[1], se = e[0] + e[1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_down_sync(~0u, sd, o), y = __shfl_up_sync(~0u, se, o);
-                if (lane + o < 32) sd += x;
+                const double x = __shfl_down_sync(~0u, sd2, o), y = __shfl_up_sync(~0u, se, o);
+                if (lane + o < 32) sd2 += x;
                 if (lane >= o) se += y;
             }
-            const double after = sd - d[0] - d[1], before = se - e[0] - e[1];
+            const double after = sd2 - d[0] - d[1], before = se - e[0] - e[1];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = c * C + 2 * lane + i;
@@ -1173,15 +1255,16 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     E *out = (E *)(isq ? a.dq : a.dk) + (((long long)t * s.B + b) * s.Hk + hk) * s.K + wg * H4;
 #pragma unroll
     for (int i0 = 0; i0 < H4; i0 += 16) {
-        float f[16];
+        float f[16], e[16];
         get16(lanes + COL_OUT + wg * H4 + i0, f);
+        get16(lanes + COL_E + wg * H4 + i0, e);
         if (t < s.T)
 #pragma unroll
             for (int g2 = 0; g2 < 2; ++g2) {
                 if (wg * H4 + i0 + g2 * 8 >= s.K) continue;
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = acc[i0 + g2 * 8 + i] + f[g2 * 8 + i];
+                for (int i = 0; i < 8; ++i) x[i] = acc[i0 + g2 * 8 + i] + f[g2 * 8 + i] + (isq ? 0.f : e[g2 * 8 + i]);
                 if constexpr (sizeof(E) == 4) {
                     *(float4 *)(out + i0 + g2 * 8) = make_float4(x[0], x[1], x[2], x[3]);
                     *(float4 *)(out + i0 + g2 * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
