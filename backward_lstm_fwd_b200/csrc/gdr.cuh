@@ -219,12 +219,14 @@ __device__ __forceinline__ void get16(uint32_t col, float (&f)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void get32(uint32_t col, float (&f)[32]) {
-    uint32_t r[32];
-    tc::tmem_ld32(col, r);
-    tc::tmem_ld_wait();
+__device__ __forceinline__ void set16(uint32_t col, const float (&f)[16]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; i += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(f[i + j]);
+        tc::tmem_st8(col + i, r);
+    }
 }
 
 // A bounded wait of a whole warp, ordered before its tensor-memory accesses.
@@ -342,17 +344,16 @@ constexpr int PREP_LD = 68;                    // floats between rows of a 64 x 
 constexpr int PREP_MAT = C * PREP_LD * 4;
 
 template <class E, int KD> struct PrepSmem {
-    // T2 and P go where the operand tiles were; the triangle behind them
-    static constexpr int tri = QK<E, KD>::bytes > 2 * PREP_MAT ? QK<E, KD>::bytes : 2 * PREP_MAT;
-    static constexpr size_t smem = tri + PREP_MAT + 1024;
+    // the triangle (then T2) and P go where the operand tiles were
+    static constexpr size_t smem = (QK<E, KD>::bytes > 2 * PREP_MAT ? QK<E, KD>::bytes : 2 * PREP_MAT) + 1024;
 };
 
 template <class E, int KD>
-__global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
+__global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
     constexpr int TB = Terms<E>::n;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float *t2 = (float *)tiles, *pm = (float *)(tiles + PREP_MAT), *tri = (float *)(tiles + PrepSmem<E, KD>::tri);
+    float *tri = (float *)tiles, *pm = (float *)(tiles + PREP_MAT);
     __shared__ Sums sums;
     __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
@@ -439,9 +440,6 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
             for (int j = 0; j < 16; j += 4) *(float4 *)(dst + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
         }
         if (warp < 2) {
-            if (!half)
-#pragma unroll
-                for (int j = 32; j < 64; j += 4) *(float4 *)(dst + j) = make_float4(0.f, 0.f, 0.f, 0.f);
             float *gates = (float *)(tp + 2 * NT * TILE);
             gates[tid] = decay(bi);
             gates[C + tid] = decay(sums.b[C - 1], bi);
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
         } else {
             __syncwarp();
             // column `lane` of the inverse of block (half, half): x_i = [i == lane] - sum_{m < i} tri[i][m] x_m
-            const float *blk = tri + half * 32 * PREP_LD + half * 32;
+            float *blk = tri + half * 32 * PREP_LD + half * 32;  // becomes its inverse
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -464,40 +462,37 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
                 }
                 x[i] = (p0 + p1) + (p2 + p3);
             }
-            float *o = t2 + half * 32 * PREP_LD + half * 32 + lane;
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i * PREP_LD] = x[i];
-            if (half)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) t2[i * PREP_LD + 32 + lane] = 0.f;  // above the diagonal
+            for (int i = 0; i < 32; ++i) blk[i * PREP_LD + lane] = x[i];
         }
         __syncthreads();
-        {  // block (1, 0): W = B A', into the triangle's upper right corner; then -D' W
+        {  // block (1, 0): W = B A', into the upper right corner; then -D' W in B's place
             const int i = tid >> 2, j0 = (tid & 3) * 8;
-            float acc[8];
+            auto product = [&](const float *l, const float *r, float sign, float *o) {
+                float acc[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float l = tri[(32 + i) * PREP_LD + k];
-                const float4 u = *(const float4 *)(t2 + k * PREP_LD + j0), v = *(const float4 *)(t2 + k * PREP_LD + j0 + 4);
-                acc[0] = fmaf(l, u.x, acc[0]); acc[1] = fmaf(l, u.y, acc[1]); acc[2] = fmaf(l, u.z, acc[2]); acc[3] = fmaf(l, u.w, acc[3]);
-                acc[4] = fmaf(l, v.x, acc[4]); acc[5] = fmaf(l, v.y, acc[5]); acc[6] = fmaf(l, v.z, acc[6]); acc[7] = fmaf(l, v.w, acc[7]);
-            }
-            *(float4 *)(tri + i * PREP_LD + 32 + j0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            *(float4 *)(tri + i * PREP_LD + 32 + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll 4
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 lv = *(const float4 *)(l + i * PREP_LD + k);
+                    const float le[4] = {sign * lv.x, sign * lv.y, sign * lv.z, sign * lv.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 u = *(const float4 *)(r + (k + q) * PREP_LD + j0), v = *(const float4 *)(r + (k + q) * PREP_LD + j0 + 4);
+                        acc[0] = fmaf(le[q], u.x, acc[0]); acc[1] = fmaf(le[q], u.y, acc[1]);
+                        acc[2] = fmaf(le[q], u.z, acc[2]); acc[3] = fmaf(le[q], u.w, acc[3]);
+                        acc[4] = fmaf(le[q], v.x, acc[4]); acc[5] = fmaf(le[q], v.y, acc[5]);
+                        acc[6] = fmaf(le[q], v.z, acc[6]); acc[7] = fmaf(le[q], v.w, acc[7]);
+                    }
+                }
+                *(float4 *)(o + i * PREP_LD + j0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                *(float4 *)(o + i * PREP_LD + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            };
+            float *low = tri + 32 * PREP_LD, *corner = tri + 32;
+            product(low, tri, 1.f, corner);
             __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float l = -t2[(32 + i) * PREP_LD + 32 + k];
-                const float4 u = *(const float4 *)(tri + k * PREP_LD + 32 + j0), v = *(const float4 *)(tri + k * PREP_LD + 32 + j0 + 4);
-                acc[0] = fmaf(l, u.x, acc[0]); acc[1] = fmaf(l, u.y, acc[1]); acc[2] = fmaf(l, u.z, acc[2]); acc[3] = fmaf(l, u.w, acc[3]);
-                acc[4] = fmaf(l, v.x, acc[4]); acc[5] = fmaf(l, v.y, acc[5]); acc[6] = fmaf(l, v.z, acc[6]); acc[7] = fmaf(l, v.w, acc[7]);
-            }
-            *(float4 *)(t2 + (32 + i) * PREP_LD + j0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            *(float4 *)(t2 + (32 + i) * PREP_LD + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            product(low + 32, corner, -1.f, low);
         }
         __syncthreads();
         if (warp == 0 && m + 1 < s.group) load_gates(s, a.g, a.beta, c, b, h + 1, len, sums);
@@ -506,8 +501,9 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
         for (int i = tid; i < 2 * C * 8; i += 128) {
             const int mat = i >> 9, r = (i >> 3) & 63, gr = i & 7;
             float f[8];
-            const float4 *src = (const float4 *)((mat ? pm : t2) + r * PREP_LD + gr * 8);
-            const float4 u = src[0], v = src[1];
+            const float4 *src = (const float4 *)((mat ? pm : tri) + r * PREP_LD + gr * 8);
+            float4 u = src[0], v = src[1];
+            if (r < 32 && gr >= 4) u = v = make_float4(0.f, 0.f, 0.f, 0.f);  // above the diagonal (T2: W's place)
             f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
             f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
             uint4 o[NT];
@@ -1021,27 +1017,31 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     const int row = tid >> 3, gr = tid & 7;  // loads: eight threads a row, eight columns each
     const int t_row = c * C + row;
     const uint32_t off = swz(row, gr * 16);  // rows 64 apart keep it
-    float acc[H4];  // this thread's quarter row of dq (rows 0..63) or dk, but for COL_OUT
-#pragma unroll
-    for (int i = 0; i < H4; ++i) acc[i] = 0.f;
-    uint32_t p12 = 0;
-    const int passes = (s.V + 63) / 64;
+    const int passes = (s.V + 63) / 64, total = passes * s.group;
     Raw8<E> ro;                                // dO, dV, X, S0, dS1 of the pass ahead
     Raw8<float> rv, rx, rs[SI], rd[SI];
-    auto load_pass = [&](int h, int v0) {
-        const long long head = (long long)b * s.Hv + h;
-        const long long at = ((long long)t_row * s.B * s.Hv + head) * s.V + v0 + gr * 8;
-        const long long sb = (((long long)c * s.B * s.Hv + head) * s.K + row) * s.V + v0 + gr * 8;
-        const bool in = v0 + gr * 8 < s.V, live = in && t_row < len;
+    // pass n is columns 64 (n % passes) .. of value head n / passes of the group
+    auto token_at = [&](int n, bool &live) {
+        const int v0 = n % passes * 64 + gr * 8;
+        live = n < total && v0 < s.V && t_row < len;
+        return (((long long)t_row * s.B + b) * s.Hv + hk * s.group + n / passes) * s.V + v0;
+    };
+    auto load_a = [&](int n) {
+        bool live;
+        const long long at = token_at(n, live);
         ro = raw8<E>((const E *)a.dout + at, live && a.dout);
         rv = raw8<float>(a.dvf + at, live);
+    };
+    auto load_x = [&](int n) {
+        bool live;
+        const long long at = token_at(n, live);
         rx = raw8<float>(a.deltas + at, live);
+    };
+    auto load_s = [&](int n, const float *base, Raw8<float> (&o)[SI]) {
+        const int v0 = n % passes * 64 + gr * 8;
+        const float *q = base + ((((long long)c * s.B + b) * s.Hv + hk * s.group + n / passes) * s.K + row) * s.V + v0;
 #pragma unroll
-        for (int n = 0; n < SI; ++n) {
-            const bool has = in && n * 64 + row < s.K;
-            rs[n] = raw8<float>(a.states + sb + (long long)n * 64 * s.V, has);
-            rd[n] = raw8<float>(a.dstates + sb + (long long)n * 64 * s.V, has);
-        }
+        for (int i = 0; i < SI; ++i) o[i] = raw8<float>(q + (long long)i * 64 * s.V, n < total && v0 < s.V && i * 64 + row < s.K);
     };
     auto put = [&](uint8_t *tile, int term, const Raw8<float> &x) {
         uint4 o[NT];
@@ -1049,34 +1049,52 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < NT; ++k) *(uint4 *)(tile + k * term + off) = o[k];
     };
-    auto put_ds = [&]() {
-#pragma unroll
-        for (int n = 0; n < SI; ++n) put(smem + L::ds_at + n * TILE, L::ds_term, rd[n]);
-    };
     constexpr Steps qk_rows = {TERM >> 4, 2, 2 * TILE >> 4}, a_rows = {2 * TILE >> 4, 2, 0}, x_rows = {L::st_term >> 4, 2, 0},
                     d_rows = {L::ds_term >> 4, 2, 0}, a_cols = {2 * TILE >> 4, 2048 >> 4, 4 * 2048 >> 4},
                     qk_cols = {TERM >> 4, 2048 >> 4, 4 * 2048 >> 4};
+    load_s(0, a.states, rs);
+    load_a(0);
+    load_x(0);
+    load_s(0, a.dstates, rd);
     wait(&loaded, 0, a.ctrl, ab, 0x631);
 #pragma unroll 1
     for (int m = 0; m < s.group; ++m) {
         const int h = hk * s.group + m;
-        load_pass(h, 0);
-        if (m > 0) wait(&m3, (m - 1) & 1, a.ctrl, ab, 0x632);  // the tiles are free
-        if (m > 0 && !isq) {  // dK's transposed part of the last head
-#pragma unroll
-            for (int i0 = 0; i0 < H4; i0 += 16) {
-                float f[16];
-                get16(lanes + COL_E + wg * H4 + i0, f);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i0 + i] += f[i];
-            }
-        }
-        tc::tc_fence_before();
-        __syncthreads();
-        if (warp == 0) load_gates(s, a.g, a.beta, c, b, h, len, sums);
-        float dot = 0.f;
+        float dot = 0.f;  // <dS1, S0>
+        // A pass: the first products run beside the conversion of dS1, E beside
+        // the next pass's conversions of S0, dO and dV; every buffer's next
+        // values are loaded as soon as it is written.
 #pragma unroll 1
         for (int p = 0; p < passes; ++p) {
+            const int n = m * passes + p;
+            if (n > 0) wait(&m1, (n - 1) & 1, a.ctrl, ab, 0x633);
+            if (!L::own_ds && p > 0) wait(&m2, (n - 1) & 1, a.ctrl, ab, 0x634);  // dS1 lies in S0's rows
+#pragma unroll
+            for (int i = 0; i < SI; ++i) {
+                put(smem + L::st + i * TILE, L::st_term, rs[i]);
+                const uint4 *x = &rs[i].a, *y = &rd[i].a;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    dot = fmaf(__uint_as_float(x[j].x), __uint_as_float(y[j].x), dot);
+                    dot = fmaf(__uint_as_float(x[j].y), __uint_as_float(y[j].y), dot);
+                    dot = fmaf(__uint_as_float(x[j].z), __uint_as_float(y[j].z), dot);
+                    dot = fmaf(__uint_as_float(x[j].w), __uint_as_float(y[j].w), dot);
+                }
+            }
+            load_s(n + 1, a.states, rs);
+            if (m > 0 && p == 0) {
+                wait(&m3, (m - 1) & 1, a.ctrl, ab, 0x632);  // the triangle's tiles are free
+                if (!isq)  // dK's transposed part of the last head
+#pragma unroll
+                    for (int i0 = 0; i0 < H4; i0 += 16) {
+                        float f[16], e[16];
+                        get16(lanes + COL_OUT + wg * H4 + i0, f);
+                        get16(lanes + COL_E + wg * H4 + i0, e);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] += e[i];
+                        set16(lanes + COL_OUT + wg * H4 + i0, f);
+                    }
+            }
             {
                 uint4 o[TB];
                 terms8<E>(ro, o);
@@ -1085,48 +1103,35 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                     *(uint4 *)(smem + L::a + k * 2 * TILE + off) = k < TB ? o[k < TB ? k : 0] : make_uint4(0, 0, 0, 0);
             }
             put(smem + L::a + TILE, 2 * TILE, rv);
+            load_a(n + 1);
+            if (L::own_ds && p > 0) wait(&m2, (n - 1) & 1, a.ctrl, ab, 0x634);
             put(smem + L::st + KD * 128, L::st_term, rx);
-#pragma unroll
-            for (int n = 0; n < SI; ++n) {
-                put(smem + L::st + n * TILE, L::st_term, rs[n]);
-                const uint4 *x = &rs[n].a, *y = &rd[n].a;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    dot = fmaf(__uint_as_float(x[i].x), __uint_as_float(y[i].x), dot);
-                    dot = fmaf(__uint_as_float(x[i].y), __uint_as_float(y[i].y), dot);
-                    dot = fmaf(__uint_as_float(x[i].z), __uint_as_float(y[i].z), dot);
-                    dot = fmaf(__uint_as_float(x[i].w), __uint_as_float(y[i].w), dot);
-                }
-            }
-            if (L::own_ds) put_ds();
+            load_x(n + 1);
             tc::fence_proxy_async_smem();
-            const auto product_e = [&]() {  // rows 64..127: E = X dS1^T (the rows above X are not used)
-                products_ss<4, NT, NT, NT>(tmem + COL_E, k_major(sx - TILE, 0), x_rows, k_major(sd, 0), d_rows,
-                                           tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
-                tc::mma_commit(&m2);
-            };
             if (hand_over(warp)) {
-                if (m == 0 && p == 0)  // [q; k] k^T, once
+                if (n == 0)  // [q; k] k^T, once
                     products_ss<KD / 16, TB, TB, NT>(tmem + COL_QK, k_major(qk, 0), qk_rows, k_major(qk + TILE, 0), qk_rows,
                                                      tc::idesc_bf16_f32(128, 64, 0, 0));
                 // [F; G | Y; Z] = [dO; dV] [S0; X]^T
                 products_ss<4, NT, NT, NT>(tmem + COL_FG, k_major(sa, 0), a_rows, k_major(ss, 0), x_rows,
                                            tc::idesc_bf16_f32(128, KD + 64, 0, 0), p > 0);
                 tc::mma_commit(&m1);
-                if (L::own_ds) product_e();
             }
             __syncwarp();
-            if (!L::own_ds) {
-                wait(&m1, p12, a.ctrl, ab, 0x633);  // S0's rows are free
-                put_ds();
-                tc::fence_proxy_async_smem();
-                if (hand_over(warp)) product_e();
-                __syncwarp();
+            if (p == 0 && warp == 2) load_gates(s, a.g, a.beta, c, b, h, len, sums);
+            if (!L::own_ds) wait(&m1, n & 1, a.ctrl, ab, 0x636);
+#pragma unroll
+            for (int i = 0; i < SI; ++i) put(smem + L::ds_at + i * TILE, L::ds_term, rd[i]);
+            load_s(n + 1, a.dstates, rd);
+            tc::fence_proxy_async_smem();
+            if (hand_over(warp)) {  // rows 64..127: E = X dS1^T (the rows above X are not used)
+                products_ss<4, NT, NT, NT>(tmem + COL_E, k_major(sx - TILE, 0), x_rows, k_major(sd, 0), d_rows,
+                                           tc::idesc_bf16_f32(128, KD, 0, 0), p > 0);
+                tc::mma_commit(&m2);
             }
-            if (p + 1 < passes) load_pass(h, (p + 1) * 64);
-            wait(&m2, p12, a.ctrl, ab, 0x634);
-            p12 ^= 1;
+            __syncwarp();
         }
+        wait(&m2, (m * passes + passes - 1) & 1, a.ctrl, ab, 0x637);
         // ---- the triangle: weights w, their row and column sums, and [Yh; -Zh]
         {
             float y[16], kq[16];
@@ -1158,15 +1163,21 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
             const float cs = transpose_sum(kq);
             if (!(lane & 1)) colp[warp & 3][wg * 16 + (lane >> 1)] = cs;
         }
-        // ---- F | G and E: a quarter row of K a thread
+        // ---- F | G and E: a quarter row of K a thread; their part of [dQ; dK]
         {
             const float gam = decay(sums.b[r]), lb = decay(sums.b[C - 1], sums.b[r]) * sums.beta[r];
             float dotf = 0.f, dote = 0.f;
 #pragma unroll
             for (int i0 = 0; i0 < H4; i0 += 16) {
-                float f[16], e[16];
+                float f[16], e[16], acc[16];
                 get16(lanes + COL_FG + wg * H4 + i0, f);
                 get16(lanes + COL_E + wg * H4 + i0, e);
+                if (m > 0) {
+                    get16(lanes + COL_OUT + wg * H4 + i0, acc);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+                }
 #pragma unroll
                 for (int g2 = 0; g2 < 2; ++g2) {
                     const int col = wg * H4 + i0 + g2 * 8;
@@ -1183,13 +1194,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                         const int n = g2 * 8 + i;
                         dotf = fmaf(x[i], f[n], dotf);
                         if (isq) {
-                            acc[i0 + n] = fmaf(s.scale * gam, f[n], acc[i0 + n]);
+                            acc[n] = fmaf(s.scale * gam, f[n], acc[n]);
                         } else {
                             dote = fmaf(x[i], e[n], dote);
-                            acc[i0 + n] += lb * e[n] - gam * f[n];
+                            acc[n] += lb * e[n] - gam * f[n];
                         }
                     }
                 }
+                set16(lanes + COL_OUT + wg * H4 + i0, acc);
             }
             rp[wg][r128] = dotf;
             if (!isq) ep[wg][r] = dote;
@@ -1202,7 +1214,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
         if (hand_over(warp)) {
             // [dQ; dK] += [Yh; -Zh] K; and in the lower rows of COL_E: [Yh; -Zh]^T [Q; K]
             products_ss<4, NT, TB, NT>(tmem + COL_OUT, k_major(sa, 0), a_rows, mn_major(qk + TILE, 0, 2 * TILE), qk_cols,
-                                       tc::idesc_bf16_f32(128, KD, 0, 1), m > 0);
+                                       tc::idesc_bf16_f32(128, KD, 0, 1), 1);
             products_ss<8, NT, TB, NT>(tmem + COL_E, mn_major(sa - 2 * TILE, 0, 2 * TILE), a_cols, mn_major(qk, 0, 2 * TILE),
                                        qk_cols, tc::idesc_bf16_f32(128, KD, 1, 1));
             tc::mma_commit(&m3);
@@ -1264,7 +1276,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                 if (wg * H4 + i0 + g2 * 8 >= s.K) continue;
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = acc[i0 + g2 * 8 + i] + f[g2 * 8 + i] + (isq ? 0.f : e[g2 * 8 + i]);
+                for (int i = 0; i < 8; ++i) x[i] = f[g2 * 8 + i] + (isq ? 0.f : e[g2 * 8 + i]);
                 if constexpr (sizeof(E) == 4) {
                     *(float4 *)(out + i0 + g2 * 8) = make_float4(x[0], x[1], x[2], x[3]);
                     *(float4 *)(out + i0 + g2 * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
