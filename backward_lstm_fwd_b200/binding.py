@@ -8,6 +8,7 @@ shared library is missing, every entry point raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -571,27 +572,34 @@ def _need(ok: bool, what: str) -> None:
 
 def _on(ref: torch.Tensor, **ts) -> None:
     """Every tensor given is on ref's CUDA device."""
-    _need(ref.is_cuda, "tensors must be on a CUDA device")
+    if not ref.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    dev = ref.get_device()
     for name, t in ts.items():
-        _need(t is None or t.device == ref.device, f"{name} is on another device")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on another device")
 
 
 def _dense(**ts) -> None:
     for name, t in ts.items():
-        _need(t is None or t.is_contiguous(), f"{name} must be contiguous")
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype=None) -> None:
     if t is not None:
-        _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
-        _need(dtype is None or t.dtype == dtype, f"{name}: {t.dtype}, want {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name}: {t.dtype}, want {dtype}")
 
 
 def _id_bytes(ids: Optional[torch.Tensor]) -> int:
-    if ids is None:
+    if ids is None or ids.dtype == torch.int64:
         return 8
-    _need(ids.dtype in (torch.int32, torch.int64), f"token ids must be int32 or int64, not {ids.dtype}")
-    return ids.element_size()
+    if ids.dtype != torch.int32:
+        raise ValueError(f"token ids must be int32 or int64, not {ids.dtype}")
+    return 4
 
 
 def _run(code: int, where: str) -> None:
@@ -601,6 +609,34 @@ def _run(code: int, where: str) -> None:
 
 def _ws_bytes(ws: torch.Tensor) -> int:
     return ws.numel() * ws.element_size()
+
+
+def _at(t: Optional[torch.Tensor]):
+    """Device pointer of a tensor that may be absent or empty."""
+    return (t.data_ptr() or None) if t is not None else None
+
+
+class _Device:
+    """The tensor's device made current where it is not (a C call works on the
+    current device), and the stream to enqueue on: `stream`, or that device's
+    current stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.index = t.get_device()
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard = None
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def embed_dims(N: int, vocab: int, I: int, dtype, id_bytes: int = 8) -> EmbedDims:
@@ -618,12 +654,12 @@ def embed(ids, table, scale: float = 1.0, out=None, stream=None) -> torch.Tensor
     vocab, I = table.shape
     shape = (*ids.shape, I)
     _shaped(out, "out", shape, table.dtype)
-    with torch.cuda.device(table.device):
+    with _Device(table, stream) as s:
         if out is None:
             out = torch.empty(shape, dtype=table.dtype, device=table.device)
         d = embed_dims(ids.numel(), vocab, I, table.dtype, _id_bytes(ids))
-        _run(load().lstm_embed_fwd(ctypes.byref(d), _p(ids), _p(table), float(scale), _p(out),
-                                   _stream(stream)), "lstm_embed_fwd")
+        _run(load().lstm_embed_fwd(ctypes.byref(d), _at(ids), _at(table), float(scale), _at(out),
+                                   s), "lstm_embed_fwd")
     return out
 
 
@@ -642,14 +678,14 @@ def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate
     _shaped(dx, "dx", (*ids.shape, I))
     _need(not accumulate or out is not None, "accumulate needs out")
     _shaped(out, "out", (vocab, I), torch.float32)
-    with torch.cuda.device(dx.device):
+    with _Device(dx, stream) as s:
         if out is None:
             out = torch.empty((vocab, I), dtype=torch.float32, device=dx.device)
         d = embed_dims(ids.numel(), vocab, I, dx.dtype, _id_bytes(ids))
         if ws is None:
             ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
-        _run(load().lstm_embed_bwd(ctypes.byref(d), _p(ids), _p(dx), float(scale), int(accumulate),
-                                   _p(out), _p(ws), _ws_bytes(ws), _stream(stream)),
+        _run(load().lstm_embed_bwd(ctypes.byref(d), _at(ids), _at(dx), float(scale), int(accumulate),
+                                   _at(out), _at(ws), _ws_bytes(ws), s),
              "lstm_embed_bwd")
     return out
 
@@ -670,7 +706,7 @@ class LogProbs:
     @property
     def lse(self) -> torch.Tensor:
         """log sum exp(logits / temperature) of every row."""
-        return self.stats[:, 0] * self.inv_temp + self.stats[:, 1]
+        return self.stats[:, 0] * self.inv_temp + self.stats[:, 1] * math.log(2.0)
 
 
 def logprob_dims(N: int, vocab: int, dtype, ld: Optional[int] = None, top: int = 0,
@@ -705,14 +741,14 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0, ws=No
     _dense(targets=targets, ws=ws)
     _shaped(targets, "targets", (N,))
     _need(temperature > 0, "temperature must be positive")
-    with torch.cuda.device(logits.device):
+    with _Device(logits, stream) as s:
         st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
         d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
         if ws is None:
             ws = empty_workspace(logprob_fwd_workspace_size(d), logits.device)
-        _run(load().lstm_logprob_fwd(ctypes.byref(d), _p(logits), _p(targets), st.inv_temp,
-                                     _p(st.logp), _p(st.entropy), _p(st.stats), _p(st.top_ids),
-                                     _p(st.top_logp), _p(ws), _ws_bytes(ws), _stream(stream)),
+        _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
+                                     _at(st.logp), _at(st.entropy), _at(st.stats), _at(st.top_ids),
+                                     _at(st.top_logp), _at(ws), _ws_bytes(ws), s),
              "lstm_logprob_fwd")
     return st
 
@@ -731,13 +767,13 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     _shaped(st.stats, "stats", (N, 2), torch.float32)
     _shaped(out, "out", (N, vocab), logits.dtype)
     _need(1.0 / temperature == st.inv_temp, "temperature differs from the forward's")
-    with torch.cuda.device(logits.device):
+    with _Device(logits, stream) as s:
         if out is None:
             out = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
         d = logprob_dims(N, vocab, logits.dtype, ld, 0, _id_bytes(targets))
-        _run(load().lstm_logprob_bwd(ctypes.byref(d), _p(logits), _p(targets), st.inv_temp,
-                                     _p(st.stats), _p(st.entropy), _p(dlogp), _p(dentropy),
-                                     _p(out), _rows(out, "out"), _stream(stream)),
+        _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
+                                     _at(st.stats), _at(st.entropy), _at(dlogp), _at(dentropy),
+                                     _at(out), _rows(out, "out"), s),
              "lstm_logprob_bwd")
     return out
 
@@ -814,7 +850,7 @@ def _gdr_call(q, k, v, g, beta, lengths, scale):
     _dense(g=g, beta=beta, lengths=lengths)
     d = gdr_dims(T, B, Hk, Hv, K, V, q.dtype, _token_stride(q, "q"), _token_stride(k, "k"),
                  _token_stride(v, "v"))
-    return d, GdrOptions(_p(lengths), K ** -0.5 if scale is None else float(scale))
+    return d, GdrOptions(_at(lengths), K ** -0.5 if scale is None else float(scale))
 
 
 def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool = False, sT=None,
@@ -829,13 +865,13 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     _shaped(s0, "s0", (d.B, d.Hv, d.K, d.V), torch.float32)
     _shaped(sT, "sT", (d.B, d.Hv, d.K, d.V), torch.float32)
     _dense(s0=s0, sT=sT, ws=ws)
-    with torch.cuda.device(q.device):
+    with _Device(q, stream) as s:
         st = GdrState(d, q.dtype, q.device, save, sT)
         if ws is None:
             ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
-        _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _p(q), _p(k), _p(v), _p(g),
-                                 _p(beta), _p(s0), _p(st.o), _p(st.sT), _p(st.states),
-                                 _p(st.deltas), _p(ws), _ws_bytes(ws), _stream(stream)),
+        _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _at(q), _at(k), _at(v), _at(g),
+                                 _at(beta), _at(s0), _at(st.o), _at(st.sT), _at(st.states),
+                                 _at(st.deltas), _at(ws), _ws_bytes(ws), s),
              "lstm_gdr_fwd")
     return st
 
@@ -851,13 +887,13 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
     _shaped(dsT, "dsT", (d.B, d.Hv, d.K, d.V), torch.float32)
     _shaped(st.o, "the state's o", (d.T, d.B, d.Hv, d.V), q.dtype)
     _dense(dout=dout, dsT=dsT, ws=ws)
-    with torch.cuda.device(q.device):
+    with _Device(q, stream) as s:
         gr = GdrGrads(d, q.dtype, q.device)
         if ws is None:
             ws = empty_workspace(gdr_bwd_workspace_size(d), q.device)
-        _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _p(dout), _p(dsT), _p(q),
-                                 _p(k), _p(v), _p(g), _p(beta), _p(st.states), _p(st.deltas),
-                                 _p(gr.dq), _p(gr.dk), _p(gr.dv), _p(gr.dg), _p(gr.dbeta),
-                                 _p(gr.ds0), _p(ws), _ws_bytes(ws), _stream(stream)),
+        _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _at(dout), _at(dsT), _at(q),
+                                 _at(k), _at(v), _at(g), _at(beta), _at(st.states), _at(st.deltas),
+                                 _at(gr.dq), _at(gr.dk), _at(gr.dv), _at(gr.dg), _at(gr.dbeta),
+                                 _at(gr.ds0), _at(ws), _ws_bytes(ws), s),
              "lstm_gdr_bwd")
     return gr

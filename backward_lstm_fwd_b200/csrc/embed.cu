@@ -9,9 +9,11 @@
 // token as zeros).
 //
 // Gradient, in launches on one stream:
-//   sort    least-significant-digit radix sort of (token, position), 9 bits a
-//           pass; per pass one launch of block histograms and one of stable
-//           scatters (the histograms only where more than one block sorts);
+//   sort    stable least-significant-digit radix sort of (token, position), 9
+//           bits a pass: one launch of block histograms, then one a pass that
+//           scatters and counts the next pass's histograms (integers: any
+//           order of the additions gives the same).  One block alone counts
+//           its own;
 //   grad    units of 32 sorted positions x column tiles: a thread adds its
 //           columns of up to 32 rows in order and stores each token that lies
 //           inside the unit; a token that crosses a unit's border leaves
@@ -113,7 +115,8 @@ int lookup(const lstm_embed_dims *d, const void *ids, const void *table, float s
 // -------------------------------------------------------------------- sort
 constexpr int kBits = 9, kBins = 1 << kBits;
 constexpr int kSortWarps = 16, kSortThreads = 32 * kSortWarps;
-constexpr int kWarpKeys = 128, kTile = kSortWarps * kWarpKeys;  // 2048 keys a tile
+constexpr int kWarpKeys = 64, kTile = kSortWarps * kWarpKeys;  // 1024 keys a tile
+constexpr int kRounds = kWarpKeys / 32;
 constexpr int kSortBlocks = 128;                                // most blocks of a sort
 static_assert(kSortThreads == kBins, "one thread per digit");
 
@@ -122,7 +125,7 @@ struct SortArgs {
     int id64, vocab;
     const int *key_in, *pos_in;
     int *key_out, *pos_out;
-    int *hist;               // [blocks][kBins]
+    int *hist, *hist_next;   // [blocks][kBins]: of this pass; of the next one, or NULL
     int N, shift, blocks, tiles;  // every block sorts `tiles` consecutive tiles
 };
 
@@ -144,6 +147,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortArgs a) {
         atomicAdd(&h[(sort_key(a, i) >> a.shift) & (kBins - 1)], 1);
     __syncthreads();
     a.hist[blockIdx.x * kBins + threadIdx.x] = h[threadIdx.x];
+    a.hist_next[blockIdx.x * kBins + threadIdx.x] = 0;
 }
 
 // Exclusive prefix sum over the block's 512 threads.
@@ -196,9 +200,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
         if (t0 >= a.N) break;  // the same for every thread
         for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
         __syncthreads();
-        int key[4], rank[4];
+        int key[kRounds], rank[kRounds];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kRounds; ++j) {
             const long long i = t0 + warp * kWarpKeys + j * 32 + lane;
             key[j] = i < a.N ? sort_key(a, (int)i) : -1;
             const int dg = key[j] < 0 ? kBins : (key[j] >> a.shift) & (kBins - 1);
@@ -224,13 +228,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kRounds; ++j) {
                 if (key[j] < 0) continue;
                 const int dg = (key[j] >> a.shift) & (kBins - 1);
                 const int o = base[dg] + cnt[warp][dg] + rank[j];
                 const int i = (int)(t0 + warp * kWarpKeys + j * 32 + lane);
                 a.key_out[o] = key[j];
                 a.pos_out[o] = a.pos_in ? a.pos_in[i] : i;
+                if (a.hist_next)
+                    atomicAdd(&a.hist_next[o / (a.tiles * kTile) * kBins + ((key[j] >> (a.shift + kBits)) & (kBins - 1))], 1);
             }
             __syncthreads();
             base[tid] = run;
@@ -248,6 +254,7 @@ struct GradArgs {
     const int *key, *pos;  // [N] sorted tokens (padding = vocab, last) and their positions
     const void *dx;
     float *dtable, *pfirst, *plast;
+    Ctrl *ctrl;
     float scale;
     int N, vocab, I, units, accumulate;
 };
@@ -295,6 +302,7 @@ __global__ void __launch_bounds__(kColThreads) grad_kernel(GradArgs a) {
     __shared__ unsigned present;
     const int tid = threadIdx.x;
     const int col = (blockIdx.y * kColThreads + tid) * W;
+    clear_ctrl(a.ctrl);
     if ((int)blockIdx.x >= a.units) {  // rows of the table without a token: zeros
         const int w0 = ((int)blockIdx.x - a.units) * kZeroRows;
         if (tid < 32) {  // lane j: the first place in the sorted tokens that row w0 + j could have
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a
 
 // --------------------------------------------------------------- workspace
 struct BwdLayout {
-    size_t key[2], pos[2], hist, pfirst, plast, total;
+    size_t key[2], pos[2], hist[2], pfirst, plast, total;
     int units;
 };
 
@@ -431,7 +439,7 @@ BwdLayout bwd_layout(const lstm_embed_dims *d) {
         l.key[i] = take((size_t)d->N * 4);
         l.pos[i] = take((size_t)d->N * 4);
     }
-    l.hist = take((size_t)kSortBlocks * kBins * 4);
+    for (int i = 0; i < 2; ++i) l.hist[i] = take((size_t)kSortBlocks * kBins * 4);
     l.pfirst = take((size_t)l.units * d->I * 4);
     l.plast = take((size_t)l.units * d->I * 4);
     l.total = o;
@@ -506,8 +514,6 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
     if (!out) return LSTM_OK;
     cudaStream_t s = (cudaStream_t)stream;
     char *w = (char *)ws;
-    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, s));
-
     // sort: enough 9-bit passes for the largest key, which is vocab (padding)
     int cur = 0;
     if (d->N > 0) {
@@ -520,21 +526,28 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
         a.id64 = d->id_bytes == 8;
         a.vocab = d->vocab;
         a.N = d->N;
-        a.hist = (int *)(w + l.hist);
         a.ids = ids;
+        int *hist[2] = {(int *)(w + l.hist[0]), (int *)(w + l.hist[1])};
+        if (a.blocks > 1) {
+            a.hist = hist[0];
+            a.hist_next = hist[1];
+            sort_hist_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
+            LSTM_CUDA_TRY(host::launched());
+        }
         for (int shift = 0; shift < bits; shift += kBits) {
+            const bool more = a.blocks > 1 && shift + kBits < bits;
             a.shift = shift;
             a.key_out = (int *)(w + l.key[cur]);
             a.pos_out = (int *)(w + l.pos[cur]);
-            if (a.blocks > 1) {
-                sort_hist_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
-                LSTM_CUDA_TRY(host::launched());
-            }
+            a.hist = hist[0];
+            a.hist_next = more ? hist[1] : nullptr;
+            if (more && shift > 0) LSTM_CUDA_TRY(cudaMemsetAsync(hist[1], 0, (size_t)a.blocks * kBins * 4, s));
             sort_scatter_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
             LSTM_CUDA_TRY(host::launched());
             a.ids = nullptr;
             a.key_in = a.key_out;
             a.pos_in = a.pos_out;
+            std::swap(hist[0], hist[1]);
             cur ^= 1;
         }
         cur ^= 1;
@@ -546,6 +559,7 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
     g.dtable = dtable;
     g.pfirst = (float *)(w + l.pfirst);
     g.plast = (float *)(w + l.plast);
+    g.ctrl = (Ctrl *)ws;
     g.scale = scale;
     g.N = d->N;
     g.vocab = d->vocab;

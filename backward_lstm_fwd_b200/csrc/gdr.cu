@@ -121,8 +121,8 @@ int chunked_fwd(const Shape &s, const void *q, const void *k, const void *v, con
 
 template <class E>
 int stepwise_fwd(const Shape &s, const void *q, const void *k, const void *v, const float *g, const float *beta,
-                 const float *s0, void *o, float *sT, cudaStream_t st) {
-    StepArgs a = {s, q, k, v, g, beta, s0, o, sT, (s.V + STEP_COLS - 1) / STEP_COLS};
+                 const float *s0, void *o, float *sT, char *w, cudaStream_t st) {
+    StepArgs a = {s, q, k, v, g, beta, s0, o, sT, (Ctrl *)w, (s.V + STEP_COLS - 1) / STEP_COLS};
     step_kernel<E><<<s.B * s.Hv * a.tiles, STEP_THREADS, 0, st>>>(a);
     LSTM_CUDA_TRY(host::launched());
     return LSTM_OK;
@@ -132,7 +132,7 @@ template <class E>
 int fwd(const lstm_gdr_dims *d, const Shape &s, const void *q, const void *k, const void *v, const float *g,
         const float *beta, const float *s0, void *o, float *sT, float *states, float *deltas, char *w,
         cudaStream_t st) {
-    if (stepwise(d, states != nullptr)) return stepwise_fwd<E>(s, q, k, v, g, beta, s0, o, sT, st);
+    if (stepwise(d, states != nullptr)) return stepwise_fwd<E>(s, q, k, v, g, beta, s0, o, sT, w, st);
     const Layout l = layout(d, false);
     if (s.K <= 64) return chunked_fwd<E, 64>(s, q, k, v, g, beta, s0, o, sT, states, deltas, w, l, st);
     return chunked_fwd<E, 128>(s, q, k, v, g, beta, s0, o, sT, states, deltas, w, l, st);
@@ -198,7 +198,6 @@ int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
     if (rc != LSTM_OK) return rc;
     if ((long long)d->B * d->Hv * d->V == 0) return LSTM_OK;
     cudaStream_t st = (cudaStream_t)stream;
-    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, st));
     const Shape s = shape_of(d, opt);
     char *w = (char *)ws;
     if (d->dtype == LSTM_F32) return fwd<float>(d, s, q, k, v, g, beta, s0, o, sT, states, deltas, w, st);
@@ -238,7 +237,6 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
         }
         return LSTM_OK;
     }
-    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, st));
     const Shape s = shape_of(d, opt);
     char *w = (char *)ws;
     if (d->dtype == LSTM_F32)

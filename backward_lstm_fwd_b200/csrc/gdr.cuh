@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
     __shared__ int abort_flag;
     const Shape &s = a.s;
     const int tid = threadIdx.x, warp = warp_id(), lane = tid & 31;
+    clear_ctrl(a.ctrl);
     int id = blockIdx.x;
     const int hk = id % s.Hk;
     id /= s.Hk;
@@ -699,6 +700,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     constexpr Steps rows = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};   // K-major q or k: K over the dims
     constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};       // MN-major k: K over the tokens
     constexpr Steps mat = {TILE >> 4, 2, 0};                           // K-major T2, P
+    if (s.NC == 0) clear_ctrl(a.ctrl);  // (else prep did)
     if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, false);
     __syncwarp();
     float S[H4], o[16];
@@ -824,6 +826,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     constexpr Steps rows = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};
     constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};
     constexpr Steps mat = {TILE >> 4, 2048 >> 4, 0};                   // MN-major T2, P: transposed
+    if (s.NC == 0) clear_ctrl(a.ctrl);
     if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, true);
     __syncwarp();
     float S[H4];
@@ -1293,9 +1296,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
 
 // -------------------------------------------------------------------- step
 // A few tokens, token by token: block (b, h, 64 columns of V), thread (part,
-// column) holds the column's state for a quarter of K in registers.  Bound:
-// the state's read and write.
-constexpr int STEP_THREADS = 256, STEP_COLS = 64, STEP_PARTS = 4, STEP_K = 128 / STEP_PARTS;
+// columns) holds four columns of the state for eight rows of K in registers.
+// Bound: the state's read and write.
+constexpr int STEP_THREADS = 256, STEP_COLS = 64, STEP_PARTS = 16, STEP_K = 128 / STEP_PARTS;
 
 struct StepArgs {
     Shape s;
@@ -1303,30 +1306,68 @@ struct StepArgs {
     const float *g, *beta, *s0;
     void *o;
     float *sT;
+    Ctrl *ctrl;
     int tiles;  // blocks of 64 columns
 };
 
 template <class E>
-__global__ void __launch_bounds__(STEP_THREADS) step_kernel(StepArgs a) {
-    __shared__ float qs[128], ks[128], part[2][STEP_PARTS][STEP_COLS];
+__global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
+    __shared__ float qs[128], ks[128];
+    __shared__ float4 part[2][8][STEP_COLS / 4];  // a warp's two parts together
     const Shape &s = a.s;
-    const int tid = threadIdx.x, part_id = tid / STEP_COLS, v0 = (blockIdx.x % a.tiles) * STEP_COLS;
-    const int col = tid % STEP_COLS, v = v0 + col, id = blockIdx.x / a.tiles, h = id % s.Hv, b = id / s.Hv, hk = h / s.group;
+    clear_ctrl(a.ctrl);
+    const int tid = threadIdx.x, warp = tid >> 5, c4 = tid & 15, v = blockIdx.x % a.tiles * STEP_COLS + c4 * 4;
+    const int id = blockIdx.x / a.tiles, h = id % s.Hv, b = id / s.Hv, hk = h / s.group;
     const long long head = (long long)b * s.Hv + h;
-    const int len = length_of(s, b), k0 = part_id * STEP_K;
-    const bool own = v < s.V;
-    float S[STEP_K];
+    const int len = length_of(s, b), k0 = (tid >> 4) * STEP_K;
+    const bool own = v < s.V;  // V is a multiple of 8: all four or none
+    float4 S[STEP_K];
 #pragma unroll
     for (int i = 0; i < STEP_K; ++i)
-        S[i] = a.s0 && own && k0 + i < s.K ? __ldcs(a.s0 + (head * s.K + k0 + i) * s.V + v) : 0.f;
+        S[i] = a.s0 && own && k0 + i < s.K ? __ldcs((const float4 *)(a.s0 + (head * s.K + k0 + i) * s.V + v))
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    // the columns' sums over K of w[k] S[k], in every thread
+    auto contract = [&](const float *w, int buf) {
+        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < STEP_K; ++i) {
+            const float x = w[k0 + i];
+            d.x = fmaf(x, S[i].x, d.x);
+            d.y = fmaf(x, S[i].y, d.y);
+            d.z = fmaf(x, S[i].z, d.z);
+            d.w = fmaf(x, S[i].w, d.w);
+        }
+        d.x += __shfl_xor_sync(~0u, d.x, 16);
+        d.y += __shfl_xor_sync(~0u, d.y, 16);
+        d.z += __shfl_xor_sync(~0u, d.z, 16);
+        d.w += __shfl_xor_sync(~0u, d.w, 16);
+        if ((tid & 16) == 0) part[buf][warp][c4] = d;
+        __syncthreads();
+        d = part[buf][0][c4];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            const float4 e = part[buf][i][c4];
+            d.x += e.x;
+            d.y += e.y;
+            d.z += e.z;
+            d.w += e.w;
+        }
+        return d;
+    };
     for (int t = 0; t < s.T; ++t) {
         const long long r = (long long)t * s.B + b;
         E *o = (E *)a.o + (r * s.Hv + h) * s.V + v;
+        const bool writes = tid < 16 && own;
         if (t >= len) {  // padding: the same for the whole block
-            if (part_id == 0 && own) *o = from_f<E>(0.f);
+            if (writes)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = from_f<E>(0.f);
             continue;
         }
-        const float x = own ? to_f(((const E *)a.v)[r * s.ldv + (long long)h * s.V + v]) : 0.f;
+        float x[4] = {};
+        if (own)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = to_f(((const E *)a.v)[r * s.ldv + (long long)h * s.V + v + i]);
         const float gt = a.g[r * s.Hv + h], be = a.beta[r * s.Hv + h];
         if (tid < 128)
             qs[tid] = tid < s.K ? to_f(((const E *)a.q)[r * s.ldq + (long long)hk * s.K + tid]) : 0.f;
@@ -1334,33 +1375,34 @@ __global__ void __launch_bounds__(STEP_THREADS) step_kernel(StepArgs a) {
             ks[tid - 128] = tid - 128 < s.K ? to_f(((const E *)a.k)[r * s.ldk + (long long)hk * s.K + tid - 128]) : 0.f;
         const float dec = expf(gt);
         __syncthreads();
-        float d0 = 0.f, d1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < STEP_K; i += 2) {
-            S[i] *= dec;
-            S[i + 1] *= dec;
-            d0 = fmaf(ks[k0 + i], S[i], d0);
-            d1 = fmaf(ks[k0 + i + 1], S[i + 1], d1);
+        for (int i = 0; i < STEP_K; ++i) {
+            S[i].x *= dec;
+            S[i].y *= dec;
+            S[i].z *= dec;
+            S[i].w *= dec;
         }
-        part[0][part_id][col] = d0 + d1;
-        __syncthreads();
-        const float u = be * (x - ((part[0][0][col] + part[0][1][col]) + (part[0][2][col] + part[0][3][col])));
-        d0 = d1 = 0.f;
+        float4 u = contract(ks, 0);
+        u = make_float4(be * (x[0] - u.x), be * (x[1] - u.y), be * (x[2] - u.z), be * (x[3] - u.w));
 #pragma unroll
-        for (int i = 0; i < STEP_K; i += 2) {
-            S[i] = fmaf(ks[k0 + i], u, S[i]);
-            S[i + 1] = fmaf(ks[k0 + i + 1], u, S[i + 1]);
-            d0 = fmaf(qs[k0 + i], S[i], d0);
-            d1 = fmaf(qs[k0 + i + 1], S[i + 1], d1);
+        for (int i = 0; i < STEP_K; ++i) {
+            const float k = ks[k0 + i];
+            S[i].x = fmaf(k, u.x, S[i].x);
+            S[i].y = fmaf(k, u.y, S[i].y);
+            S[i].z = fmaf(k, u.z, S[i].z);
+            S[i].w = fmaf(k, u.w, S[i].w);
         }
-        part[1][part_id][col] = d0 + d1;
-        __syncthreads();
-        if (part_id == 0 && own)
-            *o = from_f<E>(s.scale * ((part[1][0][col] + part[1][1][col]) + (part[1][2][col] + part[1][3][col])));
+        const float4 y = contract(qs, 1);
+        if (writes) {
+            o[0] = from_f<E>(s.scale * y.x);
+            o[1] = from_f<E>(s.scale * y.y);
+            o[2] = from_f<E>(s.scale * y.z);
+            o[3] = from_f<E>(s.scale * y.w);
+        }
     }
 #pragma unroll
     for (int i = 0; i < STEP_K; ++i)
-        if (own && k0 + i < s.K) __stcs(a.sT + (head * s.K + k0 + i) * s.V + v, S[i]);
+        if (own && k0 + i < s.K) __stcs((float4 *)(a.sT + (head * s.K + k0 + i) * s.V + v), S[i]);
 }
 
 }  // namespace gdr

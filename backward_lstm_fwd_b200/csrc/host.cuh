@@ -10,6 +10,14 @@
 #include "common.cuh"
 
 namespace lstm {
+
+// First kernel of a call: clear the workspace's control block (the status
+// word reports the call that this kernel begins).
+__device__ __forceinline__ void clear_ctrl(Ctrl *ctrl) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(Ctrl) / 4)
+        reinterpret_cast<unsigned int *>(ctrl)[threadIdx.x] = 0u;
+}
+
 namespace host {
 
 #define LSTM_CUDA_TRY(expr)                               \

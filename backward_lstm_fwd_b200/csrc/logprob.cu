@@ -5,10 +5,13 @@
 // and the `top` largest logits (ties: the lowest index first).  The gradient is
 //   dlogits = (dlogp (1[target] - p) - dentropy p (z - lse + entropy)) / temperature.
 //
-// Bound: bytes.  The forward reads the logits once: every thread keeps the
-// running maximum m of its elements with s = sum e^{z-m} and
-// w = sum e^{z-m} (x - m), rescaled when a batch of elements raises m, and the
-// threads' triples are joined at the end.  The alternatives come from the same
+// Bound: bytes.  The forward reads the logits once: with c = log2(e) /
+// temperature, every thread keeps its largest logit m, s = sum 2^{c (x - m)}
+// and w = sum 2^{c (x - m)} c (x - m), rescaled when a group of elements
+// raises m, and the threads' triples are joined at the end.  An element costs
+// one fused multiply-add, one exponential and three more operations; the 128
+// threads a block and eight blocks an SM let one row's loads run beside
+// another's joins.  The alternatives come from the same
 // pass: the first eighth of the range gives every thread its own maximum, the
 // top-th largest of those is a lower bound of the answer, and only elements at
 // or above it (a few times `top`) enter a candidate list; the eighth is looked
@@ -27,7 +30,8 @@ namespace {
 typedef __nv_bfloat16 bf16;
 typedef __half f16;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kCand = 1024;  // candidate list of a block
 constexpr int kMinPart = 2048;  // fewest elements of a part of a row
 static_assert(LSTM_LOGPROB_MAX_TOP <= 64, "the candidate list is sized for 64 alternatives");
@@ -80,34 +84,48 @@ __device__ __forceinline__ unsigned long long key_of(float x, int i) {
 __device__ __forceinline__ int index_of(unsigned long long key) { return (int)~(unsigned)key; }
 
 // --------------------------------------------------- running softmax triple
+// With c = log2(e) / temperature and m the largest logit:
 struct Stat {
-    float m, s, w;  // maximum; sum e^{c (x - m)}; sum e^{c (x - m)} (x - m)
+    float m, s, w;  // m; sum 2^{c (x - m)}; sum 2^{c (x - m)} c (x - m)
 };
-__device__ __forceinline__ void raise(Stat &a, float m, float c) {  // m >= a.m
-    const float d = floor_nan(a.m - m), f = ex2(d * c);
-    a.w = (a.w + a.s * d) * f;
-    a.s *= f;
-    a.m = m;
-}
 __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
     const float m = fmaxf(a.m, b.m);
     if (m == -INFINITY) return Stat{m, a.s + b.s, a.w + b.w};  // nothing but -inf (or NaN) yet
-    raise(a, m, c);
-    raise(b, m, c);
-    return Stat{m, a.s + b.s, a.w + b.w};
+    const float da = floor_nan((a.m - m) * c), db = floor_nan((b.m - m) * c), fa = ex2(da), fb = ex2(db);
+    return Stat{m, a.s * fa + b.s * fb, (a.w + a.s * da) * fa + (b.w + b.s * db) * fb};
 }
-template <int n> __device__ __forceinline__ void add(Stat &a, const float (&f)[n], float c, float &gmax) {
+// A thread's own sums, with the rounded c m in the place of c m, so that an
+// exponent is one fused multiply-add.
+struct Run {
+    float m, cm, s, w;
+};
+// gmax: the largest of f.
+template <int n> __device__ __forceinline__ void add(Run &a, const float (&f)[n], float c, float &gmax) {
     gmax = f[0];
 #pragma unroll
     for (int i = 1; i < n; ++i) gmax = fmaxf(gmax, f[i]);
-    if (gmax > a.m) raise(a, gmax, c);
-    const float m = a.m == -INFINITY ? 0.f : a.m;
+    if (gmax > a.m) {
+        const float cm = fmaxf(gmax * c, -3.4e38f), d = floor_nan(a.cm - cm), e = ex2(d);
+        a.w = (a.w + a.s * d) * e;
+        a.s *= e;
+        a.m = gmax;
+        a.cm = cm;
+    }
+    const float cm = a.cm == -INFINITY ? 0.f : a.cm;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-        const float d = floor_nan(f[i] - m), e = ex2(d * c);
+        const float d = floor_nan(fmaf(f[i], c, -cm)), e = ex2(d);
         a.s += e;
         a.w = fmaf(e, d, a.w);
     }
+}
+// Logits below this are masks: c m may overflow for them.  (A row of nothing
+// else is summed again by the block, see there.)
+constexpr float kMask = -1e16f;
+__device__ __forceinline__ Stat stat_of(const Run &a, float c) {
+    if (!(a.m > kMask)) return Stat{a.m, a.s, a.w};  // s and w are 0, or NaN
+    const float d = fmaf(-a.m, c, a.cm), e = ex2(d);  // what the rounding of c m left
+    return Stat{a.m, a.s * e, (a.w + a.s * d) * e};
 }
 __device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
 #pragma unroll
@@ -130,11 +148,12 @@ struct Args {
     const void *targets;
     int id64, N, vocab, top, parts;
     long long ld;
-    float inv_temp;
+    float c;  // inverse temperature times log2(e)
     float *logp, *entropy, *stats, *top_logp;
     int *top_ids;
     Stat *part_stats;                     // [N][parts]
     unsigned long long *part_keys;        // [N][parts][top]
+    Ctrl *ctrl;
 };
 
 __device__ __forceinline__ long long target_of(const void *t, int id64, int r) {
@@ -145,17 +164,17 @@ __device__ __forceinline__ long long target_of(const void *t, int id64, int r) {
 template <class T>
 __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsigned long long *keys) {
     const bool empty = st.m == -INFINITY && st.s == 0.f;  // every logit is -inf
-    const float ls = logf(st.s);
+    const float ls = log2f(st.s);
     if (threadIdx.x == 0) {
         a.stats[2LL * r] = st.m;
         a.stats[2LL * r + 1] = empty ? 0.f : ls;
-        if (a.entropy) a.entropy[r] = empty ? 0.f : ls - a.inv_temp * (st.w / st.s);
+        if (a.entropy) a.entropy[r] = empty ? 0.f : (ls - st.w / st.s) * kLn2;
         if (a.logp) {
             const long long t = target_of(a.targets, a.id64, r);
             float lp = 0.f;  // an ignored row
             if (t >= 0 && t < a.vocab) {
                 const float x = to_f(((const T *)a.logits)[(long long)r * a.ld + t]);
-                lp = empty ? -INFINITY : (x - st.m) * a.inv_temp - ls;
+                lp = empty ? -INFINITY : ((x - st.m) * a.c - ls) * kLn2;
             }
             a.logp[r] = lp;
         }
@@ -163,7 +182,7 @@ __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsi
     for (int i = threadIdx.x; i < a.top; i += kThreads) {
         const unsigned long long k = keys[i];
         a.top_ids[(long long)r * a.top + i] = index_of(k);
-        a.top_logp[(long long)r * a.top + i] = empty ? -INFINITY : (value_of(k) - st.m) * a.inv_temp - ls;
+        a.top_logp[(long long)r * a.top + i] = empty ? -INFINITY : ((value_of(k) - st.m) * a.c - ls) * kLn2;
     }
 }
 
@@ -178,16 +197,21 @@ __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n,
     __syncthreads();
 }
 
-// The top-th largest of the block's 256 thread maxima (-inf where fewer than
+// The top-th largest of the block's thread maxima (-inf where fewer than
 // `top` threads have one): at least `top` elements are at or above it.
 __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, float *bound) {
     maxima[threadIdx.x] = mine;
     if (threadIdx.x == 0) *bound = -INFINITY;
     __syncthreads();
     int rank = 0;
-    for (int j = 0; j < kThreads; ++j) {
-        const float o = maxima[j];
-        rank += o > mine || (o == mine && j < (int)threadIdx.x);
+#pragma unroll 4
+    for (int j = 0; j < kThreads; j += 4) {
+        const float4 o = *(const float4 *)(maxima + j);
+        const int t = threadIdx.x;
+        rank += o.x > mine || (o.x == mine && j < t);
+        rank += o.y > mine || (o.y == mine && j + 1 < t);
+        rank += o.z > mine || (o.z == mine && j + 2 < t);
+        rank += o.w > mine || (o.w == mine && j + 3 < t);
     }
     if (rank == top - 1) *bound = mine;
     __syncthreads();
@@ -197,16 +221,18 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, fl
 // ----------------------------------------------------------------- forward
 // Block (r, p): part p of row r.  TOP: alternatives wanted.
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
     constexpr int n = Group<T>::n, U = 4;
     __shared__ Stat warp_stats[kWarps];
     __shared__ unsigned long long cand[TOP ? kCand : 1], best[TOP ? LSTM_LOGPROB_MAX_TOP : 1];
-    __shared__ float maxima[TOP ? kThreads : 1], bound_s;
+    __shared__ __align__(16) float maxima[TOP ? kThreads : 4];
+    __shared__ float bound_s;
     __shared__ int count;
     const int tid = threadIdx.x;
     const int r = blockIdx.x / a.parts, p = blockIdx.x % a.parts;
+    clear_ctrl(a.ctrl);
     const T *row = (const T *)a.logits + (long long)r * a.ld;
-    const float c = a.inv_temp * 1.44269504088896340736f;  // log2(e)
+    const float c = a.c;
     // part p is the elements [e0, e1); its 16-byte groups [g0, g1)
     const int e0 = (int)((long long)a.vocab * p / a.parts), e1 = (int)((long long)a.vocab * (p + 1) / a.parts);
     const int mis = (int)(((uintptr_t)(row + e0) & 15u) / sizeof(T));
@@ -214,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(Args a) {
     const int groups = (e1 - h) / n;
     const uint4 *gp = (const uint4 *)(row + h);
     const int tail = h + groups * n;                  // [tail, e1): after the last one
-    Stat st = {-INFINITY, 0.f, 0.f};
+    Run sum = {-INFINITY, -INFINITY, 0.f, 0.f};
     float bound = -INFINITY, gmax;
     if (TOP && tid == 0) count = 0;
 
@@ -241,16 +267,16 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(Args a) {
 
     edge([&](float x, int) {
         const float f[1] = {x};
-        add<1>(st, f, c, gmax);
+        add<1>(sum, f, c, gmax);
     });
     const int first = TOP ? min(groups, max(groups / 8, U * kThreads)) : 0;
     if (TOP) {
         run(0, first, [&](const uint4 &v, int) {
             float f[n];
             unpack<T>(v, f);
-            add<n>(st, f, c, gmax);
+            add<n>(sum, f, c, gmax);
         });
-        bound = bound_of(st.m, a.top, maxima, &bound_s);
+        bound = bound_of(sum.m, a.top, maxima, &bound_s);
         edge([&](float x, int i) {
             if (!(x < bound)) push(x, i);
         });
@@ -265,14 +291,24 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(Args a) {
     run(first, groups, [&](const uint4 &v, int g) {
         float f[n];
         unpack<T>(v, f);
-        add<n>(st, f, c, gmax);
+        add<n>(sum, f, c, gmax);
         if (TOP && !(gmax < bound)) {
 #pragma unroll
             for (int i = 0; i < n; ++i)
                 if (!(f[i] < bound)) push(f[i], h + g * n + i);
         }
     });
-    st = block_join(st, c, warp_stats);  // its barrier also closes the candidate list
+    Stat st = block_join(stat_of(sum, c), c, warp_stats);  // its barrier also closes the candidate list
+    if (st.m <= kMask && st.m > -INFINITY) {  // nothing but masked logits: their plain sums
+        Stat mine = {st.m, 0.f, 0.f};
+        for (int i = e0 + tid; i < e1; i += kThreads) {
+            const float d = floor_nan((to_f(row[i]) - st.m) * c), e = ex2(d);
+            mine.s += e;
+            mine.w = fmaf(e, d, mine.w);
+        }
+        __syncthreads();
+        st = block_join(mine, c, warp_stats);
+    }
 
     if (TOP) {
         if (count <= kCand) {
@@ -316,16 +352,16 @@ template <class T>
 __global__ void __launch_bounds__(kThreads) join_kernel(Args a) {
     __shared__ Stat warp_stats[kWarps];
     __shared__ unsigned long long cand[kCand], best[LSTM_LOGPROB_MAX_TOP];
-    __shared__ float maxima[kThreads], bound_s;
+    __shared__ __align__(16) float maxima[kThreads];
+    __shared__ float bound_s;
     __shared__ int count;
     const int r = blockIdx.x, tid = threadIdx.x;
-    const float c = a.inv_temp * 1.44269504088896340736f;
     Stat st = {-INFINITY, 0.f, 0.f};
     if (tid < a.parts) st = a.part_stats[(long long)r * a.parts + tid];
     if (tid == 0) count = 0;
-    st = block_join(st, c, warp_stats);
+    st = block_join(st, a.c, warp_stats);
     if (a.top) {
-        // a part's first alternative is its maximum; parts <= 256 = kThreads
+        // a part's first alternative is its maximum; parts <= kThreads
         const unsigned long long *keys = a.part_keys + (long long)r * a.parts * a.top;
         const float mine = tid < a.parts ? value_of(keys[(long long)tid * a.top]) : -INFINITY;
         const float bound = bound_of(mine == mine ? mine : -INFINITY, a.top, maxima, &bound_s);
@@ -380,20 +416,19 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(BwdArgs a) {
     const int r = blockIdx.x / a.chunks, p = blockIdx.x % a.chunks;
     const T *x = (const T *)a.logits + (long long)r * a.ld;
     T *y = (T *)a.dlogits + (long long)r * a.ldd;
-    const float m = a.stats[2LL * r], ls = a.stats[2LL * r + 1], c = a.inv_temp;
-    const float dh = a.dentropy ? a.dentropy[r] : 0.f, ent = a.dentropy ? a.entropy[r] : 0.f;
+    const float m = a.stats[2LL * r], ls = a.stats[2LL * r + 1], c = a.inv_temp * kLog2e;
+    const float dh = a.dentropy ? a.dentropy[r] : 0.f, ent = a.dentropy ? a.entropy[r] * kLog2e : 0.f;
     long long t = -1;
     if (a.targets) t = target_of(a.targets, a.id64, r);
     const bool hit = t >= 0 && t < a.vocab;
-    const float dl = hit && a.dlogp ? a.dlogp[r] : 0.f;
+    const float dl = hit && a.dlogp ? a.dlogp[r] * a.inv_temp : 0.f, dhc = dh * a.inv_temp * kLn2;
     const bool empty = m == -INFINITY && ls == ls;
-    // d(z) = dl 1[target] - p (dl + dh (log p + entropy)), times 1 / temperature
+    // dl 1[target] - p (dl + dh (log p + entropy)), dl and dh over the temperature
     auto grad = [&](float v, int i) {
-        const float lp = floor_nan((v - m) * c - ls);
-        const float pr = ex2(lp * 1.44269504088896340736f);
-        float g = -pr * (dl + dh * (lp + ent));
+        const float lp = floor_nan((v - m) * c - ls);  // log2 p
+        float g = -ex2(lp) * fmaf(dhc, lp + ent, dl);
         if (i == (int)t) g += dl;
-        return empty ? 0.f : g * c;
+        return empty ? 0.f : g;
     };
     const int e0 = p * a.chunk, e1 = min(a.vocab, e0 + a.chunk);
     if (!VEC) {
@@ -440,7 +475,7 @@ bool dims_supported(const lstm_logprob_dims *d) {
 // exponential of zero at every temperature.
 bool temp_ok(float inv_temp) { return inv_temp >= 1e-20f && inv_temp <= 1e20f; }
 
-// Parts of a row: one where the rows alone fill the card four blocks an SM
+// Parts of a row: one where the rows alone fill the card two blocks an SM
 // deep; else enough for two blocks an SM, of kMinPart elements at least.
 int parts_of(const lstm_logprob_dims *d, int sms) {
     if (d->N >= 2 * sms) return 1;
@@ -519,7 +554,7 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     a.top = d->top;
     a.parts = parts;
     a.ld = d->ld;
-    a.inv_temp = inv_temp;
+    a.c = inv_temp * kLog2e;
     a.logp = logp;
     a.entropy = entropy;
     a.stats = stats;
@@ -527,7 +562,7 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     a.top_logp = top_logp;
     a.part_stats = (Stat *)((char *)ws + kCtrlBytes);
     a.part_keys = (unsigned long long *)((char *)ws + kCtrlBytes + align_up((size_t)d->N * parts * sizeof(Stat), 256));
-    LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, s));
+    a.ctrl = (Ctrl *)ws;
     if (d->dtype == LSTM_F32) return forward<float>(a, s);
     if (d->dtype == LSTM_F16) return forward<f16>(a, s);
     return forward<bf16>(a, s);

@@ -352,7 +352,8 @@ int lstm_fwd_noalloc_status(void *stream);
  * memory and workspaces of 256-byte alignment, status codes, asynchronous on
  * `stream`, nothing enqueued after an argument error); no call reads a host
  * value from the device, so each can be captured into a graph.  Empty
- * problems are valid.
+ * problems are valid (a call with nothing to compute leaves the workspace and
+ * its status word alone).
  * --------------------------------------------------------------------- */
 
 /*
@@ -462,8 +463,8 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
  *   logp [N]       float  log p[targets_r]; 0 for a target outside
  *                         0 .. vocab-1 (an ignored row); needs targets; or NULL
  *   entropy [N]    float  -sum p log p, or NULL
- *   stats [N][2]   float  the largest logit m and log sum exp(z - m inv_temp),
- *                         for the backward
+ *   stats [N][2]   float  for the backward: m, the row's largest logit, and
+ *                         log2 sum exp(z - m inv_temp)
  *   top_ids [N][top] int, top_logp [N][top] float: the `top` (0 ..
  *                         LSTM_LOGPROB_MAX_TOP, at most vocab) largest logits,
  *                         equal ones by lower id, and their log p; NULL at 0
