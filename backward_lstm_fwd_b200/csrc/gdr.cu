@@ -50,12 +50,43 @@ bool stepwise(const lstm_gdr_dims *d, bool save) { return !save && d->T <= kStep
 
 int terms_of(int dtype) { return dtype == LSTM_BF16 ? 1 : dtype == LSTM_F16 ? 2 : 3; }
 
+// Segments of the chunk sequence (see SeqArgs): the number with the lowest
+// estimated time, from microseconds per chunk of a pass that writes its
+// outputs (4.0) and of one that does not (3.2), per joined segment (3.0) and
+// for two more launches (8), measured on a B200; 1 where splitting gains less
+// than a tenth.
+struct Split {
+    int segments, chunks;
+};
+Split split_of(const lstm_gdr_dims *d) {
+    const int nc = (d->T + C - 1) / C, sms = host::sm_count();
+    const long long heads = (long long)d->B * d->Hv, vt = (d->V + LANES - 1) / LANES;
+    auto waves = [&](long long blocks) { return (double)((blocks + sms - 1) / sms); };
+    Split best = {1, std::max(nc, 1)};
+    double cost = 0.9 * waves(heads * vt) * nc * 4.0;
+    if (heads * vt > sms) return best;
+    for (int n = 2; n <= 32 && 2 * n <= nc; ++n) {
+        const int len = (nc + n - 1) / n, segs = (nc + len - 1) / len;
+        if (segs < 2) continue;
+        const long long scan = (segs - 1) * heads * (vt + 1) - heads;
+        const double t = waves(scan) * len * 3.2 + (segs - 2) * 3.0 + waves(segs * heads * vt) * len * 4.0 + 8.0;
+        if (t < cost) {
+            cost = t;
+            best = {segs, len};
+        }
+    }
+    return best;
+}
+
 struct Layout {
-    size_t qk, tp, dstates, dvf, total;
+    size_t qk, tp, starts, trans, dstates, dvf, total;
+    Split split;
 };
 Layout layout(const lstm_gdr_dims *d, bool bwd) {
     Layout l;
     const size_t nc = (d->T + C - 1) / C, kd = d->K <= 64 ? 64 : 128;
+    l.split = split_of(d);
+    const size_t joints = (size_t)(l.split.segments - 1) * d->B * d->Hv;
     size_t o = kCtrlBytes;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -64,6 +95,8 @@ Layout layout(const lstm_gdr_dims *d, bool bwd) {
     };
     l.qk = take(nc * d->B * d->Hk * (terms_of(d->dtype) * kd * 256));
     l.tp = take(nc * d->B * d->Hv * (size_t)TP_BYTES);
+    l.starts = take(joints * d->K * d->V * 4);
+    l.trans = take(joints * (NT * kd * kd * 2));
     l.dstates = bwd ? take(nc * d->B * d->Hv * (size_t)d->K * d->V * 4) : 0;
     l.dvf = bwd ? take((size_t)d->T * d->B * d->Hv * d->V * 4) : 0;
     l.total = o;
@@ -104,6 +137,25 @@ int prep(const Shape &s, const void *q, const void *k, const float *g, const flo
     return LSTM_OK;
 }
 
+// The chunks in order, by segments where the split says so.
+template <int KD, class Kern> int sequential(const SeqArgs &a, Kern scan, Kern run, size_t smem, cudaStream_t st) {
+    const int heads = a.s.B * a.s.Hv;
+    if (a.segments > 1) {
+        LSTM_CUDA_TRY(allow_smem(scan, smem));
+        scan<<<(a.segments - 1) * heads * (a.s.VT + 1), SEQ_THREADS, smem, st>>>(a);
+        LSTM_CUDA_TRY(host::launched());
+        if (a.segments > 2) {
+            LSTM_CUDA_TRY(allow_smem(scan_kernel<KD>, ScanSmem<KD>::smem));
+            scan_kernel<KD><<<heads * a.s.VT, SEQ_THREADS, ScanSmem<KD>::smem, st>>>(a);
+            LSTM_CUDA_TRY(host::launched());
+        }
+    }
+    LSTM_CUDA_TRY(allow_smem(run, smem));
+    run<<<a.segments * heads * a.s.VT, SEQ_THREADS, smem, st>>>(a);
+    LSTM_CUDA_TRY(host::launched());
+    return LSTM_OK;
+}
+
 template <class E, int KD>
 int chunked_fwd(const Shape &s, const void *q, const void *k, const void *v, const float *g, const float *beta,
                 const float *s0, void *o, float *sT, float *states, float *deltas, char *w, const Layout &l,
@@ -112,11 +164,9 @@ int chunked_fwd(const Shape &s, const void *q, const void *k, const void *v, con
         const int rc = prep<E, KD>(s, q, k, g, beta, w, l, st);
         if (rc != LSTM_OK) return rc;
     }
-    SeqArgs a = {s, w + l.qk, w + l.tp, v, s0, o, sT, states, deltas, (Ctrl *)w};
-    LSTM_CUDA_TRY(allow_smem(seq_fwd_kernel<E, KD>, Seq<E, KD>::smem));
-    seq_fwd_kernel<E, KD><<<s.B * s.Hv * s.VT, SEQ_THREADS, Seq<E, KD>::smem, st>>>(a);
-    LSTM_CUDA_TRY(host::launched());
-    return LSTM_OK;
+    SeqArgs a = {s, w + l.qk, w + l.tp, v, s0, o, sT, states, deltas, (float *)(w + l.starts), w + l.trans,
+                 l.split.segments, l.split.chunks, (Ctrl *)w};
+    return sequential<KD>(a, seq_fwd_kernel<E, KD, true>, seq_fwd_kernel<E, KD, false>, Seq<E, KD>::smem, st);
 }
 
 template <class E>
@@ -148,11 +198,10 @@ int chunked_bwd(const lstm_gdr_dims *d, const Shape &s, const void *dout, const 
         if (rc != LSTM_OK) return rc;
     }
     float *dstates = (float *)(w + l.dstates), *dvf = (float *)(w + l.dvf);
-    SeqArgs a = {s, w + l.qk, w + l.tp, dout, dsT, dv, ds0, dstates, dvf, (Ctrl *)w};
-    LSTM_CUDA_TRY(allow_smem(seq_bwd_kernel<E, KD>, Seq<E, KD>::smem));
-    seq_bwd_kernel<E, KD><<<s.B * s.Hv * s.VT, SEQ_THREADS, Seq<E, KD>::smem, st>>>(a);
-    LSTM_CUDA_TRY(host::launched());
-    if (s.NC == 0) return LSTM_OK;
+    SeqArgs a = {s, w + l.qk, w + l.tp, dout, dsT, dv, ds0, dstates, dvf, (float *)(w + l.starts), w + l.trans,
+                 l.split.segments, l.split.chunks, (Ctrl *)w};
+    const int rc = sequential<KD>(a, seq_bwd_kernel<E, KD, true>, seq_bwd_kernel<E, KD, false>, Seq<E, KD>::smem, st);
+    if (rc != LSTM_OK || s.NC == 0) return rc;
     GradArgs ga = {s, w + l.qk, g, beta, dout, states, deltas, dstates, dvf, dq, dk, dg, dbeta, (Ctrl *)w};
     LSTM_CUDA_TRY(allow_smem(grad_kernel<E, KD>, GradSmem<E, KD>::smem));
     grad_kernel<E, KD><<<s.NC * s.B * s.Hk, GRAD_THREADS, GradSmem<E, KD>::smem, st>>>(ga);

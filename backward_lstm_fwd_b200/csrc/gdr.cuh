@@ -549,6 +549,12 @@ template <class E, int KD> struct Seq {
     static constexpr int NO = sizeof(E) == 2 ? 2 : NT;
 };
 
+// Few heads and many chunks: the chunks are split into segments.  A head's
+// state is carried over a segment by S -> A S + B, with A [K][K] the same for
+// every column, so a first pass (SCAN) runs the segments side by side from a
+// zero state, which leaves B, and from the identity, which leaves A; scan_kernel
+// joins them to every segment's start, and a second pass runs all segments at
+// once.  (seg: chunks of a segment, in the order of the pass.)
 struct SeqArgs {
     Shape s;
     const char *qk, *tp;
@@ -557,6 +563,9 @@ struct SeqArgs {
     void *o;                  // forward: o; backward: dv
     float *sT;                // forward: sT; backward: ds0
     float *states, *deltas;   // forward (or NULL): S and X; backward: dS and dV, in the workspace
+    float *starts;            // [segments - 1][B][Hv][K][V]: B, then the start of the next segment
+    char *trans;              // [segments - 1][B][Hv]: A as NT terms of KD rows, swizzled
+    int segments, seg;
     Ctrl *ctrl;
 };
 
@@ -566,13 +575,34 @@ struct SeqBars {
     int abort_flag;
 };
 
-// One thread: copy the tiles of the n-th chunk in order to its stage.  The
+// What a block of the sequential kernels works on.
+template <bool SCAN> struct Job {
+    int vt, h, b, seg, first, chunks;
+    bool identity;  // SCAN: the state columns are those of the identity
+    __device__ __forceinline__ explicit Job(const SeqArgs &a) {
+        const Shape &s = a.s;
+        const int width = s.VT + (SCAN ? 1 : 0);
+        int id = blockIdx.x;
+        vt = id % width;
+        id /= width;
+        h = id % s.Hv;
+        id /= s.Hv;
+        b = id % s.B;
+        seg = id / s.B;
+        first = seg * a.seg;
+        chunks = min(a.seg, s.NC - first);
+        identity = SCAN && vt == s.VT;
+        if (identity) vt = 0;
+    }
+};
+
+// One thread: copy the tiles of the segment's n-th chunk to its stage.  The
 // caller has seen the last products that read that stage complete.
 template <class E, int KD>
-__device__ __forceinline__ void seq_load(const SeqArgs &a, uint8_t *smem, SeqBars *bar, int b, int h, int n, bool reverse) {
+__device__ __forceinline__ void seq_load(const SeqArgs &a, uint8_t *smem, SeqBars *bar, int b, int h, int n, int first, bool reverse) {
     using Q = Seq<E, KD>;
     const Shape &s = a.s;
-    const int st = n % Q::stages, c = reverse ? s.NC - 1 - n : n;
+    const int st = n % Q::stages, c = reverse ? s.NC - 1 - first - n : first + n;
     uint8_t *dst = smem + st * Q::stage;
     tc::mbar_arrive_expect_tx(&bar->full[st], Q::stage + GATES);
     const size_t cb = (size_t)c * s.B + b;
@@ -639,6 +669,32 @@ template <int N, class T> __device__ __forceinline__ void load_col(const T *p, l
         for (int i = 0; i < N; ++i, p += stride) r[i] = i < n ? *p : from_f<T>(0.f);
     }
 }
+// 16 loaded elements, 16-bit ones two to a register.
+template <class E> struct Col16 {
+    uint32_t x[sizeof(E) * 4];
+    __device__ __forceinline__ void load(const E *p, long long stride, int n) {
+        E r[16];
+        load_col(p, stride, n, r);
+        if constexpr (sizeof(E) == 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = reinterpret_cast<const uint16_t &>(r[2 * i]) |
+                       ((uint32_t) reinterpret_cast<const uint16_t &>(r[2 * i + 1]) << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(r[i]);
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(E) == 2) {
+            const uint16_t h = (uint16_t)(x[i >> 1] >> (16 * (i & 1)));
+            return to_f(reinterpret_cast<const E &>(h));
+        } else {
+            return __uint_as_float(x[i]);
+        }
+    }
+};
 template <int N, class T> __device__ __forceinline__ void store_col(T *p, long long stride, int n, const float (&r)[N]) {
     if (n >= N) {
 #pragma unroll
@@ -657,11 +713,11 @@ template <int KD> struct Lane {
     bool own;
     uint32_t lanes;
     long long head, row;  // row: elements of o, deltas between tokens
-    __device__ __forceinline__ Lane(const Shape &s, uint32_t tmem, int b, int h, int vt) {
+    __device__ __forceinline__ Lane(const Shape &s, uint32_t tmem, int b, int h, int vt, bool identity) {
         const int lane = threadIdx.x & 127;
         wg = threadIdx.x >> 7;
         v = vt * LANES + lane;
-        own = v < s.V;
+        own = v < s.V && !identity;
         len = length_of(s, b);
         lanes = tmem + ((uint32_t)(lane & 96) << 16);
         head = (long long)b * s.Hv + h;
@@ -676,11 +732,36 @@ template <int KD> struct Lane {
     __device__ __forceinline__ void store(const Shape &s, float *base, const float (&S)[KD / 4]) const {
         store_col(base + (long long)wg * (KD / 4) * s.V + v, s.V, rows(s, base), S);
     }
+    // column `lane` of the identity
+    __device__ __forceinline__ void unit(const Shape &s, float (&S)[KD / 4]) const {
+        const int lane = threadIdx.x & 127;
+#pragma unroll
+        for (int i = 0; i < KD / 4; ++i) S[i] = wg * (KD / 4) + i == lane && lane < s.K ? 1.f : 0.f;
+    }
+    // A's terms from its columns, one a lane
+    __device__ __forceinline__ void store_trans(char *base, const float (&S)[KD / 4]) const {
+        const int lane = threadIdx.x & 127;
+        if (lane < KD) {
+#pragma unroll
+            for (int i = 0; i < KD / 4; i += 2) {
+                uint32_t t[NT];
+                split2<NT>(S[i], S[i + 1], t);
+                const int k = wg * (KD / 4) + i;
+                char *p = base + (lane >> 6) * (KD * 128);
+#pragma unroll
+                for (int n = 0; n < NT; ++n, p += KD * KD * 2) {
+                    *(uint16_t *)(p + swz(k, (lane & 63) * 2)) = (uint16_t)t[n];
+                    *(uint16_t *)(p + swz(k + 1, (lane & 63) * 2)) = (uint16_t)(t[n] >> 16);
+                }
+            }
+        }
+        __syncwarp();
+    }
     // how many of the 16 tokens from t0 on are below `end`, for a lane that has a column
     __device__ __forceinline__ int tokens(int t0, int end) const { return own ? end - t0 : 0; }
 };
 
-template <class E, int KD>
+template <class E, int KD, bool SCAN>
 __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_constant__ SeqArgs a) {
     using Q = Seq<E, KD>;
     constexpr int TB = Q::TB, H4 = KD / 4;
@@ -689,94 +770,113 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
     const Shape &s = a.s;
     const int tid = threadIdx.x, warp = warp_id();
-    int id = blockIdx.x;
-    const int vt = id % s.VT;
-    id /= s.VT;
-    const int h = id % s.Hv, b = id / s.Hv;
+    const Job<SCAN> J(a);
+    if (J.identity && J.seg == 0) return;  // the first segment starts from s0: its A is not needed
     seq_setup(bar);
     const uint32_t tmem = bar->tmem_slot;
-    const Lane<KD> L(s, tmem, b, h, vt);
+    const Lane<KD> L(s, tmem, J.b, J.h, J.vt, J.identity);
     volatile int *ab = &bar->abort_flag;
     constexpr Steps rows = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};   // K-major q or k: K over the dims
     constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};       // MN-major k: K over the tokens
     constexpr Steps mat = {TILE >> 4, 2, 0};                           // K-major T2, P
     if (s.NC == 0) clear_ctrl(a.ctrl);  // (else prep did)
-    if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, false);
+    if (tid == 32 && J.chunks > 0) {
+        seq_load<E, KD>(a, smem, bar, J.b, J.h, 0, J.first, false);
+        if (Q::stages == 2 && J.chunks > 1) seq_load<E, KD>(a, smem, bar, J.b, J.h, 1, J.first, false);
+    }
     __syncwarp();
+    const long long KV = (long long)s.K * s.V, all = (long long)s.B * s.Hv * KV;  // a state; the states of all heads
     float S[H4], o[16];
-    L.load(s, a.s0 ? a.s0 + L.head * s.K * s.V : nullptr, S);
-    const E *vp = (const E *)a.v + (long long)b * s.ldv + (long long)h * s.V + L.v;
+    Col16<E> vr;
+    if (J.identity) L.unit(s, S);
+    else L.load(s, J.seg == 0 ? (a.s0 ? a.s0 + L.head * KV : nullptr)
+                              : (SCAN ? nullptr : a.starts + (J.seg - 1) * all + L.head * KV), S);
+    const E *vp = (const E *)a.v + (long long)J.b * s.ldv + (long long)J.h * s.V + L.v;
+    auto load_v = [&](int c) {
+        const int t0 = c * C + L.wg * 16;
+        vr.load(vp + (long long)t0 * s.B * s.ldv, s.B * s.ldv, L.tokens(t0, L.len));
+    };
     auto store_o = [&](int c) {
         const int t0 = c * C + L.wg * 16;
         store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), o);
     };
+    auto add_pu = [&](uint32_t ph, uint32_t site) {
+        wait(&bar->m3, ph, a.ctrl, ab, site);
+        float f[16];
+        get16(L.lanes + COL_X + L.wg * 16, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] += f[i];
+    };
+    load_v(J.first);
 #pragma unroll 1
-    for (int c = 0; c < s.NC; ++c) {
-        const int st = c % Q::stages, t0 = c * C + L.wg * 16;
-        const uint32_t ph = c & 1;
+    for (int n = 0; n < J.chunks; ++n) {
+        const int c = J.first + n, st = n % Q::stages, t0 = c * C + L.wg * 16;
+        const uint32_t ph = n & 1;
         const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
         const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + L.wg * 16;
-        E vr[16];
-        load_col(vp + (long long)t0 * s.B * s.ldv, s.B * s.ldv, L.tokens(t0, L.len), vr);
-        __syncwarp();
         put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
-        wait(&bar->full[st], (c / Q::stages) & 1, a.ctrl, ab, 0x612);
+        wait(&bar->full[st], (n / Q::stages) & 1, a.ctrl, ab, 0x612);
         if (hand_over(warp)) {  // D = K S and Q S, tokens on the columns
-            products_ts<KD / 16, NT, TB, NT>(tmem + COL_D, tmem + COL_S, KD / 2, k_major(qk + TILE, 0), rows, tc::idesc_bf16_f32(128, 64, 0, 0));
+            products_ts<KD / 16, NT, TB, NT>(tmem + COL_D, tmem + COL_S, KD / 2, k_major(qk + TILE, 0), rows,
+                                             tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m1);
-            products_ts<KD / 16, Q::NO, TB, Q::NO>(tmem + COL_D + 64, tmem + COL_S, KD / 2, k_major(qk, 0), rows, tc::idesc_bf16_f32(128, 64, 0, 0));
+            if (!SCAN)
+                products_ts<KD / 16, Q::NO, TB, Q::NO>(tmem + COL_D + 64, tmem + COL_S, KD / 2, k_major(qk, 0), rows,
+                                                       tc::idesc_bf16_f32(128, 64, 0, 0));
         }
         __syncwarp();
-        if (c > 0) {  // the last chunk's output
-            wait(&bar->m3, ph ^ 1, a.ctrl, ab, 0x616);
-            float f[16];
-            get16(L.lanes + COL_X + L.wg * 16, f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] += f[i];
-            store_o(c - 1);
-        }
-        // (the products of chunk c - 1, whose stage this is, are complete)
-        if (Q::stages == 2 && tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
+        if (!SCAN && n > 0) add_pu(ph ^ 1, 0x616);
+        // (the products of chunk n - 1, whose stage this is, are complete)
+        if (Q::stages == 2 && tid == 32 && n > 0 && n + 1 < J.chunks)
+            seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, false);
         __syncwarp();
-        L.store(s, a.states ? a.states + ((long long)c * s.B * s.Hv + L.head) * s.K * s.V : nullptr, S);
+        if (!SCAN) L.store(s, a.states ? a.states + c * all + L.head * KV : nullptr, S);
         const float last = gates[C - 1 - L.wg * 16];  // gamma of token 63
-        float f[16], gam[16], be[16], u[16];
-        load16(gates, gam);
+        float f[16], be[16], u[16];
+        load16(gates, u);  // gamma
         wait(&bar->m1, ph, a.ctrl, ab, 0x613);
         get16(L.lanes + COL_D + L.wg * 16, f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = fmaf(-gam[i], f[i], to_f(vr[i]));
+        for (int i = 0; i < 16; ++i) f[i] = fmaf(-u[i], f[i], vr[i]);
         put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
         if (hand_over(warp)) {  // X = T2 R
-            products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, k_major(tp, 0), mat, tc::idesc_bf16_f32(128, 64, 0, 0));
+            products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, k_major(tp, 0), mat,
+                                       tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m2);
         }
         __syncwarp();
+        if (n + 1 < J.chunks) load_v(c + 1);
+        if (!SCAN && n > 0) store_o(c - 1);
         load16(gates + C, u);
         load16(gates + 2 * C, be);
         wait(&bar->m2, ph, a.ctrl, ab, 0x614);  // Q S came before X
         get16(L.lanes + COL_X + L.wg * 16, f);
-        get16(L.lanes + COL_D + 64 + L.wg * 16, o);
+        if (!SCAN) get16(L.lanes + COL_D + 64 + L.wg * 16, o);
 #pragma unroll
         for (int i = 0; i < 16; ++i) u[i] *= f[i] * be[i];  // left U
         put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, u);
         if (hand_over(warp)) {  // D = K^T (left U)
-            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols, tc::idesc_bf16_f32(128, KD, 0, 1));
+            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols,
+                                       tc::idesc_bf16_f32(128, KD, 0, 1));
             tc::mma_commit(&bar->m4);
         }
         __syncwarp();
-        if (a.deltas) store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+        if (!SCAN) {
+            if (a.deltas) store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+            load16(gates, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            o[i] *= s.scale * gam[i];
-            f[i] *= be[i];  // U
+            for (int i = 0; i < 16; ++i) {
+                o[i] *= s.scale * u[i];
+                f[i] *= be[i];  // U
+            }
+            put_terms<8, Q::NO>(L.lanes + COL_R + L.wg * 8, 32, f);
+            if (hand_over(warp)) {  // P U
+                products_ts<4, Q::NO, Q::NO, Q::NO>(tmem + COL_X, tmem + COL_R, 32, k_major(tp + NT * TILE, 0), mat,
+                                                    tc::idesc_bf16_f32(128, 64, 0, 0));
+                tc::mma_commit(&bar->m3);
+            }
+            __syncwarp();
         }
-        put_terms<8, Q::NO>(L.lanes + COL_R + L.wg * 8, 32, f);
-        if (hand_over(warp)) {  // P U
-            products_ts<4, Q::NO, Q::NO, Q::NO>(tmem + COL_X, tmem + COL_R, 32, k_major(tp + NT * TILE, 0), mat, tc::idesc_bf16_f32(128, 64, 0, 0));
-            tc::mma_commit(&bar->m3);
-        }
-        __syncwarp();
         wait(&bar->m4, ph, a.ctrl, ab, 0x615);
 #pragma unroll
         for (int i0 = 0; i0 < H4; i0 += 16) {
@@ -785,28 +885,26 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
             for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
         }
         if (Q::stages == 1) {
-            wait(&bar->m3, ph, a.ctrl, ab, 0x617);
-            if (tid == 32 && c + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, c + 1, false);
+            if (!SCAN) wait(&bar->m3, ph, a.ctrl, ab, 0x617);
+            if (tid == 32 && n + 1 < J.chunks) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, false);
             __syncwarp();
         }
     }
-    if (s.NC > 0) {
-        wait(&bar->m3, (s.NC - 1) & 1, a.ctrl, ab, 0x618);
-        float f[16];
-        get16(L.lanes + COL_X + L.wg * 16, f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] += f[i];
-        store_o(s.NC - 1);
+    if (!SCAN && J.chunks > 0) {
+        add_pu((J.chunks - 1) & 1, 0x618);
+        store_o(J.first + J.chunks - 1);
     }
-    L.store(s, a.sT + L.head * s.K * s.V, S);
-    if (tid == 32) seq_drain<E, KD>(bar, s.NC);
+    if (J.identity) L.store_trans(a.trans + ((J.seg * s.B + J.b) * (long long)s.Hv + J.h) * (NT * KD * KD * 2), S);
+    else if (SCAN) L.store(s, a.starts + J.seg * all + L.head * KV, S);
+    else if (J.seg == a.segments - 1) L.store(s, a.sT + L.head * KV, S);
+    if (tid == 32) seq_drain<E, KD>(bar, J.chunks);
     seq_finish(bar);
 }
 
 // The adjoint, chunks in reverse, the same layout (dS^T in registers):
 //   K dS and P^T dO  ->  dU  ->  dV = T2^T (beta dU)  ->  dS += scale Q^T gamma dO - K^T gamma dV.
 // P^T dO of the next chunk runs beside the last product of this one.
-template <class E, int KD>
+template <class E, int KD, bool SCAN>
 __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_constant__ SeqArgs a) {
     using Q = Seq<E, KD>;
     constexpr int TB = Q::TB, H4 = KD / 4;
@@ -815,59 +913,62 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     SeqBars *bar = (SeqBars *)(smem + Q::stages * (Q::stage + GATES));
     const Shape &s = a.s;
     const int tid = threadIdx.x, warp = warp_id();
-    int id = blockIdx.x;
-    const int vt = id % s.VT;
-    id /= s.VT;
-    const int h = id % s.Hv, b = id / s.Hv;
+    const Job<SCAN> J(a);
+    if (J.identity && J.seg == 0) return;
     seq_setup(bar);
     const uint32_t tmem = bar->tmem_slot;
-    const Lane<KD> L(s, tmem, b, h, vt);
+    const Lane<KD> L(s, tmem, J.b, J.h, J.vt, J.identity);
     volatile int *ab = &bar->abort_flag;
     constexpr Steps rows = {QK<E, KD>::term >> 4, 2, 2 * TILE >> 4};
     constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};
     constexpr Steps mat = {TILE >> 4, 2048 >> 4, 0};                   // MN-major T2, P: transposed
     if (s.NC == 0) clear_ctrl(a.ctrl);
-    if (tid == 32 && s.NC > 0) seq_load<E, KD>(a, smem, bar, b, h, 0, true);
+    if (tid == 32 && J.chunks > 0) seq_load<E, KD>(a, smem, bar, J.b, J.h, 0, J.first, true);
     __syncwarp();
+    const long long KV = (long long)s.K * s.V, all = (long long)s.B * s.Hv * KV;
     float S[H4];
-    E d[16];
-    L.load(s, a.s0 ? a.s0 + L.head * s.K * s.V : nullptr, S);
+    Col16<E> d;
+    if (J.identity) L.unit(s, S);
+    else L.load(s, J.seg == 0 ? (a.s0 ? a.s0 + L.head * KV : nullptr)
+                              : (SCAN ? nullptr : a.starts + (J.seg - 1) * all + L.head * KV), S);
     const E *dop = (const E *)a.v + L.head * s.V + L.v;
     auto load_do = [&](int c) {
         const int t0 = c * C + L.wg * 16;
-        load_col(dop + t0 * L.row, L.row, a.v ? L.tokens(t0, L.len) : 0, d);
-        __syncwarp();
+        d.load(dop + t0 * L.row, L.row, a.v ? L.tokens(t0, L.len) : 0);
     };
     auto product_pdo = [&](int st) {  // X = P^T dO (one thread)
         const uint32_t tp = tc::smem_u32(smem + st * Q::stage) + QK<E, KD>::bytes;
-        products_ts<4, TB, NT, NT>(tmem + COL_X, tmem + COL_R, 32, mn_major(tp + NT * TILE, 0, TILE), mat, tc::idesc_bf16_f32(128, 64, 0, 1));
+        products_ts<4, TB, NT, NT>(tmem + COL_X, tmem + COL_R, 32, mn_major(tp + NT * TILE, 0, TILE), mat,
+                                   tc::idesc_bf16_f32(128, 64, 0, 1));
     };
     auto put_do = [&]() {
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f(d[i]);
+        for (int i = 0; i < 16; ++i) x[i] = d[i];
         put_terms<8, TB>(L.lanes + COL_R + L.wg * 8, 32, x);
     };
-    if (s.NC > 0) load_do(s.NC - 1);
+    if (J.chunks > 0) load_do(s.NC - 1 - J.first);
 #pragma unroll 1
-    for (int n = 0; n < s.NC; ++n) {
-        const int c = s.NC - 1 - n, st = n % Q::stages, t0 = c * C + L.wg * 16;
+    for (int n = 0; n < J.chunks; ++n) {
+        const int c = s.NC - 1 - J.first - n, st = n % Q::stages, t0 = c * C + L.wg * 16;
+        const bool more = n + 1 < J.chunks;
         const uint32_t ph = n & 1;
         const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
         const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + L.wg * 16;
         const bool early = Q::stages == 2 && n > 0;  // P^T dO was issued a chunk ago
-        if (Q::stages == 2 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
+        if (Q::stages == 2 && tid == 32 && more) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, true);
         __syncwarp();
         put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
         if (!early) put_do();
         wait(&bar->full[st], (n / Q::stages) & 1, a.ctrl, ab, 0x622);
         if (hand_over(warp)) {  // D = K dS
             if (!early) product_pdo(st);
-            products_ts<KD / 16, NT, TB, NT>(tmem + COL_D, tmem + COL_S, KD / 2, k_major(qk + TILE, 0), rows, tc::idesc_bf16_f32(128, 64, 0, 0));
+            products_ts<KD / 16, NT, TB, NT>(tmem + COL_D, tmem + COL_S, KD / 2, k_major(qk + TILE, 0), rows,
+                                             tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m1);
         }
         __syncwarp();
-        L.store(s, a.states + ((long long)c * s.B * s.Hv + L.head) * s.K * s.V, S);
+        if (!SCAN) L.store(s, a.states + c * all + L.head * KV, S);
         const float last = gates[C - 1 - L.wg * 16];
         float f[16], e[16], left[16], be[16];
         load16(gates + C, left);
@@ -879,33 +980,38 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         for (int i = 0; i < 16; ++i) f[i] = be[i] * fmaf(left[i], f[i], e[i]);  // beta dU
         put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
         if (hand_over(warp)) {  // dV = T2^T (beta dU)
-            products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, mn_major(tp, 0, TILE), mat, tc::idesc_bf16_f32(128, 64, 0, 1));
+            products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, mn_major(tp, 0, TILE), mat,
+                                       tc::idesc_bf16_f32(128, 64, 0, 1));
             tc::mma_commit(&bar->m2);
         }
         __syncwarp();
         load16(gates, be);  // gamma
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e[i] = s.scale * be[i] * to_f(d[i]);
+        for (int i = 0; i < 16; ++i) e[i] = s.scale * be[i] * d[i];
         put_terms<8, NT>(L.lanes + COL_S + L.wg * 8, 32, e);
-        if (c > 0) load_do(c - 1);
+        if (more) load_do(c - 1);
         wait(&bar->m2, ph, a.ctrl, ab, 0x624);
         get16(L.lanes + COL_X + L.wg * 16, f);
 #pragma unroll
         for (int i = 0; i < 16; ++i) e[i] = -be[i] * f[i];
         put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, e);
-        if (Q::stages == 2 && c > 0) put_do();
+        if (Q::stages == 2 && more) put_do();
         if (hand_over(warp)) {  // D = scale Q^T gamma dO - K^T gamma dV
-            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_S, 32, mn_major(qk, 0, 2 * TILE), cols, tc::idesc_bf16_f32(128, KD, 0, 1));
-            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols, tc::idesc_bf16_f32(128, KD, 0, 1), 1);
+            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_S, 32, mn_major(qk, 0, 2 * TILE), cols,
+                                       tc::idesc_bf16_f32(128, KD, 0, 1));
+            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols,
+                                       tc::idesc_bf16_f32(128, KD, 0, 1), 1);
             tc::mma_commit(&bar->m4);
-            if (Q::stages == 2 && c > 0) {
+            if (Q::stages == 2 && more) {
                 tc::mbar_wait(&bar->full[st ^ 1], ((n + 1) / Q::stages) & 1, a.ctrl, ab, 0x626);
                 product_pdo(st ^ 1);
             }
         }
         __syncwarp();
-        store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
-        store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+        if (!SCAN) {
+            store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+            store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+        }
         wait(&bar->m4, ph, a.ctrl, ab, 0x625);
 #pragma unroll
         for (int i0 = 0; i0 < H4; i0 += 16) {
@@ -913,11 +1019,78 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
         }
-        if (Q::stages == 1 && tid == 32 && n + 1 < s.NC) seq_load<E, KD>(a, smem, bar, b, h, n + 1, true);
+        if (Q::stages == 1 && tid == 32 && more) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, true);
         __syncwarp();
     }
-    L.store(s, a.sT ? a.sT + L.head * s.K * s.V : nullptr, S);
-    if (tid == 32) seq_drain<E, KD>(bar, s.NC);
+    if (J.identity) L.store_trans(a.trans + ((J.seg * s.B + J.b) * (long long)s.Hv + J.h) * (NT * KD * KD * 2), S);
+    else if (SCAN) L.store(s, a.starts + J.seg * all + L.head * KV, S);
+    else if (J.seg == a.segments - 1) L.store(s, a.sT ? a.sT + L.head * KV : nullptr, S);
+    if (tid == 32) seq_drain<E, KD>(bar, J.chunks);
+    seq_finish(bar);
+}
+
+// Join the segments: starts[i] becomes A_i starts[i - 1] + B_i, i = 1 .. in
+// order, block (b, h, 128 columns of V); S^T in registers and tensor memory as
+// above, A's tiles by bulk copies one segment ahead.
+template <int KD> struct ScanSmem {
+    static constexpr int tile = NT * KD * KD * 2;
+    static constexpr size_t smem = 2 * tile + 1024 + 256;
+};
+template <int KD>
+__global__ void __launch_bounds__(SEQ_THREADS, 1) scan_kernel(const __grid_constant__ SeqArgs a) {
+    constexpr int H4 = KD / 4, TILES = ScanSmem<KD>::tile;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    SeqBars *bar = (SeqBars *)(smem + 2 * TILES);
+    const Shape &s = a.s;
+    const int tid = threadIdx.x, warp = warp_id();
+    int id = blockIdx.x;
+    const int vt = id % s.VT;
+    id /= s.VT;
+    const int h = id % s.Hv, b = id / s.Hv;
+    seq_setup(bar);
+    const uint32_t tmem = bar->tmem_slot;
+    const Lane<KD> L(s, tmem, b, h, vt, false);
+    volatile int *ab = &bar->abort_flag;
+    constexpr Steps rows = {KD * KD * 2 >> 4, 2, KD * 128 >> 4};
+    const long long KV = (long long)s.K * s.V, all = (long long)s.B * s.Hv * KV;
+    const int last = a.segments - 2;  // the last start is starts[last]
+    auto fetch = [&](int i) {
+        tc::mbar_arrive_expect_tx(&bar->full[i & 1], TILES);
+        bulk_load(smem + (i & 1) * TILES, a.trans + ((i * s.B + b) * (long long)s.Hv + h) * TILES, TILES, &bar->full[i & 1]);
+    };
+    if (tid == 32 && last >= 1) fetch(1);
+    __syncwarp();
+    float S[H4], B[H4];
+    L.load(s, a.starts + L.head * KV, S);
+#pragma unroll 1
+    for (int i = 1; i <= last; ++i) {
+        if (tid == 32 && i < last) fetch(i + 1);  // (segment i - 1's product is complete)
+        __syncwarp();
+        float *start = a.starts + i * all + L.head * KV;
+        L.load(s, start, B);
+        put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
+        wait(&bar->full[i & 1], ((i - 1) >> 1) & 1, a.ctrl, ab, 0x641);
+        if (hand_over(warp)) {
+            products_ts<KD / 16, NT, NT, NT>(tmem + COL_D, tmem + COL_S, KD / 2,
+                                             k_major(tc::smem_u32(smem + (i & 1) * TILES), 0), rows,
+                                             tc::idesc_bf16_f32(128, KD, 0, 0));
+            tc::mma_commit(&bar->m1);
+        }
+        __syncwarp();
+        wait(&bar->m1, (i - 1) & 1, a.ctrl, ab, 0x642);
+#pragma unroll
+        for (int i0 = 0; i0 < H4; i0 += 16) {
+            float f[16];
+            get16(L.lanes + COL_D + L.wg * H4 + i0, f);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) S[i0 + j] = f[j] + B[i0 + j];
+        }
+        L.store(s, start, S);
+    }
+    if (tid == 32)
+        for (int i = max(1, last - 1); i <= last; ++i)  // after a time-out: the copies have landed
+            tc::mbar_wait(&bar->full[i & 1], ((i - 1) >> 1) & 1, nullptr, nullptr, 0, 200000000ull);
     seq_finish(bar);
 }
 

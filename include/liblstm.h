@@ -444,7 +444,8 @@ typedef struct lstm_gdr_options {
     float scale;
 } lstm_gdr_options;
 
-/* save: whether the forward call gets states and deltas. */
+/* save: whether the forward call gets states and deltas.  (The sizes depend on
+ * the current device: few long sequences are split by its SM count.) */
 size_t lstm_gdr_fwd_workspace_size(const lstm_gdr_dims *d, int save);
 size_t lstm_gdr_bwd_workspace_size(const lstm_gdr_dims *d);
 int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *q, const void *k,

@@ -227,9 +227,24 @@ def test_a_sequence_in_parts():
     close("whole", whole.o, ref, 3)
 
 
-def test_long():
-    x, dout, dsT = make(2050, 1, 1, 1, 128, 128, "bf16")
+@pytest.mark.parametrize("shape,dt", [((2050, 1, 1, 1, 128, 128), "bf16"), ((1500, 2, 1, 2, 64, 40), "fp16"),
+                                      ((900, 1, 1, 2, 96, 256), "fp32"), ((256, 1, 1, 1, 32, 8), "bf16"),
+                                      ((1100, 3, 1, 1, 128, 136), "fp16")], ids=str)
+def test_long_with_few_heads(shape, dt):
+    """Chunks in segments side by side, joined by their transition matrices."""
+    x, dout, dsT = make(*shape, dt)
+    d = L.gdr_dims(*shape, DT[dt])
+    state = shape[1] * shape[3] * shape[4] * shape[5] * 4
+    # (a split call keeps the starts of its segments)
+    many = L.gdr_dims(shape[0], 64, *shape[2:3], 64 * shape[2], *shape[4:], DT[dt])
+    per_chunk = lambda e, heads: L.gdr_fwd_workspace_size(e, True) / heads  # noqa: E731
+    assert per_chunk(d, shape[1] * shape[3]) > per_chunk(many, 64 * 64 * shape[2]) + state / (shape[1] * shape[3])
     check(x, dout, dsT)
+    lengths = torch.randint(0, shape[0] + 1, (shape[1],), dtype=torch.int32, device="cuda")
+    lengths[0] = shape[0] * 2 // 3
+    check(x, dout, dsT, lengths=lengths)
+    x["s0"] = None
+    check(x, dout, None)
 
 
 def test_gradient_by_differences():
