@@ -87,10 +87,14 @@ template <int n> __device__ __forceinline__ void split2(float a, float b, uint32
 #pragma unroll
     for (int i = 0; i < n; ++i) {
         t[i] = pack2(a, b);
-        if (i + 1 < n) {
-            a -= low_f(t[i]);
-            b -= high_f(t[i]);
-        }
+        if (i + 1 < n)
+            asm("{\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%0, %1};\n\t"
+                "mov.b64 y, {%2, %3};\n\t"
+                "sub.rn.f32x2 x, x, y;\n\t"
+                "mov.b64 {%0, %1}, x;\n\t}"
+                : "+f"(a), "+f"(b)
+                : "f"(low_f(t[i])), "f"(high_f(t[i])));
     }
 }
 
@@ -1193,31 +1197,28 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     const int row = tid >> 3, gr = tid & 7;  // loads: eight threads a row, eight columns each
     const int t_row = c * C + row;
     const uint32_t off = swz(row, gr * 16);  // rows 64 apart keep it
-    const int passes = (s.V + 63) / 64, total = passes * s.group;
+    const int passes = (s.V + 63) / 64;
     Raw8<E> ro;                                // dO, dV, X, S0, dS1 of the pass ahead
     Raw8<float> rv, rx, rs[SI], rd[SI];
-    // pass n is columns 64 (n % passes) .. of value head n / passes of the group
-    auto token_at = [&](int n, bool &live) {
-        const int v0 = n % passes * 64 + gr * 8;
-        live = n < total && v0 < s.V && t_row < len;
-        return (((long long)t_row * s.B + b) * s.Hv + hk * s.group + n / passes) * s.V + v0;
-    };
-    auto load_a = [&](int n) {
-        bool live;
-        const long long at = token_at(n, live);
+    // where this thread's groups of value head 0 of the group, column 0, lie;
+    // next_h, next_v: head and first column of the pass after the present one
+    const long long tok0 = (((long long)t_row * s.B + b) * s.Hv + hk * s.group) * s.V + gr * 8;
+    const long long st0 = ((((long long)c * s.B + b) * s.Hv + hk * s.group) * s.K + row) * s.V + gr * 8;
+    int next_h = 0, next_v = 0;
+    auto load_a = [&]() {
+        const bool live = next_h < s.group && next_v + gr * 8 < s.V && t_row < len;
+        const long long at = tok0 + next_h * s.V + next_v;
         ro = raw8<E>((const E *)a.dout + at, live && a.dout);
         rv = raw8<float>(a.dvf + at, live);
     };
-    auto load_x = [&](int n) {
-        bool live;
-        const long long at = token_at(n, live);
-        rx = raw8<float>(a.deltas + at, live);
+    auto load_x = [&]() {
+        rx = raw8<float>(a.deltas + tok0 + next_h * s.V + next_v, next_h < s.group && next_v + gr * 8 < s.V && t_row < len);
     };
-    auto load_s = [&](int n, const float *base, Raw8<float> (&o)[SI]) {
-        const int v0 = n % passes * 64 + gr * 8;
-        const float *q = base + ((((long long)c * s.B + b) * s.Hv + hk * s.group + n / passes) * s.K + row) * s.V + v0;
+    auto load_s = [&](const float *base, Raw8<float> (&o)[SI]) {
+        const bool live = next_h < s.group && next_v + gr * 8 < s.V;
+        const float *q = base + st0 + (long long)next_h * s.K * s.V + next_v;
 #pragma unroll
-        for (int i = 0; i < SI; ++i) o[i] = raw8<float>(q + (long long)i * 64 * s.V, n < total && v0 < s.V && i * 64 + row < s.K);
+        for (int i = 0; i < SI; ++i) o[i] = raw8<float>(q + i * 64 * s.V, live && i * 64 + row < s.K);
     };
     auto put = [&](uint8_t *tile, int term, const Raw8<float> &x) {
         uint4 o[NT];
@@ -1228,10 +1229,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     constexpr Steps qk_rows = {TERM >> 4, 2, 2 * TILE >> 4}, a_rows = {2 * TILE >> 4, 2, 0}, x_rows = {L::st_term >> 4, 2, 0},
                     d_rows = {L::ds_term >> 4, 2, 0}, a_cols = {2 * TILE >> 4, 2048 >> 4, 4 * 2048 >> 4},
                     qk_cols = {TERM >> 4, 2048 >> 4, 4 * 2048 >> 4};
-    load_s(0, a.states, rs);
-    load_a(0);
-    load_x(0);
-    load_s(0, a.dstates, rd);
+    load_s(a.states, rs);
+    load_a();
+    load_x();
+    load_s(a.dstates, rd);
     wait(&loaded, 0, a.ctrl, ab, 0x631);
 #pragma unroll 1
     for (int m = 0; m < s.group; ++m) {
@@ -1243,6 +1244,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
 #pragma unroll 1
         for (int p = 0; p < passes; ++p) {
             const int n = m * passes + p;
+            next_h = p + 1 < passes ? m : m + 1;
+            next_v = p + 1 < passes ? p * 64 + 64 : 0;
             if (n > 0) wait(&m1, (n - 1) & 1, a.ctrl, ab, 0x633);
             if (!L::own_ds && p > 0) wait(&m2, (n - 1) & 1, a.ctrl, ab, 0x634);  // dS1 lies in S0's rows
 #pragma unroll
@@ -1257,7 +1260,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                     dot = fmaf(__uint_as_float(x[j].w), __uint_as_float(y[j].w), dot);
                 }
             }
-            load_s(n + 1, a.states, rs);
+            load_s(a.states, rs);
             if (m > 0 && p == 0) {
                 wait(&m3, (m - 1) & 1, a.ctrl, ab, 0x632);  // the triangle's tiles are free
                 if (!isq)  // dK's transposed part of the last head
@@ -1279,10 +1282,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                     *(uint4 *)(smem + L::a + k * 2 * TILE + off) = k < TB ? o[k < TB ? k : 0] : make_uint4(0, 0, 0, 0);
             }
             put(smem + L::a + TILE, 2 * TILE, rv);
-            load_a(n + 1);
+            load_a();
             if (L::own_ds && p > 0) wait(&m2, (n - 1) & 1, a.ctrl, ab, 0x634);
             put(smem + L::st + KD * 128, L::st_term, rx);
-            load_x(n + 1);
+            load_x();
             tc::fence_proxy_async_smem();
             if (hand_over(warp)) {
                 if (n == 0)  // [q; k] k^T, once
@@ -1298,7 +1301,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
             if (!L::own_ds) wait(&m1, n & 1, a.ctrl, ab, 0x636);
 #pragma unroll
             for (int i = 0; i < SI; ++i) put(smem + L::ds_at + i * TILE, L::ds_term, rd[i]);
-            load_s(n + 1, a.dstates, rd);
+            load_s(a.dstates, rd);
             tc::fence_proxy_async_smem();
             if (hand_over(warp)) {  // rows 64..127: E = X dS1^T (the rows above X are not used)
                 products_ss<4, NT, NT, NT>(tmem + COL_E, k_major(sx - TILE, 0), x_rows, k_major(sd, 0), d_rows,
