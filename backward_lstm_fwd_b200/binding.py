@@ -37,7 +37,7 @@ EXPORTS = ("lstm_fwd_workspace_size", "lstm_bwd_workspace_size", "lstm_fwd_works
            "lstm_embed_fwd", "lstm_embed_bwd_workspace_size", "lstm_embed_bwd",
            "lstm_gdr_fwd_workspace_size", "lstm_gdr_bwd_workspace_size", "lstm_gdr_fwd",
            "lstm_gdr_bwd",
-           "lstm_logprob_fwd_workspace_size", "lstm_logprob_fwd", "lstm_logprob_bwd",
+           "lstm_logprob_fwd", "lstm_logprob_bwd",
            "lstm_status", "lstm_profile_begin", "lstm_profile_end", "lstm_launch_count",
            "lstm_strerror", "lstm_abi_version")
 
@@ -170,9 +170,7 @@ def load(path: str = LIB_PATH):
     lib.lstm_embed_bwd_workspace_size.restype = sz
     lib.lstm_embed_bwd.argtypes = [ep, vp, vp, fp, ip, vp, vp, sz, vp]
     lib.lstm_embed_bwd.restype = ip
-    lib.lstm_logprob_fwd_workspace_size.argtypes = [lp]
-    lib.lstm_logprob_fwd_workspace_size.restype = sz
-    lib.lstm_logprob_fwd.argtypes = [lp, vp, vp, fp] + [vp] * 5 + [vp, sz, vp]
+    lib.lstm_logprob_fwd.argtypes = [lp, vp, vp, fp] + [vp] * 6
     lib.lstm_logprob_fwd.restype = ip
     lib.lstm_logprob_bwd.argtypes = [lp, vp, vp, fp] + [vp] * 5 + [ll, vp]
     lib.lstm_logprob_bwd.restype = ip
@@ -716,10 +714,6 @@ def logprob_dims(N: int, vocab: int, dtype, ld: Optional[int] = None, top: int =
                        int(id_bytes))
 
 
-def logprob_fwd_workspace_size(d: LogprobDims) -> int:
-    return int(load().lstm_logprob_fwd_workspace_size(ctypes.byref(d)))
-
-
 def _rows(t: torch.Tensor, name: str) -> int:
     """Row stride of a [N, vocab] tensor whose rows are dense."""
     _need(t.dim() == 2, f"{name} must be [N, vocab]")
@@ -730,25 +724,23 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return ld
 
 
-def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0, ws=None,
+def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
              stream=None) -> LogProbs:
     """lstm_logprob_fwd on logits [N, vocab] (dense rows, any row stride):
     log-probability of targets [N], entropy, and the `top` best alternatives
     of every row at softmax(logits / temperature)."""
     ld = _rows(logits, "logits")
     N, vocab = logits.shape
-    _on(logits, targets=targets, ws=ws)
-    _dense(targets=targets, ws=ws)
+    _on(logits, targets=targets)
+    _dense(targets=targets)
     _shaped(targets, "targets", (N,))
     _need(temperature > 0, "temperature must be positive")
     with _Device(logits, stream) as s:
         st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
         d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
-        if ws is None:
-            ws = empty_workspace(logprob_fwd_workspace_size(d), logits.device)
         _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
                                      _at(st.logp), _at(st.entropy), _at(st.stats), _at(st.top_ids),
-                                     _at(st.top_logp), _at(ws), _ws_bytes(ws), s),
+                                     _at(st.top_logp), s),
              "lstm_logprob_fwd")
     return st
 

@@ -178,8 +178,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
     {
         int before = 0, total = 0;
         if (a.blocks > 1) {
+#pragma unroll 16
             for (int b = 0; b < a.blocks; ++b) {
-                const int h = a.hist[b * kBins + tid];
+                const int h = __ldcg(a.hist + b * kBins + tid);
                 if (b < (int)blockIdx.x) before += h;
                 total += h;
             }
@@ -373,28 +374,23 @@ template <int W>
 __global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a) {
     const int u = blockIdx.x, last = u * kUnit + kUnit - 1;
     if (last + 1 >= a.N) return;
-    const int w = a.key[last];
-    if (w >= a.vocab || a.key[last + 1] != w) return;
-    if (u > 0 && a.key[u * kUnit - 1] == w) return;  // began before this unit
-    __shared__ int end_s;
+    const int w = a.key[last], after = a.key[last + 1], before = u > 0 ? a.key[u * kUnit - 1] : -1;
+    if (w >= a.vocab || after != w) return;
+    if (before == w) return;  // began before this unit
     __shared__ float part[kJoinGroups][kJoinCols * W];
-    // units u+1 .. end-1 hold the rest: a unit past u whose first token is w
+    // units u+1 .. end-1 hold the rest: those whose first token is w
     const int tid = threadIdx.x;
-    if (tid == 0) {
-        int lo = u + 1, hi = a.units;  // key[unit * kUnit] == w for units in [u+1, lo)
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (a.key[(long long)mid * kUnit] <= w) lo = mid + 1; else hi = mid;
-        }
-        end_s = lo;
-    }
-    __syncthreads();
+    int end = u + 1, more;
+    do {
+        const int v = end + tid;
+        more = __syncthreads_count(v < a.units && a.key[(long long)min(v, a.units - 1) * kUnit] == w);
+        end += more;
+    } while (more == kJoinGroups * kJoinCols);
     const int g = tid / kJoinCols, c0 = tid % kJoinCols;
     const int col = (blockIdx.y * kJoinCols + c0) * W;
     float acc[W] = {};
     if (col < a.I) {
         if (g == 0) load_cols<float, W>(a.plast + (long long)u * a.I + col, acc);
-        const int end = end_s;
         for (int v0 = u + 1 + g; v0 < end; v0 += 8 * kJoinGroups) {
             float f[8][W];
 #pragma unroll

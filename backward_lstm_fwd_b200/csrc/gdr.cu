@@ -130,9 +130,13 @@ template <class Kern> cudaError_t allow_smem(Kern kern, size_t bytes) {
 template <class E, int KD>
 int prep(const Shape &s, const void *q, const void *k, const float *g, const float *beta, char *w, const Layout &l,
          cudaStream_t st) {
-    PrepArgs p = {s, q, k, g, beta, w + l.qk, w + l.tp, (Ctrl *)w};
+    const int blocks = s.NC * s.B * s.Hk;
+    // five blocks an SM are resident; up to two a key head each would leave its
+    // value heads one after another on a card that is not full
+    const int heads = blocks <= 2 * host::sm_count() ? 1 : s.group;
+    PrepArgs p = {s, q, k, g, beta, w + l.qk, w + l.tp, (Ctrl *)w, heads};
     LSTM_CUDA_TRY(allow_smem(prep_kernel<E, KD>, PrepSmem<E, KD>::smem));
-    prep_kernel<E, KD><<<s.NC * s.B * s.Hk, 128, PrepSmem<E, KD>::smem, st>>>(p);
+    prep_kernel<E, KD><<<blocks * (s.group / heads), 128, PrepSmem<E, KD>::smem, st>>>(p);
     LSTM_CUDA_TRY(host::launched());
     return LSTM_OK;
 }

@@ -330,7 +330,8 @@ __device__ __forceinline__ void load_gates(const Shape &s, const float *g, const
 // -------------------------------------------------------------------- prep
 // Block (c, b, hk), 128 threads: the operand tiles of q and k (swizzled, in
 // terms, zero for padding and past K), then per value head of the group T2,
-// P and the gates, all in the layout the other kernels copy in bulk.
+// P and the gates, all in the layout the other kernels copy in bulk.  (Where
+// that leaves SMs idle, a block per value head, the tiles from the first.)
 //
 // Q K^T and K K^T are one product of the stacked [Q; K] with K.  T2 is the
 // inverse of a unit lower triangular matrix [A 0; B D] of 32 x 32 blocks:
@@ -343,6 +344,7 @@ struct PrepArgs {
     const float *g, *beta;
     char *qk, *tp;
     Ctrl *ctrl;
+    int heads;  // value heads a block takes: the group, or 1
 };
 constexpr int PREP_LD = 68;                    // floats between rows of a 64 x 64 matrix in shared memory
 constexpr int PREP_MAT = C * PREP_LD * 4;
@@ -365,7 +367,9 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
     const Shape &s = a.s;
     const int tid = threadIdx.x, warp = warp_id(), lane = tid & 31;
     clear_ctrl(a.ctrl);
-    int id = blockIdx.x;
+    const int split = s.group / a.heads, m0 = blockIdx.x % split * a.heads;
+    int id = blockIdx.x / split;
+    char *out = m0 == 0 ? a.qk + (size_t)id * QK<E, KD>::bytes : nullptr;
     const int hk = id % s.Hk;
     id /= s.Hk;
     const int b = id % s.B, c = id / s.B;
@@ -380,7 +384,6 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
         tc::tmem_relinquish();
     }
     // tiles: rows 0..63 q, 64..127 k; 16-byte groups of 8 dims, eight loads in flight a thread
-    char *out = a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes;
     // (thread tid keeps its group gr and takes rows row0, row0 + step, ...)
     constexpr int step = 128 / (KD / 8), U = 8;
     const int row0 = tid / (KD / 8), gr = tid % (KD / 8);
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
                 *(uint4 *)(tiles + t * QK<E, KD>::term + off) = o[t];
-                *(uint4 *)(out + t * QK<E, KD>::term + off) = o[t];
+                if (out) *(uint4 *)(out + t * QK<E, KD>::term + off) = o[t];
             }
         }
     }
@@ -419,12 +422,12 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
         tc::mma_commit(&done);
     }
     __syncwarp();
-    if (warp == 0) load_gates(s, a.g, a.beta, c, b, hk * s.group, len, sums);
+    if (warp == 0) load_gates(s, a.g, a.beta, c, b, hk * s.group + m0, len, sums);
     wait(&done, 0, a.ctrl, &abort_flag, 0x601);
     __syncthreads();
     const int row = tid & 63;  // warps 0, 1: Q K^T; warps 2, 3: K K^T
     const int half = warp & 1;  // rows 32 half ..
-    for (int m = 0; m < s.group; ++m) {
+    for (int m = m0; m < m0 + a.heads; ++m) {
         const int h = hk * s.group + m;
         char *tp = a.tp + (((size_t)c * s.B + b) * s.Hv + h) * TP_BYTES;
         const float2 bi = sums.b[row];
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
             product(low + 32, corner, -1.f, low);
         }
         __syncthreads();
-        if (warp == 0 && m + 1 < s.group) load_gates(s, a.g, a.beta, c, b, h + 1, len, sums);
+        if (warp == 0 && m + 1 < m0 + a.heads) load_gates(s, a.g, a.beta, c, b, h + 1, len, sums);
         // terms of T2 and P: eight threads a row, whole 128-byte lines a warp
 #pragma unroll 2
         for (int i = tid; i < 2 * C * 8; i += 128) {
@@ -1159,7 +1162,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ Sums sums;
-    __shared__ float colp[4][C], rowp[4][2 * C], rp[4][2 * C], ep[4][C], dots[16];
+    __shared__ float colp[4][C], rowp[4][2 * C], rp[4][2 * C], ep[4][C], dots[16], half_e;
+    __shared__ double half_d;
     __shared__ uint64_t loaded, m1, m2, m3;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
@@ -1399,44 +1403,38 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
             tc::mma_commit(&m3);
         }
         __syncwarp();
-        if (warp == 1) {  // dg and dbeta, two tokens a lane
-            auto sum4 = [&](const float *x, int stride, int j) {
-                return ((double)x[j] + x[stride + j]) + ((double)x[2 * stride + j] + x[3 * stride + j]);
-            };
-            double d[2], e[2], all = 0;
-            float db[2];
+        if (warp == 1 || warp == 5) {  // dg and dbeta, a token a lane
+            const int j = (warp & 4) * 8 + lane, t = c * C + j;
+            auto sum4 = [&](const float *x, int stride, int i) { return (x[i] + x[stride + i]) + (x[2 * stride + i] + x[3 * stride + i]); };
+            const long long at = ((long long)min(t, s.T - 1) * s.B + b) * s.Hv + h;
+            const float gt = a.g[at], be = sums.beta[j], gam = decay(sums.b[j]), left = decay(sums.b[C - 1], sums.b[j]);
+            const float col = sum4(&colp[0][0], C, j), ke = left * sum4(&ep[0][0], C, j);
+            const float rows = sum4(&rowp[0][0], 2 * C, j) + sum4(&rowp[0][0], 2 * C, C + j);
+            const float inter = gam * (s.scale * sum4(&rp[0][0], 2 * C, j) - sum4(&rp[0][0], 2 * C, C + j));
+            float all = lane < 16 ? dots[lane] : 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) all += dots[i];
-            all *= decay(sums.b[C - 1]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = 2 * lane + i;
-                const double col = sum4(&colp[0][0], C, j);
-                const double rows = sum4(&rowp[0][0], 2 * C, j) + sum4(&rowp[0][0], 2 * C, C + j);
-                const double ke = sum4(&ep[0][0], C, j);
-                const double gam = decay(sums.b[j]), left = decay(sums.b[C - 1], sums.b[j]);
-                d[i] = rows - sums.beta[j] * col + gam * (s.scale * sum4(&rp[0][0], 2 * C, j) - sum4(&rp[0][0], 2 * C, C + j));
-                e[i] = left * sums.beta[j] * ke;
-                db[i] = (float)(col + left * ke);
-            }
-            // suffix sums of d, prefix sums (exclusive) of e
-            double sd2 = d[0] + d[1], se = e[0] + e[1];
+            for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+            all = __shfl_sync(~0u, all, 0) * decay(sums.b[C - 1]);
+            // sums of d over the tokens from j on, of e over those before (double: most of d cancels)
+            const double d = (double)rows - (double)(be * col) + (double)inter;
+            const float e = be * ke;
+            double sd = d;
+            float se = e;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_down_sync(~0u, sd2, o), y = __shfl_up_sync(~0u, se, o);
-                if (lane + o < 32) sd2 += x;
+                const double x = __shfl_down_sync(~0u, sd, o);
+                const float y = __shfl_up_sync(~0u, se, o);
+                if (lane + o < 32) sd += x;
                 if (lane >= o) se += y;
             }
-            const double after = sd2 - d[0] - d[1], before = se - e[0] - e[1];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = c * C + 2 * lane + i;
-                if (t >= s.T) continue;
-                const double v = i == 0 ? after + d[1] + d[0] + before : after + d[1] + before + e[0];
-                const long long at = ((long long)t * s.B + b) * s.Hv + h;
+            if (warp == 5 && lane == 0) half_d = sd;
+            if (warp == 1 && lane == 31) half_e = se;
+            asm volatile("bar.sync 1, 64;" ::: "memory");
+            if (t < s.T) {
+                const double v = warp == 1 ? sd + half_d + (double)(se - e) : sd + (double)(half_e + (se - e));
                 // (where e^g is zero so is its gradient, and not the rounding of the sums)
-                a.dg[at] = t < len && !(a.g[at] < -104.f) ? (float)(v + all) : 0.f;
-                a.dbeta[at] = t < len ? db[i] : 0.f;
+                a.dg[at] = t < len && !(gt < -104.f) ? (float)(v + (double)all) : 0.f;
+                a.dbeta[at] = t < len ? col + ke : 0.f;
             }
         }
         __syncwarp();

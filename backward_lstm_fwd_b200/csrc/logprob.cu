@@ -9,19 +9,19 @@
 // temperature, every thread keeps its largest logit m, s = sum 2^{c (x - m)}
 // and w = sum 2^{c (x - m)} c (x - m), rescaled when a group of elements
 // raises m, and the threads' triples are joined at the end.  An element costs
-// one fused multiply-add, one exponential and three more operations; the 128
-// threads a block and eight blocks an SM let one row's loads run beside
-// another's joins.  The alternatives come from the same
-// pass: the first eighth of the range gives every thread its own maximum, the
-// top-th largest of those is a lower bound of the answer, and only elements at
-// or above it (a few times `top`) enter a candidate list; the eighth is looked
-// at twice (the second time from L1 / L2).  Rows are split over several blocks
-// where there are few of them, and a second launch joins the parts.  The
-// backward reads the logits and writes the gradient once.
-#include "host.cuh"
-
-#include <algorithm>
+// one fused multiply-add, one exponential and three more operations.  Many
+// rows: 128 threads a block and eight blocks an SM, so that one row's loads run
+// beside another's joins.  Few rows: 512 threads, and a cluster of up to eight
+// blocks shares a row and joins its parts through distributed shared memory.
+// The alternatives come from the same pass: the first eighth of the range gives
+// every thread its own maximum, the top-th largest of those is a lower bound of
+// the answer, and only elements at or above it (a few times `top`) enter a
+// candidate list; the eighth is looked at twice (the second time from L1 / L2).
+// The backward reads the logits and writes the gradient once.
 #include <climits>
+
+#include "host.cuh"
+#include "tc_ptx.cuh"
 
 using namespace lstm;
 
@@ -31,10 +31,13 @@ typedef __nv_bfloat16 bf16;
 typedef __half f16;
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kCand = 1024;  // candidate list of a block
-constexpr int kMinPart = 2048;  // fewest elements of a part of a row
-static_assert(LSTM_LOGPROB_MAX_TOP <= 64, "the candidate list is sized for 64 alternatives");
+constexpr int kCand = 1024;     // candidate list of a block
+constexpr int kNarrow = 128;    // threads of a block: many rows
+constexpr int kWide = 512;      // few rows
+constexpr int kMaxParts = 8;    // blocks that share a row (a portable cluster)
+constexpr int kPartBytes = 32 << 10;  // what a wide block has in flight at once
+constexpr int kBwdThreads = 128;
+static_assert(kMaxParts * LSTM_LOGPROB_MAX_TOP <= kCand, "the parts' alternatives fit the candidate list");
 
 // ---------------------------------------------------------------- elements
 // 2^x (the hardware's approximation: relative error about 2^-22, results
@@ -127,7 +130,7 @@ __device__ __forceinline__ Stat stat_of(const Run &a, float c) {
     const float d = fmaf(-a.m, c, a.cm), e = ex2(d);  // what the rounding of c m left
     return Stat{a.m, a.s * e, (a.w + a.s * d) * e};
 }
-__device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
+template <int THREADS> __device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         Stat b;
@@ -139,7 +142,7 @@ __device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
     if ((threadIdx.x & 31) == 0) warp_stats[threadIdx.x >> 5] = a;
     __syncthreads();
     a = warp_stats[0];
-    for (int w = 1; w < kWarps; ++w) a = join(a, warp_stats[w], c);
+    for (int w = 1; w < THREADS / 32; ++w) a = join(a, warp_stats[w], c);
     return a;  // the same in every thread
 }
 
@@ -151,9 +154,6 @@ struct Args {
     float c;  // inverse temperature times log2(e)
     float *logp, *entropy, *stats, *top_logp;
     int *top_ids;
-    Stat *part_stats;                     // [N][parts]
-    unsigned long long *part_keys;        // [N][parts][top]
-    Ctrl *ctrl;
 };
 
 __device__ __forceinline__ long long target_of(const void *t, int id64, int r) {
@@ -161,7 +161,7 @@ __device__ __forceinline__ long long target_of(const void *t, int id64, int r) {
 }
 
 // Row outputs from the row's triple and its sorted alternatives.
-template <class T>
+template <class T, int THREADS>
 __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsigned long long *keys) {
     const bool empty = st.m == -INFINITY && st.s == 0.f;  // every logit is -inf
     const float ls = log2f(st.s);
@@ -179,7 +179,7 @@ __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsi
             a.logp[r] = lp;
         }
     }
-    for (int i = threadIdx.x; i < a.top; i += kThreads) {
+    for (int i = threadIdx.x; i < a.top; i += THREADS) {
         const unsigned long long k = keys[i];
         a.top_ids[(long long)r * a.top + i] = index_of(k);
         a.top_logp[(long long)r * a.top + i] = empty ? -INFINITY : ((value_of(k) - st.m) * a.c - ls) * kLn2;
@@ -187,8 +187,9 @@ __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsi
 }
 
 // Of n <= kCand distinct keys in shared memory, the `top` largest in order.
+template <int THREADS>
 __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, int top, unsigned long long *out) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < n; i += THREADS) {
         const unsigned long long k = keys[i];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += keys[j] > k;
@@ -197,40 +198,47 @@ __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n,
     __syncthreads();
 }
 
-// The top-th largest of the block's thread maxima (-inf where fewer than
-// `top` threads have one): at least `top` elements are at or above it.
+// The top-th largest of the maxima of 128 groups of threads (-inf where fewer
+// than `top` groups have one): at least `top` elements are at or above it.
+template <int THREADS>
 __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, float *bound) {
-    maxima[threadIdx.x] = mine;
+    constexpr int each = THREADS / 128;
+#pragma unroll
+    for (int o = 1; o < each; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(~0u, mine, o));
+    const int t = threadIdx.x / each;
+    const bool lead = threadIdx.x % each == 0;
+    if (lead) maxima[t] = mine;
     if (threadIdx.x == 0) *bound = -INFINITY;
     __syncthreads();
-    int rank = 0;
+    if (lead) {
+        int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < kThreads; j += 4) {
-        const float4 o = *(const float4 *)(maxima + j);
-        const int t = threadIdx.x;
-        rank += o.x > mine || (o.x == mine && j < t);
-        rank += o.y > mine || (o.y == mine && j + 1 < t);
-        rank += o.z > mine || (o.z == mine && j + 2 < t);
-        rank += o.w > mine || (o.w == mine && j + 3 < t);
+        for (int j = 0; j < 128; j += 4) {
+            const float4 o = *(const float4 *)(maxima + j);
+            rank += o.x > mine || (o.x == mine && j < t);
+            rank += o.y > mine || (o.y == mine && j + 1 < t);
+            rank += o.z > mine || (o.z == mine && j + 2 < t);
+            rank += o.w > mine || (o.w == mine && j + 3 < t);
+        }
+        if (rank == top - 1) *bound = mine;
     }
-    if (rank == top - 1) *bound = mine;
     __syncthreads();
     return *bound;
 }
 
 // ----------------------------------------------------------------- forward
-// Block (r, p): part p of row r.  TOP: alternatives wanted.
-template <class T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
-    constexpr int n = Group<T>::n, U = 4;
-    __shared__ Stat warp_stats[kWarps];
+// Block (r, p): part p of row r; the parts of a row are a cluster.  TOP:
+// alternatives wanted.
+template <class T, bool TOP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
+    constexpr int n = Group<T>::n, U = 4, WARPS = THREADS / 32;
+    __shared__ Stat warp_stats[WARPS], part_stat;
     __shared__ unsigned long long cand[TOP ? kCand : 1], best[TOP ? LSTM_LOGPROB_MAX_TOP : 1];
-    __shared__ __align__(16) float maxima[TOP ? kThreads : 4];
+    __shared__ __align__(16) float maxima[TOP ? 128 : 4];
     __shared__ float bound_s;
     __shared__ int count;
     const int tid = threadIdx.x;
     const int r = blockIdx.x / a.parts, p = blockIdx.x % a.parts;
-    clear_ctrl(a.ctrl);
     const T *row = (const T *)a.logits + (long long)r * a.ld;
     const float c = a.c;
     // part p is the elements [e0, e1); its 16-byte groups [g0, g1)
@@ -250,14 +258,14 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
     };
     // groups [b, e): U loads in flight a thread
     auto run = [&](int b, int e, auto &&each) {
-        for (int g = b + tid; g < e; g += U * kThreads) {
+        for (int g = b + tid; g < e; g += U * THREADS) {
             uint4 v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (g + u * kThreads < e) v[u] = __ldg(gp + g + u * kThreads);
+                if (g + u * THREADS < e) v[u] = __ldg(gp + g + u * THREADS);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (g + u * kThreads < e) each(v[u], g + u * kThreads);
+                if (g + u * THREADS < e) each(v[u], g + u * THREADS);
         }
     };
     auto edge = [&](auto &&each) {  // the elements outside whole groups: fewer than 2 n
@@ -269,14 +277,14 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
         const float f[1] = {x};
         add<1>(sum, f, c, gmax);
     });
-    const int first = TOP ? min(groups, max(groups / 8, U * kThreads)) : 0;
+    const int first = TOP ? min(groups, max(groups / 8, U * THREADS)) : 0;
     if (TOP) {
         run(0, first, [&](const uint4 &v, int) {
             float f[n];
             unpack<T>(v, f);
             add<n>(sum, f, c, gmax);
         });
-        bound = bound_of(sum.m, a.top, maxima, &bound_s);
+        bound = bound_of<THREADS>(sum.m, a.top, maxima, &bound_s);
         edge([&](float x, int i) {
             if (!(x < bound)) push(x, i);
         });
@@ -298,28 +306,28 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
                 if (!(f[i] < bound)) push(f[i], h + g * n + i);
         }
     });
-    Stat st = block_join(stat_of(sum, c), c, warp_stats);  // its barrier also closes the candidate list
+    Stat st = block_join<THREADS>(stat_of(sum, c), c, warp_stats);  // its barrier also closes the candidate list
     if (st.m <= kMask && st.m > -INFINITY) {  // nothing but masked logits: their plain sums
         Stat mine = {st.m, 0.f, 0.f};
-        for (int i = e0 + tid; i < e1; i += kThreads) {
+        for (int i = e0 + tid; i < e1; i += THREADS) {
             const float d = floor_nan((to_f(row[i]) - st.m) * c), e = ex2(d);
             mine.s += e;
             mine.w = fmaf(e, d, mine.w);
         }
         __syncthreads();
-        st = block_join(mine, c, warp_stats);
+        st = block_join<THREADS>(mine, c, warp_stats);
     }
 
     if (TOP) {
         if (count <= kCand) {
-            rank_keys(cand, count, a.top, best);
+            rank_keys<THREADS>(cand, count, a.top, best);
         } else {
             // More candidates than the list holds (long runs of equal values):
             // one exact pass over the part per alternative.
             unsigned long long prev = ~0ull;
             for (int k = 0; k < a.top; ++k) {
                 unsigned long long mine = 0;
-                for (int i = e0 + tid; i < e1; i += kThreads) {
+                for (int i = e0 + tid; i < e1; i += THREADS) {
                     const unsigned long long key = key_of(to_f(row[i]), i);
                     if (key < prev && key > mine) mine = key;
                 }
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
                 __syncthreads();
                 if ((tid & 31) == 0) cand[tid >> 5] = mine;
                 __syncthreads();
-                for (int w = 0; w < kWarps; ++w) mine = cand[w] > mine ? cand[w] : mine;
+                for (int w = 0; w < WARPS; ++w) mine = cand[w] > mine ? cand[w] : mine;
                 prev = mine;
                 if (tid == 0) best[k] = mine;
             }
@@ -339,64 +347,35 @@ __global__ void __launch_bounds__(kThreads, 8) fwd_kernel(Args a) {
         }
     }
     if (a.parts == 1) {
-        finish<T>(a, r, st, best);
+        finish<T, THREADS>(a, r, st, best);
         return;
     }
-    if (tid == 0) a.part_stats[blockIdx.x] = st;
-    if (TOP)
-        for (int i = tid; i < a.top; i += kThreads) a.part_keys[(long long)blockIdx.x * a.top + i] = best[i];
-}
-
-// Join the parts of row blockIdx.x.
-template <class T>
-__global__ void __launch_bounds__(kThreads) join_kernel(Args a) {
-    __shared__ Stat warp_stats[kWarps];
-    __shared__ unsigned long long cand[kCand], best[LSTM_LOGPROB_MAX_TOP];
-    __shared__ __align__(16) float maxima[kThreads];
-    __shared__ float bound_s;
-    __shared__ int count;
-    const int r = blockIdx.x, tid = threadIdx.x;
-    Stat st = {-INFINITY, 0.f, 0.f};
-    if (tid < a.parts) st = a.part_stats[(long long)r * a.parts + tid];
-    if (tid == 0) count = 0;
-    st = block_join(st, a.c, warp_stats);
-    if (a.top) {
-        // a part's first alternative is its maximum; parts <= kThreads
-        const unsigned long long *keys = a.part_keys + (long long)r * a.parts * a.top;
-        const float mine = tid < a.parts ? value_of(keys[(long long)tid * a.top]) : -INFINITY;
-        const float bound = bound_of(mine == mine ? mine : -INFINITY, a.top, maxima, &bound_s);
-        for (int i = tid; i < a.parts * a.top; i += kThreads) {
-            const unsigned long long k = keys[i];
-            if (!(value_of(k) < bound)) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kCand) cand[at] = k;
-            }
+    // the first block of the cluster joins the parts
+    if (tid == 0) part_stat = st;
+    tc::cluster_sync_all();
+    if (p == 0) {
+        auto peer = [&](const void *x, int q) { return tc::map_rank(tc::smem_u32(x), q); };
+        for (int q = 1; q < a.parts; ++q) {
+            const uint32_t at = peer(&part_stat, q);
+            Stat o;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.m) : "r"(at));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.s) : "r"(at + 4));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.w) : "r"(at + 8));
+            st = join(st, o, c);
         }
-        __syncthreads();
-        if (count <= kCand) {
-            rank_keys(cand, count, a.top, best);
-        } else {
-            unsigned long long prev = ~0ull;
-            for (int k = 0; k < a.top; ++k) {
-                unsigned long long m = 0;
-                for (int i = tid; i < a.parts * a.top; i += kThreads)
-                    if (keys[i] < prev && keys[i] > m) m = keys[i];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const unsigned long long y = __shfl_xor_sync(~0u, m, o);
-                    m = y > m ? y : m;
-                }
-                __syncthreads();
-                if ((tid & 31) == 0) cand[tid >> 5] = m;
-                __syncthreads();
-                for (int w = 0; w < kWarps; ++w) m = cand[w] > m ? cand[w] : m;
-                prev = m;
-                if (tid == 0) best[k] = m;
+        if (TOP) {
+            const int all = a.parts * a.top;
+            for (int i = tid; i < all; i += THREADS) {
+                unsigned long long k;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(peer(&best[i % a.top], i / a.top)));
+                cand[i] = k;
             }
             __syncthreads();
+            rank_keys<THREADS>(cand, all, a.top, best);
         }
+        finish<T, THREADS>(a, r, st, best);
     }
-    finish<T>(a, r, st, best);
+    tc::cluster_sync_all();  // no block leaves while its memory may be read
 }
 
 // ---------------------------------------------------------------- backward
@@ -410,7 +389,7 @@ struct BwdArgs {
 };
 
 template <class T, bool VEC>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) bwd_kernel(BwdArgs a) {
     constexpr int n = Group<T>::n, U = 2;
     const int tid = threadIdx.x;
     const int r = blockIdx.x / a.chunks, p = blockIdx.x % a.chunks;
@@ -432,7 +411,7 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(BwdArgs a) {
     };
     const int e0 = p * a.chunk, e1 = min(a.vocab, e0 + a.chunk);
     if (!VEC) {
-        for (int i = e0 + tid; i < e1; i += kThreads) y[i] = from_f<T>(grad(to_f(x[i]), i));
+        for (int i = e0 + tid; i < e1; i += kBwdThreads) y[i] = from_f<T>(grad(to_f(x[i]), i));
         return;
     }
     const int mis = (int)(((uintptr_t)(x + e0) & 15u) / sizeof(T));
@@ -442,14 +421,14 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(BwdArgs a) {
     if (tid < e1 - tail) y[tail + tid] = from_f<T>(grad(to_f(x[tail + tid]), tail + tid));
     const uint4 *xv = (const uint4 *)(x + h);
     uint4 *yv = (uint4 *)(y + h);
-    for (int g = tid; g < groups; g += U * kThreads) {
+    for (int g = tid; g < groups; g += U * kBwdThreads) {
         uint4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (g + u * kThreads < groups) v[u] = xv[g + u * kThreads];  // dlogits may be logits
+            if (g + u * kBwdThreads < groups) v[u] = xv[g + u * kBwdThreads];  // dlogits may be logits
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int gg = g + u * kThreads;
+            const int gg = g + u * kBwdThreads;
             if (gg >= groups) break;
             float f[n];
             unpack<T>(v[u], f);
@@ -475,33 +454,33 @@ bool dims_supported(const lstm_logprob_dims *d) {
 // exponential of zero at every temperature.
 bool temp_ok(float inv_temp) { return inv_temp >= 1e-20f && inv_temp <= 1e20f; }
 
-// Parts of a row: one where the rows alone fill the card two blocks an SM
-// deep; else enough for two blocks an SM, of kMinPart elements at least.
-int parts_of(const lstm_logprob_dims *d, int sms) {
-    if (d->N >= 2 * sms) return 1;
-    const int want = (2 * sms + std::max(d->N, 1) - 1) / std::max(d->N, 1);
-    return std::max(1, std::min({want, d->vocab / kMinPart, kThreads}));
-}
-
-size_t fwd_need(const lstm_logprob_dims *d, int parts) {
-    if (parts == 1) return kCtrlBytes;
-    const size_t rows = (size_t)d->N * parts;
-    return kCtrlBytes + align_up(rows * sizeof(Stat), 256) + align_up(rows * d->top * 8, 256);
-}
-
-template <class T> int forward(Args &a, cudaStream_t s) {
-    const long long blocks = (long long)a.N * a.parts;
-    if (blocks > INT_MAX) return LSTM_ERR_UNSUPPORTED;
-    if (a.top)
-        fwd_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    else
-        fwd_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    LSTM_CUDA_TRY(host::launched());
-    if (a.parts > 1) {
-        join_kernel<T><<<a.N, kThreads, 0, s>>>(a);
+// Rows that fill the card two narrow blocks an SM deep take a block each; of
+// fewer rows each takes a wide block, or a cluster of them where a block would
+// need more than one batch of loads in flight.
+template <class T, bool TOP> int forward(Args &a, int sms, cudaStream_t s) {
+    if (a.N >= 2 * sms) {
+        a.parts = 1;
+        fwd_kernel<T, TOP, kNarrow><<<a.N, kNarrow, 0, s>>>(a);
         LSTM_CUDA_TRY(host::launched());
+        return LSTM_OK;
     }
+    a.parts = 1;
+    while (a.parts < kMaxParts && (long long)a.vocab * (int)sizeof(T) > a.parts * kPartBytes) a.parts *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.N * a.parts));
+    cfg.blockDim = dim3(kWide);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)a.parts, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    LSTM_CUDA_TRY(cudaLaunchKernelEx(&cfg, fwd_kernel<T, TOP, kWide>, a));
+    note_launch();
     return LSTM_OK;
+}
+template <class T> int forward_t(Args &a, int sms, cudaStream_t s) {
+    return a.top ? forward<T, true>(a, sms, s) : forward<T, false>(a, sms, s);
 }
 
 template <class T> int backward(BwdArgs &a, cudaStream_t s) {
@@ -514,9 +493,9 @@ template <class T> int backward(BwdArgs &a, cudaStream_t s) {
     // 16-byte groups need logits and dlogits rows that start alike
     const bool vec = (a.ld - a.ldd) * (long long)sizeof(T) % 16 == 0;
     if (vec)
-        bwd_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+        bwd_kernel<T, true><<<(unsigned)blocks, kBwdThreads, 0, s>>>(a);
     else
-        bwd_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+        bwd_kernel<T, false><<<(unsigned)blocks, kBwdThreads, 0, s>>>(a);
     LSTM_CUDA_TRY(host::launched());
     return LSTM_OK;
 }
@@ -525,14 +504,8 @@ template <class T> int backward(BwdArgs &a, cudaStream_t s) {
 
 extern "C" {
 
-size_t lstm_logprob_fwd_workspace_size(const lstm_logprob_dims *d) {
-    if (!dims_ok(d) || !dims_supported(d)) return 0;
-    return fwd_need(d, parts_of(d, host::sm_count()));
-}
-
 int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void *targets, float inv_temp,
-                     float *logp, float *entropy, float *stats, int *top_ids, float *top_logp, void *ws,
-                     size_t ws_bytes, void *stream) {
+                     float *logp, float *entropy, float *stats, int *top_ids, float *top_logp, void *stream) {
     if (!dims_ok(d) || !temp_ok(inv_temp)) return LSTM_ERR_INVALID_ARG;
     if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
     const bool any = d->N > 0;
@@ -540,9 +513,6 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
         !host::ptr_ok(logp, any && targets) || !host::ptr_ok(entropy, false) || !host::ptr_ok(stats, any) ||
         !host::ptr_ok(top_ids, any && d->top > 0) || !host::ptr_ok(top_logp, any && d->top > 0))
         return LSTM_ERR_INVALID_ARG;
-    const int parts = parts_of(d, host::sm_count());
-    const int rc = host::ws_check(ws, ws_bytes, fwd_need(d, parts));
-    if (rc != LSTM_OK) return rc;
     if (!any) return LSTM_OK;
     cudaStream_t s = (cudaStream_t)stream;
     Args a = {};
@@ -552,7 +522,6 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     a.N = d->N;
     a.vocab = d->vocab;
     a.top = d->top;
-    a.parts = parts;
     a.ld = d->ld;
     a.c = inv_temp * kLog2e;
     a.logp = logp;
@@ -560,12 +529,10 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     a.stats = stats;
     a.top_ids = top_ids;
     a.top_logp = top_logp;
-    a.part_stats = (Stat *)((char *)ws + kCtrlBytes);
-    a.part_keys = (unsigned long long *)((char *)ws + kCtrlBytes + align_up((size_t)d->N * parts * sizeof(Stat), 256));
-    a.ctrl = (Ctrl *)ws;
-    if (d->dtype == LSTM_F32) return forward<float>(a, s);
-    if (d->dtype == LSTM_F16) return forward<f16>(a, s);
-    return forward<bf16>(a, s);
+    const int sms = host::sm_count();
+    if (d->dtype == LSTM_F32) return forward_t<float>(a, sms, s);
+    if (d->dtype == LSTM_F16) return forward_t<f16>(a, sms, s);
+    return forward_t<bf16>(a, sms, s);
 }
 
 int lstm_logprob_bwd(const lstm_logprob_dims *d, const void *logits, const void *targets, float inv_temp,

@@ -491,11 +491,9 @@ typedef struct lstm_logprob_dims {
     int id_bytes; /* 4 or 8 */
 } lstm_logprob_dims;
 
-/* (Depends on the current device: rows are split by its SM count.) */
-size_t lstm_logprob_fwd_workspace_size(const lstm_logprob_dims *d);
 int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void *targets,
                      float inv_temp, float *logp, float *entropy, float *stats, int *top_ids,
-                     float *top_logp, void *ws, size_t ws_bytes, void *stream);
+                     float *top_logp, void *stream);
 int lstm_logprob_bwd(const lstm_logprob_dims *d, const void *logits, const void *targets,
                      float inv_temp, const float *stats, const float *entropy,
                      const float *dlogp, const float *dentropy, void *dlogits, long long ldd,

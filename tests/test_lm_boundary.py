@@ -61,10 +61,9 @@ def test_embed_extents(lib):
 
 # --------------------------------------------------------- log-probabilities
 def logprob_fwd(lib, d, inv_temp=1.0, logits=FAKE, targets=FAKE, logp=FAKE, entropy=FAKE, stats=FAKE, top_ids=FAKE,
-                top_logp=FAKE, ws=FAKE, ws_bytes=None):
-    n = L.logprob_fwd_workspace_size(d) if ws_bytes is None else ws_bytes
+                top_logp=FAKE):
     return lib.lstm_logprob_fwd(ctypes.byref(d), logits, targets, inv_temp, logp, entropy, stats, top_ids, top_logp,
-                                ws, n, None)
+                                None)
 
 
 def logprob_bwd(lib, d, inv_temp=1.0, logits=FAKE, targets=FAKE, stats=FAKE, entropy=FAKE, dlogp=FAKE, dentropy=FAKE,
@@ -78,9 +77,8 @@ def logprob_bwd(lib, d, inv_temp=1.0, logits=FAKE, targets=FAKE, stats=FAKE, ent
 def test_logprob_dims(lib, kw):
     kw.setdefault("dtype", L.LSTM_F32)
     d = L.logprob_dims(**kw)
-    assert logprob_fwd(lib, d, ws_bytes=1 << 30) == L.LSTM_ERR_INVALID_ARG
+    assert logprob_fwd(lib, d) == L.LSTM_ERR_INVALID_ARG
     assert logprob_bwd(lib, d) == L.LSTM_ERR_INVALID_ARG
-    assert L.logprob_fwd_workspace_size(d) == 0
 
 
 def test_logprob_arguments(lib):
@@ -97,13 +95,11 @@ def test_logprob_arguments(lib):
         assert logprob_bwd(lib, d, **{k: FAKE + 2}) == L.LSTM_ERR_INVALID_ARG
     assert logprob_bwd(lib, d, ldd=99) == L.LSTM_ERR_INVALID_ARG
     assert logprob_bwd(lib, d, dlogits=FAKE, ldd=104) == L.LSTM_ERR_INVALID_ARG  # in place with another stride
-    need = L.logprob_fwd_workspace_size(d)
-    assert logprob_fwd(lib, d, ws_bytes=need - 1) == L.LSTM_ERR_WORKSPACE
-    assert logprob_fwd(lib, d, ws=FAKE + 128) == L.LSTM_ERR_WORKSPACE
-    assert logprob_fwd(lib, L.logprob_dims(3, 100, 0, top=65), ws_bytes=1 << 30) == L.LSTM_ERR_UNSUPPORTED
-    # few long rows are split: the parts' sums and alternatives live in the workspace
-    assert L.logprob_fwd_workspace_size(L.logprob_dims(2, 128000, 0, top=20)) > 256
-    assert L.logprob_fwd_workspace_size(L.logprob_dims(4096, 128000, 0, top=20)) == 256
+    assert logprob_fwd(lib, L.logprob_dims(3, 100, 0, top=65)) == L.LSTM_ERR_UNSUPPORTED
+    # nothing to do: nothing is enqueued
+    assert logprob_fwd(lib, L.logprob_dims(0, 100, 0, top=4), logits=None, targets=None, logp=None, stats=None, top_ids=None,
+                       top_logp=None) == L.LSTM_OK
+    assert logprob_bwd(lib, L.logprob_dims(0, 100, 0), dlogits=None) == L.LSTM_OK
 
 
 def test_binding_refuses_host_tensors_and_shapes(lib):
