@@ -9,14 +9,15 @@
 // temperature, every thread keeps its largest logit m, s = sum 2^{c (x - m)}
 // and w = sum 2^{c (x - m)} c (x - m), rescaled when a group of elements
 // raises m, and the threads' triples are joined at the end.  An element costs
-// one fused multiply-add, one exponential and three more operations.  Many
+// one exponential and half of three packed operations (and its conversion), 32
+// elements one look at the maximum.  Many
 // rows: 128 threads a block and eight blocks an SM, so that one row's loads run
 // beside another's joins.  Few rows: 512 threads, and a cluster of up to eight
 // blocks shares a row and joins its parts through distributed shared memory.
-// The alternatives come from the same pass: the first eighth of the range gives
+// The alternatives come from the same pass: the first third of the range gives
 // every thread its own maximum, the top-th largest of those is a lower bound of
 // the answer, and only elements at or above it (a few times `top`) enter a
-// candidate list; the eighth is looked at twice (the second time from L1 / L2).
+// candidate list; the third is looked at twice (the second time from L1 / L2).
 // The backward reads the logits and writes the gradient once.
 #include <climits>
 
@@ -97,39 +98,130 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
     const float da = floor_nan((a.m - m) * c), db = floor_nan((b.m - m) * c), fa = ex2(da), fb = ex2(db);
     return Stat{m, a.s * fa + b.s * fb, (a.w + a.s * da) * fa + (b.w + b.s * db) * fb};
 }
-// A thread's own sums, with the rounded c m in the place of c m, so that an
-// exponent is one fused multiply-add.
-struct Run {
-    float m, cm, s, w;
+// Two floats at once.
+struct F2 {
+    float x, y;
 };
-// gmax: the largest of f.
-template <int n> __device__ __forceinline__ void add(Run &a, const float (&f)[n], float c, float &gmax) {
-    gmax = f[0];
-#pragma unroll
-    for (int i = 1; i < n; ++i) gmax = fmaxf(gmax, f[i]);
-    if (gmax > a.m) {
-        const float cm = fmaxf(gmax * c, -3.4e38f), d = floor_nan(a.cm - cm), e = ex2(d);
-        a.w = (a.w + a.s * d) * e;
-        a.s *= e;
-        a.m = gmax;
-        a.cm = cm;
-    }
-    const float cm = a.cm == -INFINITY ? 0.f : a.cm;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-        const float d = floor_nan(fmaf(f[i], c, -cm)), e = ex2(d);
-        a.s += e;
-        a.w = fmaf(e, d, a.w);
-    }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
-// Logits below this are masks: c m may overflow for them.  (A row of nothing
-// else is summed again by the block, see there.)
-constexpr float kMask = -1e16f;
-__device__ __forceinline__ Stat stat_of(const Run &a, float c) {
-    if (!(a.m > kMask)) return Stat{a.m, a.s, a.w};  // s and w are 0, or NaN
-    const float d = fmaf(-a.m, c, a.cm), e = ex2(d);  // what the rounding of c m left
-    return Stat{a.m, a.s * e, (a.w + a.s * d) * e};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
+
+// A logit at or below kMask is a mask: raised to it on the way in (NaN stays),
+// so that nothing is infinite, and its exponential is zero beside any other
+// logit.  A row of masks alone is summed again as it stands.
+constexpr float kMask = -9007199254740992.f;  // -2^53: exact in bf16 too
+__device__ __forceinline__ float raised(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(kMask));
+    return y;
+}
+
+// A 16-byte group as pairs of floats raised to the mask value; largest() may
+// raise in place where the type holds kMask.
+template <class T> struct Pairs {
+    static constexpr int n = 4;
+    typedef typename Elem<T>::E2 E2;
+    __device__ static __forceinline__ float largest(uint4 &v) {
+        E2 *h = reinterpret_cast<E2 *>(&v);
+        if (Elem<T>::kFmt == 1) {
+            const E2 lo = Elem<T>::from_f2(kMask, kMask);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], lo);
+        }
+        const float2 m = Elem<T>::to_f2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+        return fmaxf(m.x, m.y);
+    }
+    __device__ static __forceinline__ F2 pair(const uint4 &v, int i) {
+        const float2 f = Elem<T>::to_f2(reinterpret_cast<const E2 *>(&v)[i]);
+        return Elem<T>::kFmt == 1 ? F2{f.x, f.y} : F2{raised(f.x), raised(f.y)};
+    }
+    // bit i: element i is at or above the bound (or NaN)
+    __device__ static __forceinline__ unsigned candidates(const uint4 &v, float bound) {
+        const E2 *h = reinterpret_cast<const E2 *>(&v), b = Elem<T>::from_f2(bound, bound);
+        unsigned bits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned at = ~__hlt2_mask(h[i], b);
+            bits |= ((at & 1u) | ((at >> 15) & 2u)) << (2 * i);
+        }
+        return bits;
+    }
+};
+template <> struct Pairs<float> {
+    static constexpr int n = 2;
+    __device__ static __forceinline__ float largest(uint4 &v) {
+        float *f = reinterpret_cast<float *>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = raised(f[i]);
+        return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+    }
+    __device__ static __forceinline__ F2 pair(const uint4 &v, int i) {
+        const float *f = reinterpret_cast<const float *>(&v);
+        return F2{f[2 * i], f[2 * i + 1]};
+    }
+    __device__ static __forceinline__ unsigned candidates(const uint4 &v, float bound) {
+        const float *f = reinterpret_cast<const float *>(&v);
+        unsigned bits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bits |= (unsigned)!(f[i] < bound) << i;
+        return bits;
+    }
+};
+
+// A group of masks.
+template <class T> struct Elem16 { static constexpr unsigned neg_inf = 0xff80u; };
+template <> struct Elem16<f16> { static constexpr unsigned neg_inf = 0xfc00u; };
+template <class T> __device__ __forceinline__ uint4 masks() {
+    const unsigned x = sizeof(T) == 4 ? 0xff800000u : Elem16<T>::neg_inf * 0x10001u;
+    return make_uint4(x, x, x, x);
+}
+
+// A thread's own sums, with the rounded c m in the place of c m, so that an
+// exponent is one fused multiply-add (half of a packed one).
+struct Run {
+    float m = kMask, cm = 1e30f;  // masks only so far: every exponential is zero
+    F2 s = {0.f, 0.f}, w = {0.f, 0.f};
+    __device__ __forceinline__ void see(float gmax, float c) {  // the next elements' largest
+        if (gmax > m) {
+            const float cn = gmax * c, d = m == kMask ? 0.f : cm - cn, e = ex2(d);
+            w.x = (w.x + s.x * d) * e;
+            w.y = (w.y + s.y * d) * e;
+            s.x *= e;
+            s.y *= e;
+            m = gmax;
+            cm = cn;
+        }
+    }
+    __device__ __forceinline__ void add(F2 x, float c) {
+        const F2 d = fma2(x, F2{c, c}, F2{-cm, -cm}), e = F2{ex2(d.x), ex2(d.y)};
+        s = add2(s, e);
+        w = fma2(e, d, w);
+    }
+    __device__ __forceinline__ void add1(float x, float c) {
+        see(x, c);
+        const float d = fmaf(x, c, -cm), e = ex2(d);
+        s.x += e;
+        w.x = fmaf(e, d, w.x);
+    }
+    __device__ __forceinline__ Stat stat(float c) const {
+        if (m == kMask) return Stat{-INFINITY, s.x + s.y, w.x + w.y};  // zeros, or NaN
+        const float d = fmaf(-m, c, cm), e = ex2(d);  // what the rounding of c m left
+        const float st = s.x + s.y;
+        return Stat{m, st * e, (w.x + w.y + st * d) * e};
+    }
+};
 template <int THREADS> __device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -151,7 +243,7 @@ struct Args {
     const void *targets;
     int id64, N, vocab, top, parts;
     long long ld;
-    float c;  // inverse temperature times log2(e)
+    float inv_temp, c;  // c: times log2(e)
     float *logp, *entropy, *stats, *top_logp;
     int *top_ids;
 };
@@ -174,7 +266,7 @@ __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsi
             float lp = 0.f;  // an ignored row
             if (t >= 0 && t < a.vocab) {
                 const float x = to_f(((const T *)a.logits)[(long long)r * a.ld + t]);
-                lp = empty ? -INFINITY : ((x - st.m) * a.c - ls) * kLn2;
+                lp = empty ? -INFINITY : (x - st.m) * a.inv_temp - ls * kLn2;
             }
             a.logp[r] = lp;
         }
@@ -182,7 +274,7 @@ __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsi
     for (int i = threadIdx.x; i < a.top; i += THREADS) {
         const unsigned long long k = keys[i];
         a.top_ids[(long long)r * a.top + i] = index_of(k);
-        a.top_logp[(long long)r * a.top + i] = empty ? -INFINITY : ((value_of(k) - st.m) * a.c - ls) * kLn2;
+        a.top_logp[(long long)r * a.top + i] = empty ? -INFINITY : (value_of(k) - st.m) * a.inv_temp - ls * kLn2;
     }
 }
 
@@ -231,7 +323,7 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, fl
 // alternatives wanted.
 template <class T, bool TOP, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
-    constexpr int n = Group<T>::n, U = 4, WARPS = THREADS / 32;
+    constexpr int n = Group<T>::n, U = TOP && THREADS == kNarrow ? 2 : 4, WARPS = THREADS / 32;
     __shared__ Stat warp_stats[WARPS], part_stat;
     __shared__ unsigned long long cand[TOP ? kCand : 1], best[TOP ? LSTM_LOGPROB_MAX_TOP : 1];
     __shared__ __align__(16) float maxima[TOP ? 128 : 4];
@@ -248,74 +340,94 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
     const int groups = (e1 - h) / n;
     const uint4 *gp = (const uint4 *)(row + h);
     const int tail = h + groups * n;                  // [tail, e1): after the last one
-    Run sum = {-INFINITY, -INFINITY, 0.f, 0.f};
-    float bound = -INFINITY, gmax;
+    Run sum;
+    float bound = -INFINITY;
     if (TOP && tid == 0) count = 0;
 
-    auto push = [&](float x, int i) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kCand) cand[at] = key_of(x, i);
+    // the elements of `bits`, from index i on and found at x, become candidates
+    auto push = [&](int i, unsigned bits, const T *x) {
+#pragma unroll 1
+        for (; bits; bits &= bits - 1) {
+            const int j = __ffs(bits) - 1, at = atomicAdd(&count, 1);
+            if (at < kCand) cand[at] = key_of(to_f(x[j]), i + j);
+        }
     };
-    // groups [b, e): U loads in flight a thread
-    auto run = [&](int b, int e, auto &&each) {
+    // groups b .. e-1, the next U of a thread loaded before it looks at the last
+    // ones; look: candidates too
+    auto fetch = [&](uint4 (&v)[U], int g, int e) {
+        if (g + (U - 1) * THREADS < e) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = __ldg(gp + g + u * THREADS);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = g + u * THREADS < e ? __ldg(gp + g + u * THREADS) : masks<T>();
+        }
+    };
+    auto run = [&](int b, int e, bool look) {
+        uint4 ahead[U];
+        fetch(ahead, b + tid, e);
+#pragma unroll 1
         for (int g = b + tid; g < e; g += U * THREADS) {
             uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (g + u * THREADS < e) v[u] = __ldg(gp + g + u * THREADS);
+            for (int u = 0; u < U; ++u) v[u] = ahead[u];
+            fetch(ahead, g + U * THREADS, e);
+            float gm[U], top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                gm[u] = Pairs<T>::largest(v[u]);
+                top = fmaxf(top, gm[u]);
+            }
+            sum.see(top, c);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (g + u * THREADS < e) each(v[u], g + u * THREADS);
+#pragma unroll
+                for (int i = 0; i < Pairs<T>::n; ++i) sum.add(Pairs<T>::pair(v[u], i), c);
+            if (TOP && look && !(top < bound)) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (g + u * THREADS < e && !(gm[u] < bound))
+                        push(h + (g + u * THREADS) * n, Pairs<T>::candidates(v[u], bound), (const T *)(gp + g + u * THREADS));
+            }
         }
     };
-    auto edge = [&](auto &&each) {  // the elements outside whole groups: fewer than 2 n
-        if (tid < h - e0) each(to_f(row[e0 + tid]), e0 + tid);
-        if (tid < e1 - tail) each(to_f(row[tail + tid]), tail + tid);
-    };
-
-    edge([&](float x, int) {
-        const float f[1] = {x};
-        add<1>(sum, f, c, gmax);
-    });
-    const int first = TOP ? min(groups, max(groups / 8, U * THREADS)) : 0;
+    // the elements outside whole groups: fewer than 2 n
+    const int mine0 = e0 + tid < h ? e0 + tid : -1, mine1 = tail + tid < e1 ? tail + tid : -1;
+    if (mine0 >= 0) sum.add1(raised(to_f(row[mine0])), c);
+    if (mine1 >= 0) sum.add1(raised(to_f(row[mine1])), c);
+    const int first = TOP ? min(groups, max(groups / 3, U * THREADS)) : 0;  // (an eighth measured 171 us on
+    // 2048 x 100003 with 8 alternatives, a quarter 135, a half 135, a third 132: candidates against a second look)
     if (TOP) {
-        run(0, first, [&](const uint4 &v, int) {
-            float f[n];
-            unpack<T>(v, f);
-            add<n>(sum, f, c, gmax);
-        });
+        run(0, first, false);
         bound = bound_of<THREADS>(sum.m, a.top, maxima, &bound_s);
-        edge([&](float x, int i) {
-            if (!(x < bound)) push(x, i);
-        });
-        run(0, first, [&](const uint4 &v, int g) {
-            float f[n];
-            unpack<T>(v, f);
-#pragma unroll
-            for (int i = 0; i < n; ++i)
-                if (!(f[i] < bound)) push(f[i], h + g * n + i);
-        });
-    }
-    run(first, groups, [&](const uint4 &v, int g) {
-        float f[n];
-        unpack<T>(v, f);
-        add<n>(sum, f, c, gmax);
-        if (TOP && !(gmax < bound)) {
-#pragma unroll
-            for (int i = 0; i < n; ++i)
-                if (!(f[i] < bound)) push(f[i], h + g * n + i);
+        if (mine0 >= 0) push(mine0, !(raised(to_f(row[mine0])) < bound), row + mine0);
+        if (mine1 >= 0) push(mine1, !(raised(to_f(row[mine1])) < bound), row + mine1);
+#pragma unroll 2
+        for (int g = tid; g < first; g += THREADS) {
+            uint4 v = __ldg(gp + g);
+            if (!(Pairs<T>::largest(v) < bound)) push(h + g * n, Pairs<T>::candidates(v, bound), (const T *)(gp + g));
         }
-    });
-    Stat st = block_join<THREADS>(stat_of(sum, c), c, warp_stats);  // its barrier also closes the candidate list
-    if (st.m <= kMask && st.m > -INFINITY) {  // nothing but masked logits: their plain sums
-        Stat mine = {st.m, 0.f, 0.f};
+    }
+    run(first, groups, TOP);
+    Stat st = block_join<THREADS>(sum.stat(c), c, warp_stats);  // its barrier also closes the candidate list
+    if (st.m == -INFINITY) {  // nothing but masks (or NaN): the part's plain sums
+        Stat own = {-INFINITY, 0.f, 0.f};
+        for (int i = e0 + tid; i < e1; i += THREADS) own.m = fmaxf(own.m, to_f(row[i]));
+        __syncthreads();
+        const float m = block_join<THREADS>(own, c, warp_stats).m;
+        own.m = m;
         for (int i = e0 + tid; i < e1; i += THREADS) {
-            const float d = floor_nan((to_f(row[i]) - st.m) * c), e = ex2(d);
-            mine.s += e;
-            mine.w = fmaf(e, d, mine.w);
+            const float x = to_f(row[i]);
+            if (m == -INFINITY) {  // -inf counts nothing, NaN spoils the row
+                own.s += x == m ? 0.f : x;
+                continue;
+            }
+            const float d = floor_nan((x - m) * c), e = ex2(d);
+            own.s += e;
+            own.w = fmaf(e, d, own.w);
         }
         __syncthreads();
-        st = block_join<THREADS>(mine, c, warp_stats);
+        st = block_join<THREADS>(own, c, warp_stats);
     }
 
     if (TOP) {
@@ -450,9 +562,9 @@ bool dims_supported(const lstm_logprob_dims *d) {
     return d->top <= LSTM_LOGPROB_MAX_TOP && d->vocab <= (1 << 30) && d->N <= (1 << 30);
 }
 
-// Within these limits a masked logit (-1e28 or less below the maximum) has an
-// exponential of zero at every temperature.
-bool temp_ok(float inv_temp) { return inv_temp >= 1e-20f && inv_temp <= 1e20f; }
+// Within these limits a mask has an exponential of zero beside another logit,
+// and nothing overflows.
+bool temp_ok(float inv_temp) { return inv_temp >= 1e-6f && inv_temp <= 1e6f; }
 
 // Rows that fill the card two narrow blocks an SM deep take a block each; of
 // fewer rows each takes a wide block, or a cluster of them where a block would
@@ -523,6 +635,7 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     a.vocab = d->vocab;
     a.top = d->top;
     a.ld = d->ld;
+    a.inv_temp = inv_temp;
     a.c = inv_temp * kLog2e;
     a.logp = logp;
     a.entropy = entropy;

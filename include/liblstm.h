@@ -460,7 +460,7 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
 /*
  * lstm_logprob_fwd / lstm_logprob_bwd -- log-probabilities of given tokens.
  * N rows of `vocab` logits (type dtype, row stride ld >= vocab elements),
- * z = logits * inv_temp (inverse temperature, 1e-20 .. 1e20), p = softmax(z):
+ * z = logits * inv_temp (inverse temperature, 1e-6 .. 1e6), p = softmax(z):
  *   logp [N]       float  log p[targets_r]; 0 for a target outside
  *                         0 .. vocab-1 (an ignored row); needs targets; or NULL
  *   entropy [N]    float  -sum p log p, or NULL
@@ -470,9 +470,10 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
  *                         LSTM_LOGPROB_MAX_TOP, at most vocab) largest logits,
  *                         equal ones by lower id, and their log p; NULL at 0
  * targets [N]: int or long long by id_bytes, or NULL.  Logits of -inf are
- * masked: their p is 0 and counts as 0 in the entropy.  A row of nothing but
- * -inf has logp and top_logp -inf, entropy 0 and a zero gradient.  A NaN or
- * +inf makes its row's values NaN (NaN is listed after every number).
+ * masked: their p is 0 and counts as 0 in the entropy; so is, beside any
+ * larger logit, one of -2^53 or less.  A row of nothing but -inf has logp and
+ * top_logp -inf, entropy 0 and a zero gradient.  A NaN or +inf makes its row's
+ * values NaN (NaN is listed after every number).
  *
  * lstm_logprob_bwd: dlogits [N][vocab] (type dtype, row stride ldd), the
  * gradient for dlogp [N] and dentropy [N] (float, either NULL):

@@ -221,3 +221,28 @@ def test_empty_streams_and_graphs():
     torch.cuda.synchronize()
     assert torch.equal(st.logp, want.logp) and torch.equal(st.top_ids, want.top_ids)
     assert torch.equal(d, L.logprobs_backward(want, x, t, dlogp=want.entropy))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N", [3, 400])
+def test_masked_parts(N, dt):
+    """Long rows that blocks share, whole parts of them masked, -inf and the lowest value side by side."""
+    V = 70000
+    low, inf = torch.finfo(DT[dt]).min, float("-inf")
+    x = torch.randn(N, V, device="cuda").to(DT[dt])
+    x[0, :60000] = inf
+    x[1, 5000:] = low
+    x[2] = inf
+    x[2, 100:20000:7] = low
+    t = torch.tensor([65000, 17, 107], device="cuda").repeat(N // 3 + 1)[:N]
+    st = L.logprobs(x, t, top=3)
+    n = (20000 - 100 + 6) // 7
+    assert abs(float(st.logp[2]) + math.log(n)) <= ABS and abs(float(st.entropy[2]) - math.log(n)) <= ABS * 10
+    assert st.top_ids[2].tolist() == [100, 107, 114]
+    keep = [0, 1] + list(range(3, N))
+    _, _, h, tl, _ = reference(x[keep], t[keep], 1.0)
+    assert bool(((st.logp[keep].double() - tl).abs() <= ABS).all())
+    assert bool(((st.entropy[keep].double() - h).abs() <= ABS * (1 + h)).all())
+    d = L.logprobs_backward(st, x, t, dlogp=torch.ones(N, device="cuda"))
+    assert bool(torch.isfinite(d).all()) and not d[0, :60000].any() and not d[2, 1:100].any()
+    assert abs(float(d[2, 114]) + 1 / n) <= 2 * ABS / n + torch.finfo(d.dtype).eps / 2 / n + 2.0 ** -24
