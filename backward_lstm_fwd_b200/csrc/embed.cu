@@ -39,7 +39,7 @@ template <class ID> __device__ __forceinline__ int row_of(const ID *ids, long lo
 }
 
 // ------------------------------------------------------------------ lookup
-// Vector path: rows of whole 16-byte groups.  One warp copies U x 32 groups.
+// Vector path: rows of whole, aligned 16-byte groups.  One warp copies U x 32 groups.
 template <class T> __device__ __forceinline__ uint4 scaled(uint4 v, float scale);
 template <> __device__ __forceinline__ uint4 scaled<float>(uint4 v, float s) {
     return make_uint4(__float_as_uint(__uint_as_float(v.x) * s), __float_as_uint(__uint_as_float(v.y) * s),
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) lookup_kernel(const ID *ids, const uint4 
         if (g0 + 32 * u < groups) x[(long long)r * groups + g0 + 32 * u] = scaled<T>(v[u], scale);
 }
 
-// Element path: rows that are not whole 16-byte groups.
+// Element path: any other rows.
 template <class T, class ID>
 __global__ void __launch_bounds__(256) lookup_elem_kernel(const ID *ids, const T *table, float scale,
                                                           T *x, int N, int vocab, int I) {
@@ -89,7 +89,7 @@ template <class T, class ID>
 int lookup(const lstm_embed_dims *d, const void *ids, const void *table, float scale, void *x,
            cudaStream_t s) {
     const size_t row = (size_t)d->I * sizeof(T);
-    if (row % 16) {
+    if (row % 16 || ((uintptr_t)table | (uintptr_t)x) % 16) {
         lookup_elem_kernel<T, ID><<<d->N, 256, 0, s>>>((const ID *)ids, (const T *)table, scale, (T *)x,
                                                       d->N, d->vocab, d->I);
         LSTM_CUDA_TRY(host::launched());
@@ -260,8 +260,8 @@ struct GradArgs {
     int N, vocab, I, units, accumulate;
 };
 
-// W consecutive columns a thread: 4 where rows are whole 16-byte groups of
-// both dx and dtable, else 1.
+// W consecutive columns a thread: 4 where the rows of both dx and dtable are
+// whole, aligned groups of four, else 1.
 template <class T, int W> __device__ __forceinline__ void load_cols(const T *p, float (&f)[W]);
 template <> __device__ __forceinline__ void load_cols<float, 1>(const float *p, float (&f)[1]) { f[0] = __ldg(p); }
 template <> __device__ __forceinline__ void load_cols<bf16, 1>(const bf16 *p, float (&f)[1]) { f[0] = to_f(*p); }
@@ -468,7 +468,8 @@ template <class T, int W> int grad(const lstm_embed_dims *d, GradArgs &a, cudaSt
 }
 
 template <class T> int grad_w(const lstm_embed_dims *d, GradArgs &a, cudaStream_t s) {
-    return d->I % 4 == 0 ? grad<T, 4>(d, a, s) : grad<T, 1>(d, a, s);
+    const bool wide = d->I % 4 == 0 && (uintptr_t)a.dx % (4 * sizeof(T)) == 0 && (uintptr_t)a.dtable % 16 == 0;
+    return wide ? grad<T, 4>(d, a, s) : grad<T, 1>(d, a, s);
 }
 
 }  // namespace
@@ -480,7 +481,9 @@ int lstm_embed_fwd(const lstm_embed_dims *d, const void *ids, const void *table,
     if (!dims_ok(d)) return LSTM_ERR_INVALID_ARG;
     if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
     const bool any = (long long)d->N * d->I > 0;
-    if (!host::ptr_ok(ids, any) || !host::ptr_ok(table, any && d->vocab > 0) || !host::ptr_ok(x, any))
+    const size_t e = host::elem_bytes(d->dtype);
+    if (!host::ptr_ok(ids, any, d->id_bytes) || !host::ptr_ok(table, any && d->vocab > 0, e) ||
+        !host::ptr_ok(x, any, e))
         return LSTM_ERR_INVALID_ARG;
     if (!any) return LSTM_OK;
     cudaStream_t s = (cudaStream_t)stream;
@@ -502,7 +505,8 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
     if (!dims_ok(d) || (accumulate != 0 && accumulate != 1)) return LSTM_ERR_INVALID_ARG;
     if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
     const bool any = (long long)d->N * d->I > 0, out = (long long)d->vocab * d->I > 0;
-    if (!host::ptr_ok(ids, any) || !host::ptr_ok(dx, any) || !host::ptr_ok(dtable, out))
+    if (!host::ptr_ok(ids, any, d->id_bytes) || !host::ptr_ok(dx, any, host::elem_bytes(d->dtype)) ||
+        !host::ptr_ok(dtable, out, 4))
         return LSTM_ERR_INVALID_ARG;
     const BwdLayout l = bwd_layout(d);
     const int rc = host::ws_check(ws, ws_bytes, l.total);

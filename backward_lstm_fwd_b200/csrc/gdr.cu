@@ -242,9 +242,9 @@ int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
     const long long rows = (long long)d->T * d->B * d->Hv;
     const bool any = rows > 0, state = (long long)d->B * d->Hv * d->K * d->V > 0;
     if (!host::ptr_ok(q, any && d->K) || !host::ptr_ok(k, any && d->K) || !host::ptr_ok(v, any && d->V) ||
-        !host::ptr_ok(g, any) || !host::ptr_ok(beta, any) || !host::ptr_ok(s0, false) ||
+        !host::ptr_ok(g, any, 4) || !host::ptr_ok(beta, any, 4) || !host::ptr_ok(s0, false) ||
         !host::ptr_ok(o, any && d->V) || !host::ptr_ok(sT, state) || !host::ptr_ok(states, false) ||
-        !host::ptr_ok(deltas, false) || !host::ptr_ok(opt ? opt->lengths : nullptr, false) ||
+        !host::ptr_ok(deltas, false) || !host::ptr_ok(opt ? opt->lengths : nullptr, false, 4) ||
         (states != nullptr) != (deltas != nullptr))
         return LSTM_ERR_INVALID_ARG;
     rc = host::ws_check(ws, ws_bytes, lstm_gdr_fwd_workspace_size(d, states != nullptr));
@@ -268,11 +268,11 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
     const long long rows = (long long)d->T * d->B * d->Hv;
     const bool any = rows > 0, state = any && d->K && d->V;
     if (!host::ptr_ok(dout, false) || !host::ptr_ok(dsT, false) || !host::ptr_ok(q, any && d->K) ||
-        !host::ptr_ok(k, any && d->K) || !host::ptr_ok(v, false) || !host::ptr_ok(g, any) ||
-        !host::ptr_ok(beta, any) || !host::ptr_ok(states, state) || !host::ptr_ok(deltas, any && d->V) ||
+        !host::ptr_ok(k, any && d->K) || !host::ptr_ok(v, false) || !host::ptr_ok(g, any, 4) ||
+        !host::ptr_ok(beta, any, 4) || !host::ptr_ok(states, state) || !host::ptr_ok(deltas, any && d->V) ||
         !host::ptr_ok(dq, any && d->K) || !host::ptr_ok(dk, any && d->K) || !host::ptr_ok(dv, any && d->V) ||
-        !host::ptr_ok(dg, any) || !host::ptr_ok(dbeta, any) || !host::ptr_ok(ds0, false) ||
-        !host::ptr_ok(opt ? opt->lengths : nullptr, false))
+        !host::ptr_ok(dg, any, 4) || !host::ptr_ok(dbeta, any, 4) || !host::ptr_ok(ds0, false) ||
+        !host::ptr_ok(opt ? opt->lengths : nullptr, false, 4))
         return LSTM_ERR_INVALID_ARG;
     rc = host::ws_check(ws, ws_bytes, layout(d, true).total);
     if (rc != LSTM_OK) return rc;

@@ -739,6 +739,14 @@ template <int KD> struct Lane {
     __device__ __forceinline__ void store(const Shape &s, float *base, const float (&S)[KD / 4]) const {
         store_col(base + (long long)wg * (KD / 4) * s.V + v, s.V, rows(s, base), S);
     }
+    // quarters FROM .. TO - 1 of those rows
+    template <int FROM, int TO> __device__ __forceinline__ void store_part(const Shape &s, float *base, const float (&S)[KD / 4]) const {
+        constexpr int n = KD / 16 * (TO - FROM), i0 = KD / 16 * FROM;
+        float r[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) r[i] = S[i0 + i];
+        store_col(base + (long long)(wg * (KD / 4) + i0) * s.V + v, s.V, rows(s, base) - i0, r);
+    }
     // column `lane` of the identity
     __device__ __forceinline__ void unit(const Shape &s, float (&S)[KD / 4]) const {
         const int lane = threadIdx.x & 127;
@@ -837,7 +845,10 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         if (Q::stages == 2 && tid == 32 && n > 0 && n + 1 < J.chunks)
             seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, false);
         __syncwarp();
-        if (!SCAN) L.store(s, a.states ? a.states + c * all + L.head * KV : nullptr, S);
+        // (the state's rows go out a part in each product's shadow)
+        float *kept = !SCAN && a.states ? a.states + c * all + L.head * KV : nullptr;
+        if (!SCAN && n > 0) store_o(c - 1);
+        if (kept) L.template store_part<0, 1>(s, kept, S);
         const float last = gates[C - 1 - L.wg * 16];  // gamma of token 63
         float f[16], be[16], u[16];
         load16(gates, u);  // gamma
@@ -853,7 +864,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         }
         __syncwarp();
         if (n + 1 < J.chunks) load_v(c + 1);
-        if (!SCAN && n > 0) store_o(c - 1);
+        if (kept) L.template store_part<1, 3>(s, kept, S);
         load16(gates + C, u);
         load16(gates + 2 * C, be);
         wait(&bar->m2, ph, a.ctrl, ab, 0x614);  // Q S came before X
@@ -883,6 +894,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
                 tc::mma_commit(&bar->m3);
             }
             __syncwarp();
+            if (kept) L.template store_part<3, 4>(s, kept, S);
         }
         wait(&bar->m4, ph, a.ctrl, ab, 0x615);
 #pragma unroll
@@ -975,7 +987,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
             tc::mma_commit(&bar->m1);
         }
         __syncwarp();
-        if (!SCAN) L.store(s, a.states + c * all + L.head * KV, S);
+        float *kept = a.states + c * all + L.head * KV;
+        if (!SCAN) L.template store_part<0, 1>(s, kept, S);
         const float last = gates[C - 1 - L.wg * 16];
         float f[16], e[16], left[16], be[16];
         load16(gates + C, left);
@@ -997,6 +1010,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         for (int i = 0; i < 16; ++i) e[i] = s.scale * be[i] * d[i];
         put_terms<8, NT>(L.lanes + COL_S + L.wg * 8, 32, e);
         if (more) load_do(c - 1);
+        if (!SCAN) L.template store_part<1, 3>(s, kept, S);
         wait(&bar->m2, ph, a.ctrl, ab, 0x624);
         get16(L.lanes + COL_X + L.wg * 16, f);
 #pragma unroll
@@ -1018,6 +1032,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         if (!SCAN) {
             store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
             store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+            L.template store_part<3, 4>(s, kept, S);
         }
         wait(&bar->m4, ph, a.ctrl, ab, 0x625);
 #pragma unroll

@@ -26,9 +26,10 @@ namespace host {
         if (e_ != cudaSuccess) return LSTM_ERR_CUDA;      \
     } while (0)
 
-// A pointer argument: 16-byte aligned, and not NULL where it is needed.
-inline bool ptr_ok(const void *p, bool needed) {
-    return (p != nullptr || !needed) && ((uintptr_t)p & 15u) == 0;
+// A pointer argument: aligned (to 16 bytes, or to its elements where the
+// kernels read them one by one), and not NULL where it is needed.
+inline bool ptr_ok(const void *p, bool needed, size_t align = 16) {
+    return (p != nullptr || !needed) && ((uintptr_t)p & (align - 1)) == 0;
 }
 
 inline bool dtype_ok(int dtype) {

@@ -603,7 +603,7 @@ template <class T> int backward(BwdArgs &a, cudaStream_t s) {
     const long long blocks = (long long)a.N * a.chunks;
     if (blocks > INT_MAX) return LSTM_ERR_UNSUPPORTED;
     // 16-byte groups need logits and dlogits rows that start alike
-    const bool vec = (a.ld - a.ldd) * (long long)sizeof(T) % 16 == 0;
+    const bool vec = (a.ld - a.ldd) * (long long)sizeof(T) % 16 == 0 && ((uintptr_t)a.logits - (uintptr_t)a.dlogits) % 16 == 0;
     if (vec)
         bwd_kernel<T, true><<<(unsigned)blocks, kBwdThreads, 0, s>>>(a);
     else
@@ -621,9 +621,10 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     if (!dims_ok(d) || !temp_ok(inv_temp)) return LSTM_ERR_INVALID_ARG;
     if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
     const bool any = d->N > 0;
-    if (!host::ptr_ok(logits, any && d->vocab > 0) || !host::ptr_ok(targets, any && logp) ||
-        !host::ptr_ok(logp, any && targets) || !host::ptr_ok(entropy, false) || !host::ptr_ok(stats, any) ||
-        !host::ptr_ok(top_ids, any && d->top > 0) || !host::ptr_ok(top_logp, any && d->top > 0))
+    if (!host::ptr_ok(logits, any && d->vocab > 0, host::elem_bytes(d->dtype)) ||
+        !host::ptr_ok(targets, any && logp, d->id_bytes) || !host::ptr_ok(logp, any && targets, 4) ||
+        !host::ptr_ok(entropy, false, 4) || !host::ptr_ok(stats, any, 4) ||
+        !host::ptr_ok(top_ids, any && d->top > 0, 4) || !host::ptr_ok(top_logp, any && d->top > 0, 4))
         return LSTM_ERR_INVALID_ARG;
     if (!any) return LSTM_OK;
     cudaStream_t s = (cudaStream_t)stream;
@@ -654,9 +655,10 @@ int lstm_logprob_bwd(const lstm_logprob_dims *d, const void *logits, const void 
     if (!dims_ok(d) || ldd < d->vocab || !temp_ok(inv_temp)) return LSTM_ERR_INVALID_ARG;
     if (!dims_supported(d)) return LSTM_ERR_UNSUPPORTED;
     const bool any = d->N > 0 && d->vocab > 0;
-    if (!host::ptr_ok(logits, any) || !host::ptr_ok(targets, any && dlogp) || !host::ptr_ok(stats, any) ||
-        !host::ptr_ok(entropy, any && dentropy) || !host::ptr_ok(dlogp, false) ||
-        !host::ptr_ok(dentropy, false) || !host::ptr_ok(dlogits, any))
+    const size_t e = host::elem_bytes(d->dtype);
+    if (!host::ptr_ok(logits, any, e) || !host::ptr_ok(targets, any && dlogp, d->id_bytes) || !host::ptr_ok(stats, any, 4) ||
+        !host::ptr_ok(entropy, any && dentropy, 4) || !host::ptr_ok(dlogp, false, 4) ||
+        !host::ptr_ok(dentropy, false, 4) || !host::ptr_ok(dlogits, any, e))
         return LSTM_ERR_INVALID_ARG;
     if (dlogits == logits && ldd != d->ld && any) return LSTM_ERR_INVALID_ARG;
     if (!any) return LSTM_OK;

@@ -350,10 +350,12 @@ int lstm_fwd_noalloc_status(void *stream);
  * matrix state) and the log-probabilities of tokens at its output.  The
  * conventions above hold (16-byte aligned device pointers, caller-owned
  * memory and workspaces of 256-byte alignment, status codes, asynchronous on
- * `stream`, nothing enqueued after an argument error); no call reads a host
- * value from the device, so each can be captured into a graph.  Empty
- * problems are valid (a call with nothing to compute leaves the workspace and
- * its status word alone).
+ * `stream`, nothing enqueued after an argument error), but ids, targets,
+ * lengths, the embedding's rows, logits and what has one number a row, token
+ * or head need only be aligned to their elements, so that they may start at
+ * any step of a longer sequence.  No call reads a host value from the device,
+ * so each can be captured into a graph.  Empty problems are valid (a call with
+ * nothing to compute leaves the workspace and its status word alone).
  * --------------------------------------------------------------------- */
 
 /*

@@ -151,3 +151,11 @@ def test_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_ids_from_anywhere():
+    ids = torch.arange(9, device="cuda", dtype=torch.int32)
+    table = torch.randn(9, 5, device="cuda")
+    for r in range(9):
+        assert torch.equal(L.embed(ids[r:], table), table[r:])
+        assert torch.equal(L.embed_backward(ids[r:], table[r:].contiguous(), 9)[r:], table[r:])

@@ -39,10 +39,11 @@ def test_embed_pointers_and_workspace(lib):
     d = L.embed_dims(4, 5, 8, L.LSTM_BF16)
     for k in ("ids", "table", "x"):
         assert embed_fwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
-        assert embed_fwd(lib, d, **{k: FAKE + 4}) == L.LSTM_ERR_INVALID_ARG
+        assert embed_fwd(lib, d, **{k: FAKE + 1}) == L.LSTM_ERR_INVALID_ARG
     for k in ("ids", "dx", "dtable"):
         assert embed_bwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
-        assert embed_bwd(lib, d, **{k: FAKE + 4}) == L.LSTM_ERR_INVALID_ARG
+        assert embed_bwd(lib, d, **{k: FAKE + 1}) == L.LSTM_ERR_INVALID_ARG
+    assert embed_fwd(lib, d, ids=FAKE + 4) == L.LSTM_ERR_INVALID_ARG  # ids of 8 bytes
     assert embed_bwd(lib, d, accumulate=2) == L.LSTM_ERR_INVALID_ARG
     need = L.embed_bwd_workspace_size(d)
     assert embed_bwd(lib, d, ws_bytes=need - 1) == L.LSTM_ERR_WORKSPACE
@@ -89,10 +90,11 @@ def test_logprob_arguments(lib):
     for k in ("logits", "targets", "stats", "top_ids", "top_logp"):
         assert logprob_fwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
     for k in ("logits", "targets", "logp", "entropy", "stats", "top_ids", "top_logp"):
-        assert logprob_fwd(lib, d, **{k: FAKE + 2}) == L.LSTM_ERR_INVALID_ARG
+        assert logprob_fwd(lib, d, **{k: FAKE + 1}) == L.LSTM_ERR_INVALID_ARG
+    assert logprob_fwd(lib, d, targets=FAKE + 4) == L.LSTM_ERR_INVALID_ARG
     for k in ("logits", "targets", "stats", "entropy", "dlogits"):
         assert logprob_bwd(lib, d, **{k: None}) == L.LSTM_ERR_INVALID_ARG
-        assert logprob_bwd(lib, d, **{k: FAKE + 2}) == L.LSTM_ERR_INVALID_ARG
+        assert logprob_bwd(lib, d, **{k: FAKE + 1}) == L.LSTM_ERR_INVALID_ARG
     assert logprob_bwd(lib, d, ldd=99) == L.LSTM_ERR_INVALID_ARG
     assert logprob_bwd(lib, d, dlogits=FAKE, ldd=104) == L.LSTM_ERR_INVALID_ARG  # in place with another stride
     assert logprob_fwd(lib, L.logprob_dims(3, 100, 0, top=65)) == L.LSTM_ERR_UNSUPPORTED
@@ -153,16 +155,17 @@ def test_gdr_extents(lib, big):
 
 def test_gdr_arguments(lib):
     d = L.gdr_dims(**GDR)
+    by_element = ("g", "beta", "dg", "dbeta")
     for n in ("q", "k", "v", "g", "beta", "o", "sT"):
         assert gdr_fwd(lib, d, **{n: None}) == L.LSTM_ERR_INVALID_ARG
-        assert gdr_fwd(lib, d, **{n: FAKE + 8}) == L.LSTM_ERR_INVALID_ARG
+        assert gdr_fwd(lib, d, **{n: FAKE + (2 if n in by_element else 8)}) == L.LSTM_ERR_INVALID_ARG
     assert gdr_fwd(lib, d, s0=FAKE + 8) == L.LSTM_ERR_INVALID_ARG
     assert gdr_fwd(lib, d, states=FAKE) == L.LSTM_ERR_INVALID_ARG  # the backward needs both
     assert gdr_fwd(lib, d, deltas=FAKE) == L.LSTM_ERR_INVALID_ARG
     for n in ("q", "k", "g", "beta", "states", "deltas", "dq", "dk", "dv", "dg", "dbeta"):
         assert gdr_bwd(lib, d, **{n: None}) == L.LSTM_ERR_INVALID_ARG
-        assert gdr_bwd(lib, d, **{n: FAKE + 8}) == L.LSTM_ERR_INVALID_ARG
-    for opt in (L.GdrOptions(FAKE + 4, 1.0), L.GdrOptions(None, float("nan")), L.GdrOptions(None, float("inf"))):
+        assert gdr_bwd(lib, d, **{n: FAKE + (2 if n in by_element else 8)}) == L.LSTM_ERR_INVALID_ARG
+    for opt in (L.GdrOptions(FAKE + 2, 1.0), L.GdrOptions(None, float("nan")), L.GdrOptions(None, float("inf"))):
         assert gdr_fwd(lib, d, opt=opt) == L.LSTM_ERR_INVALID_ARG
         assert gdr_bwd(lib, d, opt=opt) == L.LSTM_ERR_INVALID_ARG
     for save in (None, FAKE):

@@ -246,3 +246,21 @@ def test_masked_parts(N, dt):
     d = L.logprobs_backward(st, x, t, dlogp=torch.ones(N, device="cuda"))
     assert bool(torch.isfinite(d).all()) and not d[0, :60000].any() and not d[2, 1:100].any()
     assert abs(float(d[2, 114]) + 1 / n) <= 2 * ABS / n + torch.finfo(d.dtype).eps / 2 / n + 2.0 ** -24
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_rows_from_anywhere(dt):
+    """Slices of rows, targets and gradients that start at no 16-byte boundary."""
+    x = torch.randn(9, 1001, device="cuda").to(DT[dt])
+    t = torch.randint(0, 1001, (9,), device="cuda", dtype=torch.int32)
+    dl = torch.randn(9, device="cuda")
+    want = L.logprobs(x, t, top=4)
+    dw = L.logprobs_backward(want, x, t, dlogp=dl)
+    for r in range(1, 9):
+        st = L.logprobs(x[r:], t[r:], top=4)
+        assert bool(((st.logp - want.logp[r:]).abs() <= ABS).all()) and torch.equal(st.top_ids, want.top_ids[r:])
+        d = L.logprobs_backward(st, x[r:], t[r:], dlogp=dl[r:])
+        assert bool(((d.double() - dw[r:].double()).abs() <= 4 * ABS + torch.finfo(d.dtype).eps * dw[r:].double().abs()).all())
+    cols = x[:, 3:900]
+    st = L.logprobs(cols, top=2)
+    assert torch.equal(st.top_ids, L.logprobs(cols.contiguous(), top=2).top_ids)
