@@ -614,27 +614,25 @@ def _at(t: Optional[torch.Tensor]):
     return (t.data_ptr() or None) if t is not None else None
 
 
-class _Device:
-    """The tensor's device made current where it is not (a C call works on the
-    current device), and the stream to enqueue on: `stream`, or that device's
-    current stream."""
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """The call belongs on another device or stream than the current ones."""
+    return stream is not None or torch.cuda.current_device() != t.get_device()
 
-    def __init__(self, t: torch.Tensor, stream):
-        self.index = t.get_device()
-        self.stream = stream
 
-    def __enter__(self):
-        self.guard = None
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        if self.stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.index)
-        return _stream(self.stream)
+def _there(t: torch.Tensor, stream):
+    """Context that makes the tensor's device current, or a stream of it: what
+    a call allocates then belongs to the stream it works on."""
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    _need(stream.device == t.device, "stream is on another device")
+    return torch.cuda.stream(stream)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _here(t: torch.Tensor) -> int:
+    """The current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def embed_dims(N: int, vocab: int, I: int, dtype, id_bytes: int = 8) -> EmbedDims:
@@ -652,12 +650,14 @@ def embed(ids, table, scale: float = 1.0, out=None, stream=None) -> torch.Tensor
     vocab, I = table.shape
     shape = (*ids.shape, I)
     _shaped(out, "out", shape, table.dtype)
-    with _Device(table, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=table.dtype, device=table.device)
-        d = embed_dims(ids.numel(), vocab, I, table.dtype, _id_bytes(ids))
-        _run(load().lstm_embed_fwd(ctypes.byref(d), _at(ids), _at(table), float(scale), _at(out),
-                                   s), "lstm_embed_fwd")
+    if _elsewhere(table, stream):
+        with _there(table, stream):
+            return embed(ids, table, scale, out)
+    if out is None:
+        out = torch.empty(shape, dtype=table.dtype, device=table.device)
+    d = embed_dims(ids.numel(), vocab, I, table.dtype, _id_bytes(ids))
+    _run(load().lstm_embed_fwd(ctypes.byref(d), _at(ids), _at(table), float(scale), _at(out),
+                               _here(table)), "lstm_embed_fwd")
     return out
 
 
@@ -676,15 +676,16 @@ def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate
     _shaped(dx, "dx", (*ids.shape, I))
     _need(not accumulate or out is not None, "accumulate needs out")
     _shaped(out, "out", (vocab, I), torch.float32)
-    with _Device(dx, stream) as s:
-        if out is None:
-            out = torch.empty((vocab, I), dtype=torch.float32, device=dx.device)
-        d = embed_dims(ids.numel(), vocab, I, dx.dtype, _id_bytes(ids))
-        if ws is None:
-            ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
-        _run(load().lstm_embed_bwd(ctypes.byref(d), _at(ids), _at(dx), float(scale), int(accumulate),
-                                   _at(out), _at(ws), _ws_bytes(ws), s),
-             "lstm_embed_bwd")
+    if _elsewhere(dx, stream):
+        with _there(dx, stream):
+            return embed_backward(ids, dx, vocab, scale, out, accumulate, ws)
+    if out is None:
+        out = torch.empty((vocab, I), dtype=torch.float32, device=dx.device)
+    d = embed_dims(ids.numel(), vocab, I, dx.dtype, _id_bytes(ids))
+    if ws is None:
+        ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
+    _run(load().lstm_embed_bwd(ctypes.byref(d), _at(ids), _at(dx), float(scale), int(accumulate),
+                               _at(out), _at(ws), _ws_bytes(ws), _here(dx)), "lstm_embed_bwd")
     return out
 
 
@@ -693,13 +694,15 @@ class LogProbs:
     backward.  logp is None without targets, top_ids / top_logp with top = 0."""
 
     def __init__(self, N, top, has_targets, inv_temp, device):
-        f = dict(dtype=torch.float32, device=device)
         self.inv_temp = inv_temp
-        self.logp = torch.empty((N,), **f) if has_targets else None
-        self.entropy = torch.empty((N,), **f)
-        self.stats = torch.empty((N, 2), **f)
-        self.top_ids = torch.empty((N, top), dtype=torch.int32, device=device) if top else None
-        self.top_logp = torch.empty((N, top), **f) if top else None
+        # one allocation, of which these are parts
+        parts = torch.empty((4 + 2 * top) * N, dtype=torch.float32, device=device).split(
+            [N, N, 2 * N, top * N, top * N])
+        self.logp = parts[0] if has_targets else None
+        self.entropy = parts[1]
+        self.stats = parts[2].view(N, 2)
+        self.top_logp = parts[3].view(N, top) if top else None
+        self.top_ids = parts[4].view(torch.int32).view(N, top) if top else None
 
     @property
     def lse(self) -> torch.Tensor:
@@ -716,11 +719,14 @@ def logprob_dims(N: int, vocab: int, dtype, ld: Optional[int] = None, top: int =
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Row stride of a [N, vocab] tensor whose rows are dense."""
-    _need(t.dim() == 2, f"{name} must be [N, vocab]")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [N, vocab]")
     N, vocab = t.shape
-    _need(vocab <= 1 or t.stride(1) == 1, f"{name}: rows must be dense")
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be dense")
     ld = t.stride(0) if N > 1 else vocab
-    _need(ld >= vocab, f"{name}: rows overlap")
+    if ld < vocab:
+        raise ValueError(f"{name}: rows overlap")
     return ld
 
 
@@ -735,13 +741,14 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
     _dense(targets=targets)
     _shaped(targets, "targets", (N,))
     _need(temperature > 0, "temperature must be positive")
-    with _Device(logits, stream) as s:
-        st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
-        d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
-        _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
-                                     _at(st.logp), _at(st.entropy), _at(st.stats), _at(st.top_ids),
-                                     _at(st.top_logp), s),
-             "lstm_logprob_fwd")
+    if _elsewhere(logits, stream):
+        with _there(logits, stream):
+            return logprobs(logits, targets, top, temperature)
+    st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
+    d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
+    _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
+                                 _at(st.logp), _at(st.entropy), _at(st.stats), _at(st.top_ids),
+                                 _at(st.top_logp), _here(logits)), "lstm_logprob_fwd")
     return st
 
 
@@ -759,18 +766,22 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     _shaped(st.stats, "stats", (N, 2), torch.float32)
     _shaped(out, "out", (N, vocab), logits.dtype)
     _need(1.0 / temperature == st.inv_temp, "temperature differs from the forward's")
-    with _Device(logits, stream) as s:
-        if out is None:
-            out = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
-        d = logprob_dims(N, vocab, logits.dtype, ld, 0, _id_bytes(targets))
-        _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
-                                     _at(st.stats), _at(st.entropy), _at(dlogp), _at(dentropy),
-                                     _at(out), _rows(out, "out"), s),
-             "lstm_logprob_bwd")
+    if _elsewhere(logits, stream):
+        with _there(logits, stream):
+            return logprobs_backward(st, logits, targets, dlogp, dentropy, temperature, out)
+    if out is None:
+        out = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)
+        if ld != vocab:
+            out = out[:, :vocab]
+    d = logprob_dims(N, vocab, logits.dtype, ld, 0, _id_bytes(targets))
+    _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
+                                 _at(st.stats), _at(st.entropy), _at(dlogp), _at(dentropy),
+                                 _at(out), _rows(out, "out"), _here(logits)), "lstm_logprob_bwd")
     return out
 
 
 GDR_CHUNK = 64
+GDR_STEP_TOKENS = 16
 
 
 def gdr_dims(T: int, B: int, Hk: int, Hv: int, K: int, V: int, dtype, ldq: int = 0, ldk: int = 0,
@@ -857,14 +868,16 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     _shaped(s0, "s0", (d.B, d.Hv, d.K, d.V), torch.float32)
     _shaped(sT, "sT", (d.B, d.Hv, d.K, d.V), torch.float32)
     _dense(s0=s0, sT=sT, ws=ws)
-    with _Device(q, stream) as s:
-        st = GdrState(d, q.dtype, q.device, save, sT)
-        if ws is None:
-            ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
-        _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _at(q), _at(k), _at(v), _at(g),
-                                 _at(beta), _at(s0), _at(st.o), _at(st.sT), _at(st.states),
-                                 _at(st.deltas), _at(ws), _ws_bytes(ws), s),
-             "lstm_gdr_fwd")
+    if _elsewhere(q, stream):
+        with _there(q, stream):
+            return gdr_forward(q, k, v, g, beta, s0, lengths, scale, save, sT, ws)
+    st = GdrState(d, q.dtype, q.device, save, sT)
+    if ws is None and (save or d.T > GDR_STEP_TOKENS):
+        ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
+    _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _at(q), _at(k), _at(v), _at(g),
+                             _at(beta), _at(s0), _at(st.o), _at(st.sT), _at(st.states),
+                             _at(st.deltas), _at(ws), _ws_bytes(ws) if ws is not None else 0,
+                             _here(q)), "lstm_gdr_fwd")
     return st
 
 
@@ -879,13 +892,15 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
     _shaped(dsT, "dsT", (d.B, d.Hv, d.K, d.V), torch.float32)
     _shaped(st.o, "the state's o", (d.T, d.B, d.Hv, d.V), q.dtype)
     _dense(dout=dout, dsT=dsT, ws=ws)
-    with _Device(q, stream) as s:
-        gr = GdrGrads(d, q.dtype, q.device)
-        if ws is None:
-            ws = empty_workspace(gdr_bwd_workspace_size(d), q.device)
-        _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _at(dout), _at(dsT), _at(q),
-                                 _at(k), _at(v), _at(g), _at(beta), _at(st.states), _at(st.deltas),
-                                 _at(gr.dq), _at(gr.dk), _at(gr.dv), _at(gr.dg), _at(gr.dbeta),
-                                 _at(gr.ds0), _at(ws), _ws_bytes(ws), s),
-             "lstm_gdr_bwd")
+    if _elsewhere(q, stream):
+        with _there(q, stream):
+            return gdr_backward(st, q, k, v, g, beta, dout, dsT, lengths, scale, ws)
+    gr = GdrGrads(d, q.dtype, q.device)
+    if ws is None:
+        ws = empty_workspace(gdr_bwd_workspace_size(d), q.device)
+    _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _at(dout), _at(dsT), _at(q),
+                             _at(k), _at(v), _at(g), _at(beta), _at(st.states), _at(st.deltas),
+                             _at(gr.dq), _at(gr.dk), _at(gr.dv), _at(gr.dg), _at(gr.dbeta),
+                             _at(gr.ds0), _at(ws), _ws_bytes(ws), _here(q)),
+         "lstm_gdr_bwd")
     return gr

@@ -10,11 +10,6 @@ using namespace lstm::gdr;
 
 namespace {
 
-// Token by token or in chunks.  A token costs the step kernel two passes over
-// its registers and three barriers (about 0.6 us); a chunk costs a fixed
-// launch and chain more, whatever it holds.
-constexpr int kStepTokens = 16;
-
 bool dims_ok(const lstm_gdr_dims *d) {
     if (!d || d->T < 0 || d->B < 0 || d->Hk < 0 || d->Hv < 0 || d->K < 0 || d->V < 0) return false;
     if (!host::dtype_ok(d->dtype)) return false;
@@ -46,7 +41,8 @@ int check(const lstm_gdr_dims *d) {
     return dims_supported(d) ? LSTM_OK : LSTM_ERR_UNSUPPORTED;
 }
 
-bool stepwise(const lstm_gdr_dims *d, bool save) { return !save && d->T <= kStepTokens; }
+// Token by token or in chunks (figures at LSTM_GDR_STEP_TOKENS's kernel).
+bool stepwise(const lstm_gdr_dims *d, bool save) { return !save && d->T <= LSTM_GDR_STEP_TOKENS; }
 
 int terms_of(int dtype) { return dtype == LSTM_BF16 ? 1 : dtype == LSTM_F16 ? 2 : 3; }
 
@@ -247,8 +243,10 @@ int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
         !host::ptr_ok(deltas, false) || !host::ptr_ok(opt ? opt->lengths : nullptr, false, 4) ||
         (states != nullptr) != (deltas != nullptr))
         return LSTM_ERR_INVALID_ARG;
-    rc = host::ws_check(ws, ws_bytes, lstm_gdr_fwd_workspace_size(d, states != nullptr));
-    if (rc != LSTM_OK) return rc;
+    if (ws || !stepwise(d, states != nullptr)) {
+        rc = host::ws_check(ws, ws_bytes, lstm_gdr_fwd_workspace_size(d, states != nullptr));
+        if (rc != LSTM_OK) return rc;
+    }
     if ((long long)d->B * d->Hv * d->V == 0) return LSTM_OK;
     cudaStream_t st = (cudaStream_t)stream;
     const Shape s = shape_of(d, opt);

@@ -1504,7 +1504,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
     __shared__ float qs[128], ks[128];
     __shared__ float4 part[2][8][STEP_COLS / 4];  // a warp's two parts together
     const Shape &s = a.s;
-    clear_ctrl(a.ctrl);
+    if (a.ctrl) clear_ctrl(a.ctrl);
     const int tid = threadIdx.x, warp = tid >> 5, c4 = tid & 15, v = blockIdx.x % a.tiles * STEP_COLS + c4 * 4;
     const int id = blockIdx.x / a.tiles, h = id % s.Hv, b = id / s.Hv, hk = h / s.group;
     const long long head = (long long)b * s.Hv + h;

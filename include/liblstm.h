@@ -407,9 +407,10 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
  *   states [ceil(T / LSTM_GDR_CHUNK)][B][Hv][K][V], deltas [T][B][Hv][V] float:
  *          kept for the backward, or both NULL (serving).  states[c] is the
  *          state before token 64 c, deltas is x.
- * A call of up to 16 tokens that keeps nothing runs token by token (one token
- * is a decoding step); any other in chunks of 64 tokens on the tensor cores,
- * with the sums and states of a float computation in every compute type.
+ * A call of up to LSTM_GDR_STEP_TOKENS tokens that keeps nothing runs token by
+ * token (one token is a decoding step) and needs no workspace (ws may be
+ * NULL); any other in chunks of 64 tokens on the tensor cores, with the sums
+ * and states of a float computation in every compute type.
  *
  * ldq, ldk, ldv: elements between the rows of two tokens (0 = dense), so that
  * q, k and v may be slices of one projection; a multiple of 8.
@@ -429,6 +430,7 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
  * LSTM_ERR_UNSUPPORTED).
  */
 #define LSTM_GDR_CHUNK 64
+#define LSTM_GDR_STEP_TOKENS 16
 typedef struct lstm_gdr_dims {
     int T;
     int B;

@@ -177,6 +177,9 @@ def test_gdr_arguments(lib):
     # a few tokens that keep nothing need the control block alone
     few = L.gdr_dims(**{**GDR, "T": 1})
     assert L.gdr_fwd_workspace_size(few) == 256 < L.gdr_fwd_workspace_size(few, True)
+    assert gdr_fwd(lib, few, ws=FAKE + 16) == L.LSTM_ERR_WORKSPACE  # (NULL would do, this not)
+    assert gdr_fwd(lib, few, ws=FAKE, ws_bytes=255) == L.LSTM_ERR_WORKSPACE
+    assert gdr_fwd(lib, few, states=FAKE, deltas=FAKE, ws=None) == L.LSTM_ERR_WORKSPACE
     # nothing to do: nothing is enqueued
     none = L.gdr_dims(**{**GDR, "B": 0})
     assert gdr_fwd(lib, none, q=None, k=None, v=None, g=None, beta=None, o=None, sT=None) == L.LSTM_OK

@@ -115,3 +115,31 @@ def test_training_step_and_decoding():
         gs = L.gdr_forward(*(s.detach().contiguous() for s in project(p, ls.y)), s0=S, sT=S)
         one = L.logprobs(gs.o.reshape(B, HV * V) @ p["out"], targets[t], top=2, temperature=TEMPERATURE)
         close(f"step {t}", one.logp, logp64.view(T, B)[t])
+
+
+def test_stream_argument():
+    """A call on a stream that is not the current one works and allocates there."""
+    p = parameters()
+    ids = torch.arange(T * B, device="cuda").view(T, B) % VOCAB
+    x = L.embed(ids, p["table"], SCALE)
+    dx = torch.randn_like(x)
+    five = [t.contiguous() for t in project({n: p[n] for n in p}, torch.randn(T, B, H, device="cuda"))]
+    logits = torch.randn(T * B, VOCAB, device="cuda")
+    t = ids.reshape(-1)
+
+    def run(**kw):
+        gs = L.gdr_forward(*five, save=True, **kw)
+        gr = L.gdr_backward(gs, *five, dout=gs.o, **kw)
+        few = L.gdr_forward(*(f[:3] for f in five), **kw)
+        lp = L.logprobs(logits, t, top=2, **kw)
+        d = L.logprobs_backward(lp, logits, t, dlogp=lp.entropy, **kw)
+        return (L.embed(ids, p["table"], SCALE, **kw), L.embed_backward(ids, dx, VOCAB, **kw), gs.o, gr.dk, gr.dg, few.o,
+                lp.logp, d)
+
+    want = run()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0, torch.cuda.default_stream()):
+        torch.cuda.synchronize()
+        got = run(stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
