@@ -12,8 +12,8 @@
 //   sort    stable least-significant-digit radix sort of (token, position), 9
 //           bits a pass: one launch of block histograms, then one a pass that
 //           scatters and counts the next pass's histograms (integers: any
-//           order of the additions gives the same).  One block alone counts
-//           its own;
+//           order of the additions gives the same).  Up to 4096 keys are
+//           sorted by one block in shared memory, in one launch;
 //   grad    units of 32 sorted positions x column tiles: a thread adds its
 //           columns of up to 32 rows in order and stores each token that lies
 //           inside the unit; a token that crosses a unit's border leaves
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortArgs a) {
     a.hist_next[blockIdx.x * kBins + threadIdx.x] = 0;
 }
 
-// Exclusive prefix sum over the block's 512 threads.
+// Exclusive prefix sum over the block's threads.
 __device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -177,21 +177,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
     const long long b0 = (long long)blockIdx.x * a.tiles * kTile;
     {
         int before = 0, total = 0;
-        if (a.blocks > 1) {
 #pragma unroll 16
-            for (int b = 0; b < a.blocks; ++b) {
-                const int h = __ldcg(a.hist + b * kBins + tid);
-                if (b < (int)blockIdx.x) before += h;
-                total += h;
-            }
-        } else {  // the only block: its own histogram
-            base[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < a.N; i += kSortThreads)
-                atomicAdd(&base[(sort_key(a, i) >> a.shift) & (kBins - 1)], 1);
-            __syncthreads();
-            total = base[tid];
-            __syncthreads();
+        for (int b = 0; b < a.blocks; ++b) {
+            const int h = __ldcg(a.hist + b * kBins + tid);
+            if (b < (int)blockIdx.x) before += h;
+            total += h;
         }
         const int off = block_exclusive(total, warp_sums);
         base[tid] = off + before;
@@ -243,6 +233,77 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
             base[tid] = run;
         }
         __syncthreads();
+    }
+}
+
+// All passes of up to 4096 keys in one block: warp w holds keys 128 w .. in
+// registers, four rounds of 32, and the passes trade places in shared memory.
+constexpr int kOneWarps = 32, kOneThreads = 32 * kOneWarps, kOneRounds = 4, kOneKeys = kOneThreads * kOneRounds;
+struct OneSmem {
+    int key[kOneKeys];
+    unsigned short pos[kOneKeys];
+    unsigned short cnt[kOneWarps][kBins];  // counts, then first places, of a warp's digits
+    int warp_sums[kOneWarps];
+};
+__global__ void __launch_bounds__(kOneThreads) sort_one_kernel(SortArgs a, int bits) {
+    extern __shared__ __align__(16) unsigned char one_raw[];
+    OneSmem &m = *reinterpret_cast<OneSmem *>(one_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int key[kOneRounds], pos[kOneRounds], rank[kOneRounds];
+#pragma unroll
+    for (int j = 0; j < kOneRounds; ++j) {
+        const int i = warp * (32 * kOneRounds) + j * 32 + lane;
+        pos[j] = i;
+        key[j] = i < a.N ? sort_key(a, i) : -1;
+    }
+    for (int shift = 0; shift < bits; shift += kBits) {
+        for (int i = lane; i < kBins / 2; i += 32) ((unsigned *)m.cnt[warp])[i] = 0u;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kOneRounds; ++j) {
+            const int dg = key[j] < 0 ? kBins : (key[j] >> shift) & (kBins - 1);
+            const unsigned peers = __match_any_sync(~0u, dg);
+            rank[j] = dg < kBins ? m.cnt[warp][dg] + __popc(peers & ((1u << lane) - 1u)) : 0;
+            __syncwarp();
+            if (dg < kBins && lane == __ffs(peers) - 1) m.cnt[warp][dg] = (unsigned short)(m.cnt[warp][dg] + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        int total = 0;
+        if (tid < kBins)  // counts -> places among the digit's keys
+            for (int w = 0; w < kOneWarps; ++w) {
+                const int c = m.cnt[w][tid];
+                m.cnt[w][tid] = (unsigned short)total;
+                total += c;
+            }
+        const int first = block_exclusive(tid < kBins ? total : 0, m.warp_sums);  // of the digit
+        if (tid < kBins)
+            for (int w = 0; w < kOneWarps; ++w) m.cnt[w][tid] = (unsigned short)(m.cnt[w][tid] + first);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kOneRounds; ++j) {
+            if (key[j] < 0) continue;
+            const int o = m.cnt[warp][(key[j] >> shift) & (kBins - 1)] + rank[j];
+            m.key[o] = key[j];
+            m.pos[o] = (unsigned short)pos[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kOneRounds; ++j) {
+            const int i = warp * (32 * kOneRounds) + j * 32 + lane;
+            if (i < a.N) {
+                key[j] = m.key[i];
+                pos[j] = m.pos[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kOneRounds; ++j) {
+        const int i = warp * (32 * kOneRounds) + j * 32 + lane;
+        if (i < a.N) {
+            a.key_out[i] = key[j];
+            a.pos_out[i] = pos[j];
+        }
     }
 }
 
@@ -527,15 +588,24 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
         a.vocab = d->vocab;
         a.N = d->N;
         a.ids = ids;
+        if (d->N <= kOneKeys) {
+            a.key_out = (int *)(w + l.key[0]);
+            a.pos_out = (int *)(w + l.pos[0]);
+            LSTM_CUDA_TRY(cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(OneSmem)));
+            sort_one_kernel<<<1, kOneThreads, sizeof(OneSmem), s>>>(a, bits);
+            LSTM_CUDA_TRY(host::launched());
+            bits = 0;
+            cur = 1;
+        }
         int *hist[2] = {(int *)(w + l.hist[0]), (int *)(w + l.hist[1])};
-        if (a.blocks > 1) {
+        if (bits) {
             a.hist = hist[0];
             a.hist_next = hist[1];
             sort_hist_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
             LSTM_CUDA_TRY(host::launched());
         }
         for (int shift = 0; shift < bits; shift += kBits) {
-            const bool more = a.blocks > 1 && shift + kBits < bits;
+            const bool more = shift + kBits < bits;
             a.shift = shift;
             a.key_out = (int *)(w + l.key[cur]);
             a.pos_out = (int *)(w + l.pos[cur]);

@@ -159,3 +159,13 @@ def test_ids_from_anywhere():
     for r in range(9):
         assert torch.equal(L.embed(ids[r:], table), table[r:])
         assert torch.equal(L.embed_backward(ids[r:], table[r:].contiguous(), 9)[r:], table[r:])
+
+
+@pytest.mark.parametrize("kind", ["uniform", "same", "heavy"])
+@pytest.mark.parametrize("n,vocab", [(4095, 300), (4096, 70000), (4097, 70000), (3000, 262150), (4096, 1)])
+def test_gradient_around_the_one_block_sort(n, vocab, kind):
+    ids = make_ids(n, vocab, n, kind, torch.int64)
+    dx = torch.randn(n, 4, device="cuda")
+    got = L.embed_backward(ids, dx, vocab)
+    check_grad(got, ids, dx, vocab, 1.0)
+    assert torch.equal(got, L.embed_backward(ids, dx, vocab))
