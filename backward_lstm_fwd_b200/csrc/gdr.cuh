@@ -98,6 +98,14 @@ template <int n> __device__ __forceinline__ void split2(float a, float b, uint32
     }
 }
 
+// (x, y) += a (bx, by)
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float bx, float by) {
+    asm("{\n\t.reg .b64 d, a, b;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(bx), "f"(by));
+}
+
 // byte offset of (row, byte column) in a 128-byte swizzled tile
 __device__ __forceinline__ uint32_t swz(int row, int cb) { return row * 128 + (cb ^ ((row & 7) << 4)); }
 
@@ -289,6 +297,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 struct Sums {
     float2 b[C];    // (hi, lo)
     float beta[C];
+    float col[C], col_beta[C];  // prep: e^{b_r - b_j}, r the last token of j's 16, and times beta_j
 };
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -324,6 +333,13 @@ __device__ __forceinline__ void load_gates(const Shape &s, const float *g, const
         const double x = sum - v[1] + v[i];
         const float hi = (float)x;
         out.b[2 * lane + i] = make_float2(hi, (float)(x - hi));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = 2 * lane + i;
+        out.col[j] = decay(out.b[j | 15], out.b[j]);
+        out.col_beta[j] = out.col[j] * out.beta[j];
     }
 }
 
@@ -437,12 +453,19 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
         for (int j0 = 0; j0 < 32 * (half + 1); j0 += 16) {
             float f[16];
             get16(lanes + j0, f);
+            if (j0 + 16 <= 32 * half) {  // (of the whole warp) e^{b_i - b_r} e^{b_r - b_j}, r the block's last column
+                const float di = decay(bi, sums.b[j0 + 15]) * (warp < 2 ? s.scale : 1.f);
+                const float *col = (warp < 2 ? sums.col : sums.col_beta) + j0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int jj = j0 + j;
-                const float dec = decay(bi, sums.b[jj]);
-                if (warp < 2) f[j] = jj <= row ? s.scale * dec * f[j] : 0.f;
-                else f[j] = jj < row ? dec * sums.beta[jj] * f[j] : 0.f;
+                for (int j = 0; j < 16; ++j) f[j] *= di * col[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int jj = j0 + j;
+                    const float dec = decay(bi, sums.b[jj]);
+                    if (warp < 2) f[j] = jj <= row ? s.scale * dec * f[j] : 0.f;
+                    else f[j] = jj < row ? dec * sums.beta[jj] * f[j] : 0.f;
+                }
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 4) *(float4 *)(dst + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
@@ -475,32 +498,48 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
             for (int i = 0; i < 32; ++i) blk[i * PREP_LD + lane] = x[i];
         }
         __syncthreads();
-        {  // block (1, 0): W = B A', into the upper right corner; then -D' W in B's place
-            const int i = tid >> 2, j0 = (tid & 3) * 8;
-            auto product = [&](const float *l, const float *r, float sign, float *o) {
-                float acc[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-#pragma unroll 4
-                for (int k = 0; k < 32; k += 4) {
-                    const float4 lv = *(const float4 *)(l + i * PREP_LD + k);
-                    const float le[4] = {sign * lv.x, sign * lv.y, sign * lv.z, sign * lv.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float4 u = *(const float4 *)(r + (k + q) * PREP_LD + j0), v = *(const float4 *)(r + (k + q) * PREP_LD + j0 + 4);
-                        acc[0] = fmaf(le[q], u.x, acc[0]); acc[1] = fmaf(le[q], u.y, acc[1]);
-                        acc[2] = fmaf(le[q], u.z, acc[2]); acc[3] = fmaf(le[q], u.w, acc[3]);
-                        acc[4] = fmaf(le[q], v.x, acc[4]); acc[5] = fmaf(le[q], v.y, acc[5]);
-                        acc[6] = fmaf(le[q], v.z, acc[6]); acc[7] = fmaf(le[q], v.w, acc[7]);
-                    }
-                }
-                *(float4 *)(o + i * PREP_LD + j0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                *(float4 *)(o + i * PREP_LD + j0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-            };
+        {  // block (1, 0): W = B A', into the upper right corner; then -D' W in B's place.  A' and D' are
+           // triangles: warp w does W's columns 8 w .. (k >= 8 w), then the rows 8 w .. (k < 8 w + 8)
             float *low = tri + 32 * PREP_LD, *corner = tri + 32;
-            product(low, tri, 1.f, corner);
+            float acc[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll 2
+            for (int k = 8 * warp; k < 32; k += 4) {  // row `lane`
+                const float4 lv = *(const float4 *)(low + lane * PREP_LD + k);
+                const float le[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 u = *(const float4 *)(tri + (k + q) * PREP_LD + 8 * warp),
+                                 v = *(const float4 *)(tri + (k + q) * PREP_LD + 8 * warp + 4);
+                    fma2(acc[0], acc[1], le[q], u.x, u.y);
+                    fma2(acc[2], acc[3], le[q], u.z, u.w);
+                    fma2(acc[4], acc[5], le[q], v.x, v.y);
+                    fma2(acc[6], acc[7], le[q], v.z, v.w);
+                }
+            }
+            *(float4 *)(corner + lane * PREP_LD + 8 * warp) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            *(float4 *)(corner + lane * PREP_LD + 8 * warp + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
             __syncthreads();
-            product(low + 32, corner, -1.f, low);
+            // column `lane`, rows 8 warp ..
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll 2
+            for (int k = 0; k < 8 * warp + 8; k += 4) {
+                float w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = -corner[(k + q) * PREP_LD + lane];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 dv = *(const float4 *)(low + 32 + (8 * warp + j) * PREP_LD + k);
+                    acc[j] = fmaf(dv.x, w[0], acc[j]);
+                    acc[j] = fmaf(dv.y, w[1], acc[j]);
+                    acc[j] = fmaf(dv.z, w[2], acc[j]);
+                    acc[j] = fmaf(dv.w, w[3], acc[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) low[(8 * warp + j) * PREP_LD + lane] = acc[j];
         }
         __syncthreads();
         if (warp == 0 && m + 1 < m0 + a.heads) load_gates(s, a.g, a.beta, c, b, h + 1, len, sums);
