@@ -74,8 +74,17 @@ Split split_of(const lstm_gdr_dims *d) {
     return best;
 }
 
+// Value heads that a block of the gradient kernel takes: the group of a key
+// head, one after another, or one where a block a key head would leave more than
+// half the SMs idle, with a sum of the parts more (T = 333, 3 sequences, 2 key
+// heads of 3 value heads: 55 us against 25 + 5).
+int heads_per_block(const lstm_gdr_dims *d) {
+    const long long blocks = (long long)((d->T + C - 1) / C) * d->B * d->Hk;
+    return 2 * blocks <= host::sm_count() ? 1 : d->Hv / std::max(d->Hk, 1);
+}
+
 struct Layout {
-    size_t qk, tp, starts, trans, dstates, dvf, total;
+    size_t qk, tp, starts, trans, dstates, dvf, parts, total;
     Split split;
 };
 Layout layout(const lstm_gdr_dims *d, bool bwd) {
@@ -95,6 +104,8 @@ Layout layout(const lstm_gdr_dims *d, bool bwd) {
     l.trans = take(joints * (NT * kd * kd * 2));
     l.dstates = bwd ? take(nc * d->B * d->Hv * (size_t)d->K * d->V * 4) : 0;
     l.dvf = bwd ? take((size_t)d->T * d->B * d->Hv * d->V * 4) : 0;
+    const int heads = heads_per_block(d);
+    l.parts = bwd && d->Hk && d->Hv / d->Hk > heads ? take((size_t)(d->Hv / d->Hk) * 2 * d->T * d->B * d->Hk * d->K * 4) : 0;
     l.total = o;
     return l;
 }
@@ -127,8 +138,7 @@ template <class E, int KD>
 int prep(const Shape &s, const void *q, const void *k, const float *g, const float *beta, char *w, const Layout &l,
          cudaStream_t st) {
     const int blocks = s.NC * s.B * s.Hk;
-    // five blocks an SM are resident; up to two a key head each would leave its
-    // value heads one after another on a card that is not full
+    // five blocks an SM are resident: with two a key head or fewer, a block a value head
     const int heads = blocks <= 2 * host::sm_count() ? 1 : s.group;
     PrepArgs p = {s, q, k, g, beta, w + l.qk, w + l.tp, (Ctrl *)w, heads};
     LSTM_CUDA_TRY(allow_smem(prep_kernel<E, KD>, PrepSmem<E, KD>::smem));
@@ -202,9 +212,21 @@ int chunked_bwd(const lstm_gdr_dims *d, const Shape &s, const void *dout, const 
                  l.split.segments, l.split.chunks, (Ctrl *)w};
     const int rc = sequential<KD>(a, seq_bwd_kernel<E, KD, true>, seq_bwd_kernel<E, KD, false>, Seq<E, KD>::smem, st);
     if (rc != LSTM_OK || s.NC == 0) return rc;
-    GradArgs ga = {s, w + l.qk, g, beta, dout, states, deltas, dstates, dvf, dq, dk, dg, dbeta, (Ctrl *)w};
-    LSTM_CUDA_TRY(allow_smem(grad_kernel<E, KD>, GradSmem<E, KD>::smem));
-    grad_kernel<E, KD><<<s.NC * s.B * s.Hk, GRAD_THREADS, GradSmem<E, KD>::smem, st>>>(ga);
+    GradArgs ga = {s, w + l.qk, g, beta, dout, states, deltas, dstates, dvf, dq, dk, dg, dbeta, (float *)(w + l.parts), (Ctrl *)w};
+    constexpr size_t smem = GradSmem<E, KD>::smem;
+    const int blocks = s.NC * s.B * s.Hk;
+    if (heads_per_block(d) == s.group) {
+        LSTM_CUDA_TRY(allow_smem(grad_kernel<E, KD, false>, smem));
+        grad_kernel<E, KD, false><<<blocks, GRAD_THREADS, smem, st>>>(ga);
+        LSTM_CUDA_TRY(host::launched());
+        return LSTM_OK;
+    }
+    LSTM_CUDA_TRY(allow_smem(grad_kernel<E, KD, true>, smem));
+    grad_kernel<E, KD, true><<<blocks * s.group, GRAD_THREADS, smem, st>>>(ga);
+    LSTM_CUDA_TRY(host::launched());
+    const long long n8 = (long long)s.T * s.B * s.Hk * s.K / 8;
+    if (n8 == 0) return LSTM_OK;
+    sum_kernel<E><<<(unsigned)((2 * n8 + 255) / 256), 256, 0, st>>>((const float *)(w + l.parts), s.group, n8, (E *)dq, (E *)dk);
     LSTM_CUDA_TRY(host::launched());
     return LSTM_OK;
 }

@@ -1158,6 +1158,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) scan_kernel(const __grid_const
 // ---------------------------------------------------------------- gradients
 // Block (c, b, hk), 512 threads: dq, dk of the chunk, and dg, dbeta of every
 // value head of the group, from the saved S0 and X and seq_bwd's dS1 and dV.
+// (PARTS, where that leaves SMs idle: a block per value head, whose parts of dq
+// and dk sum_kernel adds in order.)
 // Rows are stacked so that every product has the 128 rows the tensor core
 // takes: [dO; dV] with X gives Y over Z, with S0 gives F over G; X sits in the
 // lower rows for E; [dQ; dK] += [Yh; -Zh] K, and dK += [Yh; -Zh]^T [Q; K] from
@@ -1191,6 +1193,7 @@ struct GradArgs {
     const float *states, *deltas, *dstates, *dvf;
     void *dq, *dk;
     float *dg, *dbeta;
+    float *parts;  // PARTS: [group][dq, dk][T][B][Hk][K]
     Ctrl *ctrl;
 };
 
@@ -1209,7 +1212,7 @@ __device__ __forceinline__ float transpose_sum(float (&f)[16]) {
     return f[0] + __shfl_xor_sync(~0u, f[0], 1);
 }
 
-template <class E, int KD>
+template <class E, int KD, bool PARTS>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_constant__ GradArgs a) {
     using L = GradSmem<E, KD>;
     constexpr int TB = Terms<E>::n, TERM = QK<E, KD>::term, H4 = KD / 4, SI = KD / 64;
@@ -1224,8 +1227,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     const Shape &s = a.s;
     const int tid = threadIdx.x, warp = warp_id(), lane = tid & 31, wg = tid >> 7, r128 = tid & 127, r = r128 & 63;
     const bool isq = r128 < 64;
-    int id = blockIdx.x;
-    const int hk = id % s.Hk;
+    const int heads = PARTS ? 1 : s.group, part = PARTS ? blockIdx.x % s.group : 0;
+    int id = PARTS ? blockIdx.x / s.group : blockIdx.x;
+    const char *tiles = a.qk + (size_t)id * QK<E, KD>::bytes;
+    const int hk = id % s.Hk, h0 = hk * s.group + part;
     id /= s.Hk;
     const int b = id % s.B, c = id / s.B;
     const int len = length_of(s, b);
@@ -1249,7 +1254,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     const uint32_t qk = tc::smem_u32(smem), sa = qk + L::a, ss = qk + L::st, sx = ss + KD * 128, sd = qk + L::ds_at;
     if (tid == 0) {
         tc::mbar_arrive_expect_tx(&loaded, QK<E, KD>::bytes);
-        bulk_load(smem, a.qk + (size_t)blockIdx.x * QK<E, KD>::bytes, QK<E, KD>::bytes, &loaded);
+        bulk_load(smem, tiles, QK<E, KD>::bytes, &loaded);
     }
     __syncwarp();
     const int row = tid >> 3, gr = tid & 7;  // loads: eight threads a row, eight columns each
@@ -1258,22 +1263,22 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     const int passes = (s.V + 63) / 64;
     Raw8<E> ro;                                // dO, dV, X, S0, dS1 of the pass ahead
     Raw8<float> rv, rx, rs[SI], rd[SI];
-    // where this thread's groups of value head 0 of the group, column 0, lie;
+    // where this thread's groups of the block's first value head, column 0, lie;
     // next_h, next_v: head and first column of the pass after the present one
-    const long long tok0 = (((long long)t_row * s.B + b) * s.Hv + hk * s.group) * s.V + gr * 8;
-    const long long st0 = ((((long long)c * s.B + b) * s.Hv + hk * s.group) * s.K + row) * s.V + gr * 8;
+    const long long tok0 = (((long long)t_row * s.B + b) * s.Hv + h0) * s.V + gr * 8;
+    const long long st0 = ((((long long)c * s.B + b) * s.Hv + h0) * s.K + row) * s.V + gr * 8;
     int next_h = 0, next_v = 0;
     auto load_a = [&]() {
-        const bool live = next_h < s.group && next_v + gr * 8 < s.V && t_row < len;
+        const bool live = next_h < heads && next_v + gr * 8 < s.V && t_row < len;
         const long long at = tok0 + next_h * s.V + next_v;
         ro = raw8<E>((const E *)a.dout + at, live && a.dout);
         rv = raw8<float>(a.dvf + at, live);
     };
     auto load_x = [&]() {
-        rx = raw8<float>(a.deltas + tok0 + next_h * s.V + next_v, next_h < s.group && next_v + gr * 8 < s.V && t_row < len);
+        rx = raw8<float>(a.deltas + tok0 + next_h * s.V + next_v, next_h < heads && next_v + gr * 8 < s.V && t_row < len);
     };
     auto load_s = [&](const float *base, Raw8<float> (&o)[SI]) {
-        const bool live = next_h < s.group && next_v + gr * 8 < s.V;
+        const bool live = next_h < heads && next_v + gr * 8 < s.V;
         const float *q = base + st0 + (long long)next_h * s.K * s.V + next_v;
 #pragma unroll
         for (int i = 0; i < SI; ++i) o[i] = raw8<float>(q + i * 64 * s.V, live && i * 64 + row < s.K);
@@ -1293,8 +1298,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     load_s(a.dstates, rd);
     wait(&loaded, 0, a.ctrl, ab, 0x631);
 #pragma unroll 1
-    for (int m = 0; m < s.group; ++m) {
-        const int h = hk * s.group + m;
+    for (int m = 0; m < heads; ++m) {
+        const int h = h0 + m;
         float dot = 0.f;  // <dS1, S0>
         // A pass: the first products run beside the conversion of dS1, E beside
         // the next pass's conversions of S0, dO and dV; every buffer's next
@@ -1493,9 +1498,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
         }
         __syncwarp();
     }
-    wait(&m3, (s.group - 1) & 1, a.ctrl, ab, 0x635);
+    wait(&m3, (heads - 1) & 1, a.ctrl, ab, 0x635);
     const int t = c * C + r;
-    E *out = (E *)(isq ? a.dq : a.dk) + (((long long)t * s.B + b) * s.Hk + hk) * s.K + wg * H4;
+    const long long at = (((long long)t * s.B + b) * s.Hk + hk) * s.K + wg * H4, all = (long long)s.T * s.B * s.Hk * s.K;
+    E *out = (E *)(isq ? a.dq : a.dk) + at;
+    float *out_part = PARTS ? a.parts + (2 * part + (isq ? 0 : 1)) * all + at : nullptr;
 #pragma unroll
     for (int i0 = 0; i0 < H4; i0 += 16) {
         float f[16], e[16];
@@ -1508,7 +1515,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = f[g2 * 8 + i] + (isq ? 0.f : e[g2 * 8 + i]);
-                if constexpr (sizeof(E) == 4) {
+                if constexpr (PARTS) {
+                    *(float4 *)(out_part + i0 + g2 * 8) = make_float4(x[0], x[1], x[2], x[3]);
+                    *(float4 *)(out_part + i0 + g2 * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                } else if constexpr (sizeof(E) == 4) {
                     *(float4 *)(out + i0 + g2 * 8) = make_float4(x[0], x[1], x[2], x[3]);
                     *(float4 *)(out + i0 + g2 * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
                 } else {
@@ -1520,6 +1530,27 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     tc::tc_fence_before();
     __syncthreads();
     if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// dq and dk from the parts of `split` blocks, eight elements a thread.
+template <class E> __global__ void __launch_bounds__(256) sum_kernel(const float *parts, int split, long long n8, E *dq, E *dk) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= 2 * n8) return;
+    const float *src = parts + i * 8;  // dq's elements, then dk's
+    float x[8] = {};
+    for (int p = 0; p < split; ++p, src += 16 * n8) {
+        float y[8];
+        load8<float>(src, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] += y[j];
+    }
+    E *out = i < n8 ? dq + i * 8 : dk + (i - n8) * 8;
+    if constexpr (sizeof(E) == 4) {
+        *(float4 *)out = make_float4(x[0], x[1], x[2], x[3]);
+        *((float4 *)out + 1) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *(uint4 *)out = f32x8_to<E>(x);
+    }
 }
 
 // -------------------------------------------------------------------- step

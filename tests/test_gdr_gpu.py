@@ -106,6 +106,13 @@ def test_gradients(shape, dt):
 
 
 @pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("shape", [(70, 20, 2, 4, 16, 8), (65, 40, 1, 3, 72, 72), (40, 3, 1, 4, 128, 64)], ids=str)
+def test_shared_key_heads(shape, dt):
+    """Value heads of a group one after another in a block (many blocks), or a block each (few)."""
+    check(*make(*shape, dt))
+
+
+@pytest.mark.parametrize("dt", list(DT))
 def test_lengths(dt):
     x, dout, dsT = make(150, 6, 1, 2, 64, 40, dt)
     lengths = torch.tensor([150, 0, 1, 64, 65, 149], dtype=torch.int32, device="cuda")
