@@ -781,7 +781,7 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
 
 
 GDR_CHUNK = 64
-GDR_STEP_TOKENS = 16
+GDR_STEP_TOKENS = 12
 
 
 def gdr_dims(T: int, B: int, Hk: int, Hv: int, K: int, V: int, dtype, ldq: int = 0, ldk: int = 0,
@@ -853,7 +853,7 @@ def _gdr_call(q, k, v, g, beta, lengths, scale):
     _dense(g=g, beta=beta, lengths=lengths)
     d = gdr_dims(T, B, Hk, Hv, K, V, q.dtype, _token_stride(q, "q"), _token_stride(k, "k"),
                  _token_stride(v, "v"))
-    return d, GdrOptions(_at(lengths), K ** -0.5 if scale is None else float(scale))
+    return d, GdrOptions(_at(lengths), max(K, 1) ** -0.5 if scale is None else float(scale))
 
 
 def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool = False, sT=None,

@@ -414,6 +414,9 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
  *
  * ldq, ldk, ldv: elements between the rows of two tokens (0 = dense), so that
  * q, k and v may be slices of one projection; a multiple of 8.
+ * Outputs overlap neither inputs nor one another, but sT may be s0 and ds0 may
+ * be dsT.  A NaN or an infinity in a step's inputs spoils the outputs of its
+ * sequence and head from the beginning of its chunk.
  * options: lengths [B] int (or NULL): steps t >= lengths[n] (clamped to
  * 0 .. T) are padding: the state stays, o_t is zero, and gradients are zero.
  * opt NULL: no lengths, scale 1.
@@ -430,7 +433,7 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
  * LSTM_ERR_UNSUPPORTED).
  */
 #define LSTM_GDR_CHUNK 64
-#define LSTM_GDR_STEP_TOKENS 16
+#define LSTM_GDR_STEP_TOKENS 12
 typedef struct lstm_gdr_dims {
     int T;
     int B;

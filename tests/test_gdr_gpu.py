@@ -316,3 +316,37 @@ def test_streams_graphs_and_status():
     assert torch.equal(st.o, want.o) and torch.equal(st.sT, want.sT)
     for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"):
         assert torch.equal(getattr(gr, n), getattr(wg, n)), n
+
+
+@pytest.mark.parametrize("T", [3, 100, 1500])
+def test_state_in_place(T):
+    """sT is s0, also where the sequence is split over blocks."""
+    x, _, _ = make(T, 1, 1, 2, 64, 64, "bf16")
+    want = L.gdr_forward(**x)
+    for _ in range(3):
+        state = x["s0"].clone()
+        got = L.gdr_forward(*(x[n] for n in ("q", "k", "v", "g", "beta")), s0=state, sT=state)
+        assert torch.equal(got.o, want.o) and torch.equal(state, want.sT)
+
+
+def test_gradient_in_place_and_optional_outputs():
+    """The C entry point: ds0 may be dsT, or absent."""
+    import ctypes
+    T = 1500
+    x, dout, dsT = make(T, 1, 1, 2, 64, 64, "fp16")
+    five = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    st = L.gdr_forward(**x, save=True)
+    want = L.gdr_backward(st, *five, dout=dout, dsT=dsT)
+    opt = L.GdrOptions(None, 64 ** -0.5)
+    ws = L.empty_workspace(L.gdr_bwd_workspace_size(st.dims), "cuda")
+    for ds in ("in place", None):
+        g, d = L.GdrGrads(st.dims, torch.float16, "cuda"), dsT.clone()
+        p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        rc = L.load().lstm_gdr_bwd(ctypes.byref(st.dims), ctypes.byref(opt), p(dout), p(d), p(x["q"]), p(x["k"]), None, p(x["g"]),
+                                   p(x["beta"]), p(st.states), p(st.deltas), p(g.dq), p(g.dk), p(g.dv), p(g.dg), p(g.dbeta),
+                                   p(d) if ds else None, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert rc == L.LSTM_OK
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(getattr(g, n), getattr(want, n))
+        assert torch.equal(d, want.ds0 if ds else dsT)
+    assert L.lstm_status(ws) == L.LSTM_OK
