@@ -96,9 +96,10 @@ int lookup(const lstm_embed_dims *d, const void *ids, const void *table, float s
         return LSTM_OK;
     }
     const int groups = (int)(row / 16);
-    // Four groups a lane keep enough loads in flight once the rows fill the
-    // card; below that one group a lane spreads the call over more SMs.
-    const bool wide = (long long)d->N * groups >= 148LL * 2048 * 4;
+    // Four groups a lane keep enough loads in flight; of few rows one group a
+    // lane spreads the call over more SMs.  (Rows of 128 groups, us with one / four:
+    // 128 rows 1.9 / 2.1, 1024 2.3 / 2.2, 8192 6.1 / 4.4, 32768 24.8 / 16.1.)
+    const bool wide = (long long)d->N * groups >= 1 << 17;
     const int tiles = (groups + (wide ? 128 : 32) - 1) / (wide ? 128 : 32);
     const long long blocks = ((long long)d->N * tiles + 7) / 8;
     if (blocks > INT_MAX) return LSTM_ERR_UNSUPPORTED;

@@ -12,8 +12,8 @@
 // one exponential and half of three packed operations (and its conversion), 32
 // elements one look at the maximum.  Many
 // rows: 128 threads a block and eight blocks an SM, so that one row's loads run
-// beside another's joins.  Few rows: 512 threads, and a cluster of up to eight
-// blocks shares a row and joins its parts through distributed shared memory.
+// beside another's joins.  Few rows: a cluster of up to eight blocks shares a row
+// and joins its parts through distributed shared memory.
 // The alternatives come from the same pass: the first third of the range gives
 // every thread its own maximum, the top-th largest of those is a lower bound of
 // the answer, and only elements at or above it (a few times `top`) enter a
@@ -33,10 +33,10 @@ typedef __half f16;
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 constexpr int kCand = 1024;     // candidate list of a block
-constexpr int kNarrow = 128;    // threads of a block: many rows
-constexpr int kWide = 512;      // few rows
+constexpr int kNarrow = 128;    // threads of a block
+constexpr int kWide = 512;      // alternatives of few long rows
 constexpr int kMaxParts = 8;    // blocks that share a row (a portable cluster)
-constexpr int kPartBytes = 32 << 10;  // what a wide block has in flight at once
+constexpr int kPartBytes = 16 << 10;  // a part's least share of a row
 constexpr int kBwdThreads = 128;
 static_assert(kMaxParts * LSTM_LOGPROB_MAX_TOP <= kCand, "the parts' alternatives fit the candidate list");
 
@@ -566,31 +566,39 @@ bool dims_supported(const lstm_logprob_dims *d) {
 // and nothing overflows.
 bool temp_ok(float inv_temp) { return inv_temp >= 1e-6f && inv_temp <= 1e6f; }
 
-// Rows that fill the card two narrow blocks an SM deep take a block each; of
-// fewer rows each takes a wide block, or a cluster of them where a block would
-// need more than one batch of loads in flight.
-template <class T, bool TOP> int forward(Args &a, int sms, cudaStream_t s) {
-    if (a.N >= 2 * sms) {
-        a.parts = 1;
-        fwd_kernel<T, TOP, kNarrow><<<a.N, kNarrow, 0, s>>>(a);
-        LSTM_CUDA_TRY(host::launched());
-        return LSTM_OK;
-    }
-    a.parts = 1;
-    while (a.parts < kMaxParts && (long long)a.vocab * (int)sizeof(T) > a.parts * kPartBytes) a.parts *= 2;
+template <class T, bool TOP, int THREADS> int launch_fwd(Args &a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * a.parts));
-    cfg.blockDim = dim3(kWide);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {(unsigned)a.parts, 1, 1};
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    LSTM_CUDA_TRY(cudaLaunchKernelEx(&cfg, fwd_kernel<T, TOP, kWide>, a));
+    cfg.numAttrs = a.parts > 1 ? 1 : 0;
+    LSTM_CUDA_TRY(cudaLaunchKernelEx(&cfg, fwd_kernel<T, TOP, THREADS>, a));
     note_launch();
     return LSTM_OK;
 }
+
+// Which blocks a row gets (us, bf16).  Rows share out over a cluster until every
+// SM holds four blocks or a part is 16 KB: one row of 32000 takes 4.7 in 16 KB
+// parts and 5.2 in 32 KB ones, 74 of 128000 take 9.3 in parts and 16.2 whole,
+// 296 of 5000 take 4.0 whole and 5.0 in 8 KB parts.  Blocks of 128 threads beat
+// 512 almost everywhere (32000, 148 rows: 6.7 against 17.2; 8 alternatives, 296
+// rows: 24.6 against 30.4).  The exception is alternatives of few long rows,
+// whose thresholds are joined faster by more threads: 128000, 8 alternatives, 4
+// rows 17.8 against 11.7, 16 rows 19.5 against 16.5; 37 rows, two blocks an SM,
+// 21.6 against 26.6 again.
+template <class T, bool TOP> int forward(Args &a, int sms, cudaStream_t s) {
+    const long long bytes = (long long)a.vocab * (int)sizeof(T);
+    a.parts = 1;
+    while (a.parts < kMaxParts && (long long)a.N * a.parts <= 2 * sms && bytes > a.parts * kPartBytes) a.parts *= 2;
+    if constexpr (TOP)
+        if (a.parts == kMaxParts && (long long)a.N * a.parts <= sms) return launch_fwd<T, TOP, kWide>(a, s);
+    return launch_fwd<T, TOP, kNarrow>(a, s);
+}
+
 template <class T> int forward_t(Args &a, int sms, cudaStream_t s) {
     return a.top ? forward<T, true>(a, sms, s) : forward<T, false>(a, sms, s);
 }
