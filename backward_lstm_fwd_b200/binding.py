@@ -695,14 +695,20 @@ class LogProbs:
 
     def __init__(self, N, top, has_targets, inv_temp, device):
         self.inv_temp = inv_temp
-        # one allocation, of which these are parts
-        parts = torch.empty((4 + 2 * top) * N, dtype=torch.float32, device=device).split(
-            [N, N, 2 * N, top * N, top * N])
-        self.logp = parts[0] if has_targets else None
-        self.entropy = parts[1]
-        self.stats = parts[2].view(N, 2)
-        self.top_logp = parts[3].view(N, top) if top else None
-        self.top_ids = parts[4].view(torch.int32).view(N, top) if top else None
+        # one allocation, of which these are parts: stats, entropy, logp, top_logp, top_ids
+        self._buf = buf = torch.empty((4 + 2 * top) * N, dtype=torch.float32, device=device)
+        self.entropy = buf.as_strided((N,), (1,), 2 * N)
+        self.logp = buf.as_strided((N,), (1,), 3 * N) if has_targets else None
+        self.top_logp = self.top_ids = None
+        if top:
+            self.top_logp = buf.as_strided((N, top), (top, 1), 4 * N)
+            self.top_ids = buf.view(torch.int32).as_strided((N, top), (top, 1), (4 + top) * N)
+
+    @property
+    def stats(self) -> torch.Tensor:
+        """[N, 2]: the row's largest logit and log2 sum 2^(c (x - largest)), c =
+        log2(e) / temperature."""
+        return self._buf.as_strided((self.entropy.numel(), 2), (2, 1))
 
     @property
     def lse(self) -> torch.Tensor:
@@ -747,7 +753,7 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
     st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
     d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
     _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
-                                 _at(st.logp), _at(st.entropy), _at(st.stats), _at(st.top_ids),
+                                 _at(st.logp), _at(st.entropy), _at(st._buf), _at(st.top_ids),
                                  _at(st.top_logp), _here(logits)), "lstm_logprob_fwd")
     return st
 
@@ -804,13 +810,15 @@ class GdrState:
     kept for the backward."""
 
     def __init__(self, d: GdrDims, cd, device, save, sT=None):
-        f = dict(dtype=torch.float32, device=device)
+        f = torch.float32
+        T, B, H, K, V = d.T, d.B, d.Hv, d.K, d.V
         self.dims = d
-        self.o = torch.empty((d.T, d.B, d.Hv, d.V), dtype=cd, device=device)
-        self.sT = torch.empty((d.B, d.Hv, d.K, d.V), **f) if sT is None else sT
-        nc = -(-d.T // GDR_CHUNK)
-        self.states = torch.empty((nc, d.B, d.Hv, d.K, d.V), **f) if save else None
-        self.deltas = torch.empty((d.T, d.B, d.Hv, d.V), **f) if save else None
+        self.o = torch.empty((T, B, H, V), dtype=cd, device=device)
+        self.sT = torch.empty((B, H, K, V), dtype=f, device=device) if sT is None else sT
+        self.states = self.deltas = None
+        if save:
+            self.states = torch.empty((-(-T // GDR_CHUNK), B, H, K, V), dtype=f, device=device)
+            self.deltas = torch.empty((T, B, H, V), dtype=f, device=device)
 
 
 class GdrGrads:
@@ -839,20 +847,22 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     return ld
 
 
-def _gdr_call(q, k, v, g, beta, lengths, scale):
-    """(dims, options, K**-0.5 or scale) of one call, its arguments checked."""
+def _gdr_call(q, k, v, g, beta, lengths, scale, **dense):
+    """(dims, options) of one call, its arguments checked; `dense` are its
+    other contiguous tensors."""
     _need(q.dim() == 4 and v.dim() == 4, "q, k [T, B, Hk, K] and v [T, B, Hv, V]")
-    T, B, Hk, K = q.shape
-    Hv, V = v.shape[2:]
-    _on(q, k=k, v=v, g=g, beta=beta, lengths=lengths)
-    _shaped(k, "k", q.shape, q.dtype)
-    _shaped(v, "v", (T, B, Hv, V), q.dtype)
-    _shaped(g, "g", (T, B, Hv), torch.float32)
-    _shaped(beta, "beta", (T, B, Hv), torch.float32)
+    T, B, Hk, K = shape = q.shape
+    _, _, Hv, V = v.shape
+    dt, f = q.dtype, torch.float32
+    _on(q, k=k, v=v, g=g, beta=beta, lengths=lengths, **dense)
+    _dense(g=g, beta=beta, lengths=lengths, **dense)
+    _shaped(k, "k", shape, dt)
+    _shaped(v, "v", (T, B, Hv, V), dt)
+    _shaped(g, "g", (T, B, Hv), f)
+    _shaped(beta, "beta", (T, B, Hv), f)
     _shaped(lengths, "lengths", (B,), torch.int32)
-    _dense(g=g, beta=beta, lengths=lengths)
-    d = gdr_dims(T, B, Hk, Hv, K, V, q.dtype, _token_stride(q, "q"), _token_stride(k, "k"),
-                 _token_stride(v, "v"))
+    d = GdrDims(T, B, Hk, Hv, K, V, dtype_code(dt), _token_stride(q, "q"), _token_stride(k, "k"),
+                _token_stride(v, "v"))
     return d, GdrOptions(_at(lengths), max(K, 1) ** -0.5 if scale is None else float(scale))
 
 
@@ -863,11 +873,10 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     beta [T,B,Hv] float32, state s0 [B,Hv,K,V] float32.  lengths [B] int32 marks
     padding; scale defaults to K**-0.5.  save keeps what gdr_backward needs;
     sT gives the final state's tensor (s0 itself for a state kept in place)."""
-    d, opt = _gdr_call(q, k, v, g, beta, lengths, scale)
-    _on(q, s0=s0, sT=sT, ws=ws)
-    _shaped(s0, "s0", (d.B, d.Hv, d.K, d.V), torch.float32)
-    _shaped(sT, "sT", (d.B, d.Hv, d.K, d.V), torch.float32)
-    _dense(s0=s0, sT=sT, ws=ws)
+    d, opt = _gdr_call(q, k, v, g, beta, lengths, scale, s0=s0, sT=sT, ws=ws)
+    state = (d.B, d.Hv, d.K, d.V)
+    _shaped(s0, "s0", state, torch.float32)
+    _shaped(sT, "sT", state, torch.float32)
     if _elsewhere(q, stream):
         with _there(q, stream):
             return gdr_forward(q, k, v, g, beta, s0, lengths, scale, save, sT, ws)
@@ -885,13 +894,11 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
                  ws=None, stream=None) -> GdrGrads:
     """lstm_gdr_bwd on the saved state of gdr_forward(..., save=True), with
     the forward's arguments: dout [T,B,Hv,V] (compute dtype), dsT float32."""
-    d, opt = _gdr_call(q, k, v, g, beta, lengths, scale)
     _need(st.states is not None, "the forward kept nothing: call gdr_forward(..., save=True)")
-    _on(q, dout=dout, dsT=dsT, ws=ws, states=st.states)
+    d, opt = _gdr_call(q, k, v, g, beta, lengths, scale, dout=dout, dsT=dsT, ws=ws, states=st.states)
     _shaped(dout, "dout", (d.T, d.B, d.Hv, d.V), q.dtype)
     _shaped(dsT, "dsT", (d.B, d.Hv, d.K, d.V), torch.float32)
     _shaped(st.o, "the state's o", (d.T, d.B, d.Hv, d.V), q.dtype)
-    _dense(dout=dout, dsT=dsT, ws=ws)
     if _elsewhere(q, stream):
         with _there(q, stream):
             return gdr_backward(st, q, k, v, g, beta, dout, dsT, lengths, scale, ws)
