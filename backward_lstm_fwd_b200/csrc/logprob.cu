@@ -222,6 +222,22 @@ struct Run {
         return Stat{m, st * e, (w.x + w.y + st * d) * e};
     }
 };
+// Joins n (a power of two up to 16) triples of shared memory; the result is the
+// same in every thread.
+__device__ __forceinline__ Stat join_list(const Stat *list, int n, float c) {
+    Stat a = list[(threadIdx.x & 31) % n];
+    for (int o = n / 2; o > 0; o >>= 1) {
+        Stat b;
+        b.m = __shfl_down_sync(~0u, a.m, o);
+        b.s = __shfl_down_sync(~0u, a.s, o);
+        b.w = __shfl_down_sync(~0u, a.w, o);
+        a = join(a, b, c);
+    }
+    a.m = __shfl_sync(~0u, a.m, 0);
+    a.s = __shfl_sync(~0u, a.s, 0);
+    a.w = __shfl_sync(~0u, a.w, 0);
+    return a;
+}
 template <int THREADS> __device__ __forceinline__ Stat block_join(Stat a, float c, Stat *warp_stats) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -233,9 +249,7 @@ template <int THREADS> __device__ __forceinline__ Stat block_join(Stat a, float 
     }
     if ((threadIdx.x & 31) == 0) warp_stats[threadIdx.x >> 5] = a;
     __syncthreads();
-    a = warp_stats[0];
-    for (int w = 1; w < THREADS / 32; ++w) a = join(a, warp_stats[w], c);
-    return a;  // the same in every thread
+    return join_list(warp_stats, THREADS / 32, c);
 }
 
 struct Args {
@@ -248,28 +262,23 @@ struct Args {
     int *top_ids;
 };
 
-__device__ __forceinline__ long long target_of(const void *t, int id64, int r) {
-    return id64 ? ((const long long *)t)[r] : (long long)((const int *)t)[r];
+// -1: an ignored row.
+__device__ __forceinline__ int target_of(const void *t, int id64, int r, int vocab) {
+    const long long x = id64 ? ((const long long *)t)[r] : (long long)((const int *)t)[r];
+    return x >= 0 && x < vocab ? (int)x : -1;
 }
 
-// Row outputs from the row's triple and its sorted alternatives.
-template <class T, int THREADS>
-__device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsigned long long *keys) {
+// Row outputs from the row's triple, thread 0's target t and its logit x, and
+// the row's sorted alternatives.
+template <int THREADS>
+__device__ __forceinline__ void finish(const Args &a, int r, Stat st, int t, float x, const unsigned long long *keys) {
     const bool empty = st.m == -INFINITY && st.s == 0.f;  // every logit is -inf
     const float ls = log2f(st.s);
     if (threadIdx.x == 0) {
         a.stats[2LL * r] = st.m;
         a.stats[2LL * r + 1] = empty ? 0.f : ls;
         if (a.entropy) a.entropy[r] = empty ? 0.f : (ls - st.w / st.s) * kLn2;
-        if (a.logp) {
-            const long long t = target_of(a.targets, a.id64, r);
-            float lp = 0.f;  // an ignored row
-            if (t >= 0 && t < a.vocab) {
-                const float x = to_f(((const T *)a.logits)[(long long)r * a.ld + t]);
-                lp = empty ? -INFINITY : (x - st.m) * a.inv_temp - ls * kLn2;
-            }
-            a.logp[r] = lp;
-        }
+        if (a.logp) a.logp[r] = t < 0 ? 0.f : empty ? -INFINITY : (x - st.m) * a.inv_temp - ls * kLn2;
     }
     for (int i = threadIdx.x; i < a.top; i += THREADS) {
         const unsigned long long k = keys[i];
@@ -278,14 +287,19 @@ __device__ __forceinline__ void finish(const Args &a, int r, Stat st, const unsi
     }
 }
 
-// Of n <= kCand distinct keys in shared memory, the `top` largest in order.
+// Of n <= kCand distinct keys in shared memory, the `top` largest in order:
+// four lanes count the keys above one.
 template <int THREADS>
 __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, int top, unsigned long long *out) {
-    for (int i = threadIdx.x; i < n; i += THREADS) {
-        const unsigned long long k = keys[i];
+    const int q = threadIdx.x & 3;
+    for (int b = 0; b < n; b += THREADS / 4) {
+        const int i = b + threadIdx.x / 4;
+        const unsigned long long k = keys[min(i, n - 1)];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += keys[j] > k;
-        if (rank < top) out[rank] = k;
+        for (int j = q; j < n; j += 4) rank += keys[j] > k;
+        rank += __shfl_xor_sync(~0u, rank, 1);
+        rank += __shfl_xor_sync(~0u, rank, 2);
+        if (i < n && q == 0 && rank < top) out[rank] = k;
     }
     __syncthreads();
 }
@@ -297,23 +311,22 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, fl
     constexpr int each = THREADS / 128;
 #pragma unroll
     for (int o = 1; o < each; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(~0u, mine, o));
-    const int t = threadIdx.x / each;
-    const bool lead = threadIdx.x % each == 0;
-    if (lead) maxima[t] = mine;
+    const int t = threadIdx.x / each, q = threadIdx.x % each;
+    if (q == 0) maxima[t] = mine;
     if (threadIdx.x == 0) *bound = -INFINITY;
     __syncthreads();
-    if (lead) {
-        int rank = 0;
+    int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < 128; j += 4) {
-            const float4 o = *(const float4 *)(maxima + j);
-            rank += o.x > mine || (o.x == mine && j < t);
-            rank += o.y > mine || (o.y == mine && j + 1 < t);
-            rank += o.z > mine || (o.z == mine && j + 2 < t);
-            rank += o.w > mine || (o.w == mine && j + 3 < t);
-        }
-        if (rank == top - 1) *bound = mine;
+    for (int j = 4 * q; j < 128; j += 4 * each) {
+        const float4 o = *(const float4 *)(maxima + j);
+        rank += o.x > mine || (o.x == mine && j < t);
+        rank += o.y > mine || (o.y == mine && j + 1 < t);
+        rank += o.z > mine || (o.z == mine && j + 2 < t);
+        rank += o.w > mine || (o.w == mine && j + 3 < t);
     }
+#pragma unroll
+    for (int o = 1; o < each; o <<= 1) rank += __shfl_xor_sync(~0u, rank, o);
+    if (q == 0 && rank == top - 1) *bound = mine;
     __syncthreads();
     return *bound;
 }
@@ -322,9 +335,9 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, fl
 // Block (r, p): part p of row r; the parts of a row are a cluster.  TOP:
 // alternatives wanted.
 template <class T, bool TOP, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
+__global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kernel(Args a) {
     constexpr int n = Group<T>::n, U = TOP && THREADS == kNarrow ? 2 : 4, WARPS = THREADS / 32;
-    __shared__ Stat warp_stats[WARPS], part_stat;
+    __shared__ Stat warp_stats[WARPS > kMaxParts ? WARPS : kMaxParts], part_stat;
     __shared__ unsigned long long cand[TOP ? kCand : 1], best[TOP ? LSTM_LOGPROB_MAX_TOP : 1];
     __shared__ __align__(16) float maxima[TOP ? 128 : 4];
     __shared__ float bound_s;
@@ -340,6 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
     const int groups = (e1 - h) / n;
     const uint4 *gp = (const uint4 *)(row + h);
     const int tail = h + groups * n;                  // [tail, e1): after the last one
+    const int target = a.logp && p == 0 && tid == 0 ? target_of(a.targets, a.id64, r, a.vocab) : -1;
     Run sum;
     float bound = -INFINITY;
     if (TOP && tid == 0) count = 0;
@@ -363,9 +377,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
             for (int u = 0; u < U; ++u) v[u] = g + u * THREADS < e ? __ldg(gp + g + u * THREADS) : masks<T>();
         }
     };
+    uint4 ahead[U];  // what run() looks at first
     auto run = [&](int b, int e, bool look) {
-        uint4 ahead[U];
-        fetch(ahead, b + tid, e);
 #pragma unroll 1
         for (int g = b + tid; g < e; g += U * THREADS) {
             uint4 v[U];
@@ -397,8 +410,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
     if (mine1 >= 0) sum.add1(raised(to_f(row[mine1])), c);
     const int first = TOP ? min(groups, max(groups / 3, U * THREADS)) : 0;  // (an eighth measured 171 us on
     // 2048 x 100003 with 8 alternatives, a quarter 135, a half 135, a third 132: candidates against a second look)
+    fetch(ahead, tid, TOP ? first : groups);
     if (TOP) {
         run(0, first, false);
+        fetch(ahead, first + tid, groups);  // under way while the bound is found
         bound = bound_of<THREADS>(sum.m, a.top, maxima, &bound_s);
         if (mine0 >= 0) push(mine0, !(raised(to_f(row[mine0])) < bound), row + mine0);
         if (mine1 >= 0) push(mine1, !(raised(to_f(row[mine1])) < bound), row + mine1);
@@ -409,6 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
         }
     }
     run(first, groups, TOP);
+    const float chosen = target >= 0 ? to_f(row[target]) : 0.f;
     Stat st = block_join<THREADS>(sum.stat(c), c, warp_stats);  // its barrier also closes the candidate list
     if (st.m == -INFINITY) {  // nothing but masks (or NaN): the part's plain sums
         Stat own = {-INFINITY, 0.f, 0.f};
@@ -459,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
         }
     }
     if (a.parts == 1) {
-        finish<T, THREADS>(a, r, st, best);
+        finish<THREADS>(a, r, st, target, chosen, best);
         return;
     }
     // the first block of the cluster joins the parts
@@ -467,13 +483,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
     tc::cluster_sync_all();
     if (p == 0) {
         auto peer = [&](const void *x, int q) { return tc::map_rank(tc::smem_u32(x), q); };
-        for (int q = 1; q < a.parts; ++q) {
-            const uint32_t at = peer(&part_stat, q);
+        if (tid < a.parts) {
+            const uint32_t at = peer(&part_stat, tid);
             Stat o;
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.m) : "r"(at));
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.s) : "r"(at + 4));
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.w) : "r"(at + 8));
-            st = join(st, o, c);
+            warp_stats[tid] = o;
         }
         if (TOP) {
             const int all = a.parts * a.top;
@@ -482,10 +498,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fwd_kernel(Args a) {
                 asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(peer(&best[i % a.top], i / a.top)));
                 cand[i] = k;
             }
-            __syncthreads();
-            rank_keys<THREADS>(cand, all, a.top, best);
         }
-        finish<T, THREADS>(a, r, st, best);
+        __syncthreads();
+        st = join_list(warp_stats, a.parts, c);
+        if (TOP) rank_keys<THREADS>(cand, a.parts * a.top, a.top, best);
+        finish<THREADS>(a, r, st, target, chosen, best);
     }
     tc::cluster_sync_all();  // no block leaves while its memory may be read
 }
@@ -509,16 +526,14 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_kernel(BwdArgs a) {
     T *y = (T *)a.dlogits + (long long)r * a.ldd;
     const float m = a.stats[2LL * r], ls = a.stats[2LL * r + 1], c = a.inv_temp * kLog2e;
     const float dh = a.dentropy ? a.dentropy[r] : 0.f, ent = a.dentropy ? a.entropy[r] * kLog2e : 0.f;
-    long long t = -1;
-    if (a.targets) t = target_of(a.targets, a.id64, r);
-    const bool hit = t >= 0 && t < a.vocab;
-    const float dl = hit && a.dlogp ? a.dlogp[r] * a.inv_temp : 0.f, dhc = dh * a.inv_temp * kLn2;
+    const int t = a.targets ? target_of(a.targets, a.id64, r, a.vocab) : -1;
+    const float dl = t >= 0 && a.dlogp ? a.dlogp[r] * a.inv_temp : 0.f, dhc = dh * a.inv_temp * kLn2;
     const bool empty = m == -INFINITY && ls == ls;
     // dl 1[target] - p (dl + dh (log p + entropy)), dl and dh over the temperature
     auto grad = [&](float v, int i) {
         const float lp = floor_nan((v - m) * c - ls);  // log2 p
         float g = -ex2(lp) * fmaf(dhc, lp + ent, dl);
-        if (i == (int)t) g += dl;
+        if (i == t) g += dl;
         return empty ? 0.f : g;
     };
     const int e0 = p * a.chunk, e1 = min(a.vocab, e0 + a.chunk);
