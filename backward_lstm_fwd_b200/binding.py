@@ -181,7 +181,7 @@ def load(path: str = LIB_PATH):
     lib.lstm_gdr_bwd_workspace_size.restype = sz
     lib.lstm_gdr_fwd.argtypes = [gp, go] + [vp] * 10 + [vp, sz, vp]
     lib.lstm_gdr_fwd.restype = ip
-    lib.lstm_gdr_bwd.argtypes = [gp, go] + [vp] * 15 + [vp, sz, vp]
+    lib.lstm_gdr_bwd.argtypes = [gp, go] + [vp] * 16 + [vp, sz, vp]
     lib.lstm_gdr_bwd.restype = ip
     v = lib.lstm_abi_version()
     if v // 100 != ABI_VERSION // 100 or v < ABI_VERSION:
@@ -806,8 +806,8 @@ def gdr_bwd_workspace_size(d: GdrDims) -> int:
 
 
 class GdrState:
-    """Outputs of one gdr_forward() call; states and deltas (save=True) are
-    kept for the backward."""
+    """Outputs of one gdr_forward() call; states, deltas and ws (save=True; ws
+    only where the call allocated it) are kept for the backward."""
 
     def __init__(self, d: GdrDims, cd, device, save, sT=None):
         f = torch.float32
@@ -815,7 +815,7 @@ class GdrState:
         self.dims = d
         self.o = torch.empty((T, B, H, V), dtype=cd, device=device)
         self.sT = torch.empty((B, H, K, V), dtype=f, device=device) if sT is None else sT
-        self.states = self.deltas = None
+        self.states = self.deltas = self.ws = None
         if save:
             self.states = torch.empty((-(-T // GDR_CHUNK), B, H, K, V), dtype=f, device=device)
             self.deltas = torch.empty((T, B, H, V), dtype=f, device=device)
@@ -872,7 +872,9 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     (one compute dtype; slices of one projection will do), log decay g and
     beta [T,B,Hv] float32, state s0 [B,Hv,K,V] float32.  lengths [B] int32 marks
     padding; scale defaults to K**-0.5.  save keeps what gdr_backward needs;
-    sT gives the final state's tensor (s0 itself for a state kept in place)."""
+    sT gives the final state's tensor (s0 itself for a state kept in place).
+    A ws of the caller's is free again after the call; the backward then makes
+    the operand tiles of the chunks once more."""
     d, opt = _gdr_call(q, k, v, g, beta, lengths, scale, s0=s0, sT=sT, ws=ws)
     state = (d.B, d.Hv, d.K, d.V)
     _shaped(s0, "s0", state, torch.float32)
@@ -883,6 +885,8 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     st = GdrState(d, q.dtype, q.device, save, sT)
     if ws is None and (save or d.T > GDR_STEP_TOKENS):
         ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
+        if save:
+            st.ws = ws
     _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _at(q), _at(k), _at(v), _at(g),
                              _at(beta), _at(s0), _at(st.o), _at(st.sT), _at(st.states),
                              _at(st.deltas), _at(ws), _ws_bytes(ws) if ws is not None else 0,
@@ -908,6 +912,6 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
     _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _at(dout), _at(dsT), _at(q),
                              _at(k), _at(v), _at(g), _at(beta), _at(st.states), _at(st.deltas),
                              _at(gr.dq), _at(gr.dk), _at(gr.dv), _at(gr.dg), _at(gr.dbeta),
-                             _at(gr.ds0), _at(ws), _ws_bytes(ws), _here(q)),
+                             _at(gr.ds0), _at(st.ws), _at(ws), _ws_bytes(ws), _here(q)),
          "lstm_gdr_bwd")
     return gr

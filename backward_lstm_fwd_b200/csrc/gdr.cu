@@ -208,18 +208,21 @@ int fwd(const lstm_gdr_dims *d, const Shape &s, const void *q, const void *k, co
 template <class E, int KD>
 int chunked_bwd(const lstm_gdr_dims *d, const Shape &s, const void *dout, const float *dsT, const void *q,
                 const void *k, const float *g, const float *beta, const float *states, const float *deltas, void *dq,
-                void *dk, void *dv, float *dg, float *dbeta, float *ds0, char *w, cudaStream_t st) {
+                void *dk, void *dv, float *dg, float *dbeta, float *ds0, const char *kept, char *w, cudaStream_t st) {
     const Layout l = layout(d, true);
-    if (s.NC > 0) {
+    if (kept) {  // the forward's layout begins alike
+        LSTM_CUDA_TRY(cudaMemsetAsync(w, 0, kCtrlBytes, st));
+    } else if (s.NC > 0) {
         const int rc = prep<E, KD>(s, q, k, g, beta, w, l, st);
         if (rc != LSTM_OK) return rc;
     }
+    const char *tiles = kept ? kept : w;
     float *dstates = (float *)(w + l.dstates), *dvf = (float *)(w + l.dvf);
-    SeqArgs a = {s, w + l.qk, w + l.tp, dout, dsT, dv, ds0, dstates, dvf, (float *)(w + l.starts), w + l.trans,
+    SeqArgs a = {s, tiles + l.qk, tiles + l.tp, dout, dsT, dv, ds0, dstates, dvf, (float *)(w + l.starts), w + l.trans,
                  l.split.segments, l.split.chunks, (Ctrl *)w};
     const int rc = sequential<KD>(a, (float *)(w + l.first), seq_bwd_kernel<E, KD, true>, seq_bwd_kernel<E, KD, false>, Seq<E, KD>::smem, st);
     if (rc != LSTM_OK || s.NC == 0) return rc;
-    GradArgs ga = {s, w + l.qk, g, beta, dout, states, deltas, dstates, dvf, dq, dk, dg, dbeta, (float *)(w + l.parts), (Ctrl *)w};
+    GradArgs ga = {s, tiles + l.qk, g, beta, dout, states, deltas, dstates, dvf, dq, dk, dg, dbeta, (float *)(w + l.parts), (Ctrl *)w};
     constexpr size_t smem = GradSmem<E, KD>::smem;
     const int blocks = s.NC * s.B * s.Hk;
     if (heads_per_block(d) == s.group) {
@@ -287,8 +290,8 @@ int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
 
 int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *dout, const float *dsT, const void *q,
                  const void *k, const void *v, const float *g, const float *beta, const float *states,
-                 const float *deltas, void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0, void *ws,
-                 size_t ws_bytes, void *stream) {
+                 const float *deltas, void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0,
+                 const void *fwd_ws, void *ws, size_t ws_bytes, void *stream) {
     int rc = check(d);
     if (rc != LSTM_OK) return rc;
     if (!scale_ok(opt)) return LSTM_ERR_INVALID_ARG;
@@ -299,6 +302,7 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
         !host::ptr_ok(beta, any, 4) || !host::ptr_ok(states, state) || !host::ptr_ok(deltas, any && d->V) ||
         !host::ptr_ok(dq, any && d->K) || !host::ptr_ok(dk, any && d->K) || !host::ptr_ok(dv, any && d->V) ||
         !host::ptr_ok(dg, any, 4) || !host::ptr_ok(dbeta, any, 4) || !host::ptr_ok(ds0, false) ||
+        !host::ptr_ok(fwd_ws, false, 256) ||
         !host::ptr_ok(opt ? opt->lengths : nullptr, false, 4))
         return LSTM_ERR_INVALID_ARG;
     rc = host::ws_check(ws, ws_bytes, layout(d, true).total);
@@ -318,12 +322,13 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
         return LSTM_OK;
     }
     const Shape s = shape_of(d, opt);
+    const char *kept = (const char *)fwd_ws;
     char *w = (char *)ws;
     if (d->dtype == LSTM_F32)
-        return bwd<float>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, w, st);
+        return bwd<float>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, kept, w, st);
     if (d->dtype == LSTM_F16)
-        return bwd<f16>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, w, st);
-    return bwd<bf16>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, w, st);
+        return bwd<f16>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, kept, w, st);
+    return bwd<bf16>(d, s, dout, dsT, q, k, g, beta, states, deltas, dq, dk, dv, dg, dbeta, ds0, kept, w, st);
 }
 
 }  // extern "C"

@@ -428,6 +428,9 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
  *          16-bit products of a projection's backward, as dy does), heads that
  *          share a key summed in float
  *   dg, dbeta [T][B][Hv]  float;  ds0 [B][Hv][K][V]  float, or NULL
+ * fwd_ws: the workspace of the forward call that kept states and deltas, if it
+ * is as that call left it (its chunks' operand tiles are read there), or NULL
+ * (they are made again from q, k, g and beta: less memory between the calls).
  *
  * K and V are multiples of 8 with K <= 128 and V <= 256 (else
  * LSTM_ERR_UNSUPPORTED).
@@ -461,8 +464,8 @@ int lstm_gdr_fwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
 int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void *dout,
                  const float *dsT, const void *q, const void *k, const void *v, const float *g,
                  const float *beta, const float *states, const float *deltas, void *dq, void *dk,
-                 void *dv, float *dg, float *dbeta, float *ds0, void *ws, size_t ws_bytes,
-                 void *stream);
+                 void *dv, float *dg, float *dbeta, float *ds0, const void *fwd_ws, void *ws,
+                 size_t ws_bytes, void *stream);
 
 /*
  * lstm_logprob_fwd / lstm_logprob_bwd -- log-probabilities of given tokens.

@@ -344,7 +344,7 @@ def test_gradient_in_place_and_optional_outputs():
         p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
         rc = L.load().lstm_gdr_bwd(ctypes.byref(st.dims), ctypes.byref(opt), p(dout), p(d), p(x["q"]), p(x["k"]), None, p(x["g"]),
                                    p(x["beta"]), p(st.states), p(st.deltas), p(g.dq), p(g.dk), p(g.dv), p(g.dg), p(g.dbeta),
-                                   p(d) if ds else None, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
+                                   p(d) if ds else None, None, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
         assert rc == L.LSTM_OK
         for n in ("dq", "dk", "dv", "dg", "dbeta"):
             assert torch.equal(getattr(g, n), getattr(want, n))

@@ -127,10 +127,10 @@ def gdr_fwd(lib, d, opt=None, q=FAKE, k=FAKE, v=FAKE, g=FAKE, beta=FAKE, s0=None
 
 
 def gdr_bwd(lib, d, opt=None, dout=FAKE, dsT=FAKE, q=FAKE, k=FAKE, v=None, g=FAKE, beta=FAKE, states=FAKE, deltas=FAKE, dq=FAKE,
-            dk=FAKE, dv=FAKE, dg=FAKE, dbeta=FAKE, ds0=FAKE, ws=FAKE, ws_bytes=None):
+            dk=FAKE, dv=FAKE, dg=FAKE, dbeta=FAKE, ds0=FAKE, fwd_ws=None, ws=FAKE, ws_bytes=None):
     n = L.gdr_bwd_workspace_size(d) if ws_bytes is None else ws_bytes
     return lib.lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt) if opt else None, dout, dsT, q, k, v, g, beta, states, deltas,
-                            dq, dk, dv, dg, dbeta, ds0, ws, n, None)
+                            dq, dk, dv, dg, dbeta, ds0, fwd_ws, ws, n, None)
 
 
 GDR = dict(T=100, B=2, Hk=2, Hv=4, K=64, V=64, dtype=L.LSTM_BF16)
@@ -165,6 +165,7 @@ def test_gdr_arguments(lib):
     for n in ("q", "k", "g", "beta", "states", "deltas", "dq", "dk", "dv", "dg", "dbeta"):
         assert gdr_bwd(lib, d, **{n: None}) == L.LSTM_ERR_INVALID_ARG
         assert gdr_bwd(lib, d, **{n: FAKE + (2 if n in by_element else 8)}) == L.LSTM_ERR_INVALID_ARG
+    assert gdr_bwd(lib, d, fwd_ws=FAKE + 16) == L.LSTM_ERR_INVALID_ARG
     for opt in (L.GdrOptions(FAKE + 2, 1.0), L.GdrOptions(None, float("nan")), L.GdrOptions(None, float("inf"))):
         assert gdr_fwd(lib, d, opt=opt) == L.LSTM_ERR_INVALID_ARG
         assert gdr_bwd(lib, d, opt=opt) == L.LSTM_ERR_INVALID_ARG
