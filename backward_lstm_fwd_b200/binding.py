@@ -578,10 +578,17 @@ def _on(ref: torch.Tensor, **ts) -> None:
             raise ValueError(f"{name} is on another device")
 
 
-def _dense(**ts) -> None:
+def _flat(ref: torch.Tensor, **ts) -> None:
+    """Every tensor given is contiguous and on ref's CUDA device."""
+    if not ref.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    dev = ref.get_device()
     for name, t in ts.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on another device")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
 
 
 def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype=None) -> None:
@@ -590,6 +597,11 @@ def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype=None) -> None:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{name}: {t.dtype}, want {dtype}")
+
+
+def _sizes(*n: int) -> None:
+    if max(n) >= 1 << 31:
+        raise ValueError(f"sizes {n}: each must be below 2**31")
 
 
 def _id_bytes(ids: Optional[torch.Tensor]) -> int:
@@ -645,17 +657,17 @@ def embed(ids, table, scale: float = 1.0, out=None, stream=None) -> torch.Tensor
     int32 / int64 of any shape, e.g. [T, B] for an x [T, B, I]); ids outside
     the table are padding and give zeros."""
     _need(table.dim() == 2, "table must be [vocab, I]")
-    _on(table, ids=ids, out=out)
-    _dense(ids=ids, table=table, out=out)
+    _flat(table, table=table, ids=ids, out=out)
     vocab, I = table.shape
-    shape = (*ids.shape, I)
+    N, shape = ids.numel(), (*ids.shape, I)
+    _sizes(N, vocab, I)
     _shaped(out, "out", shape, table.dtype)
     if _elsewhere(table, stream):
         with _there(table, stream):
             return embed(ids, table, scale, out)
     if out is None:
-        out = torch.empty(shape, dtype=table.dtype, device=table.device)
-    d = embed_dims(ids.numel(), vocab, I, table.dtype, _id_bytes(ids))
+        out = table.new_empty(shape)
+    d = EmbedDims(N, vocab, I, dtype_code(table.dtype), _id_bytes(ids))
     _run(load().lstm_embed_fwd(ctypes.byref(d), _at(ids), _at(table), float(scale), _at(out),
                                _here(table)), "lstm_embed_fwd")
     return out
@@ -671,16 +683,16 @@ def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate
     embed(ids, table, scale) for dx [..., I] (float32, bfloat16 or float16).
     accumulate adds to `out` instead of overwriting it."""
     I = dx.shape[-1]
-    _on(dx, ids=ids, out=out, ws=ws)
-    _dense(ids=ids, dx=dx, out=out, ws=ws)
+    _flat(dx, ids=ids, dx=dx, out=out, ws=ws)
     _shaped(dx, "dx", (*ids.shape, I))
     _need(not accumulate or out is not None, "accumulate needs out")
+    _sizes(ids.numel(), vocab, I)
     _shaped(out, "out", (vocab, I), torch.float32)
     if _elsewhere(dx, stream):
         with _there(dx, stream):
             return embed_backward(ids, dx, vocab, scale, out, accumulate, ws)
     if out is None:
-        out = torch.empty((vocab, I), dtype=torch.float32, device=dx.device)
+        out = dx.new_empty((vocab, I), dtype=torch.float32)
     d = embed_dims(ids.numel(), vocab, I, dx.dtype, _id_bytes(ids))
     if ws is None:
         ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
@@ -693,10 +705,10 @@ class LogProbs:
     """Outputs of one logprobs() call (float32; top_ids int32), kept for the
     backward.  logp is None without targets, top_ids / top_logp with top = 0."""
 
-    def __init__(self, N, top, has_targets, inv_temp, device):
+    def __init__(self, N, top, has_targets, inv_temp, logits):
         self.inv_temp = inv_temp
         # one allocation, of which these are parts: stats, entropy, logp, top_logp, top_ids
-        self._buf = buf = torch.empty((4 + 2 * top) * N, dtype=torch.float32, device=device)
+        self._buf = buf = logits.new_empty((4 + 2 * top) * N, dtype=torch.float32)
         self.entropy = buf.as_strided((N,), (1,), 2 * N)
         self.logp = buf.as_strided((N,), (1,), 3 * N) if has_targets else None
         self.top_logp = self.top_ids = None
@@ -730,6 +742,7 @@ def _rows(t: torch.Tensor, name: str) -> int:
     N, vocab = t.shape
     if vocab > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be dense")
+    _sizes(N, vocab)
     ld = t.stride(0) if N > 1 else vocab
     if ld < vocab:
         raise ValueError(f"{name}: rows overlap")
@@ -743,15 +756,14 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
     of every row at softmax(logits / temperature)."""
     ld = _rows(logits, "logits")
     N, vocab = logits.shape
-    _on(logits, targets=targets)
-    _dense(targets=targets)
+    _flat(logits, targets=targets)
     _shaped(targets, "targets", (N,))
     _need(temperature > 0, "temperature must be positive")
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return logprobs(logits, targets, top, temperature)
-    st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits.device)
-    d = logprob_dims(N, vocab, logits.dtype, ld, top, _id_bytes(targets))
+    st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits)
+    d = LogprobDims(N, vocab, ld, top, dtype_code(logits.dtype), _id_bytes(targets))
     _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
                                  _at(st.logp), _at(st.entropy), _at(st._buf), _at(st.top_ids),
                                  _at(st.top_logp), _here(logits)), "lstm_logprob_fwd")
@@ -764,24 +776,24 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     and (unless `out` is given) with their row stride; out may be logits."""
     ld = _rows(logits, "logits")
     N, vocab = logits.shape
-    _on(logits, targets=targets, dlogp=dlogp, dentropy=dentropy, out=out, stats=st.stats)
-    _dense(targets=targets, dlogp=dlogp, dentropy=dentropy)
+    _flat(logits, targets=targets, dlogp=dlogp, dentropy=dentropy, state=st.entropy)
+    _on(logits, out=out)
     _shaped(targets, "targets", (N,))
     _shaped(dlogp, "dlogp", (N,), torch.float32)
     _shaped(dentropy, "dentropy", (N,), torch.float32)
-    _shaped(st.stats, "stats", (N, 2), torch.float32)
+    _shaped(st.entropy, "the state's entropy", (N,))
     _shaped(out, "out", (N, vocab), logits.dtype)
     _need(1.0 / temperature == st.inv_temp, "temperature differs from the forward's")
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return logprobs_backward(st, logits, targets, dlogp, dentropy, temperature, out)
     if out is None:
-        out = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)
+        out = logits.new_empty((N, ld))
         if ld != vocab:
             out = out[:, :vocab]
-    d = logprob_dims(N, vocab, logits.dtype, ld, 0, _id_bytes(targets))
+    d = LogprobDims(N, vocab, ld, 0, dtype_code(logits.dtype), _id_bytes(targets))
     _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
-                                 _at(st.stats), _at(st.entropy), _at(dlogp), _at(dentropy),
+                                 _at(st._buf), _at(st.entropy), _at(dlogp), _at(dentropy),
                                  _at(out), _rows(out, "out"), _here(logits)), "lstm_logprob_bwd")
     return out
 
@@ -809,16 +821,16 @@ class GdrState:
     """Outputs of one gdr_forward() call; states, deltas and ws (save=True; ws
     only where the call allocated it) are kept for the backward."""
 
-    def __init__(self, d: GdrDims, cd, device, save, sT=None):
+    def __init__(self, d: GdrDims, q, save, sT=None):
         f = torch.float32
         T, B, H, K, V = d.T, d.B, d.Hv, d.K, d.V
         self.dims = d
-        self.o = torch.empty((T, B, H, V), dtype=cd, device=device)
-        self.sT = torch.empty((B, H, K, V), dtype=f, device=device) if sT is None else sT
+        self.o = q.new_empty((T, B, H, V))
+        self.sT = q.new_empty((B, H, K, V), dtype=f) if sT is None else sT
         self.states = self.deltas = self.ws = None
         if save:
-            self.states = torch.empty((-(-T // GDR_CHUNK), B, H, K, V), dtype=f, device=device)
-            self.deltas = torch.empty((T, B, H, V), dtype=f, device=device)
+            self.states = q.new_empty((-(-T // GDR_CHUNK), B, H, K, V), dtype=f)
+            self.deltas = q.new_empty((T, B, H, V), dtype=f)
 
 
 class GdrGrads:
@@ -854,8 +866,9 @@ def _gdr_call(q, k, v, g, beta, lengths, scale, **dense):
     T, B, Hk, K = shape = q.shape
     _, _, Hv, V = v.shape
     dt, f = q.dtype, torch.float32
-    _on(q, k=k, v=v, g=g, beta=beta, lengths=lengths, **dense)
-    _dense(g=g, beta=beta, lengths=lengths, **dense)
+    _sizes(T, B, Hk, Hv, K, V)
+    _on(q, k=k, v=v)
+    _flat(q, g=g, beta=beta, lengths=lengths, **dense)
     _shaped(k, "k", shape, dt)
     _shaped(v, "v", (T, B, Hv, V), dt)
     _shaped(g, "g", (T, B, Hv), f)
@@ -882,7 +895,7 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     if _elsewhere(q, stream):
         with _there(q, stream):
             return gdr_forward(q, k, v, g, beta, s0, lengths, scale, save, sT, ws)
-    st = GdrState(d, q.dtype, q.device, save, sT)
+    st = GdrState(d, q, save, sT)
     if ws is None and (save or d.T > GDR_STEP_TOKENS):
         ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
         if save:

@@ -169,3 +169,11 @@ def test_gradient_around_the_one_block_sort(n, vocab, kind):
     got = L.embed_backward(ids, dx, vocab)
     check_grad(got, ids, dx, vocab, 1.0)
     assert torch.equal(got, L.embed_backward(ids, dx, vocab))
+
+
+def test_sizes_past_an_int():
+    ids, table = torch.empty(2 ** 32 + 3, dtype=torch.int32, device="cuda"), torch.zeros(9, 8, device="cuda")
+    with pytest.raises(ValueError, match="below 2"):
+        L.embed(ids, table)  # (an int would hold 3)
+    with pytest.raises(ValueError, match="below 2"):
+        L.embed_backward(ids[:5], torch.zeros(5, 8, device="cuda"), 2 ** 32 + 1)

@@ -112,6 +112,8 @@ def test_binding_refuses_host_tensors_and_shapes(lib):
         L.embed_backward(ids, torch.zeros(3, 8), 5)
     with pytest.raises(ValueError, match="CUDA"):
         L.logprobs(torch.zeros(3, 5), ids)
+    with pytest.raises(ValueError, match="below 2"):
+        L.logprobs(torch.empty(1, 2 ** 31 + 5, device="meta"))  # (an int would hold 5)
     with pytest.raises(ValueError, match="rows overlap"):
         L.logprobs(torch.zeros(1, 5).expand(3, 5), ids)
     with pytest.raises(ValueError, match="dense"):
