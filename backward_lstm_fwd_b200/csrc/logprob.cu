@@ -14,10 +14,11 @@
 // rows: 128 threads a block and eight blocks an SM, so that one row's loads run
 // beside another's joins.  Few rows: a cluster of up to eight blocks shares a row
 // and joins its parts through distributed shared memory.
-// The alternatives come from the same pass: the first third of the range gives
-// every thread its own maximum, the top-th largest of those is a lower bound of
-// the answer, and only elements at or above it (a few times `top`) enter a
-// candidate list; the third is looked at twice (the second time from L1 / L2).
+// The alternatives come from the same pass: the first quarter (a third
+// above 16) of the range gives every thread its own maximum, the top-th largest
+// of those is a lower bound of the answer, and only elements at or above it (a
+// few times `top`) enter a candidate list; the quarter is looked at twice (the
+// second time from L1 / L2).
 // The backward reads the logits and writes the gradient once.
 #include <climits>
 
@@ -77,11 +78,11 @@ __device__ __forceinline__ unsigned ordered(float x) {
     const unsigned b = __float_as_uint(x);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(unsigned long long key) {
-    const unsigned o = (unsigned)(key >> 32);
+__device__ __forceinline__ float from_ordered(unsigned o) {
     if (o == 0u) return __uint_as_float(0x7fc00000u);
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
+__device__ __forceinline__ float value_of(unsigned long long key) { return from_ordered((unsigned)(key >> 32)); }
 __device__ __forceinline__ unsigned long long key_of(float x, int i) {
     return ((unsigned long long)ordered(x) << 32) | (unsigned)~i;
 }
@@ -304,31 +305,43 @@ __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n,
     __syncthreads();
 }
 
-// The top-th largest of the maxima of 128 groups of threads (-inf where fewer
-// than `top` groups have one): at least `top` elements are at or above it.
+// The top-th largest of the maxima of 32 (top <= 16) or 128 groups of threads:
+// at least `top` elements are at or above it.  (It is the least of those with
+// fewer than `top` above.)  Of 32, few more elements than `top` are (8: 9, 16:
+// 22), and every warp ranks them all, a lane each; of 128 every group ranks its own.
+__device__ __forceinline__ int above(const float *x, int n, float mine) {
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; j += 4) {
+        const float4 o = *(const float4 *)(x + j);
+        rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    }
+    return rank;
+}
 template <int THREADS>
-__device__ __forceinline__ float bound_of(float mine, int top, float *maxima, float *bound) {
+__device__ __forceinline__ float bound_of(float mine, int top, float *maxima, unsigned *bound) {
     constexpr int each = THREADS / 128;
 #pragma unroll
     for (int o = 1; o < each; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(~0u, mine, o));
-    const int t = threadIdx.x / each, q = threadIdx.x % each;
-    if (q == 0) maxima[t] = mine;
-    if (threadIdx.x == 0) *bound = -INFINITY;
-    __syncthreads();
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 4 * q; j < 128; j += 4 * each) {
-        const float4 o = *(const float4 *)(maxima + j);
-        rank += o.x > mine || (o.x == mine && j < t);
-        rank += o.y > mine || (o.y == mine && j + 1 < t);
-        rank += o.z > mine || (o.z == mine && j + 2 < t);
-        rank += o.w > mine || (o.w == mine && j + 3 < t);
+    if (top <= 16) {
+        mine = fmaxf(mine, __shfl_xor_sync(~0u, mine, each));
+        mine = fmaxf(mine, __shfl_xor_sync(~0u, mine, 2 * each));
+        if (threadIdx.x % (4 * each) == 0) maxima[threadIdx.x / (4 * each)] = mine;
+        __syncthreads();
+        mine = maxima[threadIdx.x & 31];
+        return from_ordered(__reduce_min_sync(~0u, above(maxima, 32, mine) < top ? ordered(mine) : ~0u));
     }
+    const int q = threadIdx.x % each;
+    if (q == 0) maxima[threadIdx.x / each] = mine;
+    if (threadIdx.x == 0) *bound = ~0u;
+    __syncthreads();
+    int rank = above(maxima + q * (128 / each), 128 / each, mine);
 #pragma unroll
     for (int o = 1; o < each; o <<= 1) rank += __shfl_xor_sync(~0u, rank, o);
-    if (q == 0 && rank == top - 1) *bound = mine;
+    const unsigned least = __reduce_min_sync(~0u, rank < top ? ordered(mine) : ~0u);
+    if ((threadIdx.x & 31) == 0) atomicMin(bound, least);
     __syncthreads();
-    return *bound;
+    return from_ordered(*bound);
 }
 
 // ----------------------------------------------------------------- forward
@@ -336,13 +349,13 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, fl
 // alternatives wanted.
 template <class T, bool TOP, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kernel(Args a) {
-    constexpr int n = Group<T>::n, U = TOP && THREADS == kNarrow ? 2 : 4, WARPS = THREADS / 32;
+    constexpr int n = Group<T>::n, U = TOP && THREADS == kNarrow ? 3 : 4, WARPS = THREADS / 32;
     __shared__ Stat warp_stats[WARPS > kMaxParts ? WARPS : kMaxParts], part_stat;
     __shared__ unsigned long long cand[TOP ? kCand : 1], best[TOP ? LSTM_LOGPROB_MAX_TOP : 1];
     __shared__ __align__(16) float maxima[TOP ? 128 : 4];
-    __shared__ float bound_s;
+    __shared__ unsigned bound_s;
     __shared__ int count;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int r = blockIdx.x / a.parts, p = blockIdx.x % a.parts;
     const T *row = (const T *)a.logits + (long long)r * a.ld;
     const float c = a.c;
@@ -367,7 +380,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
         }
     };
     // groups b .. e-1, the next U of a thread loaded before it looks at the last
-    // ones; look: candidates too
+    // ones; look: candidates too.  (A warp goes round together: lanes that drift
+    // apart at a candidate would go round one after another from there on, 65 us
+    // instead of 38 on such a row of 128000.)
     auto fetch = [&](uint4 (&v)[U], int g, int e) {
         if (g + (U - 1) * THREADS < e) {
 #pragma unroll
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
     uint4 ahead[U];  // what run() looks at first
     auto run = [&](int b, int e, bool look) {
 #pragma unroll 1
-        for (int g = b + tid; g < e; g += U * THREADS) {
+        for (int g = b + tid; g - lane < e; g += U * THREADS) {
             uint4 v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) v[u] = ahead[u];
@@ -396,11 +411,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < Pairs<T>::n; ++i) sum.add(Pairs<T>::pair(v[u], i), c);
-            if (TOP && look && !(top < bound)) {
+            if (TOP && look && __any_sync(~0u, !(top < bound))) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (g + u * THREADS < e && !(gm[u] < bound))
                         push(h + (g + u * THREADS) * n, Pairs<T>::candidates(v[u], bound), (const T *)(gp + g + u * THREADS));
+                __syncwarp();
             }
         }
     };
@@ -408,8 +424,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
     const int mine0 = e0 + tid < h ? e0 + tid : -1, mine1 = tail + tid < e1 ? tail + tid : -1;
     if (mine0 >= 0) sum.add1(raised(to_f(row[mine0])), c);
     if (mine1 >= 0) sum.add1(raised(to_f(row[mine1])), c);
-    const int first = TOP ? min(groups, max(groups / 3, U * THREADS)) : 0;  // (an eighth measured 171 us on
-    // 2048 x 100003 with 8 alternatives, a quarter 135, a half 135, a third 132: candidates against a second look)
+    // How much is looked at twice: candidates against a second look.  (2048 x
+    // 100003 bf16, us at an eighth, a sixth, a quarter, a third: 8 alternatives
+    // 120, 115, 106, 110; 64 alternatives 3458 (the list overflows), 311, 217, 187.)
+    const int first = TOP ? min(groups, max(groups / (a.top <= 16 ? 4 : 3), U * THREADS)) : 0;
     fetch(ahead, tid, TOP ? first : groups);
     if (TOP) {
         run(0, first, false);
@@ -417,10 +435,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
         bound = bound_of<THREADS>(sum.m, a.top, maxima, &bound_s);
         if (mine0 >= 0) push(mine0, !(raised(to_f(row[mine0])) < bound), row + mine0);
         if (mine1 >= 0) push(mine1, !(raised(to_f(row[mine1])) < bound), row + mine1);
+        __syncwarp();
 #pragma unroll 2
-        for (int g = tid; g < first; g += THREADS) {
-            uint4 v = __ldg(gp + g);
-            if (!(Pairs<T>::largest(v) < bound)) push(h + g * n, Pairs<T>::candidates(v, bound), (const T *)(gp + g));
+        for (int g = tid; g - lane < first; g += THREADS) {
+            uint4 v = g < first ? __ldg(gp + g) : masks<T>();
+            const bool at = g < first && !(Pairs<T>::largest(v) < bound);
+            if (__any_sync(~0u, at)) {
+                if (at) push(h + g * n, Pairs<T>::candidates(v, bound), (const T *)(gp + g));
+                __syncwarp();
+            }
         }
     }
     run(first, groups, TOP);
