@@ -621,19 +621,20 @@ template <class T, bool TOP, int THREADS> int launch_fwd(Args &a, cudaStream_t s
 
 // Which blocks a row gets (us, bf16).  Rows share out over a cluster until every
 // SM holds four blocks or a part is 16 KB: one row of 32000 takes 4.7 in 16 KB
-// parts and 5.2 in 32 KB ones, 74 of 128000 take 9.3 in parts and 16.2 whole,
-// 296 of 5000 take 4.0 whole and 5.0 in 8 KB parts.  Blocks of 128 threads beat
-// 512 almost everywhere (32000, 148 rows: 6.7 against 17.2; 8 alternatives, 296
-// rows: 24.6 against 30.4).  The exception is alternatives of few long rows,
-// whose thresholds are joined faster by more threads: 128000, 8 alternatives, 4
-// rows 17.8 against 11.7, 16 rows 19.5 against 16.5; 37 rows, two blocks an SM,
-// 21.6 against 26.6 again.
+// parts and 5.2 in 32 KB ones, 74 of 128000 take 8.9 in parts and 16.4 whole,
+// 296 of 5000 take 4.0 whole and 5.0 in 8 KB parts.  Alternatives of so few rows
+// that half the SMs hold a block each get 512 threads a block instead of 128
+// (more loads in flight, and fewer turns over the candidates): 4 rows of 128000,
+// 8 alternatives 8.9 against 12.1, 20 alternatives 11.5 against 16.4; one row of
+// 32000, 64 alternatives 11.7 against 22.3.  Of more rows the clusters of 512
+// threads no longer fit at once (16 rows of 128000: 16.4 against 12.8; 37: 24.0
+// against 13.5), and below four parts there is little to win (5000: 8.5 against 6.4).
 template <class T, bool TOP> int forward(Args &a, int sms, cudaStream_t s) {
     const long long bytes = (long long)a.vocab * (int)sizeof(T);
     a.parts = 1;
     while (a.parts < kMaxParts && (long long)a.N * a.parts <= 2 * sms && bytes > a.parts * kPartBytes) a.parts *= 2;
     if constexpr (TOP)
-        if (a.parts == kMaxParts && (long long)a.N * a.parts <= sms) return launch_fwd<T, TOP, kWide>(a, s);
+        if (a.parts >= 4 && 2LL * a.N * a.parts <= sms) return launch_fwd<T, TOP, kWide>(a, s);
     return launch_fwd<T, TOP, kNarrow>(a, s);
 }
 
