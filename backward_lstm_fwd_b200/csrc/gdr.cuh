@@ -349,6 +349,10 @@ __device__ __forceinline__ void load_gates(const Shape &s, const float *g, const
 // P and the gates, all in the layout the other kernels copy in bulk.  (Where
 // that leaves SMs idle, a block per value head, the tiles from the first.)
 //
+// Bound by the latency of the substitution's steps between its loads: bf16, K =
+// 128, 2048 blocks of two value heads 105 us (334 MB, 3.2 TB/s), 1024 blocks 57.
+// Five blocks an SM (six need spills: no gain).
+//
 // Q K^T and K K^T are one product of the stacked [Q; K] with K.  T2 is the
 // inverse of a unit lower triangular matrix [A 0; B D] of 32 x 32 blocks:
 // [A' 0; -D' B A', D'].  A' and D' come from forward substitution, a thread a
@@ -578,7 +582,9 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
 // Bound: the chain's latency (three products and three passes over registers
 // a chunk) where there are few heads.  512 threads rather than 256: a pass
 // over the registers is short code for many warps (with 256 threads the warps
-// waited for instructions more than for anything else).
+// waited for instructions more than for anything else).  bf16, K = V = 128: 6.6
+// us a chunk, forward with the states stored or backward alike; 256 heads of 16
+// chunks, up to two blocks an SM in turn, 217 us and 213 us.
 constexpr int SEQ_THREADS = 512;
 // tensor-memory columns: S terms, then left U terms | K S, Q S, then K^T (left
 // U) | R terms, then U terms | X, then P U
@@ -600,7 +606,9 @@ template <class E, int KD> struct Seq {
 // every column, so a first pass (SCAN) runs the segments side by side from a
 // zero state, which leaves B, and from the identity, which leaves A; scan_kernel
 // joins them to every segment's start, and a second pass runs all segments at
-// once.  (seg: chunks of a segment, in the order of the pass.)
+// once.  (seg: chunks of a segment, in the order of the pass.)  16 heads of 128
+// chunks: 91 us to scan, 21 to join, 107 to run, 267 with the preparation, against
+// 16 SMs that walk 128 chunks each at 6.6 us.
 struct SeqArgs {
     Shape s;
     const char *qk, *tp;
@@ -1090,7 +1098,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     seq_finish(bar);
 }
 
-// Join the segments: starts[i] becomes A_i starts[i - 1] + B_i, i = 1 .. in
+// Join the segments (3 us each, one after another: the products of a chain are
+// bound by latency): starts[i] becomes A_i starts[i - 1] + B_i, i = 1 .. in
 // order, block (b, h, 128 columns of V); S^T in registers and tensor memory as
 // above, A's tiles by bulk copies one segment ahead.
 template <int KD> struct ScanSmem {
@@ -1166,6 +1175,11 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) scan_kernel(const __grid_const
 // the same tiles read the other way.  V is contracted 64 columns a pass.
 // dg's double sum needs no matrix: sum_{r >= i > j} M_rj is the sum over
 // r >= i of (row sum - column sum), for the lower triangle M.
+//
+// Bound by the conversions between the products (every operand is a float that
+// becomes three terms) and by the one block an SM that the tiles leave room for:
+// bf16, K = V = 128, 2048 blocks of two value heads 465 us, 0.94 GB at 2.0 TB/s,
+// the tensor cores busy 36 % of the time.
 constexpr int GRAD_THREADS = 512;
 // [q; k] k^T | F over G, then Y over Z | E, then the transposed triangle's product | [dQ; dK]
 constexpr uint32_t COL_QK = 0, COL_FG = 64, COL_E = 256, COL_OUT = 384;
@@ -1532,7 +1546,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
-// dq and dk from the parts of `split` blocks, eight elements a thread.
+// dq and dk from the parts of `split` blocks, eight elements a thread (5 us on
+// the 2 MB of T = 333, 3 sequences, 2 key heads of 3).
 template <class E> __global__ void __launch_bounds__(256) sum_kernel(const float *parts, int split, long long n8, E *dq, E *dk) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= 2 * n8) return;
@@ -1556,7 +1571,9 @@ template <class E> __global__ void __launch_bounds__(256) sum_kernel(const float
 // -------------------------------------------------------------------- step
 // A few tokens, token by token: block (b, h, 64 columns of V), thread (part,
 // columns) holds four columns of the state for eight rows of K in registers.
-// Bound: the state's read and write.
+// Bound: the state's read and write.  64 sequences of 16 heads, K = V = 128, one
+// token: 25 us, 134 MB at 5.3 TB/s; a further token costs 7 us (1024 heads) or
+// 1 us (4 heads).
 constexpr int STEP_THREADS = 256, STEP_COLS = 64, STEP_PARTS = 16, STEP_K = 128 / STEP_PARTS;
 
 struct StepArgs {

@@ -345,6 +345,11 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, un
 }
 
 // ----------------------------------------------------------------- forward
+// 8192 x 32000 bf16: 104 to 110 us, 524 MB at 4.8 to 5.0 TB/s (the exponentials
+// and their packed sums share the issue slots with the loads); with 8
+// alternatives 2048 x 100003 bf16 107 us, 410 MB at 3.8 TB/s: the quarter looked
+// at twice and the joins of a row.  4 x 128000 float, 20 alternatives: 12 us, the
+// latency of one row's steps.
 // Block (r, p): part p of row r; the parts of a row are a cluster.  TOP:
 // alternatives wanted.
 template <class T, bool TOP, int THREADS>
@@ -531,6 +536,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
 }
 
 // ---------------------------------------------------------------- backward
+// 8192 x 32000 bf16: 162 us, 1.05 GB at 6.5 TB/s, memory's rate.
 struct BwdArgs {
     const void *logits, *targets;
     int id64, N, vocab, chunk, chunks;  // blocks of a row, elements each
