@@ -686,14 +686,15 @@ def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate
     _flat(dx, ids=ids, dx=dx, out=out, ws=ws)
     _shaped(dx, "dx", (*ids.shape, I))
     _need(not accumulate or out is not None, "accumulate needs out")
-    _sizes(ids.numel(), vocab, I)
+    N = ids.numel()
+    _sizes(N, vocab, I)
     _shaped(out, "out", (vocab, I), torch.float32)
     if _elsewhere(dx, stream):
         with _there(dx, stream):
             return embed_backward(ids, dx, vocab, scale, out, accumulate, ws)
     if out is None:
         out = dx.new_empty((vocab, I), dtype=torch.float32)
-    d = embed_dims(ids.numel(), vocab, I, dx.dtype, _id_bytes(ids))
+    d = EmbedDims(N, vocab, I, dtype_code(dx.dtype), _id_bytes(ids))
     if ws is None:
         ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
     _run(load().lstm_embed_bwd(ctypes.byref(d), _at(ids), _at(dx), float(scale), int(accumulate),
@@ -817,6 +818,10 @@ def gdr_bwd_workspace_size(d: GdrDims) -> int:
     return int(load().lstm_gdr_bwd_workspace_size(ctypes.byref(d)))
 
 
+def _sizes_of(d: GdrDims) -> tuple:
+    return d.T, d.B, d.Hk, d.Hv, d.K, d.V, d.dtype
+
+
 class GdrState:
     """Outputs of one gdr_forward() call; states, deltas and ws (save=True; ws
     only where the call allocated it) are kept for the backward."""
@@ -915,7 +920,7 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
     d, opt = _gdr_call(q, k, v, g, beta, lengths, scale, dout=dout, dsT=dsT, ws=ws, states=st.states)
     _shaped(dout, "dout", (d.T, d.B, d.Hv, d.V), q.dtype)
     _shaped(dsT, "dsT", (d.B, d.Hv, d.K, d.V), torch.float32)
-    _shaped(st.o, "the state's o", (d.T, d.B, d.Hv, d.V), q.dtype)
+    _need(_sizes_of(d) == _sizes_of(st.dims), "the state belongs to a forward of other sizes")
     if _elsewhere(q, stream):
         with _there(q, stream):
             return gdr_backward(st, q, k, v, g, beta, dout, dsT, lengths, scale, ws)

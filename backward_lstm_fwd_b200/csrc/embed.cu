@@ -5,20 +5,21 @@
 // inputs give equal bits whatever the token frequencies.
 //
 // Bound: bytes.  The lookup reads each id and row once and writes x; the
-// gradient reads dx once and writes every table row once (rows without a
-// token as zeros).
+// gradient reads dx once and writes every table row once, those with a token
+// twice (first as zeros, in the shadow of the sort).
 //
 // Gradient, in launches on one stream:
 //   sort    stable least-significant-digit radix sort of (token, position), 9
 //           bits a pass: one launch of block histograms, then one a pass that
 //           scatters and counts the next pass's histograms (integers: any
 //           order of the additions gives the same).  Up to 4096 keys are
-//           sorted by one block in shared memory, in one launch;
+//           sorted by one block in shared memory, in one launch.  Further
+//           blocks of these launches, bound by latency on few SMs, set the
+//           table to zero meanwhile;
 //   grad    units of 32 sorted positions x column tiles: a thread adds its
 //           columns of up to 32 rows in order and stores each token that lies
 //           inside the unit; a token that crosses a unit's border leaves
-//           partial sums.  Further blocks of the same launch write the zero
-//           rows, found by binary searches in the sorted tokens;
+//           partial sums;
 //   join    adds the partial sums of a token that spans units, in order.
 #include "host.cuh"
 
@@ -123,6 +124,21 @@ constexpr int kRounds = kWarpKeys / 32;
 constexpr int kSortBlocks = 128;                                // most blocks of a sort
 static_assert(kSortThreads == kBins, "one thread per digit");
 
+// A piece of the table that the blocks behind a sort's own set to zero meanwhile.
+struct Fill {
+    float *p;
+    long long n;
+};
+__device__ __forceinline__ void fill(const Fill &f, int block, int blocks) {
+    const int head = (int)min(f.n, (long long)(-((uintptr_t)f.p / 4) & 3)), tid = threadIdx.x;
+    const long long groups = (f.n - head) / 4, tail = head + groups * 4;
+    if (block == 0 && tid < head) f.p[tid] = 0.f;
+    if (block == 0 && tail + tid < f.n) f.p[tail + tid] = 0.f;
+    float4 *q = (float4 *)(f.p + head);
+    for (long long i = (long long)block * blockDim.x + tid; i < groups; i += (long long)blocks * blockDim.x)
+        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 struct SortArgs {
     const void *ids;         // pass 0: token ids (id64 or not); later passes: NULL
     int id64, vocab;
@@ -130,6 +146,7 @@ struct SortArgs {
     int *key_out, *pos_out;
     int *hist, *hist_next;   // [blocks][kBins]: of this pass; of the next one, or NULL
     int N, shift, blocks, tiles;  // every block sorts `tiles` consecutive tiles
+    Fill zero;               // by the launch's blocks from `blocks` on
 };
 
 // The sort key of input i: its token, or vocab for padding.
@@ -141,6 +158,7 @@ __device__ __forceinline__ int sort_key(const SortArgs &a, int i) {
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortArgs a) {
+    if ((int)blockIdx.x >= a.blocks) return fill(a.zero, blockIdx.x - a.blocks, gridDim.x - a.blocks);
     __shared__ int h[kBins];
     h[threadIdx.x] = 0;
     __syncthreads();
@@ -174,7 +192,10 @@ __device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
 // 32 at a time in order; equal digits among 32 are ranked by lane.  Bound by the
 // latency of its steps (the tile's histogram, two sums, the scatter): 7.7 us a
 // pass on 32768 keys, of which two passes sort ids below 2^18; histograms 3.5 us.
+// With their shares of 131 MB to clear 13 and 8 us, where the gradient's launch
+// took 13 us more to write the rows without a token itself.
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) {
+    if ((int)blockIdx.x >= a.blocks) return fill(a.zero, blockIdx.x - a.blocks, gridDim.x - a.blocks);
     __shared__ int base[kBins];                     // next output place of each digit
     __shared__ unsigned short cnt[kSortWarps][kBins];
     __shared__ int warp_sums[kSortWarps];
@@ -243,7 +264,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a) 
 
 // All passes of up to 4096 keys in one block: warp w holds keys 128 w .. in
 // registers, four rounds of 32, and the passes trade places in shared memory.
-// 10.4 us on 2049 keys (two passes), where the launches above took 19.
+// 10.4 us on 2049 keys (two passes), where the launches above took 19; with 52 MB
+// of table cleared beside it 11.7.
 constexpr int kOneWarps = 32, kOneThreads = 32 * kOneWarps, kOneRounds = 4, kOneKeys = kOneThreads * kOneRounds;
 struct OneSmem {
     int key[kOneKeys];
@@ -252,6 +274,7 @@ struct OneSmem {
     int warp_sums[kOneWarps];
 };
 __global__ void __launch_bounds__(kOneThreads) sort_one_kernel(SortArgs a, int bits) {
+    if (blockIdx.x > 0) return fill(a.zero, blockIdx.x - 1, gridDim.x - 1);
     extern __shared__ __align__(16) unsigned char one_raw[];
     OneSmem &m = *reinterpret_cast<OneSmem *>(one_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -314,8 +337,7 @@ __global__ void __launch_bounds__(kOneThreads) sort_one_kernel(SortArgs a, int b
 }
 
 // ---------------------------------------------------------------- gradient
-constexpr int kUnit = 32;       // sorted positions of a unit
-constexpr int kZeroRows = 32;   // table rows a zero-fill block looks after
+constexpr int kUnit = 32, kShortUnit = 8;  // sorted positions of a unit; of one where units are few
 constexpr int kColThreads = 256;
 
 struct GradArgs {
@@ -364,36 +386,16 @@ __device__ __forceinline__ void store_row(const GradArgs &a, int w, int col, con
     store_cols<W>(p, f);
 }
 
-// Bound by memory: 32768 rows x 1024 float into a table of 32000 rows 41 us, 265
-// MB at 6.5 TB/s.  2049 rows x 260 into 50001 rows 15 us, 54 MB at 3.6 TB/s: the
-// searches for the zero rows.
-template <class T, int W>
+// 32768 rows x 1024 float into a table of 32000 rows 28 us (134 MB read, 83
+// written: 7.7 TB/s, the written part in L2); of 2049 x 260 the latency of eight
+// rows.
+template <class T, int W, int UNIT>
 __global__ void __launch_bounds__(kColThreads) grad_kernel(GradArgs a) {
-    __shared__ int skey[kUnit + 2], spos[kUnit];
-    __shared__ unsigned present;
+    __shared__ int skey[UNIT + 2], spos[UNIT];
     const int tid = threadIdx.x;
     const int col = (blockIdx.y * kColThreads + tid) * W;
     clear_ctrl(a.ctrl);
-    if ((int)blockIdx.x >= a.units) {  // rows of the table without a token: zeros
-        const int w0 = ((int)blockIdx.x - a.units) * kZeroRows;
-        if (tid < 32) {  // lane j: the first place in the sorted tokens that row w0 + j could have
-            int lo = 0, hi = a.N;
-            while (lo < hi) {
-                const int mid = (int)(((unsigned)lo + (unsigned)hi) / 2);
-                if (__ldg(a.key + mid) < w0 + tid) lo = mid + 1; else hi = mid;
-            }
-            const unsigned has = __ballot_sync(~0u, lo < a.N && __ldg(a.key + min(lo, a.N - 1)) == w0 + tid);
-            if (tid == 0) present = has;
-        }
-        __syncthreads();
-        if (col < a.I) {
-            const float z[W] = {};
-            for (int j = 0; j < kZeroRows && w0 + j < a.vocab; ++j)
-                if (!((present >> j) & 1u)) store_cols<W>(a.dtable + (long long)(w0 + j) * a.I + col, z);
-        }
-        return;
-    }
-    const int u0 = blockIdx.x * kUnit, n = min(kUnit, a.N - u0);
+    const int u0 = blockIdx.x * UNIT, n = min(UNIT, a.N - u0);
     if (tid < n) {
         skey[tid + 1] = a.key[u0 + tid];
         spos[tid] = a.pos[u0 + tid];
@@ -438,14 +440,14 @@ __global__ void __launch_bounds__(kColThreads) grad_kernel(GradArgs a) {
 
 // One block per unit; only a unit in which a token begins that goes on in the
 // next one has work.  Four thread groups take every fourth of the units the
-// token goes on in; their sums are added in a fixed order.  10 us of the 41 + 10
-// above: the most frequent tokens, whose units one block adds.
+// token goes on in; their sums are added in a fixed order.  10 us
+// beside the 28 above: the most frequent tokens, whose units one block adds.
 constexpr int kJoinGroups = 4, kJoinCols = 64;
-template <int W>
+template <int W, int UNIT>
 __global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a) {
-    const int u = blockIdx.x, last = u * kUnit + kUnit - 1;
+    const int u = blockIdx.x, last = u * UNIT + UNIT - 1;
     if (last + 1 >= a.N) return;
-    const int w = a.key[last], after = a.key[last + 1], before = u > 0 ? a.key[u * kUnit - 1] : -1;
+    const int w = a.key[last], after = a.key[last + 1], before = u > 0 ? a.key[u * UNIT - 1] : -1;
     if (w >= a.vocab || after != w) return;
     if (before == w) return;  // began before this unit
     __shared__ float part[kJoinGroups][kJoinCols * W];
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a
     int end = u + 1, more;
     do {
         const int v = end + tid;
-        more = __syncthreads_count(v < a.units && a.key[(long long)min(v, a.units - 1) * kUnit] == w);
+        more = __syncthreads_count(v < a.units && a.key[(long long)min(v, a.units - 1) * UNIT] == w);
         end += more;
     } while (more == kJoinGroups * kJoinCols);
     const int g = tid / kJoinCols, c0 = tid % kJoinCols;
@@ -490,9 +492,17 @@ __global__ void __launch_bounds__(kJoinGroups *kJoinCols) join_kernel(GradArgs a
 // --------------------------------------------------------------- workspace
 struct BwdLayout {
     size_t key[2], pos[2], hist[2], pfirst, plast, total;
-    int units;
+    int unit, units;
 };
 
+// Units of 32 positions keep the partial sums few; where they would leave SMs
+// without a block, units of 8.  (us, of 8 / of 32: 128 ids x 1024 into 32000 rows
+// 27 / 33, 2049 x 260 into 50001 18 / 21, 4096 x 1024 36 / 37; 8192 x 1024 49 / 47,
+// 16384 x 512 40 / 35, 32768 x 64 39 / 31.)
+int unit_of(const lstm_embed_dims *d) {
+    const long long blocks = (((long long)d->N + kUnit - 1) / kUnit) * ((d->I + 4 * kColThreads - 1) / (4 * kColThreads));
+    return blocks < host::sm_count() ? kShortUnit : kUnit;
+}
 BwdLayout bwd_layout(const lstm_embed_dims *d) {
     BwdLayout l;
     size_t o = kCtrlBytes;
@@ -501,7 +511,8 @@ BwdLayout bwd_layout(const lstm_embed_dims *d) {
         o = align_up(o + bytes, 256);
         return at;
     };
-    l.units = (d->N + kUnit - 1) / kUnit;
+    l.unit = unit_of(d);
+    l.units = (d->N + l.unit - 1) / l.unit;
     for (int i = 0; i < 2; ++i) {
         l.key[i] = take((size_t)d->N * 4);
         l.pos[i] = take((size_t)d->N * 4);
@@ -523,16 +534,14 @@ bool dims_ok(const lstm_embed_dims *d) {
 // 32-bit index of the kernels (sort keys up to vocab, columns + tile).
 bool dims_supported(const lstm_embed_dims *d) { return d->vocab <= (1 << 30) && d->I <= (1 << 24) && d->N <= INT_MAX - 4 * kTile * kSortBlocks; }
 
-template <class T, int W> int grad(const lstm_embed_dims *d, GradArgs &a, cudaStream_t s) {
-    const int zero_blocks = a.accumulate ? 0 : (d->vocab + kZeroRows - 1) / kZeroRows;
+template <class T, int W, int UNIT> int grad(const lstm_embed_dims *d, GradArgs &a, cudaStream_t s) {
     const int tiles = (d->I + kColThreads * W - 1) / (kColThreads * W);
     const int jtiles = (d->I + kJoinCols * W - 1) / (kJoinCols * W);
     if (tiles > 65535 || jtiles > 65535) return LSTM_ERR_UNSUPPORTED;
-    if (a.units + zero_blocks == 0) return LSTM_OK;
-    grad_kernel<T, W><<<dim3(a.units + zero_blocks, tiles), kColThreads, 0, s>>>(a);
+    grad_kernel<T, W, UNIT><<<dim3(a.units, tiles), kColThreads, 0, s>>>(a);
     LSTM_CUDA_TRY(host::launched());
     if (a.units > 1) {
-        join_kernel<W><<<dim3(a.units, jtiles), kJoinGroups * kJoinCols, 0, s>>>(a);
+        join_kernel<W, UNIT><<<dim3(a.units, jtiles), kJoinGroups * kJoinCols, 0, s>>>(a);
         LSTM_CUDA_TRY(host::launched());
     }
     return LSTM_OK;
@@ -540,7 +549,8 @@ template <class T, int W> int grad(const lstm_embed_dims *d, GradArgs &a, cudaSt
 
 template <class T> int grad_w(const lstm_embed_dims *d, GradArgs &a, cudaStream_t s) {
     const bool wide = d->I % 4 == 0 && (uintptr_t)a.dx % (4 * sizeof(T)) == 0 && (uintptr_t)a.dtable % 16 == 0;
-    return wide ? grad<T, 4>(d, a, s) : grad<T, 1>(d, a, s);
+    if (unit_of(d) == kUnit) return wide ? grad<T, 4, kUnit>(d, a, s) : grad<T, 1, kUnit>(d, a, s);
+    return wide ? grad<T, 4, kShortUnit>(d, a, s) : grad<T, 1, kShortUnit>(d, a, s);
 }
 
 }  // namespace
@@ -586,43 +596,53 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
     cudaStream_t s = (cudaStream_t)stream;
     char *w = (char *)ws;
     // sort: enough 9-bit passes for the largest key, which is vocab (padding)
-    int cur = 0;
-    if (d->N > 0) {
-        int bits = 1;
-        while (bits < 31 && (d->vocab >> bits) != 0) ++bits;
-        SortArgs a = {};
-        const long long tiles = ((long long)d->N + kTile - 1) / kTile;
-        a.tiles = (int)((tiles + kSortBlocks - 1) / kSortBlocks);
-        a.blocks = (int)((tiles + a.tiles - 1) / a.tiles);
-        a.id64 = d->id_bytes == 8;
-        a.vocab = d->vocab;
-        a.N = d->N;
-        a.ids = ids;
-        if (d->N <= kOneKeys) {
-            a.key_out = (int *)(w + l.key[0]);
-            a.pos_out = (int *)(w + l.pos[0]);
-            LSTM_CUDA_TRY(cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(OneSmem)));
-            sort_one_kernel<<<1, kOneThreads, sizeof(OneSmem), s>>>(a, bits);
-            LSTM_CUDA_TRY(host::launched());
-            bits = 0;
-            cur = 1;
-        }
+    if (d->N == 0) {
+        LSTM_CUDA_TRY(cudaMemsetAsync(ws, 0, kCtrlBytes, s));
+        if (!accumulate) LSTM_CUDA_TRY(cudaMemsetAsync(dtable, 0, (size_t)d->vocab * d->I * 4, s));
+        return LSTM_OK;
+    }
+    int cur = 0, bits = 1;
+    while (bits < 31 && (d->vocab >> bits) != 0) ++bits;
+    SortArgs a = {};
+    const long long tiles = ((long long)d->N + kTile - 1) / kTile;
+    a.tiles = (int)((tiles + kSortBlocks - 1) / kSortBlocks);
+    a.blocks = (int)((tiles + a.tiles - 1) / a.tiles);
+    a.id64 = d->id_bytes == 8;
+    a.vocab = d->vocab;
+    a.N = d->N;
+    a.ids = ids;
+    // a launch clears the parts from .. to - 1 of `of` of the table: its blocks for that
+    const long long cells = accumulate ? 0 : (long long)d->vocab * d->I;
+    auto share = [&](int from, int to, int of, int threads) {
+        const long long b = cells / of * from, e = to == of ? cells : cells / of * to;
+        a.zero = {dtable + b, e - b};
+        return (int)std::min<long long>(2 * host::sm_count(), (a.zero.n + 4 * threads - 1) / (4 * threads));
+    };
+    if (d->N <= kOneKeys) {
+        a.key_out = (int *)(w + l.key[0]);
+        a.pos_out = (int *)(w + l.pos[0]);
+        const int extra = share(0, 1, 1, kOneThreads);
+        LSTM_CUDA_TRY(cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(OneSmem)));
+        sort_one_kernel<<<1 + extra, kOneThreads, sizeof(OneSmem), s>>>(a, bits);
+        LSTM_CUDA_TRY(host::launched());
+    } else {
         int *hist[2] = {(int *)(w + l.hist[0]), (int *)(w + l.hist[1])};
-        if (bits) {
-            a.hist = hist[0];
-            a.hist_next = hist[1];
-            sort_hist_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
-            LSTM_CUDA_TRY(host::launched());
-        }
-        for (int shift = 0; shift < bits; shift += kBits) {
-            const bool more = shift + kBits < bits;
-            a.shift = shift;
+        const int passes = (bits + kBits - 1) / kBits, shares = 2 * passes + 1;  // a scatter takes twice as long as the histograms
+        a.hist = hist[0];
+        a.hist_next = hist[1];
+        int extra = share(0, 1, shares, kSortThreads);
+        sort_hist_kernel<<<a.blocks + extra, kSortThreads, 0, s>>>(a);
+        LSTM_CUDA_TRY(host::launched());
+        for (int pass = 0; pass < passes; ++pass) {
+            const bool more = pass + 1 < passes;
+            a.shift = pass * kBits;
             a.key_out = (int *)(w + l.key[cur]);
             a.pos_out = (int *)(w + l.pos[cur]);
             a.hist = hist[0];
             a.hist_next = more ? hist[1] : nullptr;
-            if (more && shift > 0) LSTM_CUDA_TRY(cudaMemsetAsync(hist[1], 0, (size_t)a.blocks * kBins * 4, s));
-            sort_scatter_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
+            if (more && pass > 0) LSTM_CUDA_TRY(cudaMemsetAsync(hist[1], 0, (size_t)a.blocks * kBins * 4, s));
+            extra = share(2 * pass + 1, 2 * pass + 3, shares, kSortThreads);
+            sort_scatter_kernel<<<a.blocks + extra, kSortThreads, 0, s>>>(a);
             LSTM_CUDA_TRY(host::launched());
             a.ids = nullptr;
             a.key_in = a.key_out;

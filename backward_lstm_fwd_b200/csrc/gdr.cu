@@ -28,7 +28,7 @@ int strides_check(const lstm_gdr_dims *d) {
 }
 
 bool dims_supported(const lstm_gdr_dims *d) {
-    if (d->K % 8 || d->V % 8 || d->K > 128 || d->V > 256) return false;
+    if (d->K % 8 || d->V % 8 || d->K > 128 || d->V > 256 || d->T > INT_MAX - C) return false;
     if (or_dense(d->ldq, 0) % 8 || or_dense(d->ldk, 0) % 8 || or_dense(d->ldv, 0) % 8) return false;
     const long long nc = (d->T + C - 1) / C;
     return (long long)d->B * d->Hv * 4 <= INT_MAX && nc * d->B * std::max(d->Hk, d->Hv) <= INT_MAX;

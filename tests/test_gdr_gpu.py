@@ -329,6 +329,23 @@ def test_state_in_place(T):
         assert torch.equal(got.o, want.o) and torch.equal(state, want.sT)
 
 
+def test_state_of_other_sizes():
+    """A backward whose sizes are not its forward's would read past what the
+    forward kept."""
+    x, dout, dsT = make(100, 2, 2, 4, 64, 64, "bf16")
+    st = L.gdr_forward(**x, save=True)
+    five = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    wide = [t.repeat(1, 1, 2, 1) for t in five[:2]]  # four key heads
+    long = [torch.cat([t, t[..., :32]], -1).contiguous() for t in five[:2]]  # K = 96
+    for q, k in (wide, long, [t.half() for t in five[:2]]):
+        with pytest.raises(ValueError):
+            L.gdr_backward(st, q, k, five[2].to(q.dtype), *five[3:], dout=dout.to(q.dtype), dsT=dsT if q.shape[-1] == 64 else None)
+    with pytest.raises(ValueError, match="other sizes"):
+        L.gdr_backward(st, *wide, *five[2:], dout=dout, dsT=dsT)
+    with pytest.raises(ValueError, match="kept nothing"):
+        L.gdr_backward(L.gdr_forward(**x), *five, dout=dout, dsT=dsT)
+
+
 def test_gradient_in_place_and_optional_outputs():
     """The C entry point: ds0 may be dsT, or absent."""
     import ctypes

@@ -189,6 +189,12 @@ def test_gdr_arguments(lib):
     assert gdr_bwd(lib, none) == L.LSTM_OK
 
 
+def test_gdr_lengths_past_an_int(lib):
+    d = L.gdr_dims(2 ** 31 - 1, 1, 1, 1, 8, 8, torch.bfloat16)  # (its chunks' count would wrap)
+    assert gdr_fwd(lib, d, ws_bytes=1 << 60) == L.LSTM_ERR_UNSUPPORTED
+    assert gdr_bwd(lib, d, ws_bytes=1 << 60) == L.LSTM_ERR_UNSUPPORTED
+
+
 def test_gdr_binding_refusals(lib):
     q = torch.zeros(4, 2, 1, 8)
     with pytest.raises(ValueError, match="CUDA"):
