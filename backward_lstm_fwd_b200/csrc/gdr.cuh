@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     seq_finish(bar);
 }
 
-// Join the segments (3 us each, one after another: the products of a chain are
+// Join the segments (4 us each, one after another: the products of a chain are
 // bound by latency): starts[i] becomes A_i starts[i - 1] + B_i, i = 1 .. in
 // order, block (b, h, 128 columns of V); S^T in registers and tensor memory as
 // above, A's tiles by bulk copies one segment ahead.

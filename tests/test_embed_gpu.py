@@ -40,7 +40,7 @@ def expect(ids, dx, vocab, scale):
     """(sum, sum of magnitudes) of the table's gradient in float64."""
     i = ids.long().reshape(-1)
     ok = (i >= 0) & (i < vocab)
-    d = dx.double().reshape(len(i), -1)[ok]
+    d = dx.double().reshape(len(i), dx.shape[-1])[ok]
     out = torch.zeros(vocab, dx.shape[-1], dtype=torch.float64, device=dx.device)
     mag = out.clone().index_add_(0, i[ok], d.abs())
     return out.index_add_(0, i[ok], d) * scale, mag * abs(scale)
@@ -177,3 +177,17 @@ def test_sizes_past_an_int():
         L.embed(ids, table)  # (an int would hold 3)
     with pytest.raises(ValueError, match="below 2"):
         L.embed_backward(ids[:5], torch.zeros(5, 8, device="cuda"), 2 ** 32 + 1)
+
+
+@pytest.mark.parametrize("n", [0, 50, 5000])
+@pytest.mark.parametrize("at", [0, 1, 2, 3])
+def test_gradient_inside_a_buffer(n, at):
+    """A table at any element of a buffer: every row is written, nothing beside it is."""
+    vocab, I = 777, 5
+    buf = torch.full((vocab * I + 8,), 7.0, device="cuda")
+    table = buf[at:at + vocab * I].view(vocab, I)
+    ids = make_ids(n, vocab, n + at, "heavy", torch.int32)
+    dx = torch.randn(n, I, device="cuda")
+    got = L.embed_backward(ids, dx, vocab, out=table)
+    check_grad(got, ids, dx, vocab, 1.0)
+    assert bool((buf[:at] == 7.0).all()) and bool((buf[at + vocab * I:] == 7.0).all())

@@ -74,7 +74,8 @@ def check(logits, targets, top, temperature, grads=True):
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("N,V,pad,top", [(1, 1, 0, 1), (3, 2, 1, 2), (2, 7, 0, 7), (5, 63, 2, 20), (4, 4095, 1, 5),
                                          (1, 128000, 0, 20), (3, 50001, 7, 64), (700, 1003, 5, 8), (2, 9000, 0, 0),
-                                         (301, 5000, 3, 1)])
+                                         (301, 5000, 3, 1), (20, 40000, 3, 5), (37, 70001, 1, 17), (37, 70001, 1, 0),
+                                         (150, 30000, 5, 16), (18, 33000, 0, 64), (19, 33000, 0, 33)])
 def test_against_64_bits(N, V, pad, top, dt):
     g = torch.Generator(device="cuda").manual_seed(N + V)
     logits = (4 * torch.randn(N, V + pad, generator=g, device="cuda")).to(DT[dt])[:, :V]
@@ -147,6 +148,18 @@ def test_equal_values(N):
     y = torch.zeros(N, 20000, device="cuda")
     y[:, ::2] = -0.0  # the zeros are equal
     assert L.logprobs(y, top=3).top_ids[0].tolist() == [0, 1, 2]
+
+
+@pytest.mark.parametrize("N", [2, 20, 400])
+@pytest.mark.parametrize("step", [1, -1])
+def test_sorted_rows(N, step):
+    """Rows that rise make every element a candidate (the list overflows), rows that fall the first ones alone."""
+    x = (torch.arange(40000, device="cuda", dtype=torch.float32) * (step * 1e-3)).repeat(N, 1)
+    for top in (1, 16, 20):
+        st = L.logprobs(x, top=top)
+        want = torch.arange(top, device="cuda") if step < 0 else 39999 - torch.arange(top, device="cuda")
+        assert bool((st.top_ids == want).all())
+        check(x, torch.arange(N, device="cuda"), top, 1.0)
 
 
 def test_confident_row():
