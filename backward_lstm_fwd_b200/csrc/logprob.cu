@@ -129,24 +129,20 @@ __device__ __forceinline__ float raised(float x) {
     return y;
 }
 
-// A 16-byte group as pairs of floats raised to the mask value; largest() may
-// raise in place where the type holds kMask.
+// A 16-byte group as pairs of floats raised to the mask value (as floats: the
+// 16-bit maximum that keeps NaN costs more; 8192 x 32000 bf16 93 us against 103).
+// float's largest() raises in place.
 template <class T> struct Pairs {
     static constexpr int n = 4;
     typedef typename Elem<T>::E2 E2;
     __device__ static __forceinline__ float largest(uint4 &v) {
         E2 *h = reinterpret_cast<E2 *>(&v);
-        if (Elem<T>::kFmt == 1) {
-            const E2 lo = Elem<T>::from_f2(kMask, kMask);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], lo);
-        }
         const float2 m = Elem<T>::to_f2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
         return fmaxf(m.x, m.y);
     }
     __device__ static __forceinline__ F2 pair(const uint4 &v, int i) {
         const float2 f = Elem<T>::to_f2(reinterpret_cast<const E2 *>(&v)[i]);
-        return Elem<T>::kFmt == 1 ? F2{f.x, f.y} : F2{raised(f.x), raised(f.y)};
+        return F2{raised(f.x), raised(f.y)};
     }
     // bit i: element i is at or above the bound (or NaN)
     __device__ static __forceinline__ unsigned candidates(const uint4 &v, float bound) {
@@ -345,9 +341,10 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, un
 }
 
 // ----------------------------------------------------------------- forward
-// 8192 x 32000 bf16: 104 to 110 us, 524 MB at 4.8 to 5.0 TB/s (the exponentials
-// and their packed sums share the issue slots with the loads); with 8
-// alternatives 2048 x 100003 bf16 107 us, 410 MB at 3.8 TB/s: the quarter looked
+// 8192 x 32000 bf16: 93 us, 524 MB at 5.6 TB/s (the exponentials and their packed
+// sums share the issue slots with the loads; a block that walks rows and loads the
+// next one's beginning before it joins a row took 110 to 118); with 8
+// alternatives 2048 x 100003 bf16 100 us, 410 MB at 4.1 TB/s: the quarter looked
 // at twice and the joins of a row.  4 x 128000 float, 20 alternatives: 12 us, the
 // latency of one row's steps.
 // Block (r, p): part p of row r; the parts of a row are a cluster.  TOP:
@@ -425,19 +422,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
             }
         }
     };
-    // the elements outside whole groups: fewer than 2 n
-    const int mine0 = e0 + tid < h ? e0 + tid : -1, mine1 = tail + tid < e1 ? tail + tid : -1;
-    if (mine0 >= 0) sum.add1(raised(to_f(row[mine0])), c);
-    if (mine1 >= 0) sum.add1(raised(to_f(row[mine1])), c);
     // How much is looked at twice: candidates against a second look.  (2048 x
     // 100003 bf16, us at an eighth, a sixth, a quarter, a third: 8 alternatives
     // 120, 115, 106, 110; 64 alternatives 3458 (the list overflows), 311, 217, 187.)
     const int first = TOP ? min(groups, max(groups / (a.top <= 16 ? 4 : 3), U * THREADS)) : 0;
     fetch(ahead, tid, TOP ? first : groups);
+    // the elements outside whole groups: fewer than 2 n
+    const int mine0 = e0 + tid < h ? e0 + tid : -1, mine1 = tail + tid < e1 ? tail + tid : -1;
+    if (mine0 >= 0) sum.add1(raised(to_f(row[mine0])), c);
+    if (mine1 >= 0) sum.add1(raised(to_f(row[mine1])), c);
     if (TOP) {
         run(0, first, false);
         fetch(ahead, first + tid, groups);  // under way while the bound is found
         bound = bound_of<THREADS>(sum.m, a.top, maxima, &bound_s);
+        if (bound == kMask) bound = -INFINITY;  // masks are among the alternatives
         if (mine0 >= 0) push(mine0, !(raised(to_f(row[mine0])) < bound), row + mine0);
         if (mine1 >= 0) push(mine1, !(raised(to_f(row[mine1])) < bound), row + mine1);
         __syncwarp();
