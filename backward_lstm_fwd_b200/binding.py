@@ -599,6 +599,11 @@ def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype=None) -> None:
             raise ValueError(f"{name}: {t.dtype}, want {dtype}")
 
 
+def _workspace(like: torch.Tensor, nbytes: int) -> torch.Tensor:
+    """empty_workspace() beside a tensor."""
+    return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
+
+
 def _sizes(*n: int) -> None:
     if max(n) >= 1 << 31:
         raise ValueError(f"sizes {n}: each must be below 2**31")
@@ -666,7 +671,7 @@ def embed(ids, table, scale: float = 1.0, out=None, stream=None) -> torch.Tensor
         with _there(table, stream):
             return embed(ids, table, scale, out)
     if out is None:
-        out = table.new_empty(shape)
+        out = table.new_empty(*shape)
     d = EmbedDims(N, vocab, I, dtype_code(table.dtype), _id_bytes(ids))
     _run(load().lstm_embed_fwd(ctypes.byref(d), _at(ids), _at(table), float(scale), _at(out),
                                _here(table)), "lstm_embed_fwd")
@@ -693,10 +698,10 @@ def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate
         with _there(dx, stream):
             return embed_backward(ids, dx, vocab, scale, out, accumulate, ws)
     if out is None:
-        out = dx.new_empty((vocab, I), dtype=torch.float32)
+        out = dx.new_empty(vocab, I, dtype=torch.float32)
     d = EmbedDims(N, vocab, I, dtype_code(dx.dtype), _id_bytes(ids))
     if ws is None:
-        ws = empty_workspace(embed_bwd_workspace_size(d), dx.device)
+        ws = _workspace(dx, embed_bwd_workspace_size(d))
     _run(load().lstm_embed_bwd(ctypes.byref(d), _at(ids), _at(dx), float(scale), int(accumulate),
                                _at(out), _at(ws), _ws_bytes(ws), _here(dx)), "lstm_embed_bwd")
     return out
@@ -708,10 +713,10 @@ class LogProbs:
 
     def __init__(self, N, top, has_targets, inv_temp, logits):
         self.inv_temp = inv_temp
-        # one allocation, of which these are parts: stats, entropy, logp, top_logp, top_ids
-        self._buf = buf = logits.new_empty((4 + 2 * top) * N, dtype=torch.float32)
-        self.entropy = buf.as_strided((N,), (1,), 2 * N)
-        self.logp = buf.as_strided((N,), (1,), 3 * N) if has_targets else None
+        # one allocation: rows of N for stats (2), entropy and logp, then top_logp and top_ids
+        self._buf = buf = logits.new_empty(4 + 2 * top, N, dtype=torch.float32)
+        self.entropy = buf[2]
+        self.logp = buf[3] if has_targets else None
         self.top_logp = self.top_ids = None
         if top:
             self.top_logp = buf.as_strided((N, top), (top, 1), 4 * N)
@@ -721,7 +726,7 @@ class LogProbs:
     def stats(self) -> torch.Tensor:
         """[N, 2]: the row's largest logit and log2 sum 2^(c (x - largest)), c =
         log2(e) / temperature."""
-        return self._buf.as_strided((self.entropy.numel(), 2), (2, 1))
+        return self._buf[:2].view(-1, 2)
 
     @property
     def lse(self) -> torch.Tensor:
@@ -788,14 +793,17 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return logprobs_backward(st, logits, targets, dlogp, dentropy, temperature, out)
-    if out is None:
-        out = logits.new_empty((N, ld))
+    ldd = ld
+    if out is not None:
+        ldd = _rows(out, "out")
+    else:
+        out = logits.new_empty(N, ld)
         if ld != vocab:
             out = out[:, :vocab]
     d = LogprobDims(N, vocab, ld, 0, dtype_code(logits.dtype), _id_bytes(targets))
     _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
                                  _at(st._buf), _at(st.entropy), _at(dlogp), _at(dentropy),
-                                 _at(out), _rows(out, "out"), _here(logits)), "lstm_logprob_bwd")
+                                 _at(out), ldd, _here(logits)), "lstm_logprob_bwd")
     return out
 
 
@@ -830,8 +838,8 @@ class GdrState:
         f = torch.float32
         T, B, H, K, V = d.T, d.B, d.Hv, d.K, d.V
         self.dims = d
-        self.o = q.new_empty((T, B, H, V))
-        self.sT = q.new_empty((B, H, K, V), dtype=f) if sT is None else sT
+        self.o = q.new_empty(T, B, H, V)
+        self.sT = q.new_empty(B, H, K, V, dtype=f) if sT is None else sT
         self.states = self.deltas = self.ws = None
         if save:
             self.states = q.new_empty((-(-T // GDR_CHUNK), B, H, K, V), dtype=f)
@@ -902,7 +910,7 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
             return gdr_forward(q, k, v, g, beta, s0, lengths, scale, save, sT, ws)
     st = GdrState(d, q, save, sT)
     if ws is None and (save or d.T > GDR_STEP_TOKENS):
-        ws = empty_workspace(gdr_fwd_workspace_size(d, save), q.device)
+        ws = _workspace(q, gdr_fwd_workspace_size(d, save))
         if save:
             st.ws = ws
     _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _at(q), _at(k), _at(v), _at(g),
@@ -926,7 +934,7 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
             return gdr_backward(st, q, k, v, g, beta, dout, dsT, lengths, scale, ws)
     gr = GdrGrads(d, q.dtype, q.device)
     if ws is None:
-        ws = empty_workspace(gdr_bwd_workspace_size(d), q.device)
+        ws = _workspace(q, gdr_bwd_workspace_size(d))
     _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _at(dout), _at(dsT), _at(q),
                              _at(k), _at(v), _at(g), _at(beta), _at(st.states), _at(st.deltas),
                              _at(gr.dq), _at(gr.dk), _at(gr.dv), _at(gr.dg), _at(gr.dbeta),
