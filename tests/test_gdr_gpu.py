@@ -318,6 +318,35 @@ def test_streams_graphs_and_status():
         assert torch.equal(getattr(gr, n), getattr(wg, n)), n
 
 
+def test_step_in_one_graph():
+    """Forward and backward captured together, the forward's workspace kept between them; replayed on new
+    inputs, and the backward taken twice from one state."""
+    x, dout, dsT = make(150, 2, 2, 4, 64, 72, "fp16")
+    y, _, _ = make(150, 2, 2, 4, 64, 72, "fp16", seed=1)
+    buf = {n: t.clone() for n, t in x.items()}
+    names = ("q", "k", "v", "g", "beta")
+    five = [buf[n] for n in names]
+    L.gdr_forward(**buf, save=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st = L.gdr_forward(**buf, save=True)
+        once = L.gdr_backward(st, *five, dout=dout, dsT=dsT)
+        again = L.gdr_backward(st, *five, dout=dout, dsT=dsT)
+    for z in (y, x):
+        for n in z:
+            buf[n].copy_(z[n] if n != "beta" else z[n] * 0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        ws = L.empty_workspace(L.gdr_bwd_workspace_size(st.dims), "cuda")
+        own = L.gdr_forward(**{n: t.clone() for n, t in buf.items()}, save=True, ws=ws)  # keeps no workspace
+        assert own.ws is None and st.ws is not None
+        want = L.gdr_backward(own, *[t.clone() for t in five], dout=dout, dsT=dsT, ws=ws)
+        assert torch.equal(st.o, own.o) and L.lstm_status(ws) == L.LSTM_OK
+        for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"):
+            assert torch.equal(getattr(once, n), getattr(want, n)) and torch.equal(getattr(again, n), getattr(want, n)), n
+
+
 @pytest.mark.parametrize("T", [3, 100, 1500])
 def test_state_in_place(T):
     """sT is s0, also where the sequence is split over blocks."""
