@@ -1571,10 +1571,12 @@ template <class E> __global__ void __launch_bounds__(256) sum_kernel(const float
 // -------------------------------------------------------------------- step
 // A few tokens, token by token: block (b, h, 64 columns of V), thread (part,
 // columns) holds four columns of the state for eight rows of K in registers.
-// Bound: the state's read and write.  64 sequences of 16 heads, K = V = 128, one
-// token: 25 us, 134 MB at 5.3 TB/s; a further token costs 7 us (1024 heads) or
-// 1 us (4 heads).
-constexpr int STEP_THREADS = 256, STEP_COLS = 64, STEP_PARTS = 16, STEP_K = 128 / STEP_PARTS;
+// Bound: the state's read and write.  16 heads, K = V = 128, one token: of 64
+// sequences 26 us, 134 MB at 5.2 TB/s, of 256 85 us, 6.3 TB/s; a further token
+// costs 6 us (1024 heads) or 1 us (4 heads).  (Blocks of 32 or 128 columns 26.3 and
+// 30.5 us, of 8 parts 27.2, of 32 columns and 32 parts 28.8.)
+constexpr int STEP_COLS = 64, STEP_LANES = STEP_COLS / 4, STEP_PARTS = 16, STEP_K = 128 / STEP_PARTS;
+constexpr int STEP_THREADS = STEP_PARTS * STEP_LANES, STEP_WARPS = STEP_THREADS / 32;
 
 struct StepArgs {
     Shape s;
@@ -1587,15 +1589,15 @@ struct StepArgs {
 };
 
 template <class E>
-__global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
+__global__ void __launch_bounds__(STEP_THREADS, 1024 / STEP_THREADS) step_kernel(StepArgs a) {
     __shared__ float qs[128], ks[128];
-    __shared__ float4 part[2][8][STEP_COLS / 4];  // a warp's two parts together
+    __shared__ float4 part[2][STEP_WARPS][STEP_LANES];  // a warp's parts together
     const Shape &s = a.s;
     if (a.ctrl) clear_ctrl(a.ctrl);
-    const int tid = threadIdx.x, warp = tid >> 5, c4 = tid & 15, v = blockIdx.x % a.tiles * STEP_COLS + c4 * 4;
+    const int tid = threadIdx.x, warp = tid >> 5, c4 = tid % STEP_LANES, v = blockIdx.x % a.tiles * STEP_COLS + c4 * 4;
     const int id = blockIdx.x / a.tiles, h = id % s.Hv, b = id / s.Hv, hk = h / s.group;
     const long long head = (long long)b * s.Hv + h;
-    const int len = length_of(s, b), k0 = (tid >> 4) * STEP_K;
+    const int len = length_of(s, b), k0 = tid / STEP_LANES * STEP_K;
     const bool own = v < s.V;  // V is a multiple of 8: all four or none
     float4 S[STEP_K];
 #pragma unroll
@@ -1613,15 +1615,18 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
             d.z = fmaf(x, S[i].z, d.z);
             d.w = fmaf(x, S[i].w, d.w);
         }
-        d.x += __shfl_xor_sync(~0u, d.x, 16);
-        d.y += __shfl_xor_sync(~0u, d.y, 16);
-        d.z += __shfl_xor_sync(~0u, d.z, 16);
-        d.w += __shfl_xor_sync(~0u, d.w, 16);
-        if ((tid & 16) == 0) part[buf][warp][c4] = d;
+#pragma unroll
+        for (int o = STEP_LANES; o < 32; o *= 2) {
+            d.x += __shfl_xor_sync(~0u, d.x, o);
+            d.y += __shfl_xor_sync(~0u, d.y, o);
+            d.z += __shfl_xor_sync(~0u, d.z, o);
+            d.w += __shfl_xor_sync(~0u, d.w, o);
+        }
+        if ((tid & 31) < STEP_LANES) part[buf][warp][c4] = d;
         __syncthreads();
         d = part[buf][0][c4];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
+        for (int i = 1; i < STEP_WARPS; ++i) {
             const float4 e = part[buf][i][c4];
             d.x += e.x;
             d.y += e.y;
@@ -1633,7 +1638,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
     for (int t = 0; t < s.T; ++t) {
         const long long r = (long long)t * s.B + b;
         E *o = (E *)a.o + (r * s.Hv + h) * s.V + v;
-        const bool writes = tid < 16 && own;
+        const bool writes = tid < STEP_LANES && own;
         if (t >= len) {  // padding: the same for the whole block
             if (writes)
 #pragma unroll
@@ -1645,10 +1650,12 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = to_f(((const E *)a.v)[r * s.ldv + (long long)h * s.V + v + i]);
         const float gt = a.g[r * s.Hv + h], be = a.beta[r * s.Hv + h];
-        if (tid < 128)
-            qs[tid] = tid < s.K ? to_f(((const E *)a.q)[r * s.ldq + (long long)hk * s.K + tid]) : 0.f;
-        else
-            ks[tid - 128] = tid - 128 < s.K ? to_f(((const E *)a.k)[r * s.ldk + (long long)hk * s.K + tid - 128]) : 0.f;
+        for (int i = tid; i < 256; i += STEP_THREADS) {
+            const bool isq = i < 128;
+            const int j = i & 127;
+            const E *w = isq ? (const E *)a.q + r * s.ldq : (const E *)a.k + r * s.ldk;
+            (isq ? qs : ks)[j] = j < s.K ? to_f(w[(long long)hk * s.K + j]) : 0.f;
+        }
         const float dec = expf(gt);
         __syncthreads();
 #pragma unroll
