@@ -596,9 +596,6 @@ template <class E, int KD> struct Seq {
     static constexpr int stages = 2 * (stage + GATES) + extra <= 232448 ? 2 : 1;
     static constexpr size_t smem = (size_t)stages * (stage + GATES) + extra;
     static constexpr int TB = Terms<E>::n;
-    // terms and orders of what only an output of type E sees: two terms leave
-    // 2^-17 of the product, far below a 16-bit output's rounding
-    static constexpr int NO = sizeof(E) == 2 ? 2 : NT;
 };
 
 // Few heads and many chunks: the chunks are split into segments.  A head's
@@ -883,8 +880,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
                                              tc::idesc_bf16_f32(128, 64, 0, 0));
             tc::mma_commit(&bar->m1);
             if (!SCAN)
-                products_ts<KD / 16, Q::NO, TB, Q::NO>(tmem + COL_D + 64, tmem + COL_S, KD / 2, k_major(qk, 0), rows,
-                                                       tc::idesc_bf16_f32(128, 64, 0, 0));
+                products_ts<KD / 16, NT, TB, NT>(tmem + COL_D + 64, tmem + COL_S, KD / 2, k_major(qk, 0), rows,
+                                                 tc::idesc_bf16_f32(128, 64, 0, 0));
         }
         __syncwarp();
         if (!SCAN && n > 0) add_pu(ph ^ 1, 0x616);
@@ -934,10 +931,10 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
                 o[i] *= s.scale * u[i];
                 f[i] *= be[i];  // U
             }
-            put_terms<8, Q::NO>(L.lanes + COL_R + L.wg * 8, 32, f);
+            put_terms<8, NT>(L.lanes + COL_R + L.wg * 8, 32, f);
             if (hand_over(warp)) {  // P U
-                products_ts<4, Q::NO, Q::NO, Q::NO>(tmem + COL_X, tmem + COL_R, 32, k_major(tp + NT * TILE, 0), mat,
-                                                    tc::idesc_bf16_f32(128, 64, 0, 0));
+                products_ts<4, NT, NT, NT>(tmem + COL_X, tmem + COL_R, 32, k_major(tp + NT * TILE, 0), mat,
+                                           tc::idesc_bf16_f32(128, 64, 0, 0));
                 tc::mma_commit(&bar->m3);
             }
             __syncwarp();

@@ -396,3 +396,20 @@ def test_gradient_in_place_and_optional_outputs():
             assert torch.equal(getattr(g, n), getattr(want, n))
         assert torch.equal(d, want.ds0 if ds else dsT)
     assert L.lstm_status(ws) == L.LSTM_OK
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,K,V", [(64, 64, 72), (128, 128, 136), (50, 64, 8)])
+def test_outputs_where_large_parts_cancel(T, K, V, dt):
+    """A large state overwritten token by token: o_t = v_t is the sum of q S0 and P U, each thousands of times as large.
+
+    Keys and queries are unit vectors, so that every product has one term: besides the rounding to the output's type
+    only v - S0, the sum and what an accumulator's alignment drops are rounded, 8 steps of 2^-24 of the parts at most."""
+    gen = torch.Generator(device="cuda").manual_seed(T + V)
+    k = torch.eye(K, device="cuda")[:T].to(DT[dt]).view(T, 1, 1, K)
+    v = torch.randn(T, 1, 1, V, generator=gen, device="cuda").to(DT[dt])
+    s0 = 1e4 * torch.randn(1, 1, K, V, generator=gen, device="cuda")
+    st = L.gdr_forward(k, k, v, torch.zeros(T, 1, 1, device="cuda"), torch.ones(T, 1, 1, device="cuda"), s0, scale=1.0, save=True)
+    err = (st.o.double() - v.double()).abs()[:, 0, 0]
+    parts = s0[0, 0, :T].double().abs() + v.double().abs()[:, 0, 0]
+    assert bool((err <= torch.finfo(DT[dt]).eps / 2 * v.double().abs()[:, 0, 0] + 8 * 2.0 ** -24 * parts).all()), float((err / parts).max())
