@@ -21,6 +21,7 @@
 // second time from L1 / L2).
 // The backward reads the logits and writes the gradient once.
 #include <climits>
+#include <cmath>
 
 #include "host.cuh"
 #include "tc_ptx.cuh"
@@ -119,13 +120,19 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     return r;
 }
 
-// A logit at or below kMask is a mask: raised to it on the way in (NaN stays),
-// so that nothing is infinite, and its exponential is zero beside any other
-// logit.  A row of masks alone is summed again as it stands.
-constexpr float kMask = -9007199254740992.f;  // -2^53: exact in bf16 too
-__device__ __forceinline__ float raised(float x) {
+// A thread takes the exponent c (x - m) as c x - round(c m), one fused operation, and
+// corrects its sums by the remainder of c m at the end.  The remainder is half a
+// unit of round(c m): at most half of one below 2^24, and at 2^31 the largest (64)
+// that keeps a sum of exponentials in a float's range.  So:
+// - logits at or below a.mask, the power of two with c |mask| in [2^30, 2^31), are
+//   raised to it on the way in (NaN stays) and given no weight;
+// - a part whose largest logit is a mask or has c |m| above kExact is summed again
+//   as it stands, from c (x - m).  (In any other part the raised ones lie 2^29 and
+//   more below it, their exponentials are zero.)
+constexpr float kExact = 16777216.f;  // 2^24
+__device__ __forceinline__ float raised(float x, float mask) {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(kMask));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(mask));
     return y;
 }
 
@@ -135,14 +142,14 @@ __device__ __forceinline__ float raised(float x) {
 template <class T> struct Pairs {
     static constexpr int n = 4;
     typedef typename Elem<T>::E2 E2;
-    __device__ static __forceinline__ float largest(uint4 &v) {
+    __device__ static __forceinline__ float largest(uint4 &v, float mask) {
         E2 *h = reinterpret_cast<E2 *>(&v);
         const float2 m = Elem<T>::to_f2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
         return fmaxf(m.x, m.y);
     }
-    __device__ static __forceinline__ F2 pair(const uint4 &v, int i) {
+    __device__ static __forceinline__ F2 pair(const uint4 &v, int i, float mask) {
         const float2 f = Elem<T>::to_f2(reinterpret_cast<const E2 *>(&v)[i]);
-        return F2{raised(f.x), raised(f.y)};
+        return F2{raised(f.x, mask), raised(f.y, mask)};
     }
     // bit i: element i is at or above the bound (or NaN)
     __device__ static __forceinline__ unsigned candidates(const uint4 &v, float bound) {
@@ -158,13 +165,13 @@ template <class T> struct Pairs {
 };
 template <> struct Pairs<float> {
     static constexpr int n = 2;
-    __device__ static __forceinline__ float largest(uint4 &v) {
+    __device__ static __forceinline__ float largest(uint4 &v, float mask) {
         float *f = reinterpret_cast<float *>(&v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = raised(f[i]);
+        for (int i = 0; i < 4; ++i) f[i] = raised(f[i], mask);
         return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
     }
-    __device__ static __forceinline__ F2 pair(const uint4 &v, int i) {
+    __device__ static __forceinline__ F2 pair(const uint4 &v, int i, float mask) {
         const float *f = reinterpret_cast<const float *>(&v);
         return F2{f[2 * i], f[2 * i + 1]};
     }
@@ -188,11 +195,12 @@ template <class T> __device__ __forceinline__ uint4 masks() {
 // A thread's own sums, with the rounded c m in the place of c m, so that an
 // exponent is one fused multiply-add (half of a packed one).
 struct Run {
-    float m = kMask, cm = 1e30f;  // masks only so far: every exponential is zero
+    float mask, m, cm = 1e30f;  // masks only so far: every exponential is zero
     F2 s = {0.f, 0.f}, w = {0.f, 0.f};
+    __device__ __forceinline__ explicit Run(float mask) : mask(mask), m(mask) {}
     __device__ __forceinline__ void see(float gmax, float c) {  // the next elements' largest
         if (gmax > m) {
-            const float cn = gmax * c, d = m == kMask ? 0.f : cm - cn, e = ex2(d);
+            const float cn = gmax * c, d = m == mask ? 0.f : cm - cn, e = ex2(d);
             w.x = (w.x + s.x * d) * e;
             w.y = (w.y + s.y * d) * e;
             s.x *= e;
@@ -213,7 +221,7 @@ struct Run {
         w.x = fmaf(e, d, w.x);
     }
     __device__ __forceinline__ Stat stat(float c) const {
-        if (m == kMask) return Stat{-INFINITY, s.x + s.y, w.x + w.y};  // zeros, or NaN
+        if (m == mask) return Stat{-INFINITY, s.x + s.y, w.x + w.y};  // zeros, or NaN
         const float d = fmaf(-m, c, cm), e = ex2(d);  // what the rounding of c m left
         const float st = s.x + s.y;
         return Stat{m, st * e, (w.x + w.y + st * d) * e};
@@ -254,7 +262,7 @@ struct Args {
     const void *targets;
     int id64, N, vocab, top, parts;
     long long ld;
-    float inv_temp, c;  // c: times log2(e)
+    float inv_temp, c, mask;  // c: times log2(e)
     float *logp, *entropy, *stats, *top_logp;
     int *top_ids;
 };
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
     const int tid = threadIdx.x, lane = tid & 31;
     const int r = blockIdx.x / a.parts, p = blockIdx.x % a.parts;
     const T *row = (const T *)a.logits + (long long)r * a.ld;
-    const float c = a.c;
+    const float c = a.c, mask = a.mask;
     // part p is the elements [e0, e1); its 16-byte groups [g0, g1)
     const int e0 = (int)((long long)a.vocab * p / a.parts), e1 = (int)((long long)a.vocab * (p + 1) / a.parts);
     const int mis = (int)(((uintptr_t)(row + e0) & 15u) / sizeof(T));
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
     const uint4 *gp = (const uint4 *)(row + h);
     const int tail = h + groups * n;                  // [tail, e1): after the last one
     const int target = a.logp && p == 0 && tid == 0 ? target_of(a.targets, a.id64, r, a.vocab) : -1;
-    Run sum;
+    Run sum(mask);
     float bound = -INFINITY;
     if (TOP && tid == 0) count = 0;
 
@@ -405,14 +413,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
             float gm[U], top = -INFINITY;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                gm[u] = Pairs<T>::largest(v[u]);
+                gm[u] = Pairs<T>::largest(v[u], mask);
                 top = fmaxf(top, gm[u]);
             }
             sum.see(top, c);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < Pairs<T>::n; ++i) sum.add(Pairs<T>::pair(v[u], i), c);
+                for (int i = 0; i < Pairs<T>::n; ++i) sum.add(Pairs<T>::pair(v[u], i, mask), c);
             if (TOP && look && __any_sync(~0u, !(top < bound))) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -429,20 +437,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
     fetch(ahead, tid, TOP ? first : groups);
     // the elements outside whole groups: fewer than 2 n
     const int mine0 = e0 + tid < h ? e0 + tid : -1, mine1 = tail + tid < e1 ? tail + tid : -1;
-    if (mine0 >= 0) sum.add1(raised(to_f(row[mine0])), c);
-    if (mine1 >= 0) sum.add1(raised(to_f(row[mine1])), c);
+    if (mine0 >= 0) sum.add1(raised(to_f(row[mine0]), mask), c);
+    if (mine1 >= 0) sum.add1(raised(to_f(row[mine1]), mask), c);
     if (TOP) {
         run(0, first, false);
         fetch(ahead, first + tid, groups);  // under way while the bound is found
         bound = bound_of<THREADS>(sum.m, a.top, maxima, &bound_s);
-        if (bound == kMask) bound = -INFINITY;  // masks are among the alternatives
-        if (mine0 >= 0) push(mine0, !(raised(to_f(row[mine0])) < bound), row + mine0);
-        if (mine1 >= 0) push(mine1, !(raised(to_f(row[mine1])) < bound), row + mine1);
+        if (bound == mask) bound = -INFINITY;  // masks are among the alternatives
+        if (mine0 >= 0) push(mine0, !(raised(to_f(row[mine0]), mask) < bound), row + mine0);
+        if (mine1 >= 0) push(mine1, !(raised(to_f(row[mine1]), mask) < bound), row + mine1);
         __syncwarp();
 #pragma unroll 2
         for (int g = tid; g - lane < first; g += THREADS) {
             uint4 v = g < first ? __ldg(gp + g) : masks<T>();
-            const bool at = g < first && !(Pairs<T>::largest(v) < bound);
+            const bool at = g < first && !(Pairs<T>::largest(v, mask) < bound);
             if (__any_sync(~0u, at)) {
                 if (at) push(h + g * n, Pairs<T>::candidates(v, bound), (const T *)(gp + g));
                 __syncwarp();
@@ -452,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
     run(first, groups, TOP);
     const float chosen = target >= 0 ? to_f(row[target]) : 0.f;
     Stat st = block_join<THREADS>(sum.stat(c), c, warp_stats);  // its barrier also closes the candidate list
-    if (st.m == -INFINITY) {  // nothing but masks (or NaN): the part's plain sums
+    if (!(fabsf(st.m) * c <= kExact)) {  // masks (or NaN) alone, or large logits: the part's plain sums
         Stat own = {-INFINITY, 0.f, 0.f};
         for (int i = e0 + tid; i < e1; i += THREADS) own.m = fmaxf(own.m, to_f(row[i]));
         __syncthreads();
@@ -604,8 +612,7 @@ bool dims_supported(const lstm_logprob_dims *d) {
     return d->top <= LSTM_LOGPROB_MAX_TOP && d->vocab <= (1 << 30) && d->N <= (1 << 30);
 }
 
-// Within these limits a mask has an exponential of zero beside another logit,
-// and nothing overflows.
+// (Within these limits the mask value and c = inv_temp log2(e) are ordinary floats.)
 bool temp_ok(float inv_temp) { return inv_temp >= 1e-6f && inv_temp <= 1e6f; }
 
 template <class T, bool TOP, int THREADS> int launch_fwd(Args &a, cudaStream_t s) {
@@ -689,6 +696,9 @@ int lstm_logprob_fwd(const lstm_logprob_dims *d, const void *logits, const void 
     a.ld = d->ld;
     a.inv_temp = inv_temp;
     a.c = inv_temp * kLog2e;
+    int e;
+    (void)frexpf(a.c, &e);  // c in [2^(e-1), 2^e)
+    a.mask = -ldexpf(1.f, 31 - e);
     a.logp = logp;
     a.entropy = entropy;
     a.stats = stats;

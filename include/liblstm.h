@@ -480,8 +480,8 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
  *                         LSTM_LOGPROB_MAX_TOP, at most vocab) largest logits,
  *                         equal ones by lower id, and their log p; NULL at 0
  * targets [N]: int or long long by id_bytes, or NULL.  Logits of -inf are
- * masked: their p is 0 and counts as 0 in the entropy; so is, beside any
- * larger logit, one of -2^53 or less.  A row of nothing but -inf has logp and
+ * masked: their p is 0 and counts as 0 in the entropy.  (Finite masks, whatever
+ * their size, are logits like any other.)  A row of nothing but -inf has logp and
  * top_logp -inf, entropy 0 and a zero gradient.  A NaN or +inf makes its row's
  * values NaN (NaN is listed after every number).
  *

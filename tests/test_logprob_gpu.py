@@ -277,3 +277,64 @@ def test_rows_from_anywhere(dt):
     cols = x[:, 3:900]
     st = L.logprobs(cols, top=2)
     assert torch.equal(st.top_ids, L.logprobs(cols.contiguous(), top=2).top_ids)
+
+
+def check_large(x, t, top, temperature):
+    """check() where log p may be large: it takes four roundings of its size more (x - m, 1 / temperature, their product,
+    the sum), the logarithm of the sum one of the largest z; beyond a float's range it is infinite."""
+    N = len(x)
+    st = L.logprobs(x, t, top=top, temperature=temperature)
+    lp, p, h, tl, ok = reference(x, t, temperature)
+
+    def near(got, want):
+        fits = torch.isfinite(want.float())
+        assert torch.equal(torch.isfinite(got), fits) and bool((got[~fits] == want.float()[~fits]).all())
+        assert bool(((got.double() - want).abs()[fits] <= ABS + 2.0 ** -22 * want.abs()[fits]).all())
+
+    near(st.logp, tl)
+    assert bool(((st.entropy.double() - h).abs() <= ABS * (1 + h)).all())
+    z = x.double() / temperature
+    big = z.abs().amax(1) > 1e38
+    assert bool(((st.lse.double() - torch.logsumexp(z, 1)).abs()[~big] <= ABS + 2.0 ** -22 * z.abs().amax(1)[~big]).all())
+    if top:
+        order = torch.argsort(-x.double(), dim=1, stable=True)[:, :top]
+        assert torch.equal(st.top_ids.long(), order)
+        near(st.top_logp, lp.gather(1, order))
+    dlogp, dh = (temperature * torch.randn(N, device="cuda") for _ in range(2))
+    d = L.logprobs_backward(st, x, t, dlogp=dlogp, dentropy=dh, temperature=temperature)
+    want = reference_grad(lp, p, h, t, ok, dlogp, dh, temperature)
+    mag = (dlogp.double().abs()[:, None] * (p + (want != 0)) + dh.double().abs()[:, None] * p * (lp.abs().clamp(max=1e30) + h[:, None] + 1)) / temperature
+    assert bool(((d.double() - want).abs() <= 2 * ABS * mag + torch.finfo(d.dtype).eps / 2 * want.abs() + 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("temperature", [1.0, 0.3, 0.1])
+@pytest.mark.parametrize("value", [-1e5, -3e7, -1e9, -1e10, -1e12, -1e15, -3e38])
+def test_masks_of_any_value(value, temperature, dt):
+    """Finite masks from small ones to the lowest: a range, scattered, all but one, all; rows in one block and shared."""
+    for N, V, top in ((6, 3001, 3), (6, 3001, 0), (6, 70001, 4), (6, 70001, 20), (300, 3001, 0), (300, 3001, 5)):
+        g = torch.Generator(device="cuda").manual_seed(N + V + top)
+        x = (3 * torch.randn(N, V, generator=g, device="cuda")).to(DT[dt])
+        x[0, : V * 3 // 4] = value
+        x[1, ::2] = value
+        x[2, :] = value
+        x[2, V // 3] = 2.5
+        x[3, :] = value
+        x[4, 100:] = value
+        check_large(x, torch.tensor([V - 3, 0, V // 3, 5, 200, 7], device="cuda").repeat(N // 6 + 1)[:N], top, temperature)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dt,size,temperature", [("fp32", 1e7, 1.0), ("fp32", 2e9, 1.0), ("fp32", 3e12, 1.0), ("fp32", 1e17, 0.5),
+                                                 ("bf16", 1e10, 1.0), ("bf16", 3e38, 1.0), ("fp16", 3000.0, 1e-5),
+                                                 ("fp16", 60000.0, 1e-6), ("fp32", 700.0, 1e-6), ("fp32", 1e30, 1e-6),
+                                                 ("fp32", 1e12, 1e6), ("fp32", 3e38, 1e6)])
+def test_large_logits(dt, size, temperature, sign):
+    """Rows of large logits, a few steps of their type or a factor of two apart, or all equal."""
+    for N, V, top in ((4, 2050, 3), (4, 70001, 0), (4, 70001, 17), (300, 2050, 0)):
+        g = torch.Generator(device="cuda").manual_seed(V + top)
+        steps = 1 + torch.randint(0, 4, (N, V), generator=g, device="cuda") * torch.finfo(DT[dt]).eps
+        spread = 0.5 + 0.5 * torch.rand(N, V, generator=g, device="cuda")
+        x = (sign * size * 0.9 * torch.where(torch.arange(N, device="cuda")[:, None] % 2 == 0, steps, spread)).to(DT[dt])
+        x[3] = x[3, 0]
+        check_large(x, torch.randint(0, V, (N,), generator=g, device="cuda"), top, temperature)
