@@ -50,10 +50,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// max(x, -1e28) that keeps NaN: -inf - m stays usable as a factor of zero.
-__device__ __forceinline__ float floor_nan(float x) {
+// max(x, least) that keeps NaN: -inf - m stays usable as a factor of zero.
+__device__ __forceinline__ float floor_nan(float x, float least = -1e28f) {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-1e28f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(least));
     return y;
 }
 // Elements of one 16-byte group.
@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_kernel(BwdArgs a) {
     const bool empty = m == -INFINITY && ls == ls;
     // dl 1[target] - p (dl + dh (log p + entropy)), dl and dh over the temperature
     auto grad = [&](float v, int i) {
-        const float lp = floor_nan((v - m) * c - ls);  // log2 p
+        // log2 p, from -256 up (2^-127 and less is zero already): a finite factor of zero
+        const float lp = floor_nan((v - m) * c - ls, -256.f);
         float g = -ex2(lp) * fmaf(dhc, lp + ent, dl);
         if (i == t) g += dl;
         return empty ? 0.f : g;

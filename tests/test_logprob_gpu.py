@@ -338,3 +338,16 @@ def test_large_logits(dt, size, temperature, sign):
         x = (sign * size * 0.9 * torch.where(torch.arange(N, device="cuda")[:, None] % 2 == 0, steps, spread)).to(DT[dt])
         x[3] = x[3, 0]
         check_large(x, torch.randint(0, V, (N,), generator=g, device="cuda"), top, temperature)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_masked_logits_under_a_large_entropy_gradient(dt):
+    """p = 0 has no gradient, however large that of the entropy (a scaled loss, a low temperature)."""
+    x = torch.randn(3, 700, device="cuda").to(DT[dt])
+    x[:, 5:300] = float("-inf")
+    x[1, 400:] = torch.finfo(DT[dt]).min
+    dh = torch.tensor([65536.0, 1e12, -3e14], device="cuda")
+    for temperature in (1.0, 1e-6):
+        st = L.logprobs(x, temperature=temperature)
+        d = L.logprobs_backward(st, x, dentropy=dh, temperature=temperature)
+        assert not d[:, 5:300].any() and not torch.isnan(d).any()
