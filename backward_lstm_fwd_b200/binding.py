@@ -778,8 +778,9 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
 
 def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=None,
                       temperature: float = 1.0, out=None, stream=None) -> torch.Tensor:
-    """lstm_logprob_bwd: the gradient [N, vocab] of the logits, in their type
-    and (unless `out` is given) with their row stride; out may be logits."""
+    """lstm_logprob_bwd: the gradient [N, vocab] of the logits, in their type; out
+    may be logits.  Without `out` it has their row stride where that is the
+    vocabulary and some padding (rows cut from a wider tensor lie close)."""
     ld = _rows(logits, "logits")
     N, vocab = logits.shape
     _flat(logits, targets=targets, dlogp=dlogp, dentropy=dentropy, state=st.entropy)
@@ -797,8 +798,10 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     if out is not None:
         ldd = _rows(out, "out")
     else:
-        out = logits.new_empty(N, ld)
-        if ld != vocab:
+        if ld - vocab > max(64, vocab // 8):  # closer, with rows that still start alike modulo 16 bytes
+            ldd = vocab + (ld - vocab) % (16 // logits.element_size())
+        out = logits.new_empty(N, ldd)
+        if ldd != vocab:
             out = out[:, :vocab]
     d = LogprobDims(N, vocab, ld, 0, dtype_code(logits.dtype), _id_bytes(targets))
     _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,

@@ -351,3 +351,24 @@ def test_masked_logits_under_a_large_entropy_gradient(dt):
         st = L.logprobs(x, temperature=temperature)
         d = L.logprobs_backward(st, x, dentropy=dh, temperature=temperature)
         assert not d[:, 5:300].any() and not torch.isnan(d).any()
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("V", [1000, 1001])
+def test_gradient_of_rows_far_apart(V, dt):
+    """The last step's logits of a [B, T, V] tensor, one sequence of a [T, B, V] one: the gradient holds no more than itself."""
+    wide = torch.randn(6, 50, V, device="cuda").to(DT[dt])
+    t = torch.randint(0, V, (6,), device="cuda")
+    dl = torch.randn(6, device="cuda")
+    for x in (wide[:, -1], wide[:, 0], wide[1:6, 7]):
+        n = len(x)
+        st = L.logprobs(x, t[:n])
+        d = L.logprobs_backward(st, x, t[:n], dlogp=dl[:n])
+        assert d.untyped_storage().nbytes() <= n * (V + 8) * d.element_size()
+        out = torch.empty_like(d).contiguous()
+        L.logprobs_backward(st, x, t[:n], dlogp=dl[:n], out=out)
+        assert torch.equal(d, out)
+    padded = wide.view(6, -1)[:, : V - 60]  # (of rows far apart too)
+    assert L.logprobs_backward(L.logprobs(padded), padded).stride(0) < V
+    near = wide.view(300, V)[:, : V - 60]  # a padded vocabulary keeps its stride
+    assert L.logprobs_backward(L.logprobs(near), near).stride() == near.stride()
