@@ -837,10 +837,10 @@ class GdrState:
     """Outputs of one gdr_forward() call; states, deltas and ws (save=True; ws
     only where the call allocated it) are kept for the backward."""
 
-    def __init__(self, d: GdrDims, q, save, sT=None):
+    def __init__(self, d: GdrDims, q, save, sT=None, scale=None, lengths=None):
         f = torch.float32
         T, B, H, K, V = d.T, d.B, d.Hv, d.K, d.V
-        self.dims = d
+        self.dims, self.scale, self.lengths = d, scale, lengths
         self.o = q.new_empty(T, B, H, V)
         self.sT = q.new_empty(B, H, K, V, dtype=f) if sT is None else sT
         self.states = self.deltas = self.ws = None
@@ -911,7 +911,7 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     if _elsewhere(q, stream):
         with _there(q, stream):
             return gdr_forward(q, k, v, g, beta, s0, lengths, scale, save, sT, ws)
-    st = GdrState(d, q, save, sT)
+    st = GdrState(d, q, save, sT, opt.scale, lengths)
     if ws is None and (save or d.T > GDR_STEP_TOKENS):
         ws = _workspace(q, gdr_fwd_workspace_size(d, save))
         if save:
@@ -923,18 +923,31 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     return st
 
 
+def _same_lengths(kept, given, T: int) -> None:
+    """The backward's lengths (clamped to 0 .. T) are the forward's."""
+    if kept is not None and given is not None and kept.data_ptr() != given.data_ptr():
+        _need(not torch.cuda.is_current_stream_capturing(),
+              "a backward inside a graph takes the forward's own lengths tensor")
+        _need(torch.equal(kept.clamp(0, T), given.clamp(0, T)), "lengths differ from the forward's")
+    _need((kept is None) == (given is None), "lengths differ from the forward's")
+
+
 def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=None, scale=None,
                  ws=None, stream=None) -> GdrGrads:
     """lstm_gdr_bwd on the saved state of gdr_forward(..., save=True), with
-    the forward's arguments: dout [T,B,Hv,V] (compute dtype), dsT float32."""
+    the forward's arguments: dout [T,B,Hv,V] (compute dtype), dsT float32.
+    (lengths in another tensor than the forward's are compared with those on
+    the host, which waits for the device and is refused inside a graph.)"""
     _need(st.states is not None, "the forward kept nothing: call gdr_forward(..., save=True)")
     d, opt = _gdr_call(q, k, v, g, beta, lengths, scale, dout=dout, dsT=dsT, ws=ws, states=st.states)
     _shaped(dout, "dout", (d.T, d.B, d.Hv, d.V), q.dtype)
     _shaped(dsT, "dsT", (d.B, d.Hv, d.K, d.V), torch.float32)
     _need(_sizes_of(d) == _sizes_of(st.dims), "the state belongs to a forward of other sizes")
+    _need(opt.scale == st.scale, f"scale {opt.scale} differs from the forward's {st.scale}")
     if _elsewhere(q, stream):
         with _there(q, stream):
             return gdr_backward(st, q, k, v, g, beta, dout, dsT, lengths, scale, ws)
+    _same_lengths(st.lengths, lengths, d.T)
     gr = GdrGrads(d, q.dtype, q.device)
     if ws is None:
         ws = _workspace(q, gdr_bwd_workspace_size(d))

@@ -413,3 +413,38 @@ def test_outputs_where_large_parts_cancel(T, K, V, dt):
     err = (st.o.double() - v.double()).abs()[:, 0, 0]
     parts = s0[0, 0, :T].double().abs() + v.double().abs()[:, 0, 0]
     assert bool((err <= torch.finfo(DT[dt]).eps / 2 * v.double().abs()[:, 0, 0] + 8 * 2.0 ** -24 * parts).all()), float((err / parts).max())
+
+
+def test_options_of_another_forward():
+    """A backward whose scale or lengths are not its forward's would mix two problems (P and the gates are the forward's)."""
+    x, dout, dsT = make(100, 3, 1, 2, 64, 64, "bf16")
+    five = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    lengths = torch.tensor([100, 7, 64], dtype=torch.int32, device="cuda")
+    kw = dict(dout=dout, dsT=dsT)
+    for st in (L.gdr_forward(**x, save=True, scale=0.5, lengths=lengths),
+               L.gdr_forward(**x, save=True, scale=0.5, lengths=lengths, ws=L.empty_workspace(L.gdr_fwd_workspace_size(L.gdr_dims(100, 3, 1, 2, 64, 64, torch.bfloat16), True), "cuda"))):
+        want = L.gdr_backward(st, *five, **kw, scale=0.5, lengths=lengths)
+        for scale in (None, 0.25, 0.5001):
+            with pytest.raises(ValueError, match="scale"):
+                L.gdr_backward(st, *five, **kw, scale=scale, lengths=lengths)
+        for other in (None, lengths.flip(0), lengths + 1):
+            with pytest.raises(ValueError, match="lengths"):
+                L.gdr_backward(st, *five, **kw, scale=0.5, lengths=other)
+        copy = L.gdr_backward(st, *five, **kw, scale=0.5, lengths=lengths.clone())  # the same lengths in another tensor
+        assert torch.equal(copy.dk, want.dk) and torch.equal(copy.dg, want.dg)
+    st = L.gdr_forward(**x, save=True)
+    assert torch.equal(L.gdr_backward(st, *five, **kw, scale=64 ** -0.5).dq, L.gdr_backward(st, *five, **kw).dq)
+    with pytest.raises(ValueError, match="lengths"):
+        L.gdr_backward(st, *five, **kw, lengths=lengths)
+    graph = torch.cuda.CUDAGraph()
+    copy = lengths.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        st = L.gdr_forward(**x, save=True, lengths=lengths)
+        gr = L.gdr_backward(st, *five, **kw, lengths=lengths)
+        with pytest.raises(ValueError, match="own lengths"):
+            L.gdr_backward(st, *five, **kw, lengths=copy)
+    graph.replay()
+    torch.cuda.synchronize()
+    st = L.gdr_forward(**x, save=True, lengths=lengths)
+    assert torch.equal(gr.dk, L.gdr_backward(st, *five, **kw, lengths=lengths).dk)
