@@ -367,8 +367,8 @@ int lstm_fwd_noalloc_status(void *stream);
  * long (8).  An id outside 0 .. vocab-1 is padding: a row of zeros, no
  * gradient.  Forward: table [vocab][I] and x [N][I] are of type dtype; the
  * product is rounded once.  Backward: dx [N][I] is of type dtype (LSTM_F32
- * for lstm_bwd's dx), sums are float in the order of r (the same bits every
- * time); dtable [vocab][I] float is overwritten (accumulate 0) or added to
+ * for lstm_bwd's dx), sums are float over up to 32 of a token's rows and double
+ * over those, in the order of r (the same bits every time); dtable [vocab][I] float is overwritten (accumulate 0) or added to
  * (1: rows without a token are neither read nor written).
  */
 typedef struct lstm_embed_dims {

@@ -191,3 +191,19 @@ def test_gradient_inside_a_buffer(n, at):
     got = L.embed_backward(ids, dx, vocab, out=table)
     check_grad(got, ids, dx, vocab, 1.0)
     assert bool((buf[:at] == 7.0).all()) and bool((buf[at + vocab * I:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("I", [1024, 259])
+def test_sums_of_a_frequent_token(I, dt):
+    """Rows whose sums over any 32 are exact in float: the gradient of a token of 130000 rows is its sum rounded once,
+    which chains of float partial sums (2^17 in the end, 2^-18 their digits) are not."""
+    n, bits = 131072, {"fp32": 18, "bf16": 7, "fp16": 10}[dt]  # 1 + 5 + 18 bits
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ids[::1000] = 1
+    gen = torch.Generator(device="cuda").manual_seed(I)
+    dx = (1 + torch.randint(0, 1 << bits, (n, I), generator=gen, device="cuda").double() / (1 << bits)).to(DT[dt])
+    want = torch.stack([dx.double()[ids == w].sum(0) for w in range(3)]).float()
+    assert torch.equal(L.embed_backward(ids, dx, 3), want)
+    base = torch.randn(3, I, generator=gen, device="cuda")
+    assert torch.equal(L.embed_backward(ids, dx, 3, scale=0.5, out=base.clone(), accumulate=True), base + 0.5 * want)
