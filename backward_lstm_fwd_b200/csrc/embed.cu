@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(256) lookup_kernel(const ID *ids, const uint4 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (g0 + 32 * u < groups) x[(long long)r * groups + g0 + 32 * u] = scaled<T>(v[u], scale);
+        if (g0 + 32 * u < groups)  // (padding: zeros, whatever the scale)
+            x[(long long)r * groups + g0 + 32 * u] = w >= 0 ? scaled<T>(v[u], scale) : v[u];
 }
 
 // Element path: any other rows.

@@ -207,3 +207,12 @@ def test_sums_of_a_frequent_token(I, dt):
     assert torch.equal(L.embed_backward(ids, dx, 3), want)
     base = torch.randn(3, I, generator=gen, device="cuda")
     assert torch.equal(L.embed_backward(ids, dx, 3, scale=0.5, out=base.clone(), accumulate=True), base + 0.5 * want)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,I", [(3, 8), (3, 7), (70000, 16)])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_padding_is_zero_at_any_scale(scale, N, I, dt):
+    ids = torch.tensor([-1, 2, 4], device="cuda").repeat(N // 3 + 1)[:N]
+    x = L.embed(ids, torch.ones(4, I, device="cuda", dtype=DT[dt]), scale)
+    assert not x[ids != 2].any() and not torch.isfinite(x[ids == 2]).any()
