@@ -208,6 +208,25 @@ __device__ __forceinline__ void products_ts(uint32_t d, uint32_t a, uint32_t a_t
             }
         }
 }
+// The sum of two such products, A in tensor memory.
+template <int steps, int ta, int tb, int orders>
+__device__ __forceinline__ void two_products_ts(uint32_t d, uint32_t a0, uint64_t b0, uint32_t a1, uint64_t b1,
+                                                uint32_t a_term, const Steps bs, uint32_t idesc) {
+    uint32_t acc = 0;
+#pragma unroll
+    for (int o = orders - 1; o >= 0; --o)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int t = 0; t < ta; ++t) {
+                if (t > o || o - t >= tb) continue;
+#pragma unroll
+                for (int ks = 0; ks < steps; ++ks) {
+                    tc::mma_bf16_ts(d, (p ? a1 : a0) + t * a_term + 8 * ks, (p ? b1 : b0) + at_step(bs, o - t, ks), idesc, acc);
+                    acc = 1;
+                }
+            }
+}
 template <int steps, int ta, int tb, int orders>
 __device__ __forceinline__ void products_ss(uint32_t d, uint64_t a, const Steps as, uint64_t b, const Steps bs,
                                             uint32_t idesc, uint32_t acc = 0) {
@@ -1062,10 +1081,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         put_terms<8, NT>(L.lanes + COL_W + L.wg * 8, 32, e);
         if (Q::stages == 2 && more) put_do();
         if (hand_over(warp)) {  // D = scale Q^T gamma dO - K^T gamma dV
-            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_S, 32, mn_major(qk, 0, 2 * TILE), cols,
-                                       tc::idesc_bf16_f32(128, KD, 0, 1));
-            products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_W, 32, mn_major(qk + TILE, 0, 2 * TILE), cols,
-                                       tc::idesc_bf16_f32(128, KD, 0, 1), 1);
+            two_products_ts<4, NT, TB, NT>(tmem + COL_D, tmem + COL_S, mn_major(qk, 0, 2 * TILE), tmem + COL_W,
+                                           mn_major(qk + TILE, 0, 2 * TILE), 32, cols, tc::idesc_bf16_f32(128, KD, 0, 1));
             tc::mma_commit(&bar->m4);
             if (Q::stages == 2 && more) {
                 tc::mbar_wait(&bar->full[st ^ 1], ((n + 1) / Q::stages) & 1, a.ctrl, ab, 0x626);

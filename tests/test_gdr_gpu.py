@@ -448,3 +448,20 @@ def test_options_of_another_forward():
     torch.cuda.synchronize()
     st = L.gdr_forward(**x, save=True, lengths=lengths)
     assert torch.equal(gr.dk, L.gdr_backward(st, *five, **kw, lengths=lengths).dk)
+
+
+def off(got, want):
+    return float((got.double() - want.double()).norm() / want.double().norm())
+
+
+@pytest.mark.parametrize("shape", [(256, 2, 1, 2, 128, 128), (512, 1, 2, 2, 64, 64), (600, 1, 1, 1, 96, 72)], ids=str)
+def test_state_gradient_as_close_as_a_float_sum(shape):
+    """ds0 in norm.  A tensor core's accumulator drops what lies below its last place, half a unit (2^-24) on average, at
+    every step that meets the full sum: the 8 steps of the two large products, if every small one comes before them."""
+    x, dout, dsT = make(*shape, "fp32")
+    d = {n: t.double().requires_grad_() for n, t in x.items()}
+    o, S = reference(**d, lengths=None, scale=shape[4] ** -0.5)
+    want, = torch.autograd.grad((o * dout.double()).sum() + (S * dsT.double()).sum(), [d["s0"]])
+    st = L.gdr_forward(**x, save=True)
+    gr = L.gdr_backward(st, *(x[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT)
+    assert off(gr.ds0, want) <= 8 * 2.0 ** -24
