@@ -465,3 +465,40 @@ def test_state_gradient_as_close_as_a_float_sum(shape):
     st = L.gdr_forward(**x, save=True)
     gr = L.gdr_backward(st, *(x[n] for n in ("q", "k", "v", "g", "beta")), dout=dout, dsT=dsT)
     assert off(gr.ds0, want) <= 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("shape,dt", [((2050, 1, 1, 1, 128, 128), "fp32"), ((1500, 2, 1, 2, 64, 40), "fp32"), ((900, 1, 1, 2, 96, 256), "fp32"),
+                                      ((3000, 1, 2, 2, 128, 136), "bf16"), ((1100, 3, 1, 1, 128, 72), "fp16")], ids=str)
+def test_segments_against_pieces(shape, dt):
+    """What passes from segment to segment where little is forgotten: a split call is the same sequence in pieces of three
+    chunks (too short to split), the state and its gradient handed on.
+
+    In norm.  A chunk's or a joint's sums lose 8 half units of a float (see above), the same share of the state in both
+    forms but for their order; over the 12 chunks of a segment at most 96 * 2^-24 < 2^-17.  A transition matrix short of
+    its second terms would be off by 2^-9."""
+    T = shape[0]
+    d, piece = (L.gdr_dims(t, *shape[1:], DT[dt]) for t in (T, 192))
+    assert L.gdr_fwd_workspace_size(d) - 256 > -(-T // 64) / 3 * (L.gdr_fwd_workspace_size(piece) - 256)  # it is split
+    x, dout, dsT = make(*shape, dt)
+    x["g"] *= 0.002
+    x["beta"] *= 0.1
+    names = ("q", "k", "v", "g", "beta")
+    one = L.gdr_forward(**x, save=True)
+    gone = L.gdr_backward(one, *(x[n] for n in names), dout=dout, dsT=dsT)
+    s0, parts = x["s0"], []
+    for t in range(0, T, 192):
+        y = [x[n][t:t + 192] for n in names]
+        parts.append((L.gdr_forward(*y, s0=s0, save=True), y, dout[t:t + 192]))
+        s0 = parts[-1][0].sT
+    ds, grads = dsT, []
+    for st, y, do in reversed(parts):
+        grads.insert(0, L.gdr_backward(st, *y, dout=do, dsT=ds))
+        ds = grads[0].ds0
+    assert off(one.sT, s0) <= 2.0 ** -17 and off(gone.ds0, ds) <= 2.0 ** -17
+    assert off(one.states[len(one.states) - 1], parts[-1][0].states[-1]) <= 2.0 ** -17
+    half = torch.finfo(DT[dt]).eps / 2 if dt != "fp32" else 0  # (two roundings to the type may differ by a step)
+    assert off(one.o, torch.cat([st.o for st, _, _ in parts])) <= 2.0 ** -17 + half
+    for n in ("dq", "dk", "dv"):
+        assert off(getattr(gone, n), torch.cat([getattr(g, n) for g in grads])) <= 2.0 ** -16 + half
+    for n in ("dg", "dbeta"):
+        assert off(getattr(gone, n), torch.cat([getattr(g, n) for g in grads])) <= 2.0 ** -16
