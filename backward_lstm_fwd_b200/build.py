@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -41,11 +42,23 @@ def _stale(out: str) -> bool:
     return any(os.path.getmtime(s) > t for s in _sources() + [__file__])
 
 
+def _sweep(*dirs: str) -> None:
+    """Remove what builds that were killed have left (their process is gone)."""
+    for path in (f for d in dirs for f in glob.glob(os.path.join(d, "*.tmp[0-9]*"))):
+        try:
+            os.kill(int(re.search(r"\.tmp(\d+)", path).group(1)), 0)
+        except ProcessLookupError:
+            os.remove(path)
+        except PermissionError:  # someone else's, and alive
+            pass
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale(LIB_PATH):
         return LIB_PATH
     obj_dir = os.path.join(PKG, "_build")
     os.makedirs(obj_dir, exist_ok=True)
+    _sweep(obj_dir, PKG)
     flags = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2,-Wall",
              "-I", os.path.join(ROOT, "include")]
     if verbose:
@@ -60,14 +73,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
             continue
         tmp = obj + f".tmp{os.getpid()}.o"
         jobs.append((subprocess.Popen([*flags, "-c", "-o", tmp, src]), tmp, obj, src))
-    failed = [src for p, _, _, src in jobs if p.wait() != 0]
-    if failed:
-        raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
-    for _, tmp, obj, _ in jobs:
-        os.replace(tmp, obj)
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    subprocess.run([*flags, "-shared", "-o", tmp, *objs], check=True)
-    os.replace(tmp, LIB_PATH)
+    lib_tmp = LIB_PATH + f".tmp{os.getpid()}"
+    try:
+        failed = [src for p, _, _, src in jobs if p.wait() != 0]
+        if failed:
+            raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
+        for _, tmp, obj, _ in jobs:
+            os.replace(tmp, obj)
+        subprocess.run([*flags, "-shared", "-o", lib_tmp, *objs], check=True)
+        os.replace(lib_tmp, LIB_PATH)
+    finally:  # of a failed or interrupted build nothing goes on or stays
+        for p, _, _, _ in jobs:
+            if p.poll() is None:
+                p.terminate()
+                p.wait()
+        for tmp in [lib_tmp, *(tmp for _, tmp, _, _ in jobs)]:
+            if os.path.exists(tmp):
+                os.remove(tmp)
     return LIB_PATH
 
 
