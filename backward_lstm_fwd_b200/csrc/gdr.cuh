@@ -645,9 +645,10 @@ struct SeqBars {
     int abort_flag;
 };
 
-// What a block of the sequential kernels works on.
+// What a block of the sequential kernels works on.  Only chunks with tokens in
+// them (c < live) are walked: padding leaves the state as it is, whatever it holds.
 template <bool SCAN> struct Job {
-    int vt, h, b, seg, first, chunks;
+    int vt, h, b, seg, first, chunks, live;
     bool identity;  // SCAN: the state columns are those of the identity
     __device__ __forceinline__ explicit Job(const SeqArgs &a) {
         const Shape &s = a.s;
@@ -661,6 +662,7 @@ template <bool SCAN> struct Job {
         seg = id / s.B;
         first = seg * a.seg;
         chunks = min(a.seg, s.NC - first);
+        live = (length_of(s, b) + C - 1) / C;
         identity = SCAN && vt == s.VT;
         if (identity) vt = 0;
     }
@@ -835,6 +837,14 @@ template <int KD> struct Lane {
         }
         __syncwarp();
     }
+    // the rows of chunk c's padding are zero
+    template <class T> __device__ __forceinline__ void clear_padding(const Shape &s, T *p, int c) const {
+        const int t0 = c * C + wg * 16;
+        p += head * s.V + v + t0 * row;
+#pragma unroll 1
+        for (int i = max(0, len - t0); i < tokens(t0, s.T) && i < 16; ++i) p[i * row] = from_f<T>(0.f);
+        __syncwarp();
+    }
     // how many of the 16 tokens from t0 on are below `end`, for a lane that has a column
     __device__ __forceinline__ int tokens(int t0, int end) const { return own ? end - t0 : 0; }
 };
@@ -850,6 +860,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     const int tid = threadIdx.x, warp = warp_id();
     const Job<SCAN> J(a);
     if (J.identity && J.seg == 0) return;  // the first segment starts from s0: its A is not needed
+    const int chunks = max(0, min(J.chunks, J.live - J.first));
     seq_setup(bar);
     const uint32_t tmem = bar->tmem_slot;
     const Lane<KD> L(s, tmem, J.b, J.h, J.vt, J.identity);
@@ -858,16 +869,16 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};       // MN-major k: K over the tokens
     constexpr Steps mat = {TILE >> 4, 2, 0};                           // K-major T2, P
     if (s.NC == 0) clear_ctrl(a.ctrl);  // (else prep did)
-    if (tid == 32 && J.chunks > 0) {
+    if (tid == 32 && chunks > 0) {
         seq_load<E, KD>(a, smem, bar, J.b, J.h, 0, J.first, false);
-        if (Q::stages == 2 && J.chunks > 1) seq_load<E, KD>(a, smem, bar, J.b, J.h, 1, J.first, false);
+        if (Q::stages == 2 && chunks > 1) seq_load<E, KD>(a, smem, bar, J.b, J.h, 1, J.first, false);
     }
     __syncwarp();
     const long long KV = (long long)s.K * s.V, all = (long long)s.B * s.Hv * KV;  // a state; the states of all heads
     float S[H4], o[16];
     Col16<E> vr;
     if (J.identity) L.unit(s, S);
-    else L.load(s, J.seg == 0 ? (a.s0 ? a.s0 + L.head * KV : nullptr)
+    else L.load(s, J.seg == 0 || (!SCAN && J.live == 0) ? (a.s0 ? a.s0 + L.head * KV : nullptr)  // (no token: of every segment)
                               : (SCAN ? nullptr : a.starts + (J.seg - 1) * all + L.head * KV), S);
     const E *vp = (const E *)a.v + (long long)J.b * s.ldv + (long long)J.h * s.V + L.v;
     auto load_v = [&](int c) {
@@ -876,7 +887,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     };
     auto store_o = [&](int c) {
         const int t0 = c * C + L.wg * 16;
-        store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), o);
+        store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, L.len), o);
     };
     auto add_pu = [&](uint32_t ph, uint32_t site) {
         wait(&bar->m3, ph, a.ctrl, ab, site);
@@ -887,7 +898,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
     };
     load_v(J.first);
 #pragma unroll 1
-    for (int n = 0; n < J.chunks; ++n) {
+    for (int n = 0; n < chunks; ++n) {
         const int c = J.first + n, st = n % Q::stages, t0 = c * C + L.wg * 16;
         const uint32_t ph = n & 1;
         const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
@@ -905,7 +916,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         __syncwarp();
         if (!SCAN && n > 0) add_pu(ph ^ 1, 0x616);
         // (the products of chunk n - 1, whose stage this is, are complete)
-        if (Q::stages == 2 && tid == 32 && n > 0 && n + 1 < J.chunks)
+        if (Q::stages == 2 && tid == 32 && n > 0 && n + 1 < chunks)
             seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, false);
         __syncwarp();
         // (the state's rows go out a part in each product's shadow)
@@ -926,7 +937,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
             tc::mma_commit(&bar->m2);
         }
         __syncwarp();
-        if (n + 1 < J.chunks) load_v(c + 1);
+        if (n + 1 < chunks) load_v(c + 1);
         if (kept) L.template store_part<1, 3>(s, kept, S);
         load16(gates + C, u);
         load16(gates + 2 * C, be);
@@ -943,7 +954,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         }
         __syncwarp();
         if (!SCAN) {
-            if (a.deltas) store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+            if (a.deltas) store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, L.len), f);
             load16(gates, u);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -968,18 +979,26 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_fwd_kernel(const __grid_co
         }
         if (Q::stages == 1) {
             if (!SCAN) wait(&bar->m3, ph, a.ctrl, ab, 0x617);
-            if (tid == 32 && n + 1 < J.chunks) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, false);
+            if (tid == 32 && n + 1 < chunks) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, false);
             __syncwarp();
         }
     }
-    if (!SCAN && J.chunks > 0) {
-        add_pu((J.chunks - 1) & 1, 0x618);
-        store_o(J.first + J.chunks - 1);
+    if (!SCAN && chunks > 0) {
+        add_pu((chunks - 1) & 1, 0x618);
+        store_o(J.first + chunks - 1);
+    }
+    if (!SCAN) {
+#pragma unroll 1
+        for (int c = J.first + max(0, chunks - 1); c < J.first + J.chunks; ++c) {
+            L.clear_padding(s, (E *)a.o, c);
+            if (a.deltas) L.clear_padding(s, a.deltas, c);
+            if (a.states && c >= J.live) L.store(s, a.states + c * all + L.head * KV, S);
+        }
     }
     if (J.identity) L.store_trans(a.trans + ((J.seg * s.B + J.b) * (long long)s.Hv + J.h) * (NT * KD * KD * 2), S);
     else if (SCAN) L.store(s, a.starts + J.seg * all + L.head * KV, S);
     else if (J.seg == a.segments - 1) L.store(s, a.sT + L.head * KV, S);
-    if (tid == 32) seq_drain<E, KD>(bar, J.chunks);
+    if (tid == 32) seq_drain<E, KD>(bar, chunks);
     seq_finish(bar);
 }
 
@@ -997,6 +1016,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     const int tid = threadIdx.x, warp = warp_id();
     const Job<SCAN> J(a);
     if (J.identity && J.seg == 0) return;
+    // chunk n of the segment is NC - 1 - first - n: the first `skip` are padding
+    const int skip = max(0, min(J.chunks, s.NC - J.first - J.live)), first = J.first + skip, chunks = J.chunks - skip;
     seq_setup(bar);
     const uint32_t tmem = bar->tmem_slot;
     const Lane<KD> L(s, tmem, J.b, J.h, J.vt, J.identity);
@@ -1005,13 +1026,13 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
     constexpr Steps cols = {QK<E, KD>::term >> 4, 2048 >> 4, 0};
     constexpr Steps mat = {TILE >> 4, 2048 >> 4, 0};                   // MN-major T2, P: transposed
     if (s.NC == 0) clear_ctrl(a.ctrl);
-    if (tid == 32 && J.chunks > 0) seq_load<E, KD>(a, smem, bar, J.b, J.h, 0, J.first, true);
+    if (tid == 32 && chunks > 0) seq_load<E, KD>(a, smem, bar, J.b, J.h, 0, first, true);
     __syncwarp();
     const long long KV = (long long)s.K * s.V, all = (long long)s.B * s.Hv * KV;
     float S[H4];
     Col16<E> d;
     if (J.identity) L.unit(s, S);
-    else L.load(s, J.seg == 0 ? (a.s0 ? a.s0 + L.head * KV : nullptr)
+    else L.load(s, J.seg == 0 || (!SCAN && J.live == 0) ? (a.s0 ? a.s0 + L.head * KV : nullptr)  // (no token: of every segment)
                               : (SCAN ? nullptr : a.starts + (J.seg - 1) * all + L.head * KV), S);
     const E *dop = (const E *)a.v + L.head * s.V + L.v;
     auto load_do = [&](int c) {
@@ -1029,16 +1050,20 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         for (int i = 0; i < 16; ++i) x[i] = d[i];
         put_terms<8, TB>(L.lanes + COL_R + L.wg * 8, 32, x);
     };
-    if (J.chunks > 0) load_do(s.NC - 1 - J.first);
+    if (chunks > 0) load_do(s.NC - 1 - first);
+    if (!SCAN) {
 #pragma unroll 1
-    for (int n = 0; n < J.chunks; ++n) {
-        const int c = s.NC - 1 - J.first - n, st = n % Q::stages, t0 = c * C + L.wg * 16;
-        const bool more = n + 1 < J.chunks;
+        for (int n = -skip; n < min(1, chunks); ++n) L.clear_padding(s, (E *)a.o, s.NC - 1 - first - n);
+    }
+#pragma unroll 1
+    for (int n = 0; n < chunks; ++n) {
+        const int c = s.NC - 1 - first - n, st = n % Q::stages, t0 = c * C + L.wg * 16;
+        const bool more = n + 1 < chunks;
         const uint32_t ph = n & 1;
         const uint32_t qk = tc::smem_u32(smem + st * Q::stage), tp = qk + QK<E, KD>::bytes;
         const float *gates = (const float *)(smem + Q::stages * Q::stage + st * GATES) + L.wg * 16;
         const bool early = Q::stages == 2 && n > 0;  // P^T dO was issued a chunk ago
-        if (Q::stages == 2 && tid == 32 && more) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, true);
+        if (Q::stages == 2 && tid == 32 && more) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, first, true);
         __syncwarp();
         put_terms<H4 / 2, NT>(L.lanes + COL_S + L.wg * (H4 / 2), KD / 2, S);
         if (!early) put_do();
@@ -1091,8 +1116,8 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
         }
         __syncwarp();
         if (!SCAN) {
-            store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
-            store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, s.T), f);
+            store_col(a.deltas + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, L.len), f);
+            store_col((E *)a.o + L.head * s.V + L.v + t0 * L.row, L.row, L.tokens(t0, L.len), f);
             L.template store_part<3, 4>(s, kept, S);
         }
         wait(&bar->m4, ph, a.ctrl, ab, 0x625);
@@ -1102,13 +1127,13 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) seq_bwd_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(last, S[i0 + i], f[i]);
         }
-        if (Q::stages == 1 && tid == 32 && more) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, J.first, true);
+        if (Q::stages == 1 && tid == 32 && more) seq_load<E, KD>(a, smem, bar, J.b, J.h, n + 1, first, true);
         __syncwarp();
     }
     if (J.identity) L.store_trans(a.trans + ((J.seg * s.B + J.b) * (long long)s.Hv + J.h) * (NT * KD * KD * 2), S);
     else if (SCAN) L.store(s, a.starts + J.seg * all + L.head * KV, S);
     else if (J.seg == a.segments - 1) L.store(s, a.sT ? a.sT + L.head * KV : nullptr, S);
-    if (tid == 32) seq_drain<E, KD>(bar, J.chunks);
+    if (tid == 32) seq_drain<E, KD>(bar, chunks);
     seq_finish(bar);
 }
 
@@ -1263,6 +1288,21 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
     const int b = id % s.B, c = id / s.B;
     const int len = length_of(s, b);
     volatile int *ab = &abort_s;
+    if (c * C >= len) {  // (what seq_bwd keeps of a chunk ends with the tokens)
+        const int n = min(C, s.T - c * C);
+        const long long all = (long long)s.T * s.B * s.Hk * s.K;
+        for (int i = tid; i < 2 * n * s.K; i += GRAD_THREADS) {
+            const int of = i / (n * s.K), j = i % (n * s.K);
+            const long long at = (((long long)(c * C + j / s.K) * s.B + b) * s.Hk + hk) * s.K + j % s.K;
+            if constexpr (PARTS) a.parts[(2 * part + of) * all + at] = 0.f;
+            else ((E *)(of ? a.dk : a.dq))[at] = from_f<E>(0.f);
+        }
+        for (long long i = tid; i < (long long)n * heads; i += GRAD_THREADS) {
+            const long long at = ((c * C + i / heads) * s.B + b) * s.Hv + h0 + i % heads;
+            a.dg[at] = a.dbeta[at] = 0.f;
+        }
+        return;
+    }
     if (tid == 0) {
         tc::mbar_init(&loaded, 1);
         tc::mbar_init(&m1, 1);
@@ -1542,7 +1582,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) grad_kernel(const __grid_cons
                 if (wg * H4 + i0 + g2 * 8 >= s.K) continue;
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = f[g2 * 8 + i] + (isq ? 0.f : e[g2 * 8 + i]);
+                for (int i = 0; i < 8; ++i) x[i] = t < len ? f[g2 * 8 + i] + (isq ? 0.f : e[g2 * 8 + i]) : 0.f;
                 if constexpr (PARTS) {
                     *(float4 *)(out_part + i0 + g2 * 8) = make_float4(x[0], x[1], x[2], x[3]);
                     *(float4 *)(out_part + i0 + g2 * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);

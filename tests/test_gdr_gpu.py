@@ -502,3 +502,77 @@ def test_segments_against_pieces(shape, dt):
         assert off(getattr(gone, n), torch.cat([getattr(g, n) for g in grads])) <= 2.0 ** -16 + half
     for n in ("dg", "dbeta"):
         assert off(getattr(gone, n), torch.cat([getattr(g, n) for g in grads])) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [9, 100, 1500])
+def test_state_of_a_sequence_without_tokens(T, dt):
+    """NaN and infinities in the state (or its gradient) of an empty place of the batch stay there, bit by bit; its outputs
+    and gradients are zero and the other sequences' what they were."""
+    x, dout, dsT = make(T, 3, 1, 2, 64, 72, dt)
+    lengths = torch.tensor([T, 0, T - 1], dtype=torch.int32, device="cuda")
+    names = ("q", "k", "v", "g", "beta")
+
+    def run(x, dsT):
+        few = L.gdr_forward(**x, lengths=lengths)
+        st = L.gdr_forward(**x, lengths=lengths, save=True)
+        return few, st, L.gdr_backward(st, *(x[n] for n in names), dout=dout, dsT=dsT, lengths=lengths)
+
+    want = run(x, dsT)
+    y, ds = {n: t.clone() for n, t in x.items()}, dsT.clone()
+    y["s0"][1, 0, 3, ::5] = float("nan")
+    y["s0"][1, 1, ::7] = float("inf")
+    ds[1, 0, ::9] = float("nan")
+    got = run(y, ds)
+    bits = lambda t: t.view(torch.int32)  # noqa: E731
+    for a, b in zip(got[:2], want[:2]):
+        assert torch.equal(a.o, b.o) and torch.equal(a.sT[::2], b.sT[::2]) and torch.equal(bits(a.sT[1]), bits(y["s0"][1]))
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        g = getattr(got[2], n)
+        assert torch.equal(g, getattr(want[2], n)) and not g[:, 1].any(), n
+    assert torch.equal(got[2].ds0[::2], want[2].ds0[::2]) and torch.equal(bits(got[2].ds0[1]), bits(ds[1]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [9, 100, 1500])
+def test_state_of_a_sequence_without_tokens(T, dt):
+    """NaN and infinities in the state (or its gradient) of an empty place of the batch stay there, bit by bit; its outputs
+    and gradients are zero and the other sequences' what they were."""
+    x, dout, dsT = make(T, 3, 1, 2, 64, 72, dt)
+    lengths = torch.tensor([T, 0, T - 1], dtype=torch.int32, device="cuda")
+    names = ("q", "k", "v", "g", "beta")
+
+    def run(x, dsT):
+        few = L.gdr_forward(**x, lengths=lengths)
+        st = L.gdr_forward(**x, lengths=lengths, save=True)
+        return few, st, L.gdr_backward(st, *(x[n] for n in names), dout=dout, dsT=dsT, lengths=lengths)
+
+    want = run(x, dsT)
+    y, ds = {n: t.clone() for n, t in x.items()}, dsT.clone()
+    y["s0"][1, 0, 3, ::5] = float("nan")
+    y["s0"][1, 1, ::7] = float("inf")
+    ds[1, 0, ::9] = float("nan")
+    got = run(y, ds)
+    bits = lambda t: t.view(torch.int32)  # noqa: E731
+    for a, b in zip(got[:2], want[:2]):
+        assert torch.equal(a.o, b.o) and torch.equal(a.sT[::2], b.sT[::2]) and torch.equal(bits(a.sT[1]), bits(y["s0"][1]))
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        g = getattr(got[2], n)
+        assert torch.equal(g, getattr(want[2], n)) and not g[:, 1].any(), n
+    assert torch.equal(got[2].ds0[::2], want[2].ds0[::2]) and torch.equal(bits(got[2].ds0[1]), bits(ds[1]))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("shape", [(300, 4, 1, 3, 40, 136), (1500, 3, 1, 1, 64, 64), (260, 40, 2, 4, 128, 24)], ids=str)
+def test_chunks_of_padding(shape, dt):
+    """Sequences that end chunks before the longest (in other segments of a split one): as the same sequences alone, padding
+    zero, the kept states those of the end."""
+    x, dout, dsT = make(*shape, dt)
+    T, B = shape[:2]
+    lengths = torch.tensor([(T, 1, 64, 65, 130, T - 64, 0)[b % 7] for b in range(B)], dtype=torch.int32, device="cuda")
+    st, gr = check(x, dout, dsT, lengths=lengths)
+    for b, n in enumerate(lengths.tolist()):
+        for t in (st.o, gr.dq, gr.dk, gr.dv, gr.dg, gr.dbeta):
+            assert not t[n:, b].any()
+        for c in range(-(-n // 64), -(-T // 64)):
+            assert torch.equal(st.states[c, b], st.sT[b])
