@@ -765,6 +765,8 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
     _flat(logits, targets=targets)
     _shaped(targets, "targets", (N,))
     _need(temperature > 0, "temperature must be positive")
+    if not 0 <= top <= LOGPROB_MAX_TOP:  # (before the outputs are allocated)
+        raise LstmError(LSTM_ERR_INVALID_ARG if top < 0 else LSTM_ERR_UNSUPPORTED, "lstm_logprob_fwd")
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return logprobs(logits, targets, top, temperature)

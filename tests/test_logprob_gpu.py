@@ -372,3 +372,10 @@ def test_gradient_of_rows_far_apart(V, dt):
     assert L.logprobs_backward(L.logprobs(padded), padded).stride(0) < V
     near = wide.view(300, V)[:, : V - 60]  # a padded vocabulary keeps its stride
     assert L.logprobs_backward(L.logprobs(near), near).stride() == near.stride()
+
+
+@pytest.mark.parametrize("top", [-1, -5, 65, 1 << 40])
+def test_number_of_alternatives_is_refused_first(top):
+    """Before outputs of that many are allocated (or their number is cut to an int)."""
+    with pytest.raises(L.LstmError, match="lstm_logprob_fwd"):
+        L.logprobs(torch.randn(2, 100, device="cuda"), top=top)
