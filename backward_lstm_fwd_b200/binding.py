@@ -636,15 +636,27 @@ def _elsewhere(t: torch.Tensor, stream) -> bool:
     return stream is not None or torch.cuda.current_device() != t.get_device()
 
 
-def _there(t: torch.Tensor, stream):
+def _there(t: torch.Tensor, stream, *used):
     """Context that makes the tensor's device current, or a stream of it: what
-    a call allocates then belongs to the stream it works on."""
+    a call allocates then belongs to the stream it works on.  The tensors that
+    a given stream uses are known to the allocator: their memory is not reused
+    before the call is done, even if the caller lets go of them at once."""
     if stream is None:
         return torch.cuda.device(t.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device)
     _need(stream.device == t.device, "stream is on another device")
+    for u in (t, *used):
+        if u is not None:
+            u.record_stream(stream)
     return torch.cuda.stream(stream)
+
+
+def _used_here(*kept) -> None:
+    """What a forward kept is used on another stream than it was made on."""
+    for u in kept:
+        if u is not None:
+            u.record_stream(torch.cuda.current_stream(u.device))
 
 
 def _here(t: torch.Tensor) -> int:
@@ -668,7 +680,7 @@ def embed(ids, table, scale: float = 1.0, out=None, stream=None) -> torch.Tensor
     _sizes(N, vocab, I)
     _shaped(out, "out", shape, table.dtype)
     if _elsewhere(table, stream):
-        with _there(table, stream):
+        with _there(table, stream, ids, out):
             return embed(ids, table, scale, out)
     if out is None:
         out = table.new_empty(*shape)
@@ -695,7 +707,7 @@ def embed_backward(ids, dx, vocab: int, scale: float = 1.0, out=None, accumulate
     _sizes(N, vocab, I)
     _shaped(out, "out", (vocab, I), torch.float32)
     if _elsewhere(dx, stream):
-        with _there(dx, stream):
+        with _there(dx, stream, ids, out, ws):
             return embed_backward(ids, dx, vocab, scale, out, accumulate, ws)
     if out is None:
         out = dx.new_empty(vocab, I, dtype=torch.float32)
@@ -711,8 +723,8 @@ class LogProbs:
     """Outputs of one logprobs() call (float32; top_ids int32), kept for the
     backward.  logp is None without targets, top_ids / top_logp with top = 0."""
 
-    def __init__(self, N, top, has_targets, inv_temp, logits):
-        self.inv_temp = inv_temp
+    def __init__(self, N, top, has_targets, inv_temp, logits, made_on):
+        self.inv_temp, self.made_on = inv_temp, made_on  # (a raw stream)
         # one allocation: rows of N for stats (2), entropy and logp, then top_logp and top_ids
         self._buf = buf = logits.new_empty(4 + 2 * top, N, dtype=torch.float32)
         self.entropy = buf[2]
@@ -768,13 +780,14 @@ def logprobs(logits, targets=None, top: int = 0, temperature: float = 1.0,
     if not 0 <= top <= LOGPROB_MAX_TOP:  # (before the outputs are allocated)
         raise LstmError(LSTM_ERR_INVALID_ARG if top < 0 else LSTM_ERR_UNSUPPORTED, "lstm_logprob_fwd")
     if _elsewhere(logits, stream):
-        with _there(logits, stream):
+        with _there(logits, stream, targets):
             return logprobs(logits, targets, top, temperature)
-    st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits)
+    here = _here(logits)
+    st = LogProbs(N, top, targets is not None, 1.0 / temperature, logits, here)
     d = LogprobDims(N, vocab, ld, top, dtype_code(logits.dtype), _id_bytes(targets))
     _run(load().lstm_logprob_fwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
                                  _at(st.logp), _at(st.entropy), _at(st._buf), _at(st.top_ids),
-                                 _at(st.top_logp), _here(logits)), "lstm_logprob_fwd")
+                                 _at(st.top_logp), here), "lstm_logprob_fwd")
     return st
 
 
@@ -794,8 +807,11 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     _shaped(out, "out", (N, vocab), logits.dtype)
     _need(1.0 / temperature == st.inv_temp, "temperature differs from the forward's")
     if _elsewhere(logits, stream):
-        with _there(logits, stream):
+        with _there(logits, stream, targets, dlogp, dentropy, out):
             return logprobs_backward(st, logits, targets, dlogp, dentropy, temperature, out)
+    here = _here(logits)
+    if here != st.made_on:
+        _used_here(st._buf)
     ldd = ld
     if out is not None:
         ldd = _rows(out, "out")
@@ -808,7 +824,7 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     d = LogprobDims(N, vocab, ld, 0, dtype_code(logits.dtype), _id_bytes(targets))
     _run(load().lstm_logprob_bwd(ctypes.byref(d), _at(logits), _at(targets), st.inv_temp,
                                  _at(st._buf), _at(st.entropy), _at(dlogp), _at(dentropy),
-                                 _at(out), ldd, _here(logits)), "lstm_logprob_bwd")
+                                 _at(out), ldd, here), "lstm_logprob_bwd")
     return out
 
 
@@ -839,10 +855,10 @@ class GdrState:
     """Outputs of one gdr_forward() call; states, deltas and ws (save=True; ws
     only where the call allocated it) are kept for the backward."""
 
-    def __init__(self, d: GdrDims, q, save, sT=None, scale=None, lengths=None):
+    def __init__(self, d: GdrDims, q, save, sT=None, scale=None, lengths=None, made_on=None):
         f = torch.float32
         T, B, H, K, V = d.T, d.B, d.Hv, d.K, d.V
-        self.dims, self.scale, self.lengths = d, scale, lengths
+        self.dims, self.scale, self.lengths, self.made_on = d, scale, lengths, made_on
         self.o = q.new_empty(T, B, H, V)
         self.sT = q.new_empty(B, H, K, V, dtype=f) if sT is None else sT
         self.states = self.deltas = self.ws = None
@@ -911,9 +927,10 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     _shaped(s0, "s0", state, torch.float32)
     _shaped(sT, "sT", state, torch.float32)
     if _elsewhere(q, stream):
-        with _there(q, stream):
+        with _there(q, stream, k, v, g, beta, s0, lengths, sT, ws):
             return gdr_forward(q, k, v, g, beta, s0, lengths, scale, save, sT, ws)
-    st = GdrState(d, q, save, sT, opt.scale, lengths)
+    here = _here(q)
+    st = GdrState(d, q, save, sT, opt.scale, lengths, here)
     if ws is None and (save or d.T > GDR_STEP_TOKENS):
         ws = _workspace(q, gdr_fwd_workspace_size(d, save))
         if save:
@@ -921,7 +938,7 @@ def gdr_forward(q, k, v, g, beta, s0=None, lengths=None, scale=None, save: bool 
     _run(load().lstm_gdr_fwd(ctypes.byref(d), ctypes.byref(opt), _at(q), _at(k), _at(v), _at(g),
                              _at(beta), _at(s0), _at(st.o), _at(st.sT), _at(st.states),
                              _at(st.deltas), _at(ws), _ws_bytes(ws) if ws is not None else 0,
-                             _here(q)), "lstm_gdr_fwd")
+                             here), "lstm_gdr_fwd")
     return st
 
 
@@ -947,15 +964,18 @@ def gdr_backward(st: GdrState, q, k, v, g, beta, dout=None, dsT=None, lengths=No
     _need(_sizes_of(d) == _sizes_of(st.dims), "the state belongs to a forward of other sizes")
     _need(opt.scale == st.scale, f"scale {opt.scale} differs from the forward's {st.scale}")
     if _elsewhere(q, stream):
-        with _there(q, stream):
+        with _there(q, stream, k, v, g, beta, dout, dsT, lengths, ws):
             return gdr_backward(st, q, k, v, g, beta, dout, dsT, lengths, scale, ws)
     _same_lengths(st.lengths, lengths, d.T)
+    here = _here(q)
+    if here != st.made_on:
+        _used_here(st.states, st.deltas, st.ws)
     gr = GdrGrads(d, q.dtype, q.device)
     if ws is None:
         ws = _workspace(q, gdr_bwd_workspace_size(d))
     _run(load().lstm_gdr_bwd(ctypes.byref(d), ctypes.byref(opt), _at(dout), _at(dsT), _at(q),
                              _at(k), _at(v), _at(g), _at(beta), _at(st.states), _at(st.deltas),
                              _at(gr.dq), _at(gr.dk), _at(gr.dv), _at(gr.dg), _at(gr.dbeta),
-                             _at(gr.ds0), _at(st.ws), _at(ws), _ws_bytes(ws), _here(q)),
+                             _at(gr.ds0), _at(st.ws), _at(ws), _ws_bytes(ws), here),
          "lstm_gdr_bwd")
     return gr

@@ -143,3 +143,52 @@ def test_stream_argument():
         got = run(stream=stream)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_inputs_let_go_while_another_stream_works():
+    """Temporaries given to a call on another stream, and a state used on another stream than it was made on: their memory
+    is not handed out again before the call is done."""
+    p = parameters()
+    ids = torch.arange(T * B, device="cuda").view(T, B) % VOCAB
+    t = torch.arange(300, device="cuda")
+    logits = torch.randn(300, 2111, device="cuda")
+    five = [f.contiguous().repeat(4, 5, *[1] * (f.dim() - 2)) for f in project(p, torch.randn(T, B, H, device="cuda"))]
+    lp = L.logprobs(logits, t)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    for call, inputs in (
+            (lambda i, w, **kw: [L.embed(i, w, **kw)], [ids, torch.randn(VOCAB, 20000, device="cuda")]),
+            (lambda i, d, **kw: [L.embed_backward(i, d, VOCAB, **kw)], [ids, torch.randn(T, B, 3000, device="cuda")]),
+            (lambda x, t, **kw: [L.logprobs(x, t, **kw).logp], [logits, t]),
+            (lambda x, t, g, **kw: [L.logprobs_backward(lp, x, t, dlogp=g, **kw)], [logits, t, torch.rand(300, device="cuda")]),
+            (lambda *f, **kw: [L.gdr_forward(*f, **kw).o], five),
+            (lambda *f, **kw: [L.gdr_forward(*(x[:5] for x in f), **kw).o], five)):
+        want = call(*inputs)
+        given = [x.clone() for x in inputs]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # (some 50 ms)
+        got = call(*given, stream=side)
+        del given
+        again = [torch.ones_like(x) for x in inputs]  # would take the places of what was let go
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del again
+    # states
+    st = L.gdr_forward(*five, save=True)
+    want, wd = L.gdr_backward(st, *five, dout=st.o), L.logprobs_backward(lp, logits, t, dlogp=lp.entropy)
+    with torch.cuda.stream(side):
+        side.wait_stream(here)
+        st, lp = L.gdr_forward(*five, save=True), L.logprobs(logits, t)
+        dout, dl = st.o.clone(), lp.entropy.clone()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    got, gd = L.gdr_backward(st, *five, dout=dout), L.logprobs_backward(lp, logits, t, dlogp=dl)
+    sizes = [x.numel() * x.element_size() for x in (st.states, st.deltas, st.ws, lp._buf)]
+    del st, lp
+    with torch.cuda.stream(side):
+        again = [torch.full((n,), 1, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    assert torch.equal(gd, wd)
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(getattr(got, n), getattr(want, n)), n
+    del again
