@@ -725,6 +725,7 @@ class LogProbs:
 
     def __init__(self, N, top, has_targets, inv_temp, logits, made_on):
         self.inv_temp, self.made_on = inv_temp, made_on  # (a raw stream)
+        self.vocab = logits.shape[1]
         # one allocation: rows of N for stats (2), entropy and logp, then top_logp and top_ids
         self._buf = buf = logits.new_empty(4 + 2 * top, N, dtype=torch.float32)
         self.entropy = buf[2]
@@ -806,6 +807,7 @@ def logprobs_backward(st: LogProbs, logits, targets=None, dlogp=None, dentropy=N
     _shaped(st.entropy, "the state's entropy", (N,))
     _shaped(out, "out", (N, vocab), logits.dtype)
     _need(1.0 / temperature == st.inv_temp, "temperature differs from the forward's")
+    _need(vocab == st.vocab, "the state belongs to a forward of another vocabulary")
     if _elsewhere(logits, stream):
         with _there(logits, stream, targets, dlogp, dentropy, out):
             return logprobs_backward(st, logits, targets, dlogp, dentropy, temperature, out)

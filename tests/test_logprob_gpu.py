@@ -379,3 +379,14 @@ def test_number_of_alternatives_is_refused_first(top):
     """Before outputs of that many are allocated (or their number is cut to an int)."""
     with pytest.raises(L.LstmError, match="lstm_logprob_fwd"):
         L.logprobs(torch.randn(2, 100, device="cuda"), top=top)
+
+
+def test_state_of_another_forward():
+    """Rows of another width (a padded vocabulary, or the same without its padding) are another softmax."""
+    x = torch.randn(5, 120, device="cuda")
+    st = L.logprobs(x[:, :100])
+    for y in (x, x[:, :99], x[:4, :100]):
+        with pytest.raises(ValueError):
+            L.logprobs_backward(st, y, dentropy=torch.ones(len(y), device="cuda"))
+    with pytest.raises(ValueError, match="temperature"):
+        L.logprobs_backward(st, x[:, :100], dentropy=torch.ones(5, device="cuda"), temperature=2.0)
