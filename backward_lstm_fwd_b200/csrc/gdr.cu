@@ -49,10 +49,15 @@ bool stepwise(const lstm_gdr_dims *d, bool save) { return !save && d->T <= LSTM_
 int terms_of(int dtype) { return dtype == LSTM_BF16 ? 1 : dtype == LSTM_F16 ? 2 : 3; }
 
 // Segments of the chunk sequence (see SeqArgs): the number with the lowest
-// estimated time, from microseconds per chunk of a pass that writes its
-// outputs (4.0) and of one that does not (3.2), per joined segment (3.0) and
-// for two more launches (8), measured on a B200; 1 where splitting gains less
-// than a tenth.
+// estimate, from weights of a chunk of a pass that writes its outputs (4.0; it
+// takes 5.1 us, 7.1 with the states), of one that does not (3.2; 4.1 us), of a
+// joined segment (3.0; about 4 us) and of two more launches (8); 1 where
+// splitting gains less than a tenth.  Measured for K = V = 128, bf16, us of a
+// forward whole / split, heads x chunks: 4 x 8 53 / 56, 4 x 128 571 / 161, 16 x 32
+// 166 / 106, 32 x 16 99 / 94, 64 x 32 225 / 229, 128 x 16 164 / 213; of a forward
+// that keeps its states and its backward: 4 x 128 1548 / 409, 32 x 16 303 / 268, 64 x
+// 32 734 / 720.  Of 4 to 128 heads and 8 to 128 chunks the choice is within 4 % of
+// the best, but for 32 x 64 (302, where three segments take 278).
 struct Split {
     int segments, chunks;
 };

@@ -29,10 +29,13 @@
 // Numbers.  The contractions run on the tensor cores in bf16 with float
 // accumulators, every float operand split into three bf16 terms (8 + 8 + 8
 // bits of its 24) and the products of orders 0, 1 and 2 kept: what is dropped
-// is 2^-24 of the operands, below the rounding of a float sum.  bf16 inputs are
-// one term, fp16 two, fp32 three, each exactly the input.  Running sums of g
-// are double: b_i - b_j of a float sum would lose the digits that a strong
-// decay needs between its neighbours.
+// is 2^-24 of the operands, below the rounding of a float sum.  (An accumulator
+// drops what lies below its last place at every step; the small products come first,
+// so that few steps meet the full sum.  Errors in norm: 1e-7 to 3e-7 of o, the states
+// and their gradient, up to 1.7e-6 of dq and dk at V = 256, sums of four passes.)
+// bf16 inputs are one term, fp16 two, fp32 three, each exactly the input.  Running
+// sums of g are double: b_i - b_j of a float sum would lose the digits that a
+// strong decay needs between its neighbours.
 #pragma once
 
 #include "host.cuh"
@@ -601,9 +604,9 @@ __global__ void __launch_bounds__(128, 5) prep_kernel(PrepArgs a) {
 // Bound: the chain's latency (three products and three passes over registers
 // a chunk) where there are few heads.  512 threads rather than 256: a pass
 // over the registers is short code for many warps (with 256 threads the warps
-// waited for instructions more than for anything else).  bf16, K = V = 128: 6.6
-// us a chunk, forward with the states stored or backward alike; 256 heads of 16
-// chunks, up to two blocks an SM in turn, 217 us and 213 us.
+// waited for instructions more than for anything else).  bf16, K = V = 128: 7.1
+// us a chunk forward with the states stored, 5.1 without, 6.8 backward; 256 heads of
+// 16 chunks, up to two blocks an SM in turn, 227 us and 218 us.
 constexpr int SEQ_THREADS = 512;
 // tensor-memory columns: S terms, then left U terms | K S, Q S, then K^T (left
 // U) | R terms, then U terms | X, then P U
@@ -623,8 +626,8 @@ template <class E, int KD> struct Seq {
 // zero state, which leaves B, and from the identity, which leaves A; scan_kernel
 // joins them to every segment's start, and a second pass runs all segments at
 // once.  (seg: chunks of a segment, in the order of the pass.)  16 heads of 128
-// chunks: 91 us to scan, 21 to join, 107 to run, 267 with the preparation, against
-// 16 SMs that walk 128 chunks each at 6.6 us.
+// chunks on 8 key heads: 90 us to scan, 21 to join, 112 to run, 274 with the
+// preparation (on 16 key heads 289, where 16 SMs that walk 128 chunks each take 648).
 struct SeqArgs {
     Shape s;
     const char *qk, *tp;
@@ -1217,7 +1220,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 1) scan_kernel(const __grid_const
 //
 // Bound by the conversions between the products (every operand is a float that
 // becomes three terms) and by the one block an SM that the tiles leave room for:
-// bf16, K = V = 128, 2048 blocks of two value heads 465 us, 0.94 GB at 2.0 TB/s,
+// bf16, K = V = 128, 2048 blocks of two value heads 461 us, 0.94 GB at 2.0 TB/s,
 // the tensor cores busy 36 % of the time.
 constexpr int GRAD_THREADS = 512;
 // [q; k] k^T | F over G, then Y over Z | E, then the transposed triangle's product | [dQ; dK]

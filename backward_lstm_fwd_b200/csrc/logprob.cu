@@ -349,11 +349,11 @@ __device__ __forceinline__ float bound_of(float mine, int top, float *maxima, un
 }
 
 // ----------------------------------------------------------------- forward
-// 8192 x 32000 bf16: 93 us, 524 MB at 5.6 TB/s (the exponentials and their packed
+// 8192 x 32000 bf16: 97 us, 524 MB at 5.4 TB/s (the exponentials and their packed
 // sums share the issue slots with the loads; a block that walks rows and loads the
 // next one's beginning before it joins a row took 110 to 118); with 8
-// alternatives 2048 x 100003 bf16 100 us, 410 MB at 4.1 TB/s: the quarter looked
-// at twice and the joins of a row.  4 x 128000 float, 20 alternatives: 12 us, the
+// alternatives 2048 x 100003 bf16 104 us, 410 MB at 3.9 TB/s: the quarter looked
+// at twice and the joins of a row.  4 x 128000 float, 20 alternatives: 13 us, the
 // latency of one row's steps.
 // Block (r, p): part p of row r; the parts of a row are a cluster.  TOP:
 // alternatives wanted.
@@ -484,8 +484,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNarrow ? 8 : 1) fwd_kerne
         if (count <= kCand) {
             rank_keys<THREADS>(cand, count, a.top, best);
         } else {
-            // More candidates than the list holds (long runs of equal values):
-            // one exact pass over the part per alternative.
+            // More candidates than the list holds (long runs of equal values, or
+            // fewer unmasked ones than `top` in the first look): one exact pass
+            // over the part per alternative.  2048 x 100003 bf16, three quarters
+            // masked: 8 alternatives 2.3 ms, 64 16 ms; 4 x 128000 float 39 and 200 us.
             unsigned long long prev = ~0ull;
             for (int k = 0; k < a.top; ++k) {
                 unsigned long long mine = 0;

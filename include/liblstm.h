@@ -399,6 +399,7 @@ int lstm_embed_bwd(const lstm_embed_dims *d, const void *ids, const void *dx, fl
  *   q, k   [T][B][Hk][K]  compute type   (row t*B + n at a stride of ldq, ldk)
  *   v      [T][B][Hv][V]  compute type   (ldv)
  *   g      [T][B][Hv]     float, log decay, <= 0 as a rule; -inf forgets all
+ *                         (in chunks, sums of g above 87 overflow)
  *   beta   [T][B][Hv]     float
  *   s0     [B][Hv][K][V]  float, or NULL for zero
  * outputs (overwritten):
@@ -484,6 +485,11 @@ int lstm_gdr_bwd(const lstm_gdr_dims *d, const lstm_gdr_options *opt, const void
  * their size, are logits like any other.)  A row of nothing but -inf has logp and
  * top_logp -inf, entropy 0 and a zero gradient.  A NaN or +inf makes its row's
  * values NaN (NaN is listed after every number).
+ * Alternatives are found in one pass where the first quarter (top > 16: third) of
+ * a row has `top` unmasked, distinct logits in it; rows masked to fewer there, or
+ * of long runs of equal ones, take a pass for each alternative (2048 x 100003
+ * bf16: 2.3 ms instead of 0.1 for 8, 16 ms instead of 0.2 for 64; 4 rows of
+ * 128000 float: 39 us instead of 15 for 8, 200 instead of 24 for 64).
  *
  * lstm_logprob_bwd: dlogits [N][vocab] (type dtype, row stride ldd), the
  * gradient for dlogp [N] and dentropy [N] (float, either NULL):
