@@ -8,6 +8,7 @@ machines without a GPU driver; only its compute calls need a device.
 """
 from __future__ import annotations
 
+import contextlib
 import glob
 import os
 import re
@@ -46,9 +47,10 @@ def _sweep(*dirs: str) -> None:
     """Remove what builds that were killed have left (their process is gone)."""
     for path in (f for d in dirs for f in glob.glob(os.path.join(d, "*.tmp[0-9]*"))):
         try:
-            os.kill(int(re.search(r"\.tmp(\d+)", path).group(1)), 0)
+            os.kill(int(re.search(r"\.tmp(\d+)", os.path.basename(path)).group(1)), 0)
         except ProcessLookupError:
-            os.remove(path)
+            with contextlib.suppress(FileNotFoundError):  # (another build swept it)
+                os.remove(path)
         except PermissionError:  # someone else's, and alive
             pass
 

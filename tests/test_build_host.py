@@ -26,6 +26,8 @@ exit 0
 
 @pytest.fixture()
 def tree(tmp_path, monkeypatch):
+    tmp_path = tmp_path / f"in.tmp{os.getpid()}"  # (a folder's own name says nothing)
+    tmp_path.mkdir()
     csrc = tmp_path / "csrc"
     csrc.mkdir()
     for n in ("a", "b", "c"):
