@@ -576,3 +576,26 @@ def test_chunks_of_padding(shape, dt):
             assert not t[n:, b].any()
         for c in range(-(-n // 64), -(-T // 64)):
             assert torch.equal(st.states[c, b], st.sT[b])
+
+
+def test_lengths_change_between_replays():
+    """A captured step reads its lengths when it is replayed: whole chunks of padding come and go."""
+    x, dout, dsT = make(1500, 3, 1, 2, 64, 72, "bf16")
+    names = ("q", "k", "v", "g", "beta")
+    five = [x[n] for n in names]
+    lengths = torch.tensor([1500, 1500, 1500], dtype=torch.int32, device="cuda")
+    L.gdr_forward(**x, save=True, lengths=lengths)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st = L.gdr_forward(**x, save=True, lengths=lengths)
+        gr = L.gdr_backward(st, *five, dout=dout, dsT=dsT, lengths=lengths)
+    for now in ([1500, 0, 64], [65, 1400, 1], [0, 0, 0], [1500, 1500, 1500]):
+        lengths.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = L.gdr_forward(**x, save=True, lengths=lengths)
+        wg = L.gdr_backward(want, *five, dout=dout, dsT=dsT, lengths=lengths)
+        assert torch.equal(st.o, want.o) and torch.equal(st.sT, want.sT) and torch.equal(st.states, want.states)
+        for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"):
+            assert torch.equal(getattr(gr, n), getattr(wg, n)), (now, n)

@@ -192,3 +192,30 @@ def test_inputs_let_go_while_another_stream_works():
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert torch.equal(getattr(got, n), getattr(want, n)), n
     del again
+
+
+def test_other_streams_inside_a_graph():
+    """Calls on a stream forked from a captured one, their inputs' memory known to the allocator there too."""
+    ids = torch.arange(T * B, device="cuda").view(T, B) % VOCAB
+    table, dx, logits = torch.randn(VOCAB, I, device="cuda"), torch.randn(T, B, I, device="cuda"), torch.randn(T * B, VOCAB, device="cuda")
+    five = [t.contiguous() for t in project(parameters(), torch.randn(T, B, H, device="cuda"))]
+
+    def run(**kw):
+        gs = L.gdr_forward(*(f + 0 for f in five), save=True, **kw)
+        lp = L.logprobs(logits, ids.reshape(-1), **kw)
+        return [L.embed(ids, table, **kw), L.embed_backward(ids, dx, VOCAB, **kw), gs.o, L.gdr_backward(gs, *five, dout=gs.o, **kw).dk,
+                lp.logp, L.logprobs_backward(lp, logits, ids.reshape(-1), dlogp=lp.entropy, **kw)]
+
+    want = run()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = run(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
